@@ -21,13 +21,18 @@ MSA_OK = 0
 STATUS = {0: "MSA_OK", -1: "MSA_ERR_INVALID_ARG", -2: "MSA_ERR_UNSUPPORTED", -3: "MSA_ERR_CUDA",
           -4: "MSA_ERR_WORKSPACE", -5: "MSA_ERR_BAD_TABLE", -6: "MSA_ERR_TIMEOUT"}
 FLAG_BAD_PAGE, FLAG_BAD_LENGTH, FLAG_TIMEOUT, FLAG_BAD_IDS, FLAG_BAD_SLOT = 0x1, 0x2, 0x4, 0x8, 0x10
+FLAG_NO_PAGE, FLAG_BAD_SEQ = 0x20, 0x40
+TYPE_E4M3, TYPE_BF16, TYPE_F16, TYPE_F32 = 0, 1, 2, 3
+MAX_PLANES = 16
 
 # symbols include/msa.h declares (checked by the CPU tests)
 EXPORTS = ("msa_status_string", "msa_workspace_size", "msa_workspace_init", "msa_get_error", "msa_index_scores",
            "msa_block_maxpool_topk", "msa_select_blocks", "msa_select_blocks_noalloc", "msa_sparse_attn_decode",
            "msa_decode", "msa_dequant_rows", "msa_kv_insert_nvfp4", "msa_select_blocks_exact",
            "msa_select_blocks_noalloc_get_error", "msa_dcp_local_topk", "msa_dcp_merge_topk",
-           "msa_selftest_wait_timeout", "msa_sparse_attn_decode_small_rows")
+           "msa_selftest_wait_timeout", "msa_sparse_attn_decode_small_rows", "msa_kv8_append",
+           "msa_kv8_attn_workspace_size", "msa_kv8_attn", "msa_pages_workspace_size", "msa_pages_copy",
+           "msa_pages_fork", "msa_pages_reserve", "msa_pages_free", "msa_pages_compact")
 
 
 class MSAError(RuntimeError):
@@ -56,6 +61,42 @@ class KvInsertArgs(ctypes.Structure):
                 ("k_data", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_data", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
                 ("ki_data", ctypes.c_void_p), ("ki_scale", ctypes.c_void_p)]
+
+
+class Kv8AppendArgs(ctypes.Structure):
+    """Mirror of msa_kv8_append_args."""
+    _fields_ = [("num_reqs", ctypes.c_int32), ("total_rows", ctypes.c_int32), ("max_rows_per_req", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_pages_per_req", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("src_type", ctypes.c_int32),
+                ("k_token_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64),
+                ("context_lens", ctypes.c_void_p), ("q_indptr", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_data", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_data", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class Kv8AttnArgs(ctypes.Structure):
+    """Mirror of msa_kv8_attn_args."""
+    _fields_ = [("num_reqs", ctypes.c_int32), ("total_rows", ctypes.c_int32), ("max_rows_per_req", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_pages_per_req", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("q_per_kv", ctypes.c_int32), ("n_block_ids", ctypes.c_int32),
+                ("q_type", ctypes.c_int32), ("sm_scale", ctypes.c_float), ("q_row_stride", ctypes.c_int64),
+                ("context_lens", ctypes.c_void_p), ("q_indptr", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("block_ids", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k_data", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_data", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
+
+
+class PagePlane(ctypes.Structure):
+    """Mirror of msa_page_plane."""
+    _fields_ = [("data", ctypes.c_void_p), ("strips", ctypes.c_int32), ("slot_bytes", ctypes.c_int32),
+                ("page_bytes", ctypes.c_int32)]
+
+
+class PagePoolArgs(ctypes.Structure):
+    """Mirror of msa_page_pool."""
+    _fields_ = [("num_seqs", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
+                ("num_planes", ctypes.c_int32), ("seq_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("ref_counts", ctypes.c_void_p), ("planes", PagePlane * MAX_PLANES)]
 
 
 _lock = threading.Lock()
@@ -93,6 +134,16 @@ def load(path: str = LIB_PATH):
             lib.msa_dcp_local_topk.argtypes = [ap, i32, i32, vp, vp, sz, vp]
             lib.msa_dcp_merge_topk.argtypes = [ap, i32, i32, i32, vp, vp, vp, sz, vp]
             lib.msa_selftest_wait_timeout.argtypes = [vp, sz, vp]
+            lib.msa_kv8_append.argtypes = [ctypes.POINTER(Kv8AppendArgs), vp, sz, vp]
+            lib.msa_kv8_attn_workspace_size.argtypes = [ctypes.POINTER(Kv8AttnArgs), ctypes.POINTER(sz)]
+            lib.msa_kv8_attn.argtypes = [ctypes.POINTER(Kv8AttnArgs), vp, sz, vp]
+            pp = ctypes.POINTER(PagePoolArgs)
+            lib.msa_pages_workspace_size.argtypes = [pp, ctypes.POINTER(sz)]
+            lib.msa_pages_copy.argtypes = [pp, i32, vp, vp, vp, vp, sz, vp]
+            lib.msa_pages_fork.argtypes = [pp, i32, vp, vp, vp, sz, vp]
+            lib.msa_pages_reserve.argtypes = [pp, i32, vp, vp, vp, sz, vp]
+            lib.msa_pages_free.argtypes = [pp, i32, vp, vp, sz, vp]
+            lib.msa_pages_compact.argtypes = [pp, vp, vp, vp, vp, sz, vp]
             for f in EXPORTS[1:]:
                 getattr(lib, f).restype = ctypes.c_int
             _lib = lib

@@ -84,6 +84,45 @@ struct KvInsertParams {
   uint32_t* flags;
 };
 
+constexpr int kKv8MaxHeads = 64, kKv8MaxQPerKv = 64, kKv8MaxIds = 32;
+
+// Append to the 8-bit cache (msa_kv8_append).
+struct Kv8AppendParams {
+  int num_reqs, total_rows, max_rows, num_pages, max_pages, num_kv_heads;
+  const int32_t* context_lens;
+  const int32_t* q_indptr;
+  const int32_t* block_table;
+  const void* k;
+  const void* v;
+  long long k_stride, v_stride;  // elements between tokens
+  uint8_t* k_data;
+  float* k_scale;
+  uint8_t* v_data;
+  float* v_scale;
+  uint32_t* flags;
+};
+
+// Attention over the 8-bit cache (msa_kv8_attn).
+struct Kv8AttnParams {
+  int num_reqs, total_rows, max_rows, num_pages, max_pages, num_kv_heads, q_per_kv;
+  int n_ids;                 // block ids per (request, KV head), 0: every block
+  const int32_t* context_lens;
+  const int32_t* q_indptr;
+  const int32_t* block_table;
+  const int32_t* block_ids;
+  const void* q;
+  long long q_stride;        // elements between rows of q
+  const uint8_t* k_data;
+  const float* k_scale;
+  const uint8_t* v_data;
+  const float* v_scale;
+  float sm_scale_log2;       // sm_scale * log2(e)
+  uint32_t* flags;
+  uint16_t* out;
+  float* lse;
+};
+cudaError_t launch_kv8_attn(const Kv8AttnParams& prm, bool q_bf16, int sm_count, cudaStream_t st);
+
 // Merge of the rank-local candidate lists of indexer decode context parallelism
 // (msa_dcp_merge_topk).
 struct DcpMergeParams {

@@ -87,6 +87,8 @@ typedef enum {
 #define MSA_FLAG_TIMEOUT     0x4u   /* an mbarrier / async-copy wait hit its time limit */
 #define MSA_FLAG_BAD_IDS     0x8u   /* msa_sparse_attn_decode got a block id outside the context, or msa_dcp_merge_topk a bad candidate list */
 #define MSA_FLAG_BAD_SLOT    0x10u  /* msa_kv_insert_nvfp4 got a slot on a page outside [0, num_pages) */
+#define MSA_FLAG_NO_PAGE     0x20u  /* msa_pages_fork / msa_pages_reserve ran out of free pages */
+#define MSA_FLAG_BAD_SEQ     0x40u  /* a page operator got a sequence id outside the table, listed twice, or a fork target that is not empty */
 
 typedef struct {
   int32_t num_reqs;            /* B >= 0 */
@@ -328,6 +330,182 @@ typedef struct {
 } msa_kv_insert_args;
 
 msa_status msa_kv_insert_nvfp4(const msa_kv_insert_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- 8-bit cache
+ *
+ * A second paged K/V cache, for layers and models whose keys and values are kept in 8 bits:
+ * E4M3 codes with one FP32 scale for each block of tokens (a 128-token page) and KV head,
+ *   k_data, v_data   [P][H][128][128]  (H = num_kv_heads)   k_scale, v_scale   [P][H]
+ * and the stored value is E4M3(code) * scale. Pages, block tables, lengths and row
+ * pointers are those of msa_decode_args. Data pointers must be 16-byte aligned. Scales are
+ * 0 or in [2^-60, 2^60]. */
+typedef enum { MSA_TYPE_E4M3 = 0, MSA_TYPE_BF16 = 1, MSA_TYPE_F16 = 2, MSA_TYPE_F32 = 3 } msa_type;
+
+/* Append: request b's R = q_indptr[b+1] - q_indptr[b] new tokens, rows q_indptr[b] .. of
+ * k and v, are quantised into positions N - R .. N - 1 of its pages, N = context_lens[b]
+ * (which counts them). For a page and KV head, with f the first slot written there:
+ *   need  = the smallest power of two s >= 2^-60 with |x| <= 448 s for every finite new x
+ *   scale = need if f = 0 (the page starts anew, whatever it held), else
+ *           max(need, old scale rounded up to a power of two)
+ *   slots >= f written: code = E4M3(x / scale), nearest, ties to even, saturating
+ *   slots <  f, when the scale changed: code = E4M3(E4M3(code) * old / scale)
+ * E4M3 is a floating format, so a power-of-two scale costs no precision against any other
+ * and a later growth of the scale re-rounds only what falls among the subnormals. An
+ * infinity saturates to 448 scales and takes no part in `need`; a NaN stays a NaN. An old
+ * scale that is not positive and finite counts as 0 (the old slots become 0). Slots past
+ * the new tokens are left as they are. A NULL source (k or v) leaves its planes untouched
+ * (its plane pointers may then be NULL).
+ * Two requests that write into the same page race; the caller keeps written pages
+ * unshared (msa_pages_fork does). A page id outside [0, num_pages) skips that page and sets
+ * MSA_FLAG_BAD_PAGE; inconsistent lengths or row pointers skip the request and set
+ * MSA_FLAG_BAD_LENGTH. ws is any workspace of at least 256 bytes, zero-filled once. */
+typedef struct {
+  int32_t num_reqs;            /* 0 .. 4096 */
+  int32_t total_rows;          /* rows of k and v = q_indptr[B] (host copy) */
+  int32_t max_rows_per_req;    /* upper bound on any request's rows, >= 1 */
+  int32_t num_pages;
+  int32_t max_pages_per_req;   /* row length of block_table */
+  int32_t num_kv_heads;        /* 1 .. 64 */
+  int32_t src_type;            /* MSA_TYPE_BF16, _F16 or _F32 */
+  int64_t k_token_stride;      /* elements from a token's first head to the next token's, >= 128 H; */
+  int64_t v_token_stride;      /*   the heads of a token are contiguous; 16-byte multiples */
+  const int32_t* context_lens; /* [B] */
+  const int32_t* q_indptr;     /* [B+1] */
+  const int32_t* block_table;  /* [B][max_pages_per_req] */
+  const void* k;               /* [total_rows][H][128] src_type, or NULL; 16-byte aligned */
+  const void* v;
+  uint8_t* k_data;
+  float* k_scale;
+  uint8_t* v_data;
+  float* v_scale;
+} msa_kv8_append_args;
+
+msa_status msa_kv8_append(const msa_kv8_append_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention over the 8-bit cache: row r of request b sits at position N - R + r and sees
+ * the keys at positions <= its own, of all blocks (block_ids NULL) or of the listed ones:
+ *   out[row][head] = sum_t softmax_t(sm_scale q . k_t) v_t,  lse = ln(sum_t exp(sm_scale q . k_t)).
+ * Query head h uses KV head h / q_per_kv. Any number of rows per request: single tokens,
+ * speculative rows and whole prompts (causal) take the same call. A row that sees no key
+ * gets 0 and lse -inf. NaN and infinities in slots that a row does not see never reach it.
+ *
+ * Queries are E4M3 codes or BF16. Sums are FP32; softmax weights are rounded to FP16 for
+ * the product with V, the output to BF16. A BF16 query row is taken as the sum of two E4M3
+ * rows times a power of two (8 + 8 bits of significand for elements down to 2^-14 of
+ * the row's largest, an absolute error below 2^-18 of it for smaller ones).
+ *
+ * block_ids [B][H][n_block_ids]: logical blocks of each (request, KV head), in any order,
+ * -1 = unused; an id outside the context, or one listed twice, sets MSA_FLAG_BAD_IDS and
+ * is left out (the second time). Blocks on pages outside [0, num_pages) are left out and set
+ * MSA_FLAG_BAD_PAGE; inconsistent lengths set MSA_FLAG_BAD_LENGTH and the request's rows are
+ * left unwritten. Rows past q_indptr[B] are left as they are. */
+typedef struct {
+  int32_t num_reqs;            /* 0 .. 4096 */
+  int32_t total_rows;          /* query rows = q_indptr[B] (host copy) */
+  int32_t max_rows_per_req;    /* upper bound on any request's rows, >= 1 */
+  int32_t num_pages;
+  int32_t max_pages_per_req;
+  int32_t num_kv_heads;        /* 1 .. 64 */
+  int32_t q_per_kv;            /* 1 .. 64 */
+  int32_t n_block_ids;         /* 1 .. 32 with block_ids, else 0 */
+  int32_t q_type;              /* MSA_TYPE_E4M3 or MSA_TYPE_BF16 */
+  float sm_scale;              /* > 0 */
+  int64_t q_row_stride;        /* elements between rows of q, >= 128 H q_per_kv; a 16-byte multiple */
+  const int32_t* context_lens; /* [B] */
+  const int32_t* q_indptr;     /* [B+1] */
+  const int32_t* block_table;  /* [B][max_pages_per_req] */
+  const int32_t* block_ids;    /* [B][H][n_block_ids] or NULL */
+  const void* q;               /* [total_rows][H q_per_kv][128], 16-byte aligned */
+  const uint8_t* k_data;
+  const float* k_scale;
+  const uint8_t* v_data;
+  const float* v_scale;
+  uint16_t* out;               /* [total_rows][H q_per_kv][128] BF16 bits, 16-byte aligned */
+  float* lse;                  /* [total_rows][H q_per_kv] FP32, or NULL */
+} msa_kv8_attn_args;
+
+/* Bytes of workspace msa_kv8_attn needs for `args` on the current device (by the sizes in
+ * args and the SM count; not by the lengths). Host-only. */
+msa_status msa_kv8_attn_workspace_size(const msa_kv8_attn_args* args, size_t* bytes);
+
+/* ws: 256-byte aligned, zero-filled once (msa_workspace_init); rules as above. */
+msa_status msa_kv8_attn(const msa_kv8_attn_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- pages
+ *
+ * A pool of pages shared by sequences, and the operators that move them. All state is on
+ * the device and no call synchronises: seq_lens and block_table are the context_lens and
+ * block_table of the decode calls, ref_counts[p] says how many block-table rows hold page p
+ * (0 = free). A sequence of n tokens holds the first ceil(n / 128) entries of its row; the
+ * others are never read.
+ *
+ * The caches that live on the pages are given as planes. A plane with slot_bytes > 0 holds,
+ * for each page, `strips` runs of 128 slots of slot_bytes (a multiple of 8): K codes of the
+ * NVFP4 cache are 4 strips of 64-byte slots. One with slot_bytes = 0 holds page_bytes (a
+ * multiple of 4) that belong to the page as a whole, such as the scales of the 8-bit cache.
+ * Data pointers are 16-byte aligned. At most 2^20 pages and 2^20 sequences.
+ *
+ * Lists (src, dst, parents, ...) are device arrays of n int32. Sequence and page ids outside
+ * the pool set MSA_FLAG_BAD_SEQ or MSA_FLAG_BAD_PAGE, and their entry does nothing. */
+#define MSA_MAX_PLANES 16
+typedef struct {
+  void* data;
+  int32_t strips;
+  int32_t slot_bytes;
+  int32_t page_bytes;          /* of planes with slot_bytes = 0 */
+} msa_page_plane;
+
+typedef struct {
+  int32_t num_seqs;            /* rows of block_table */
+  int32_t num_pages;
+  int32_t max_pages_per_seq;   /* row length of block_table */
+  int32_t num_planes;          /* 0 .. MSA_MAX_PLANES */
+  int32_t* seq_lens;           /* [num_seqs] */
+  int32_t* block_table;        /* [num_seqs][max_pages_per_seq] */
+  int32_t* ref_counts;         /* [num_pages] */
+  msa_page_plane planes[MSA_MAX_PLANES];
+} msa_page_pool;
+
+/* Bytes of workspace the page operators need (by num_seqs and num_pages). Host-only. */
+msa_status msa_pages_workspace_size(const msa_page_pool* pool, size_t* bytes);
+
+/* Copy page src[i] to page dst[i] in every plane, i < n: the first tokens[i] slots of each
+ * strip exactly (tokens NULL: all 128), and what the page keeps once. Reads and writes no
+ * counts or tables (seq_lens, block_table and ref_counts may be NULL). A negative src or
+ * dst skips the pair; so does src = dst; tokens outside 0 .. 128 set MSA_FLAG_BAD_LENGTH. Targets are distinct and no target is a source of
+ * the same call (they would race). */
+msa_status msa_pages_copy(const msa_page_pool* pool, int32_t n, const int32_t* src, const int32_t* dst,
+                          const int32_t* tokens, void* ws, size_t ws_bytes, void* stream);
+
+/* Fork: child[i] becomes a copy of parents[i]. Full pages are shared (their counts grow by
+ * one); a partly filled last page is copied to a free page, so that both can append. The
+ * free pages are the lowest ids with count 0, given out in list order. All parents are
+ * read as they were before the call. A child must be an empty sequence (length 0) and
+ * appear once (MSA_FLAG_BAD_SEQ otherwise; of a repeated child the first entry stands).
+ * When the free pages run out, this and all later entries that need one do nothing
+ * (MSA_FLAG_NO_PAGE). n <= num_seqs. */
+msa_status msa_pages_fork(const msa_page_pool* pool, int32_t n, const int32_t* parents, const int32_t* children,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/* Grow seqs[i] to new_lens[i] tokens: free pages (lowest ids first, in list order) are put
+ * behind its pages as needed, and its length is set. A length that is not larger changes
+ * nothing. MSA_FLAG_BAD_LENGTH: longer than the row; MSA_FLAG_NO_PAGE and MSA_FLAG_BAD_SEQ
+ * as for msa_pages_fork. n <= num_seqs. */
+msa_status msa_pages_reserve(const msa_page_pool* pool, int32_t n, const int32_t* seqs, const int32_t* new_lens,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/* End seqs[i]: the counts of its pages fall by one, its length becomes 0 (its row is left as
+ * it is). A sequence listed twice is freed once. A count that is already 0 stays 0 and
+ * sets MSA_FLAG_BAD_PAGE. */
+msa_status msa_pages_free(const msa_page_pool* pool, int32_t n, const int32_t* seqs, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/* Compact: with L pages live (count > 0), those with ids >= L move to the free ids below L,
+ * the k-th of them to the k-th, in every plane; new_block_table and new_ref_counts get the
+ * tables after the move (they may be the pool's own: in place; entries that no sequence holds
+ * are copied as they are). num_live (device, one int32, or NULL) gets L. */
+msa_status msa_pages_compact(const msa_page_pool* pool, int32_t* new_block_table, int32_t* new_ref_counts,
+                             int32_t* num_live, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
