@@ -82,6 +82,19 @@ msa_status encode_code_map(CUtensorMap* map, const uint8_t* base, long long rows
   return r == CUDA_SUCCESS ? MSA_OK : MSA_ERR_CUDA;
 }
 
+// 2-D view of an 8-bit plane [rows][128 bytes], boxes of 128 rows, 128-byte swizzle.
+msa_status encode_kv8_map(CUtensorMap* map, const uint8_t* base, long long rows) {
+  if (get_encode_fn() != cudaSuccess) return MSA_ERR_CUDA;
+  cuuint64_t dims[2] = {kDim, static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {kDim};
+  cuuint32_t box[2] = {kDim, static_cast<cuuint32_t>(kBlock)};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MSA_OK : MSA_ERR_CUDA;
+}
+
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -117,11 +117,14 @@ struct Kv8AttnParams {
   const uint8_t* v_data;
   const float* v_scale;
   float sm_scale_log2;       // sm_scale * log2(e)
+  int chunk, chunk_log2;     // query rows of an item: a power of two, at most 128
   uint32_t* flags;
+  uint8_t* parts;            // workspace: the CTAs' headers and partials
   uint16_t* out;
   float* lse;
 };
-cudaError_t launch_kv8_attn(const Kv8AttnParams& prm, bool q_bf16, int sm_count, cudaStream_t st);
+cudaError_t launch_kv8_attn(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8AttnParams& prm, bool q_bf16,
+                            int grid, cudaStream_t st);
 
 // Merge of the rank-local candidate lists of indexer decode context parallelism
 // (msa_dcp_merge_topk).
@@ -188,6 +191,7 @@ cudaError_t launch_dequant_rows(const uint8_t* codes, const uint8_t* scales, lon
 msa_status validate(const msa_decode_args* a, bool need_kv, bool need_idx);
 msa_status check_device(int* sm_count);
 msa_status encode_code_map(CUtensorMap* map, const uint8_t* base, long long rows);
+msa_status encode_kv8_map(CUtensorMap* map, const uint8_t* base, long long rows);
 msa_status launch_selection(const msa_decode_args* args, int mode, int32_t* ids, float* scores_out, float* tok,
                             long long stride, uint32_t* flags, float* block_S, int sm_count, cudaStream_t st,
                             bool with_topk = true, int shard = 0, int nshards = 1, uint64_t* dcp_keys = nullptr);

@@ -1,16 +1,47 @@
 // Attention over the 8-bit cache (msa_kv8_attn): E4M3 keys and values with one FP32 scale for
 // each 128-token page and KV head.
 //
-// For a query row at position p, keys t <= p of the listed blocks (or of all):
-//   s_t = sm_scale k_scale (q . k_t),  out = sum_t 2^(s_t log2e - m) v_scale v_t / sum_t 2^(s_t log2e - m)
-// with the running maximum m and sum of an online softmax in FP32.
+// For a query row at position p, over the keys t <= p of the listed blocks (or of all), with
+// x_t = sm_scale log2(e) k_scale (q . k_t) + log2(v_scale):
+//   out = sum_t 2^(x_t - m) v_t / sum_t 2^(x_t - m) / v_scale_t,  m the running maximum of x,
+// an online softmax in FP32. The value scale sits in the exponent, so the weights that meet the
+// V codes have one range whatever the pages' scales are, and the sum divides it out again.
 //
-// This form is the plain one: a CTA of 128 threads per (query row, query head), a thread per key
-// of a page for the scores and a thread per dim for the products with V.
+// Products. S = Q K^T is an FP8 product straight from the cache's bytes: K is copied into
+// shared memory and never converted. BF16 queries become two E4M3 rows, q = (hi + lo) 2^e (8
+// significant bits = two 4-bit significands), so S costs two FP8 products instead of a
+// conversion of K. P V runs in FP16: V codes are widened (exact), P is FP16 (an E4M3 P loses
+// 2^-4 of a weight, and two E4M3 parts lose weights below 2^-18 of the largest, which a long
+// context's tail adds up to).
+//
+// Bound: memory for few rows (a token and head is 256 bytes; the MMAs of a 128-token tile take
+// less than its copy), tensor and exponential rate for prompts.
+//
+// Work. An item is a (request, KV head, chunk of query rows); its tiles are the pages its
+// last row sees, or its block ids. All items' tiles form one line that the CTAs (one per SM)
+// take in equal contiguous ranges, so ragged lengths balance and one long request uses the whole
+// GPU. A CTA's part of an item is a segment; segments that are not whole items leave (O, m, l)
+// in the workspace and kv8_merge_kernel joins them (log-sum-exp), in tile order: no atomics,
+// the same bits every time.
+//
+// A CTA's M = rows x q_per_kv query rows are repeated C = 4, 2 or 1 times down the 128 rows of
+// the MMA tile; copy c takes tokens 128 c / C .. of every tile with its own maximum and sum, so
+// that few rows still spread the exponentials over all four SM sub-partitions (P is zero in the
+// other copies' columns). Roles, as in the sparse attention over the NVFP4 cache (msa_attn.cu):
+//   * load warp: finds the tiles (32 block-table entries and scales at a time, one per lane) and
+//     copies K and V of a tile (16 KB each) into a 3-stage ring; what the others need of a
+//     tile or segment goes into small rings beside it;
+//   * 8 converting warps in two groups taking alternate tiles: V to FP16, rows past the context
+//     to zero; the group that has a segment's first tile also lays out its queries;
+//   * S warp, and a P V warp for each of the two softmax sets;
+//   * 8 softmax warps in two sets taking alternate tiles, each with its own O in tensor memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cudaTypedefs.h>
 
+#include <climits>
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 
 #include "msa_common.cuh"
@@ -19,96 +50,906 @@
 namespace msa {
 namespace {
 
-__device__ __forceinline__ float e4m3_f32(uint32_t c) {
+constexpr int kSoftWarps = 8;                        // warps 0..7: two sets of 4, one per TMEM lane quadrant
+constexpr int kMmaWarp = 8, kPvWarp0 = 9, kLoadWarp = 11;
+constexpr int kCvWarp0 = 12, kCvWarps = 8;           // two groups of 4
+constexpr int kThreads = (kCvWarp0 + kCvWarps) * 32;
+constexpr int kStages = 3;
+// A wait on a barrier's parity has to be for its current phase or the one before. The two
+// converting groups take alternate tiles, so V stages signal through 2 x 3 barriers, each of
+// which serves one group; a group loads the queries of some segments only, so the freeing of
+// the query tile goes round 4 barriers (at most two segments are in that state).
+constexpr int kVBars = 2 * kStages, kQBars = 4;
+constexpr int kRing = 16;                            // tiles and segments whose description is kept
+constexpr int kRows = 8;                             // segments whose query scales and NaN marks are kept
+constexpr uint32_t kTileBytes = kBlock * kDim;       // K or V of a tile
+constexpr uint32_t kHalfBytes = kBlock * 128;        // FP16 V: 128 tokens x 64 dims
+constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
+constexpr float kRescaleLog2 = 8.f;                  // O is rescaled when the maximum grows by more than 2^8
+constexpr int kNoPos = 1 << 30;                      // position of a tile that nobody sees
+constexpr int kRedStride = 17;
+constexpr int kMergeThreads = 256;
+
+struct Tile {
+  int pos0;      // position of its first token
+  int nvalid;    // tokens inside the context; 0: nothing to read
+  int seg;       // the CTA's segment
+  int last;      // last tile of that segment
+  int end;       // no tile: the CTA's work is over
+  int vzero;     // the page's value scale is 0
+  float kscale, vscale;
+};
+
+struct Seg {
+  int first;     // its first tile
+  int row0;      // first query row
+  int rows;
+  int head;      // KV head
+  int pos;       // position of row0
+  int slot;      // -1: a whole item, else the CTA's partial 0 or 1
+};
+
+template <int NP>
+struct Smem {
+  uint8_t q[NP][kTileBytes];                         // A of S: copies of the query rows, by part
+  uint8_t k[kStages][kTileBytes];                    // B of S (K-major), 128-byte swizzle
+  uint8_t v[kStages][kTileBytes];                    // V codes, 128-byte swizzle
+  uint8_t v16[2][2][kHalfBytes];                     // B of O (MN-major): [set][half][token][64 dims]
+  float red[2][128 * kRedStride];                    // copies of a row joined, 16 dims at a time
+  float qscale[kRows][128];                          // 2^e of each tile row (BF16 queries)
+  int nanpos[kRows][kDim];                           // first position with a NaN value in a dim, of partly seen tokens
+  int nanany[kRows];
+  float xm[2][128], xl[2][128];
+  Tile tile[kRing];
+  Seg seg[kRing];
+  uint64_t k_full[kStages], v_full[kVBars], k_empty[kStages], v_empty[kStages];
+  uint64_t q_full, q_free[kQBars], s_full[2], p_full[2], v16_full[2], pv_done[2], drain[3];
+  uint64_t sets_met, set_met[2];                     // the softmax warps of both sets, or of one, have come here
+  long long part[kThreads / 32];
+  long long lo, hi;
+  int start_b;
+  long long start_off;
+  uint32_t taddr;
+};
+static_assert(sizeof(Smem<2>) + 1024 <= 227 * 1024, "shared memory a CTA may opt into");
+static_assert(offsetof(Smem<2>, k) % 1024 == 0 && offsetof(Smem<2>, v16) % 1024 == 0 && offsetof(Smem<1>, k) % 1024 == 0,
+              "swizzled tiles");
+
+// What a CTA leaves for the merge: [grid] headers, then 2 partials for each CTA.
+struct Header {
+  int tail;          // 1: partial 1 starts an item that goes on in the next CTA's partial 0
+  int row0, rows, head;
+  int cont;          // 1: partial 0 is a part of an item that an earlier CTA started
+  int cont_end;      //    and its last one
+  int pad[2];
+};
+constexpr long long kPartFloats = 128LL * kDim + 256;  // O, m, l
+__host__ __device__ inline size_t headers_bytes(int grid) { return (grid * sizeof(Header) + 255) / 256 * 256; }
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t* flags) {
+  return mbar_try(bar, parity) || mbar_wait(bar, parity, flags);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t c) {  // the low two codes
   uint32_t h;
-  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(h) : "r"(c & 0xFFu));
-  return __half2float(__low2half(*reinterpret_cast<const __half2*>(&h)));
+  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(h) : "r"(c));
+  return h;
+}
+__device__ __forceinline__ uint32_t f32x2_e4m3x2(float a, float b) {  // a in the low byte
+  uint32_t r;
+  asm("{ .reg .b16 t; cvt.rn.satfinite.e4m3x2.f32 t, %2, %1; cvt.u32.u16 %0, t; }" : "=r"(r) : "f"(a), "f"(b));
+  return r;
 }
 
-__device__ __forceinline__ float cta_max(float v, float* s) {
-  for (int d = 16; d; d /= 2) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-  __syncthreads();
-  return v;
+// ---- the line of tiles
+struct Req {
+  int N, R, r0;
+};
+__device__ __forceinline__ bool load_req(const Kv8AttnParams& p, int b, Req* q) {
+  q->N = p.context_lens[b];
+  q->r0 = p.q_indptr[b];
+  q->R = p.q_indptr[b + 1] - q->r0;
+  return q->N >= 0 && q->N <= p.max_pages * static_cast<long long>(kBlock) && q->R >= 0 && q->R <= p.max_rows &&
+         q->R <= q->N && q->r0 >= 0 && q->r0 <= p.total_rows - q->R;
 }
-__device__ __forceinline__ float cta_sum(float v, float* s) {
-  for (int d = 16; d; d /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = (s[0] + s[1]) + (s[2] + s[3]);
-  __syncthreads();
-  return v;
+__device__ __forceinline__ int chunks_of(const Kv8AttnParams& p, int R) { return (R + p.chunk - 1) >> p.chunk_log2; }
+// Tiles of row chunk i: the pages up to its last row's position.
+__device__ __forceinline__ int tiles_of(const Kv8AttnParams& p, const Req& q, int i) {
+  if (p.n_ids) return p.n_ids;
+  const int end = (i + 1) << p.chunk_log2;
+  const int last = q.N - q.R + (end < q.R ? end : q.R) - 1;
+  return (last >> 7) + 1;
+}
+// Tiles of the chunks before i (i at most the last chunk, so each of them is whole). With
+// base = N - R - 1 = 128 a + r0 and u = 128 / chunk chunks to a page, chunk k has
+// 1 + a + floor((r0 / chunk + k + 1) / u) tiles; the floors sum in closed form.
+__device__ __forceinline__ long long tiles_before(const Kv8AttnParams& p, const Req& q, int i) {
+  if (p.n_ids) return static_cast<long long>(i) * p.n_ids;
+  const int base = q.N - q.R - 1, a = base >> 7, c0 = (base & 127) >> p.chunk_log2, lu = 7 - p.chunk_log2;
+  auto floors = [lu](long long m) {  // sum of j >> lu over j < m
+    const long long w = m >> lu, rem = m & ((1LL << lu) - 1);
+    return (w * (w - 1) / 2 << lu) + w * rem;
+  };
+  return static_cast<long long>(i) * (1 + a) + floors(c0 + i + 1LL) - floors(c0 + 1LL);
+}
+// Tiles of one KV head of the request.
+__device__ __forceinline__ long long head_tiles(const Kv8AttnParams& p, const Req& q) {
+  if (q.R == 0) return 0;
+  const int n = chunks_of(p, q.R);
+  return tiles_before(p, q, n - 1) + tiles_of(p, q, n - 1);
 }
 
-template <bool kBf16>
-__global__ void __launch_bounds__(128) kv8_attn_kernel(const Kv8AttnParams p) {
-  __shared__ float q[kDim], w[kBlock], red[4];
-  const int row = blockIdx.x, head = blockIdx.y, tid = threadIdx.x, h = head / p.q_per_kv;
-  const int heads = p.num_kv_heads * p.q_per_kv;
-  int lo = 0, hi = p.num_reqs;  // the last request with q_indptr[b] <= row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (p.q_indptr[mid] <= row) lo = mid;
-    else hi = mid;
+// C copies of the query rows down the MMA tile (128 / C rows each); NP = E4M3 parts of a query.
+template <int C, int NP>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                    const Kv8AttnParams p) {
+  constexpr int kMpad = 128 / C;
+  extern __shared__ uint8_t smem_raw[];
+  Smem<NP>& sm = *reinterpret_cast<Smem<NP>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.q_per_kv;
+
+  pdl_launch_dependents();  // the merge waits for this grid's end; its CTAs may be set up before
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&sm.k_full[s]), 1);
+      mbar_init(smem_u32(&sm.k_empty[s]), 1);
+      mbar_init(smem_u32(&sm.v_empty[s]), kCvWarps / 2);
+    }
+    mbar_init(smem_u32(&sm.q_full), kCvWarps / 2);
+    for (int s = 0; s < kVBars; ++s) mbar_init(smem_u32(&sm.v_full[s]), 1);
+    for (int s = 0; s < kQBars; ++s) mbar_init(smem_u32(&sm.q_free[s]), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&sm.s_full[s]), 1);
+      mbar_init(smem_u32(&sm.p_full[s]), kSoftWarps / 2);
+      mbar_init(smem_u32(&sm.v16_full[s]), kCvWarps / 2);
+      mbar_init(smem_u32(&sm.pv_done[s]), 1);
+    }
+    for (int s = 0; s < 3; ++s) mbar_init(smem_u32(&sm.drain[s]), 1);
+    mbar_init(smem_u32(&sm.sets_met), kSoftWarps);
+    for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&sm.set_met[s]), kSoftWarps / 2);
+    mbar_fence_init();
+    sm.lo = sm.hi = 0;
   }
-  const int b = lo, N = p.context_lens[b], r0 = p.q_indptr[b], R = p.q_indptr[b + 1] - r0;
-  const bool ok = N >= 0 && N <= p.max_pages * static_cast<long long>(kBlock) && R >= 0 && R <= p.max_rows && R <= N &&
-                  r0 >= 0 && r0 <= p.total_rows - R;
-  if (!ok || row >= r0 + R || row < r0) {
-    if (!ok && tid == 0) set_flag(p.flags, kFlagBadLength);
-    return;
+  for (int i = tid; i < kRows * kDim; i += kThreads) (&sm.nanpos[0][0])[i] = INT_MAX;
+  if (tid < kRows) sm.nanany[tid] = 0;
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(&sm.taddr), kTmemCols);
+  if (warp == kLoadWarp && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
   }
-  if (kBf16)
-    q[tid] = __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[row * p.q_stride + head * kDim + tid]);
-  else
-    q[tid] = e4m3_f32(static_cast<const uint8_t*>(p.q)[row * p.q_stride + head * kDim + tid]);
-  __syncthreads();
-  const int nb = (N + kBlock - 1) / kBlock, pos = N - R + (row - r0);
-  const int32_t* ids = p.n_ids ? p.block_ids + (static_cast<long long>(b) * p.num_kv_heads + h) * p.n_ids : nullptr;
-  const int tiles = ids ? p.n_ids : pos / kBlock + 1;
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int j = 0; j < tiles; ++j) {
-    const int c = ids ? ids[j] : j;
-    if (c < 0 || c >= nb) {
-      if (c != -1 && tid == 0) set_flag(p.flags, kFlagBadIds);
-      continue;
+
+  // ---- this CTA's range of the line: every thread sums a run of requests
+  {
+    const int per = (p.num_reqs + kThreads - 1) / kThreads;
+    const int b0 = tid * per < p.num_reqs ? tid * per : p.num_reqs;
+    const int b1 = b0 + per < p.num_reqs ? b0 + per : p.num_reqs;
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      Req q;
+      if (load_req(p, b, &q)) mine += p.num_kv_heads * head_tiles(p, q);
+      else if (blockIdx.x == 0) set_flag(p.flags, kFlagBadLength);
     }
-    bool twice = false;
-    for (int i = 0; ids && i < j; ++i) twice |= ids[i] == c;
-    if (twice) {
-      if (tid == 0) set_flag(p.flags, kFlagBadIds);
-      continue;
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl += o;
     }
-    const int phys = p.block_table[static_cast<long long>(b) * p.max_pages + c];
-    if (phys < 0 || phys >= p.num_pages) {
-      if (tid == 0) set_flag(p.flags, kFlagBadPage);
-      continue;
-    }
-    const long long ph = static_cast<long long>(phys) * p.num_kv_heads + h;
-    const int seen = pos - c * kBlock + 1 < kBlock ? pos - c * kBlock + 1 : kBlock;
-    float s = -INFINITY;
-    if (tid < seen) {
-      const uint8_t* k = p.k_data + (ph * kBlock + tid) * kDim;
-      s = 0.f;
-      for (int d = 0; d < kDim; ++d) s += q[d] * e4m3_f32(k[d]);
-      s *= p.k_scale[ph] * p.sm_scale_log2;
-    }
-    const float mx = cta_max(s, red);
-    const float m_new = fmaxf(m, mx), ref = m_new == -INFINITY ? 0.f : m_new;
-    const float e = tid < seen ? exp2f(s - ref) : 0.f, alpha = exp2f(m - ref);
-    w[tid] = e;
-    l = l * alpha + cta_sum(e, red);
-    o *= alpha;
-    const float vs = p.v_scale[ph];
-    for (int t = 0; t < seen; ++t) o += w[t] * vs * e4m3_f32(p.v_data[(ph * kBlock + t) * kDim + tid]);
-    m = m_new;
+    if (lane == 31) sm.part[warp] = incl;
     __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += sm.part[w];
+      total += sm.part[w];
+    }
+    // fewer tiles than CTAs: the last CTAs have none (a partial's continuation is in the next CTA)
+    const long long use = total < gridDim.x ? total : gridDim.x;
+    const long long lo = blockIdx.x < use ? total * blockIdx.x / use : 0;
+    const long long hi = blockIdx.x < use ? total * (blockIdx.x + 1) / use : 0;
+    long long at = before + incl - mine;
+    if (lo < hi && at <= lo && lo < at + mine) {  // the range starts among this thread's requests
+      for (int b = b0; b < b1; ++b) {
+        Req q;
+        const long long n = load_req(p, b, &q) ? p.num_kv_heads * head_tiles(p, q) : 0;
+        if (lo < at + n) {
+          sm.start_b = b;
+          sm.start_off = lo - at;
+          break;
+        }
+        at += n;
+      }
+      sm.lo = lo;
+      sm.hi = hi;
+    }
   }
-  const long long at = static_cast<long long>(row) * heads + head;
-  p.out[at * kDim + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(l == 0.f ? 0.f : o / l));
-  if (tid == 0 && p.lse != nullptr) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = sm.taddr;
+
+  if (warp == kLoadWarp) {
+    // ================= load warp
+    int t = 0, nseg = 0;
+    bool good = true;
+    Header hd = {};
+    // Waits until tile t's stage is free, writes its description and starts its copies.
+    auto emit = [&](int pos0, int nvalid, int last, int end, int phys_row, float ks, float vs) {
+      const int st = t % kStages;
+      if (t >= kStages) {
+        const uint32_t par = ((t / kStages) - 1) & 1;
+        good = wait_bar(smem_u32(&sm.k_empty[st]), par, p.flags) && wait_bar(smem_u32(&sm.v_empty[st]), par, p.flags);
+        good = __all_sync(0xFFFFFFFFu, good);
+        if (!good) return;
+      }
+      if (lane == 0) {
+        Tile& x = sm.tile[t % kRing];
+        x.pos0 = pos0;
+        x.nvalid = nvalid;
+        x.seg = nseg;
+        x.last = last;
+        x.end = end;
+        x.vzero = vs == 0.f;
+        x.kscale = ks;
+        x.vscale = vs == 0.f ? 1.f : vs;
+        const uint32_t kb = smem_u32(&sm.k_full[st]), vb = smem_u32(&sm.v_full[t % kVBars]);
+        if (nvalid > 0) {
+          mbar_arrive_expect_tx(kb, kTileBytes);
+          tma_load_2d(smem_u32(sm.k[st]), &kmap, 0, phys_row, kb);
+          mbar_arrive_expect_tx(vb, kTileBytes);
+          tma_load_2d(smem_u32(sm.v[st]), &vmap, 0, phys_row, vb);
+        } else {
+          mbar_arrive(kb);
+          mbar_arrive(vb);
+        }
+      }
+      __syncwarp();
+      ++t;
+    };
+
+    long long left = sm.hi - sm.lo;
+    if (left > 0) {
+      int b = sm.start_b;
+      Req q;
+      load_req(p, b, &q);
+      int h, ch, j0, n_ch = chunks_of(p, q.R);
+      {
+        const long long ht = head_tiles(p, q);
+        h = static_cast<int>(sm.start_off / ht);
+        const long long off = sm.start_off % ht;
+        int a = 0, e = n_ch;  // tiles_before(a) <= off < tiles_before(e)
+        while (e - a > 1) {
+          const int mid = (a + e) / 2;
+          if (tiles_before(p, q, mid) <= off) a = mid;
+          else e = mid;
+        }
+        ch = a;
+        j0 = static_cast<int>(off - tiles_before(p, q, a));
+      }
+      while (left > 0 && good) {
+        const int nt = tiles_of(p, q, ch);
+        const int j1 = j0 + left < nt ? static_cast<int>(j0 + left) : nt;
+        const int nb = (q.N + kBlock - 1) / kBlock;
+        const bool begin = j0 == 0, end = j1 == nt;
+        const int row0 = ch << p.chunk_log2, rows = q.R - row0 < p.chunk ? q.R - row0 : p.chunk;
+        const int32_t* table = p.block_table + static_cast<long long>(b) * p.max_pages;
+        // listed blocks: lane j holds id j; the ones of this segment that count
+        int id = -1;
+        unsigned use = 0u;
+        if (p.n_ids) {
+          if (lane < p.n_ids) id = p.block_ids[(static_cast<long long>(b) * p.num_kv_heads + h) * p.n_ids + lane];
+          const bool in = id >= 0 && id < nb;
+          const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
+          const bool twice = in && (__ffs(same) - 1) != lane;
+          if (ch == 0 && lane >= j0 && lane < j1 && ((!in && id != -1) || twice)) set_flag(p.flags, kFlagBadIds);
+          use = __ballot_sync(0xFFFFFFFFu, in && !twice && lane >= j0 && lane < j1);
+        }
+        const int count = p.n_ids ? (use ? __popc(use) : 1) : j1 - j0;
+        const int last = t + count - 1;
+        const int slot = begin && end ? -1 : (begin ? 1 : 0);
+        if (lane == 0) {
+          Seg& s = sm.seg[nseg % kRing];
+          s.first = t;
+          s.row0 = q.r0 + row0;
+          s.rows = rows;
+          s.head = h;
+          s.pos = q.N - q.R + row0;
+          s.slot = slot;
+        }
+        if (slot == 1) {
+          hd.tail = 1;
+          hd.row0 = q.r0 + row0;
+          hd.rows = rows;
+          hd.head = h;
+        } else if (slot == 0) {
+          hd.cont = 1;
+          hd.cont_end = end;
+        }
+        __syncwarp();
+        for (int base = p.n_ids ? 0 : j0; base < (p.n_ids ? 1 : j1) && good; base += 32) {
+          const int c = p.n_ids ? id : base + lane;
+          const bool on = p.n_ids ? (use >> lane) & 1u : c < j1;
+          int phys = -1;
+          float ks = 1.f, vs = 1.f;
+          if (on) {
+            phys = table[c];
+            if (phys < 0 || phys >= p.num_pages) {
+              set_flag(p.flags, kFlagBadPage);
+              phys = -1;
+            } else {
+              const long long ph = static_cast<long long>(phys) * p.num_kv_heads + h;
+              ks = p.k_scale[ph];
+              vs = p.v_scale[ph];
+            }
+          }
+          for (unsigned m = __ballot_sync(0xFFFFFFFFu, on); m != 0u && good; m &= m - 1u) {
+            const int src = __ffs(m) - 1;
+            const int cc = __shfl_sync(0xFFFFFFFFu, c, src), pp = __shfl_sync(0xFFFFFFFFu, phys, src);
+            const float kk = __shfl_sync(0xFFFFFFFFu, ks, src), vv = __shfl_sync(0xFFFFFFFFu, vs, src);
+            const int pos0 = cc * kBlock, nv = q.N - pos0 < kBlock ? q.N - pos0 : kBlock;
+            if (pp < 0) emit(kNoPos, 0, last, 0, 0, 1.f, 1.f);
+            else emit(pos0, nv, last, 0, (pp * p.num_kv_heads + h) * kBlock, kk, vv);
+          }
+        }
+        if (p.n_ids && use == 0u && good) emit(kNoPos, 0, last, 0, 0, 1.f, 1.f);
+        ++nseg;
+        left -= j1 - j0;
+        // the next item
+        j0 = 0;
+        if (left > 0 && ++ch == n_ch) {
+          ch = 0;
+          if (++h == p.num_kv_heads) {
+            h = 0;
+            do ++b; while (b < p.num_reqs && (!load_req(p, b, &q) || q.R == 0));
+            if (b == p.num_reqs) break;  // never, unless the lengths changed meanwhile
+            n_ch = chunks_of(p, q.R);
+          }
+        }
+      }
+    }
+    for (int e = 0; e < 2 && good; ++e) emit(kNoPos, 0, INT_MAX, 1, 0, 1.f, 1.f);
+    // no copy may still be landing when the CTA leaves
+    for (int j = t - kStages < 0 ? 0 : t - kStages; j < t; ++j) {
+      if (!wait_bar(smem_u32(&sm.k_full[j % kStages]), (j / kStages) & 1, p.flags)) break;
+      if (!wait_bar(smem_u32(&sm.v_full[j % kVBars]), (j / kVBars) & 1, p.flags)) break;
+    }
+    if (lane == 0) reinterpret_cast<Header*>(p.parts)[blockIdx.x] = hd;
+    __syncwarp();
+  } else if (warp >= kCvWarp0) {
+    // ================= converting warps: group g takes tiles t = g, g + 2, ...; thread = token
+    const int th = tid - kCvWarp0 * 32, grp = th >> 7, r = th & 127, r7 = r & 7;
+    for (int t = grp;; t += 2) {
+      const int st = t % kStages;
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.v_full[t % kVBars]), (t / kVBars) & 1, p.flags))) break;
+      const Tile x = sm.tile[t % kRing];
+      const Seg& sg = sm.seg[x.seg % kRing];
+      if (!x.end && sg.first == t) {
+        // the segment's queries, once the last segment's scores are computed
+        const int k = x.seg;
+        if (k > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.q_free[(k - 1) % kQBars]), ((k - 1) / kQBars) & 1, p.flags)))
+          break;
+        const int m = r % kMpad;
+        const bool real = m < G * sg.rows;
+        const long long at = real ? static_cast<long long>(sg.row0 + m / G) * p.q_stride + (sg.head * G + m % G) * kDim : 0;
+        const uint32_t row = smem_u32(sm.q[0]) + static_cast<uint32_t>(r) * 128u;
+        if constexpr (NP == 1) {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) + at);
+          uint4 v[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] = real ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            st_shared_v4(row + (static_cast<uint32_t>(c ^ r7) << 4), v[c].x, v[c].y, v[c].z, v[c].w);
+        } else {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at);
+          // largest magnitude by its bits: BF16 pairs, both halves at once
+          uint32_t big = 0u;
+#pragma unroll 4
+          for (int c = 0; c < 16; ++c) {
+            const uint4 v = real ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+            big = __vmaxu2(big, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                         __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+          }
+          const uint32_t amax = max(big & 0xFFFFu, big >> 16);
+          const bool odd = amax >= 0x7F80u;  // an infinity or a NaN: the whole row becomes NaN
+          // smallest 2^e with amax <= 448 2^e; below 2^-120 nothing a score could show is left
+          int e = static_cast<int>(amax >> 7) - 127 - 8 + ((amax & 0x7Fu) > 0x60u ? 1 : 0);
+          e = e < -120 ? -120 : e;
+          const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          sm.qscale[k % kRows][r] = odd ? 1.f : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          const uint32_t row2 = row + kTileBytes;
+#pragma unroll 2
+          for (int c = 0; c < 8; ++c) {  // 16 elements: 16 code bytes of each part
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint4 v = real ? src[2 * c + u] : make_uint4(0u, 0u, 0u, 0u);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float a = __uint_as_float(w[i] << 16) * inv, b2 = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
+                const uint32_t hc = f32x2_e4m3x2(a, b2);
+                const uint32_t hh = e4m3x2_f16x2(hc);
+                const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&hh));
+                const uint32_t lc = f32x2_e4m3x2(a - hv.x, b2 - hv.y);
+                if (i & 1) {
+                  hi[2 * u + i / 2] |= hc << 16;
+                  lo[2 * u + i / 2] |= lc << 16;
+                } else {
+                  hi[2 * u + i / 2] = hc;
+                  lo[2 * u + i / 2] = lc;
+                }
+              }
+            }
+            if (odd)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                hi[i] = 0x7F7F7F7Fu;
+                lo[i] = 0u;
+              }
+            const uint32_t o = static_cast<uint32_t>(c ^ r7) << 4;
+            st_shared_v4(row + o, hi[0], hi[1], hi[2], hi[3]);
+            st_shared_v4(row2 + o, lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
+      }
+      // the token's codes to registers, and the stage back to the load warp
+      const bool live = r < x.nvalid && !x.vzero;
+      uint4 v[8];
+      const uint32_t raw = smem_u32(sm.v[st]) + static_cast<uint32_t>(r) * 128u;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] = live ? lds_u4(raw + (static_cast<uint32_t>(c ^ r7) << 4)) : make_uint4(0u, 0u, 0u, 0u);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.v_empty[st]));
+      // a token that some rows of the segment do not see: its weight is 0 there, but 0 x NaN is
+      // NaN, so its NaN codes become 0 here and are put back for the rows that see it
+      if (live && x.pos0 + r > sg.pos) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(&v[c]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t nan = __vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            if (nan) {
+              for (int y = 0; y < 4; ++y)
+                if ((nan >> (8 * y)) & 1u) atomicMin(&sm.nanpos[x.seg % kRows][16 * c + 4 * i + y], x.pos0 + r);
+              sm.nanany[x.seg % kRows] = 1;
+              w[i] &= ~nan;
+            }
+          }
+        }
+      }
+      // the set's previous P V has read the FP16 tile
+      if (t >= 2 && !__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.pv_done[grp]), ((t >> 1) - 1) & 1, p.flags))) break;
+      if (!x.end) {
+        const uint32_t dst = smem_u32(sm.v16[grp][0]) + static_cast<uint32_t>(r) * 128u;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+          uint32_t f[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f[2 * i] = e4m3x2_f16x2(w[i] & 0xFFFFu);
+            f[2 * i + 1] = e4m3x2_f16x2(w[i] >> 16);
+          }
+          const uint32_t half = dst + static_cast<uint32_t>(c >> 2) * kHalfBytes;
+          const int ch = 2 * (c & 3);
+          st_shared_v4(half + (static_cast<uint32_t>(ch ^ r7) << 4), f[0], f[1], f[2], f[3]);
+          st_shared_v4(half + (static_cast<uint32_t>((ch + 1) ^ r7) << 4), f[4], f[5], f[6], f[7]);
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.v16_full[grp]));
+      if (x.end) break;
+    }
+  } else if (warp == kMmaWarp) {
+    // ================= S warp: S_t = Q K_t^T into buffer t % 2
+    if (lane == 0) {
+      const uint64_t qdesc = sdesc_kmajor_sw128(smem_u32(sm.q[0]));
+      const uint32_t idesc = idesc_e4m3_f32(128, kBlock, false, false);
+      int seg = -1;
+      bool any = false;
+      for (int t = 0;; ++t) {
+        const int st = t % kStages, sb = t & 1;
+        if (!wait_bar(smem_u32(&sm.k_full[st]), (t / kStages) & 1, p.flags)) break;
+        const Tile x = sm.tile[t % kRing];
+        // the buffer's previous weights have been used
+        if (t >= 2 && !wait_bar(smem_u32(&sm.pv_done[sb]), ((t >> 1) - 1) & 1, p.flags)) break;
+        if (x.end) {
+          mbar_arrive(smem_u32(&sm.s_full[sb]));
+          mbar_arrive(smem_u32(&sm.k_empty[st]));
+          if (t > 0 && sm.tile[(t - 1) % kRing].end) break;  // both sets know
+          continue;
+        }
+        if (x.seg != seg) {
+          seg = x.seg;
+          if (!wait_bar(smem_u32(&sm.q_full), seg & 1, p.flags)) break;
+        }
+        tc_fence_after();
+        any = true;
+        const uint64_t kdesc = sdesc_kmajor_sw128(smem_u32(sm.k[st]));
+#pragma unroll
+        for (int part = 0; part < NP; ++part)
+#pragma unroll
+          for (int kk = 0; kk < kDim / 32; ++kk)  // 32 bytes along the rows: + 2 in the address field
+            mma_f8_ss(tbase + kColS + kBlock * sb, qdesc + part * (kTileBytes >> 4) + 2 * kk, kdesc + 2 * kk, idesc,
+                      part > 0 || kk > 0);
+        mma_commit(smem_u32(&sm.s_full[sb]));
+        mma_commit(smem_u32(&sm.k_empty[st]));
+        if (t == x.last) mma_commit(smem_u32(&sm.q_free[x.seg % kQBars]));
+      }
+      if (any) {  // every MMA of this thread has finished before the tensor memory is released
+        mma_commit(smem_u32(&sm.drain[0]));
+        mbar_wait(smem_u32(&sm.drain[0]), 0, p.flags);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kPvWarp0 || warp == kPvWarp0 + 1) {
+    // ================= P V warp of set s: O_s (+)= P_t V_t
+    const int s = warp - kPvWarp0;
+    if (lane == 0) {
+      const uint32_t idesc = idesc_f16_f32(128, kDim, true);
+      // 128 dims = two 64-dim halves (the leading offset), 8-token groups 1 KB apart, 16 tokens = 2 KB
+      const uint64_t vdesc = sdesc_mn_sw128(smem_u32(sm.v16[s][0]), kHalfBytes);
+      int seg = -1;
+      for (int t = s;; t += 2) {
+        if (!wait_bar(smem_u32(&sm.v16_full[s]), (t >> 1) & 1, p.flags)) break;
+        const Tile x = sm.tile[t % kRing];
+        if (x.end) break;
+        if (!wait_bar(smem_u32(&sm.p_full[s]), (t >> 1) & 1, p.flags)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kBlock / 16; ++kk)
+          mma_f16_tmemA(tbase + kColO + kDim * s, tbase + kColS + kBlock * s + 8 * kk, vdesc + 128 * kk, idesc,
+                        x.seg == seg || kk > 0 ? 1u : 0u);
+        seg = x.seg;
+        mma_commit(smem_u32(&sm.pv_done[s]));
+      }
+      if (seg >= 0) {
+        mma_commit(smem_u32(&sm.drain[1 + s]));
+        mbar_wait(smem_u32(&sm.drain[1 + s]), 0, p.flags);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ================= softmax warps of set s: TMEM lane l = query row m of copy c, which takes
+    // tokens k0 .. k0 + kMpad - 1 of every tile
+    const int s = warp / 4, quad = warp % 4;
+    const int l = 32 * quad + lane, m = l % kMpad, c = l / kMpad, k0 = c * kMpad;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
+    const uint32_t s_cols = tbase + lane_base + kColS + kBlock * s;
+    const int row = m / G;
+    float mref = -INFINITY, lrun = 0.f, coef_q = 0.f;
+    int pos_max = 0, seg = 0, mine = 0, t_last = 0;  // mine: tiles of the segment that this set has done
+    uint32_t met_all = 0, met_set = 0;               // phases of the meeting points
+    // A meeting of warps, bounded like every other wait: after a timeout anywhere each warp leaves
+    // by itself.
+    auto meet = [&](uint64_t* bar, uint32_t& phase) -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(bar));
+      return __all_sync(0xFFFFFFFFu, wait_bar(smem_u32(bar), phase++ & 1u, p.flags));
+    };
+
+    // The segment's output or partial. Both sets take part: set s writes dims 64 s .. 64 s + 63.
+    auto finish = [&](int k) -> bool {
+      const Seg sg = sm.seg[k % kRing];
+      bool ok = true;
+      if (mine > 0) {
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.pv_done[s]), (t_last >> 1) & 1, p.flags));
+        tc_fence_after();
+      }
+      const bool have = mine > 0 && ok;
+      sm.xm[s][l] = have ? mref : -INFINITY;
+      sm.xl[s][l] = have ? lrun : 0.f;
+      tc_fence_before();
+      if (!meet(&sm.sets_met, met_all)) return false;
+      tc_fence_after();  // the other set's O too: it has waited for its last P V
+      float mt = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 2 * C; ++i) mt = fmaxf(mt, sm.xm[i & 1][(i >> 1) * kMpad + m]);
+      const float ref = mt == -INFINITY ? 0.f : mt;
+      float lt = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2 * C; ++i) {
+        const float mi = sm.xm[i & 1][(i >> 1) * kMpad + m];
+        lt += sm.xl[i & 1][(i >> 1) * kMpad + m] * ex2(mi - ref);
+      }
+      const float w0 = ex2(sm.xm[0][l] - ref), w1 = ex2(sm.xm[1][l] - ref);
+      // an O that no tile was added to is undefined: read only with a weight
+      const bool rd0 = __any_sync(0xFFFFFFFFu, w0 != 0.f), rd1 = __any_sync(0xFFFFFFFFu, w1 != 0.f);
+      const bool real = m < G * sg.rows;
+      const bool whole = sg.slot < 0;
+      const float inv = !whole ? 1.f : (lt == 0.f ? 0.f : 1.f / lt);
+      const bool nans = sm.nanany[k % kRows] != 0;
+      const long long orow = static_cast<long long>(sg.row0 + row) * (p.num_kv_heads * G) + sg.head * G + m % G;
+      float* part = reinterpret_cast<float*>(p.parts + headers_bytes(gridDim.x)) +
+                    (2LL * blockIdx.x + (whole ? 0 : sg.slot)) * kPartFloats;
+      constexpr int kW = 16 / C;  // dims of its row that a thread writes of every 16
+#pragma unroll 1
+      for (int step = 0; step < 4; ++step) {
+        const int d0 = 64 * s + 16 * step;
+        uint32_t a[16], b[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) a[u] = b[u] = 0u;
+        if (rd0) tmem_ld16(tbase + lane_base + kColO + d0, a);
+        if (rd1) tmem_ld16(tbase + lane_base + kColO + kDim + d0, b);
+        tc_wait_ld();
+        float o[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+          o[u] = (w0 != 0.f ? w0 * __uint_as_float(a[u]) : 0.f) + (w1 != 0.f ? w1 * __uint_as_float(b[u]) : 0.f);
+        float y[kW];
+        if constexpr (C == 1) {
+#pragma unroll
+          for (int u = 0; u < 16; ++u) y[u] = o[u];
+        } else {
+          float* red = sm.red[s];
+#pragma unroll
+          for (int u = 0; u < 16; ++u) red[l * kRedStride + u] = o[u];
+          if (!meet(&sm.set_met[s], met_set)) return false;
+#pragma unroll
+          for (int u = 0; u < kW; ++u) {
+            y[u] = 0.f;
+#pragma unroll
+            for (int i = 0; i < C; ++i) y[u] += red[(i * kMpad + m) * kRedStride + c * kW + u];
+          }
+          if (!meet(&sm.set_met[s], met_set)) return false;
+        }
+        const int d = d0 + c * kW;
+#pragma unroll
+        for (int u = 0; u < kW; ++u) {
+          y[u] *= inv;
+          if (nans && sm.nanpos[k % kRows][d + u] <= sg.pos + row) y[u] = __int_as_float(0x7FFFFFFF);
+        }
+        if (real && whole) {
+          uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * kDim + d);
+#pragma unroll
+          for (int u = 0; u < kW; u += 4)
+            *reinterpret_cast<uint2*>(dst + u / 2) = make_uint2(bf16x2_bits(y[u], y[u + 1]), bf16x2_bits(y[u + 2], y[u + 3]));
+        } else if (real) {
+#pragma unroll
+          for (int u = 0; u < kW; u += 4)
+            *reinterpret_cast<float4*>(part + m * kDim + d + u) = make_float4(y[u], y[u + 1], y[u + 2], y[u + 3]);
+        }
+      }
+      if (real && s == 0 && c == 0) {
+        if (!whole) {
+          part[128 * kDim + m] = mt;
+          part[128 * kDim + 128 + m] = lt;
+        } else if (p.lse != nullptr) {
+          p.lse[orow] = lt == 0.f ? -INFINITY : (ref + log2f(lt)) * 0.69314718055994531f;
+        }
+      }
+      // O, the exchange and the NaN marks are free again
+      tc_fence_before();
+      if (!meet(&sm.sets_met, met_all)) return false;
+      if (nans) {
+        if (s == 0) sm.nanpos[k % kRows][l] = INT_MAX;
+        if (tid == 0) sm.nanany[k % kRows] = 0;
+      }
+      mref = -INFINITY;
+      lrun = 0.f;
+      mine = 0;
+      return ok;
+    };
+
+    for (int t = s;; t += 2) {
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.s_full[s]), (t >> 1) & 1, p.flags))) break;
+      const Tile x = sm.tile[t % kRing];
+      bool good = true;
+      while (good && seg < x.seg) good = finish(seg++);  // segments that had no (further) tile for this set
+      if (x.end || !good) break;
+      tc_fence_after();
+      if (mine == 0) {
+        pos_max = sm.seg[seg % kRing].pos + row;
+        coef_q = p.sm_scale_log2 * (NP == 1 ? 1.f : sm.qscale[seg % kRows][l]);
+      }
+      const bool full_vis = x.pos0 + kBlock - 1 <= pos_max - row;  // every token visible to every row
+      const int lim = pos_max - x.pos0 - k0;                        // token k0 + n visible iff n <= lim
+      // the floor keeps a masked score at -inf when a scale is 0
+      const float coef = fmaxf(coef_q * x.kscale, 1e-30f);
+      const float lv = log2f(x.vscale);
+      constexpr int kCh = kMpad / 32;
+      constexpr bool kHold = kCh <= 2;  // all of the thread's scores in registers
+      uint32_t v[kHold ? kMpad : 32];
+      float mx = -INFINITY;
+      if constexpr (kHold) {
+#pragma unroll
+        for (int ch = 0; ch < kCh; ++ch) tmem_ld32(s_cols + k0 + 32 * ch, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * ch));
+        tc_wait_ld();
+        if (!full_vis) {
+#pragma unroll
+          for (int u = 0; u < kMpad; ++u) v[u] = u <= lim ? v[u] : __float_as_uint(-INFINITY);
+        }
+#pragma unroll
+        for (int u = 0; u < kMpad; u += 2) mx = fmax3(mx, __uint_as_float(v[u]), __uint_as_float(v[u + 1]));
+      } else {
+#pragma unroll 1
+        for (int ch = 0; ch < kCh; ++ch) {
+          tmem_ld32(s_cols + 32 * ch, *reinterpret_cast<uint32_t(*)[32]>(v));
+          tc_wait_ld();
+          if (!full_vis) {
+#pragma unroll
+            for (int u = 0; u < 32; ++u) v[u] = 32 * ch + u <= lim ? v[u] : __float_as_uint(-INFINITY);
+          }
+#pragma unroll
+          for (int u = 0; u < 32; u += 2) mx = fmax3(mx, __uint_as_float(v[u]), __uint_as_float(v[u + 1]));
+        }
+      }
+      // P is taken relative to a reference that moves only when the maximum passes it by more
+      // than kRescaleLog2 (P stays within FP16); O / l does not depend on it
+      const float bmax = fmaf(mx, coef, lv);
+      const bool move = bmax > mref + kRescaleLog2 || (mref == -INFINITY && bmax != -INFINITY);
+      const float m_new = move ? bmax : mref;
+      const float ref = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = ex2(mref - ref);  // 0 while nothing was seen yet
+      const bool rescale = move && mref != -INFINITY;
+      const float off = lv - ref;
+      const float2 coef2 = make_float2(coef, coef), off2 = make_float2(off, off);
+      float lsum = 0.f;
+      auto weights = [&](uint32_t* w, uint32_t col) {  // 32 scores -> 16 columns of FP16 pairs
+        float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const float2 d = __ffma2_rn(make_float2(__uint_as_float(w[2 * u]), __uint_as_float(w[2 * u + 1])), coef2, off2);
+          const float2 e = make_float2(ex2(d.x), ex2(d.y));
+          acc = __fadd2_rn(acc, e);
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[u]) : "f"(e.y), "f"(e.x));
+        }
+        lsum += acc.x + acc.y;
+        tmem_st16(col, w);
+      };
+      if constexpr (kHold) {
+#pragma unroll
+        for (int ch = 0; ch < kCh; ++ch) weights(v + 32 * ch, s_cols + (k0 + 32 * ch) / 2);
+        // the columns of the other copies' tokens (their scores were there)
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          if (z < c * kCh || z >= (c + 1) * kCh) tmem_zero16(s_cols + 16 * z);
+      } else {
+#pragma unroll 1
+        for (int ch = 0; ch < kCh; ++ch) {
+          tmem_ld32(s_cols + 32 * ch, *reinterpret_cast<uint32_t(*)[32]>(v));
+          tc_wait_ld();
+          if (!full_vis) {
+#pragma unroll
+            for (int u = 0; u < 32; ++u) v[u] = 32 * ch + u <= lim ? v[u] : __float_as_uint(-INFINITY);
+          }
+          weights(v, s_cols + 16 * ch);
+        }
+      }
+      if (mine > 0 && __any_sync(0xFFFFFFFFu, rescale)) {
+        // O holds the set's earlier tiles of the segment once their P V is done
+        if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.pv_done[s]), ((t >> 1) - 1) & 1, p.flags))) break;
+        tc_fence_after();
+        const float a = rescale ? alpha : 1.f;
+#pragma unroll 1
+        for (int qc = 0; qc < 4; ++qc) {
+          uint32_t o[32];
+          tmem_ld32(tbase + lane_base + kColO + kDim * s + 32 * qc, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * a);
+          tmem_st32(tbase + lane_base + kColO + kDim * s + 32 * qc, o);
+        }
+      }
+      lrun = lrun * alpha + lsum * (1.f / x.vscale);
+      mref = m_new;
+      ++mine;
+      t_last = t;
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[s]));
+      if (t + 2 > x.last && !finish(seg++)) break;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tbase, kTmemCols);
+  }
+}
+
+// Joins the partials of an item that starts in CTA blockIdx.x's range and ends in a later one's.
+// A warp takes one query row: the partials' maxima and sums by lanes, then 4 dims per lane.
+__global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnParams p, int grid) {
+  pdl_wait_primary();
+  const Header* hd = reinterpret_cast<const Header*>(p.parts);
+  const int cta = blockIdx.x, lane = threadIdx.x & 31;
+  const Header me = hd[cta];
+  if (!me.tail) return;
+  const int m = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  if (m >= me.rows * p.q_per_kv) return;
+  int end = cta + 1;  // the last CTA with a part of the item
+  while (end < grid && hd[end].cont && !hd[end].cont_end) ++end;
+  const int n = end - cta + 1;
+  const float* parts = reinterpret_cast<const float*>(p.parts + headers_bytes(grid));
+  auto part = [&](int i) { return parts + (i == 0 ? 2LL * cta + 1 : 2LL * (cta + i)) * kPartFloats; };
+  float mt = -INFINITY;
+  for (int i = lane; i < n; i += 32) mt = fmaxf(mt, part(i)[128 * kDim + m]);
+#pragma unroll
+  for (int d = 16; d; d /= 2) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, d));
+  const float ref = mt == -INFINITY ? 0.f : mt;
+  float lt = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float w = 0.f, l = 0.f;
+    if (i0 + lane < n) {
+      w = ex2(part(i0 + lane)[128 * kDim + m] - ref);
+      l = part(i0 + lane)[128 * kDim + 128 + m] * w;
+    }
+    const int k = n - i0 < 32 ? n - i0 : 32;
+#pragma unroll 4
+    for (int i = 0; i < k; ++i) {
+      const float wi = __shfl_sync(0xFFFFFFFFu, w, i);
+      lt += __shfl_sync(0xFFFFFFFFu, l, i);
+      const float4 x = *reinterpret_cast<const float4*>(part(i0 + i) + m * kDim + 4 * lane);
+      if (wi != 0.f) {
+        o.x += wi * x.x;
+        o.y += wi * x.y;
+        o.z += wi * x.z;
+        o.w += wi * x.w;
+      }
+    }
+  }
+  const float inv = lt == 0.f ? 0.f : 1.f / lt;
+  const long long orow = static_cast<long long>(me.row0 + m / p.q_per_kv) * (p.num_kv_heads * p.q_per_kv) +
+                         me.head * p.q_per_kv + m % p.q_per_kv;
+  *reinterpret_cast<uint2*>(p.out + orow * kDim + 4 * lane) =
+      make_uint2(bf16x2_bits(o.x * inv, o.y * inv), bf16x2_bits(o.z * inv, o.w * inv));
+  if (lane == 0 && p.lse != nullptr) p.lse[orow] = lt == 0.f ? -INFINITY : (ref + log2f(lt)) * 0.69314718055994531f;
+}
+
+template <int C, int NP>
+cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8AttnParams& prm, int grid, cudaStream_t st) {
+  const int smem = static_cast<int>(sizeof(Smem<NP>)) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<C, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kv8_attn_kernel<C, NP><<<grid, kThreads, smem, st>>>(kmap, vmap, prm);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, (128 / C) / (kMergeThreads / 32));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel, prm, grid);
+}
+
+// Copies of the query rows that a request of max_rows rows (taken as a power of two) leaves room
+// for, and the rows of a chunk.
+int copies_for(int max_rows, int q_per_kv) {
+  long long r = 1;
+  while (r < max_rows && r < 128) r *= 2;
+  const long long m = r * q_per_kv;
+  return m <= 32 ? 4 : m <= 64 ? 2 : 1;
 }
 
 msa_status check_args(const msa_kv8_attn_args* a) {
@@ -130,11 +971,14 @@ msa_status check_args(const msa_kv8_attn_args* a) {
 
 }  // namespace
 
-cudaError_t launch_kv8_attn(const Kv8AttnParams& prm, bool q_bf16, int, cudaStream_t st) {
-  const dim3 grid(prm.total_rows, prm.num_kv_heads * prm.q_per_kv);
-  if (q_bf16) kv8_attn_kernel<true><<<grid, 128, 0, st>>>(prm);
-  else kv8_attn_kernel<false><<<grid, 128, 0, st>>>(prm);
-  return cudaGetLastError();
+cudaError_t launch_kv8_attn(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8AttnParams& prm, bool q_bf16,
+                            int grid, cudaStream_t st) {
+  const int c = copies_for(prm.max_rows, prm.q_per_kv);
+  if (q_bf16)
+    return c == 4 ? launch<4, 2>(kmap, vmap, prm, grid, st)
+           : c == 2 ? launch<2, 2>(kmap, vmap, prm, grid, st) : launch<1, 2>(kmap, vmap, prm, grid, st);
+  return c == 4 ? launch<4, 1>(kmap, vmap, prm, grid, st)
+         : c == 2 ? launch<2, 1>(kmap, vmap, prm, grid, st) : launch<1, 1>(kmap, vmap, prm, grid, st);
 }
 
 }  // namespace msa
@@ -147,7 +991,11 @@ msa_status msa_kv8_attn_workspace_size(const msa_kv8_attn_args* a, size_t* bytes
   if (bytes == nullptr) return MSA_ERR_INVALID_ARG;
   const msa_status s = check_args(a);
   if (s != MSA_OK) return s;
-  *bytes = 256;
+  int sms = 0;
+  const msa_status d = check_device(&sms);
+  if (d != MSA_OK) return d;
+  // flags, the CTAs' headers, two partials for each CTA
+  *bytes = 256 + headers_bytes(sms) + 2 * static_cast<size_t>(sms) * kPartFloats * sizeof(float);
   return MSA_OK;
 }
 
@@ -195,9 +1043,17 @@ msa_status msa_kv8_attn(const msa_kv8_attn_args* a, void* ws, size_t ws_bytes, v
   p.v_scale = a->v_scale;
   p.sm_scale_log2 = a->sm_scale * 1.4426950408889634f;
   p.flags = static_cast<uint32_t*>(ws);
+  p.parts = static_cast<uint8_t*>(ws) + 256;
   p.out = a->out;
   p.lse = a->lse;
-  return launch_kv8_attn(p, a->q_type == MSA_TYPE_BF16, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  const int room = 128 / copies_for(p.max_rows, p.q_per_kv) / p.q_per_kv;
+  p.chunk = 1;
+  while (2 * p.chunk <= room) p.chunk *= 2, ++p.chunk_log2;
+  CUtensorMap kmap, vmap;
+  const long long token_rows = static_cast<long long>(a->num_pages) * a->num_kv_heads * kBlock;
+  if ((s = encode_kv8_map(&kmap, a->k_data, token_rows)) != MSA_OK) return s;
+  if ((s = encode_kv8_map(&vmap, a->v_data, token_rows)) != MSA_OK) return s;
+  return launch_kv8_attn(kmap, vmap, p, a->q_type == MSA_TYPE_BF16, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MSA_OK
              : MSA_ERR_CUDA;
 }
