@@ -106,6 +106,8 @@ _lib = None
 def load(path: str = LIB_PATH):
     """Load libmsa.so (built by block_sparse_attention_nvfp4_gb300.build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):

@@ -123,8 +123,7 @@ struct Kv8AttnParams {
   uint16_t* out;
   float* lse;
 };
-cudaError_t launch_kv8_attn(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8AttnParams& prm, bool q_bf16,
-                            int grid, cudaStream_t st);
+cudaError_t launch_kv8_attn(const CUtensorMap& kmap, const Kv8AttnParams& prm, bool q_bf16, int grid, cudaStream_t st);
 
 // Merge of the rank-local candidate lists of indexer decode context parallelism
 // (msa_dcp_merge_topk).

@@ -28,13 +28,16 @@
 // the MMA tile; copy c takes tokens 128 c / C .. of every tile with its own maximum and sum, so
 // that few rows still spread the exponentials over all four SM sub-partitions (P is zero in the
 // other copies' columns). Roles, as in the sparse attention over the NVFP4 cache (msa_attn.cu):
-//   * load warp: finds the tiles (32 block-table entries and scales at a time, one per lane) and
-//     copies K and V of a tile (16 KB each) into a 3-stage ring; what the others need of a
-//     tile or segment goes into small rings beside it;
-//   * 8 converting warps in two groups taking alternate tiles: V to FP16, rows past the context
-//     to zero; the group that has a segment's first tile also lays out its queries;
-//   * S warp, and a P V warp for each of the two softmax sets;
-//   * 8 softmax warps in two sets taking alternate tiles, each with its own O in tensor memory.
+//   * K warp: finds the tiles (32 block-table entries and scales at a time, one per lane) and
+//     copies their K (16 KB) into a ring; what the others need of a tile or segment goes into
+//     small rings beside it. V warp: copies their V. Each runs ahead as its own ring allows: a
+//     K stage is held until its S is computed, a V stage only until it is in registers;
+//   * 4 converting warps: V to FP16, rows past the context to zero; at a segment's first tile
+//     they also lay out its queries;
+//   * S warp (three score buffers in tensor memory) and P V warp (one O);
+//   * 8 softmax warps in two sets taking alternate tiles. A lane of the O belongs to one thread
+//     of each set; the reference its weights are relative to goes from tile to tile through
+//     shared memory, and a set waits only for the other's decision on it, not for its weights.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -51,20 +54,22 @@ namespace msa {
 namespace {
 
 constexpr int kSoftWarps = 8;                        // warps 0..7: two sets of 4, one per TMEM lane quadrant
-constexpr int kMmaWarp = 8, kPvWarp0 = 9, kLoadWarp = 11;
-constexpr int kCvWarp0 = 12, kCvWarps = 8;           // two groups of 4
+constexpr int kMmaWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11;
+constexpr int kCvWarp0 = 12, kCvWarps = 4;
 constexpr int kThreads = (kCvWarp0 + kCvWarps) * 32;
-constexpr int kStages = 3;
-// A wait on a barrier's parity has to be for its current phase or the one before. The two
-// converting groups take alternate tiles, so V stages signal through 2 x 3 barriers, each of
-// which serves one group; a group loads the queries of some segments only, so the freeing of
-// the query tile goes round 4 barriers (at most two segments are in that state).
-constexpr int kVBars = 2 * kStages, kQBars = 4;
+constexpr int kVStages = 3;
+// A wait on a barrier's parity has to be for its current phase or the one before. Waiters that
+// skip tiles, or fall behind, therefore have barriers that go round 6 tiles (even: each serves one
+// softmax set; no wait is 6 tiles behind), or 12 for a tile's description (up to 8 ahead).
+constexpr int kBars = 6, kTold = 12;
 constexpr int kRing = 16;                            // tiles and segments whose description is kept
 constexpr int kRows = 8;                             // segments whose query scales and NaN marks are kept
 constexpr uint32_t kTileBytes = kBlock * kDim;       // K or V of a tile
 constexpr uint32_t kHalfBytes = kBlock * 128;        // FP16 V: 128 tokens x 64 dims
-constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
+// TMEM columns: three score buffers (128 FP32; the weights, FP16 pairs, go over the first 64), O.
+constexpr int kSBufs = 3;
+constexpr uint32_t kColS = 0, kColO = kSBufs * kBlock, kTmemCols = 512;
+static_assert(kColO + kDim <= kTmemCols, "TMEM");
 constexpr float kRescaleLog2 = 8.f;                  // O is rescaled when the maximum grows by more than 2^8
 constexpr int kNoPos = 1 << 30;                      // position of a tile that nobody sees
 constexpr int kRedStride = 17;
@@ -73,6 +78,7 @@ constexpr int kMergeThreads = 256;
 struct Tile {
   int pos0;      // position of its first token
   int nvalid;    // tokens inside the context; 0: nothing to read
+  int page;      // physical page x KV heads + head
   int seg;       // the CTA's segment
   int last;      // last tile of that segment
   int end;       // no tile: the CTA's work is over
@@ -82,6 +88,7 @@ struct Tile {
 
 struct Seg {
   int first;     // its first tile
+  int last;
   int row0;      // first query row
   int rows;
   int head;      // KV head
@@ -91,19 +98,22 @@ struct Seg {
 
 template <int NP>
 struct Smem {
+  static constexpr int kKStages = NP == 1 ? 4 : 3;
   uint8_t q[NP][kTileBytes];                         // A of S: copies of the query rows, by part
-  uint8_t k[kStages][kTileBytes];                    // B of S (K-major), 128-byte swizzle
-  uint8_t v[kStages][kTileBytes];                    // V codes, 128-byte swizzle
+  uint8_t k[kKStages][kTileBytes];                   // B of S (K-major), 128-byte swizzle
+  uint8_t v[kVStages][kTileBytes];                   // V codes as they are in the page
   uint8_t v16[2][2][kHalfBytes];                     // B of O (MN-major): [set][half][token][64 dims]
   float red[2][128 * kRedStride];                    // copies of a row joined, 16 dims at a time
   float qscale[kRows][128];                          // 2^e of each tile row (BF16 queries)
   int nanpos[kRows][kDim];                           // first position with a NaN value in a dim, of partly seen tokens
   int nanany[kRows];
+  float ref[128];                                    // what the weights of a lane are relative to now
   float xm[2][128], xl[2][128];
   Tile tile[kRing];
   Seg seg[kRing];
-  uint64_t k_full[kStages], v_full[kVBars], k_empty[kStages], v_empty[kStages];
-  uint64_t q_full, q_free[kQBars], s_full[2], p_full[2], v16_full[2], pv_done[2], drain[3];
+  uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], told[kTold];
+  uint64_t q_full, q_free, s_full[kBars], p_full[kBars], v16_full[2], pv_done[kBars], drain[2];
+  uint64_t decided[2][4];                            // by set and quadrant: the tile's reference stands
   uint64_t sets_met, set_met[2];                     // the softmax warps of both sets, or of one, have come here
   long long part[kThreads / 32];
   long long lo, hi;
@@ -198,9 +208,9 @@ __device__ __forceinline__ long long head_tiles(const Kv8AttnParams& p, const Re
 // C copies of the query rows down the MMA tile (128 / C rows each); NP = E4M3 parts of a query.
 template <int C, int NP>
 __global__ void __launch_bounds__(kThreads, 1)
-    kv8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                    const Kv8AttnParams p) {
+    kv8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const Kv8AttnParams p) {
   constexpr int kMpad = 128 / C;
+  constexpr int kStages = Smem<NP>::kKStages;
   extern __shared__ uint8_t smem_raw[];
   Smem<NP>& sm = *reinterpret_cast<Smem<NP>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -211,18 +221,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&sm.k_full[s]), 1);
       mbar_init(smem_u32(&sm.k_empty[s]), 1);
-      mbar_init(smem_u32(&sm.v_empty[s]), kCvWarps / 2);
     }
-    mbar_init(smem_u32(&sm.q_full), kCvWarps / 2);
-    for (int s = 0; s < kVBars; ++s) mbar_init(smem_u32(&sm.v_full[s]), 1);
-    for (int s = 0; s < kQBars; ++s) mbar_init(smem_u32(&sm.q_free[s]), 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(smem_u32(&sm.v_full[s]), 1);
+      mbar_init(smem_u32(&sm.v_empty[s]), kCvWarps);
+    }
+    for (int s = 0; s < kTold; ++s) mbar_init(smem_u32(&sm.told[s]), 1);
+    mbar_init(smem_u32(&sm.q_full), kCvWarps);
+    mbar_init(smem_u32(&sm.q_free), 1);
+    for (int s = 0; s < kBars; ++s) {
       mbar_init(smem_u32(&sm.s_full[s]), 1);
       mbar_init(smem_u32(&sm.p_full[s]), kSoftWarps / 2);
-      mbar_init(smem_u32(&sm.v16_full[s]), kCvWarps / 2);
       mbar_init(smem_u32(&sm.pv_done[s]), 1);
     }
-    for (int s = 0; s < 3; ++s) mbar_init(smem_u32(&sm.drain[s]), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&sm.v16_full[s]), kCvWarps);
+      for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sm.decided[s][w]), 1);
+    }
+    for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&sm.drain[s]), 1);
     mbar_init(smem_u32(&sm.sets_met), kSoftWarps);
     for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&sm.set_met[s]), kSoftWarps / 2);
     mbar_fence_init();
@@ -231,10 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = tid; i < kRows * kDim; i += kThreads) (&sm.nanpos[0][0])[i] = INT_MAX;
   if (tid < kRows) sm.nanany[tid] = 0;
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&sm.taddr), kTmemCols);
-  if (warp == kLoadWarp && lane == 0) {
+  if (warp == kKWarp && lane == 0)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
-  }
 
   // ---- this CTA's range of the line: every thread sums a run of requests
   {
@@ -286,39 +300,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = sm.taddr;
 
-  if (warp == kLoadWarp) {
-    // ================= load warp
+  if (warp == kKWarp) {
+    // ================= K warp
     int t = 0, nseg = 0;
     bool good = true;
     Header hd = {};
-    // Waits until tile t's stage is free, writes its description and starts its copies.
-    auto emit = [&](int pos0, int nvalid, int last, int end, int phys_row, float ks, float vs) {
+    // Waits until tile t's stage is free, writes its description and starts its K copy.
+    auto emit = [&](int pos0, int nvalid, int last, int end, int page, float ks, float vs) {
       const int st = t % kStages;
       if (t >= kStages) {
-        const uint32_t par = ((t / kStages) - 1) & 1;
-        good = wait_bar(smem_u32(&sm.k_empty[st]), par, p.flags) && wait_bar(smem_u32(&sm.v_empty[st]), par, p.flags);
-        good = __all_sync(0xFFFFFFFFu, good);
+        good = __all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.k_empty[st]), ((t / kStages) - 1) & 1, p.flags));
         if (!good) return;
       }
       if (lane == 0) {
         Tile& x = sm.tile[t % kRing];
         x.pos0 = pos0;
         x.nvalid = nvalid;
+        x.page = page;
         x.seg = nseg;
         x.last = last;
         x.end = end;
         x.vzero = vs == 0.f;
         x.kscale = ks;
         x.vscale = vs == 0.f ? 1.f : vs;
-        const uint32_t kb = smem_u32(&sm.k_full[st]), vb = smem_u32(&sm.v_full[t % kVBars]);
+        mbar_arrive(smem_u32(&sm.told[t % kTold]));
+        const uint32_t kb = smem_u32(&sm.k_full[st]);
         if (nvalid > 0) {
           mbar_arrive_expect_tx(kb, kTileBytes);
-          tma_load_2d(smem_u32(sm.k[st]), &kmap, 0, phys_row, kb);
-          mbar_arrive_expect_tx(vb, kTileBytes);
-          tma_load_2d(smem_u32(sm.v[st]), &vmap, 0, phys_row, vb);
+          tma_load_2d(smem_u32(sm.k[st]), &kmap, 0, page * kBlock, kb);
         } else {
           mbar_arrive(kb);
-          mbar_arrive(vb);
         }
       }
       __syncwarp();
@@ -368,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           Seg& s = sm.seg[nseg % kRing];
           s.first = t;
+          s.last = last;
           s.row0 = q.r0 + row0;
           s.rows = rows;
           s.head = h;
@@ -406,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float kk = __shfl_sync(0xFFFFFFFFu, ks, src), vv = __shfl_sync(0xFFFFFFFFu, vs, src);
             const int pos0 = cc * kBlock, nv = q.N - pos0 < kBlock ? q.N - pos0 : kBlock;
             if (pp < 0) emit(kNoPos, 0, last, 0, 0, 1.f, 1.f);
-            else emit(pos0, nv, last, 0, (pp * p.num_kv_heads + h) * kBlock, kk, vv);
+            else emit(pos0, nv, last, 0, pp * p.num_kv_heads + h, kk, vv);
           }
         }
         if (p.n_ids && use == 0u && good) emit(kNoPos, 0, last, 0, 0, 1.f, 1.f);
@@ -427,25 +439,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int e = 0; e < 2 && good; ++e) emit(kNoPos, 0, INT_MAX, 1, 0, 1.f, 1.f);
     // no copy may still be landing when the CTA leaves
-    for (int j = t - kStages < 0 ? 0 : t - kStages; j < t; ++j) {
+    for (int j = t - kStages < 0 ? 0 : t - kStages; j < t; ++j)
       if (!wait_bar(smem_u32(&sm.k_full[j % kStages]), (j / kStages) & 1, p.flags)) break;
-      if (!wait_bar(smem_u32(&sm.v_full[j % kVBars]), (j / kVBars) & 1, p.flags)) break;
-    }
     if (lane == 0) reinterpret_cast<Header*>(p.parts)[blockIdx.x] = hd;
     __syncwarp();
   } else if (warp >= kCvWarp0) {
-    // ================= converting warps: group g takes tiles t = g, g + 2, ...; thread = token
-    const int th = tid - kCvWarp0 * 32, grp = th >> 7, r = th & 127, r7 = r & 7;
-    for (int t = grp;; t += 2) {
-      const int st = t % kStages;
-      if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.v_full[t % kVBars]), (t / kVBars) & 1, p.flags))) break;
+    // ================= converting warps; thread = one 16-byte piece of every 16th row
+    const int r = tid - kCvWarp0 * 32, r7 = r & 7;                             // r: the query row it lays out
+    const int vr = r >> 3, vc = r & 7;                                         // V row (mod 16) and 16-byte piece
+    for (int t = 0;; ++t) {
+      const int st = t % kVStages;
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.v_full[st]), (t / kVStages) & 1, p.flags))) break;
       const Tile x = sm.tile[t % kRing];
       const Seg& sg = sm.seg[x.seg % kRing];
       if (!x.end && sg.first == t) {
         // the segment's queries, once the last segment's scores are computed
         const int k = x.seg;
-        if (k > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.q_free[(k - 1) % kQBars]), ((k - 1) / kQBars) & 1, p.flags)))
-          break;
+        if (k > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.q_free), (k - 1) & 1, p.flags))) break;
         const int m = r % kMpad;
         const bool real = m < G * sg.rows;
         const long long at = real ? static_cast<long long>(sg.row0 + m / G) * p.q_stride + (sg.head * G + m % G) * kDim : 0;
@@ -461,13 +471,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at);
           // largest magnitude by its bits: BF16 pairs, both halves at once
+          uint4 v[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) v[c] = real ? src[c] : make_uint4(0u, 0u, 0u, 0u);
           uint32_t big = 0u;
-#pragma unroll 4
-          for (int c = 0; c < 16; ++c) {
-            const uint4 v = real ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-            big = __vmaxu2(big, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                         __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            big = __vmaxu2(big, __vmaxu2(__vmaxu2(v[c].x & 0x7FFF7FFFu, v[c].y & 0x7FFF7FFFu),
+                                         __vmaxu2(v[c].z & 0x7FFF7FFFu, v[c].w & 0x7FFF7FFFu)));
           const uint32_t amax = max(big & 0xFFFFu, big >> 16);
           const bool odd = amax >= 0x7F80u;  // an infinity or a NaN: the whole row becomes NaN
           // smallest 2^e with amax <= 448 2^e; below 2^-120 nothing a score could show is left
@@ -476,13 +487,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
           sm.qscale[k % kRows][r] = odd ? 1.f : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
           const uint32_t row2 = row + kTileBytes;
-#pragma unroll 2
+#pragma unroll
           for (int c = 0; c < 8; ++c) {  // 16 elements: 16 code bytes of each part
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              const uint4 v = real ? src[2 * c + u] : make_uint4(0u, 0u, 0u, 0u);
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              const uint32_t w[4] = {v[2 * c + u].x, v[2 * c + u].y, v[2 * c + u].z, v[2 * c + u].w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const float a = __uint_as_float(w[i] << 16) * inv, b2 = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
@@ -514,71 +524,105 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
       }
-      // the token's codes to registers, and the stage back to the load warp
-      const bool live = r < x.nvalid && !x.vzero;
+      // the tile's codes to registers, and the stage back to the V warp
+      const int rows = x.vzero ? 0 : x.nvalid;
       uint4 v[8];
-      const uint32_t raw = smem_u32(sm.v[st]) + static_cast<uint32_t>(r) * 128u;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] = live ? lds_u4(raw + (static_cast<uint32_t>(c ^ r7) << 4)) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < 8; ++i)
+        v[i] = 16 * i + vr < rows ? lds_u4(smem_u32(sm.v[st]) + static_cast<uint32_t>(r + 128 * i) * 16u)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+      __threadfence_block();  // the loads are over, not only issued, when the stage is given back
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.v_empty[st]));
       // a token that some rows of the segment do not see: its weight is 0 there, but 0 x NaN is
       // NaN, so its NaN codes become 0 here and are put back for the rows that see it
-      if (live && x.pos0 + r > sg.pos) {
+      if (x.nvalid > 0 && x.pos0 + x.nvalid - 1 > sg.pos) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t* w = reinterpret_cast<uint32_t*>(&v[c]);
+        for (int i = 0; i < 8; ++i) {
+          if (x.pos0 + 16 * i + vr <= sg.pos) continue;
+          uint32_t* w = reinterpret_cast<uint32_t*>(&v[i]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t nan = __vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t nan = __vcmpeq4(w[y] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
             if (nan) {
-              for (int y = 0; y < 4; ++y)
-                if ((nan >> (8 * y)) & 1u) atomicMin(&sm.nanpos[x.seg % kRows][16 * c + 4 * i + y], x.pos0 + r);
+              for (int z = 0; z < 4; ++z)
+                if ((nan >> (8 * z)) & 1u)
+                  atomicMin(&sm.nanpos[x.seg % kRows][16 * vc + 4 * y + z], x.pos0 + 16 * i + vr);
               sm.nanany[x.seg % kRows] = 1;
-              w[i] &= ~nan;
+              w[y] &= ~nan;
             }
           }
         }
       }
-      // the set's previous P V has read the FP16 tile
-      if (t >= 2 && !__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.pv_done[grp]), ((t >> 1) - 1) & 1, p.flags))) break;
+      // the P V two tiles before has read the FP16 tile
+      if (t >= 2 && !__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.pv_done[(t - 2) % kBars]), ((t - 2) / kBars) & 1, p.flags)))
+        break;
       if (!x.end) {
-        const uint32_t dst = smem_u32(sm.v16[grp][0]) + static_cast<uint32_t>(r) * 128u;
+        // 16 codes -> two 16-byte pieces of half vc / 4; the second half's threads store theirs the
+        // other way round, so that a row's 8 threads meet 8 different banks
+        const int flip = vc >> 2, ch = 2 * (vc & 3);
+        const uint32_t dst = smem_u32(sm.v16[t & 1][flip]) + static_cast<uint32_t>(vr) * 128u;
+        const uint32_t o0 = static_cast<uint32_t>((ch + flip) ^ (vr & 7)) << 4, o1 = o0 ^ 16u;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
           uint32_t f[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f[2 * i] = e4m3x2_f16x2(w[i] & 0xFFFFu);
-            f[2 * i + 1] = e4m3x2_f16x2(w[i] >> 16);
+          for (int y = 0; y < 4; ++y) {
+            f[2 * y] = e4m3x2_f16x2(w[y] & 0xFFFFu);
+            f[2 * y + 1] = e4m3x2_f16x2(w[y] >> 16);
           }
-          const uint32_t half = dst + static_cast<uint32_t>(c >> 2) * kHalfBytes;
-          const int ch = 2 * (c & 3);
-          st_shared_v4(half + (static_cast<uint32_t>(ch ^ r7) << 4), f[0], f[1], f[2], f[3]);
-          st_shared_v4(half + (static_cast<uint32_t>((ch + 1) ^ r7) << 4), f[4], f[5], f[6], f[7]);
+          const uint32_t row = dst + 16u * 128u * i;
+          st_shared_v4(row + o0, flip ? f[4] : f[0], flip ? f[5] : f[1], flip ? f[6] : f[2], flip ? f[7] : f[3]);
+          st_shared_v4(row + o1, flip ? f[0] : f[4], flip ? f[1] : f[5], flip ? f[2] : f[6], flip ? f[3] : f[7]);
         }
         fence_proxy_async_smem();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.v16_full[grp]));
+      if (lane == 0) mbar_arrive(smem_u32(&sm.v16_full[t & 1]));
       if (x.end) break;
     }
+  } else if (warp == kVWarp) {
+    // ================= V warp
+    if (lane == 0) {
+      int t = 0;
+      for (;; ++t) {
+        const int st = t % kVStages;
+        if (!wait_bar(smem_u32(&sm.told[t % kTold]), (t / kTold) & 1, p.flags)) break;
+        const Tile x = sm.tile[t % kRing];
+        if (t >= kVStages && !wait_bar(smem_u32(&sm.v_empty[st]), ((t / kVStages) - 1) & 1, p.flags)) break;
+        const uint32_t bar = smem_u32(&sm.v_full[st]);
+        if (x.nvalid > 0 && !x.vzero) {
+          mbar_arrive_expect_tx(bar, kTileBytes);
+          bulk_load(smem_u32(sm.v[st]), p.v_data + static_cast<long long>(x.page) * kTileBytes, kTileBytes, bar);
+        } else {
+          mbar_arrive(bar);
+        }
+        if (x.end) {
+          ++t;
+          break;
+        }
+      }
+      // no copy may still be landing when the CTA leaves
+      for (int j = t - kVStages < 0 ? 0 : t - kVStages; j < t; ++j)
+        if (!wait_bar(smem_u32(&sm.v_full[j % kVStages]), (j / kVStages) & 1, p.flags)) break;
+    }
+    __syncwarp();
   } else if (warp == kMmaWarp) {
-    // ================= S warp: S_t = Q K_t^T into buffer t % 2
+    // ================= S warp: S_t = Q K_t^T into buffer t % 3
     if (lane == 0) {
       const uint64_t qdesc = sdesc_kmajor_sw128(smem_u32(sm.q[0]));
       const uint32_t idesc = idesc_e4m3_f32(128, kBlock, false, false);
       int seg = -1;
       bool any = false;
       for (int t = 0;; ++t) {
-        const int st = t % kStages, sb = t & 1;
+        const int st = t % kStages, sb = t % kSBufs;
         if (!wait_bar(smem_u32(&sm.k_full[st]), (t / kStages) & 1, p.flags)) break;
         const Tile x = sm.tile[t % kRing];
         // the buffer's previous weights have been used
-        if (t >= 2 && !wait_bar(smem_u32(&sm.pv_done[sb]), ((t >> 1) - 1) & 1, p.flags)) break;
+        if (t >= kSBufs && !wait_bar(smem_u32(&sm.pv_done[(t - kSBufs) % kBars]), ((t - kSBufs) / kBars) & 1, p.flags)) break;
         if (x.end) {
-          mbar_arrive(smem_u32(&sm.s_full[sb]));
+          mbar_arrive(smem_u32(&sm.s_full[t % kBars]));
           mbar_arrive(smem_u32(&sm.k_empty[st]));
           if (t > 0 && sm.tile[(t - 1) % kRing].end) break;  // both sets know
           continue;
@@ -596,9 +640,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < kDim / 32; ++kk)  // 32 bytes along the rows: + 2 in the address field
             mma_f8_ss(tbase + kColS + kBlock * sb, qdesc + part * (kTileBytes >> 4) + 2 * kk, kdesc + 2 * kk, idesc,
                       part > 0 || kk > 0);
-        mma_commit(smem_u32(&sm.s_full[sb]));
+        mma_commit(smem_u32(&sm.s_full[t % kBars]));
         mma_commit(smem_u32(&sm.k_empty[st]));
-        if (t == x.last) mma_commit(smem_u32(&sm.q_free[x.seg % kQBars]));
+        if (t == x.last) mma_commit(smem_u32(&sm.q_free));
       }
       if (any) {  // every MMA of this thread has finished before the tensor memory is released
         mma_commit(smem_u32(&sm.drain[0]));
@@ -606,43 +650,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == kPvWarp0 || warp == kPvWarp0 + 1) {
-    // ================= P V warp of set s: O_s (+)= P_t V_t
-    const int s = warp - kPvWarp0;
+  } else if (warp == kPvWarp) {
+    // ================= P V warp: O (+)= P_t V_t
     if (lane == 0) {
       const uint32_t idesc = idesc_f16_f32(128, kDim, true);
-      // 128 dims = two 64-dim halves (the leading offset), 8-token groups 1 KB apart, 16 tokens = 2 KB
-      const uint64_t vdesc = sdesc_mn_sw128(smem_u32(sm.v16[s][0]), kHalfBytes);
       int seg = -1;
-      for (int t = s;; t += 2) {
+      for (int t = 0;; ++t) {
+        const int s = t & 1;
         if (!wait_bar(smem_u32(&sm.v16_full[s]), (t >> 1) & 1, p.flags)) break;
         const Tile x = sm.tile[t % kRing];
         if (x.end) break;
-        if (!wait_bar(smem_u32(&sm.p_full[s]), (t >> 1) & 1, p.flags)) break;
+        if (!wait_bar(smem_u32(&sm.p_full[t % kBars]), (t / kBars) & 1, p.flags)) break;
         tc_fence_after();
+        // 128 dims = two 64-dim halves (the leading offset), 8-token groups 1 KB apart, 16 tokens = 2 KB
+        const uint64_t vdesc = sdesc_mn_sw128(smem_u32(sm.v16[s][0]), kHalfBytes);
+        const uint32_t pcol = tbase + kColS + kBlock * (t % kSBufs);
 #pragma unroll
         for (int kk = 0; kk < kBlock / 16; ++kk)
-          mma_f16_tmemA(tbase + kColO + kDim * s, tbase + kColS + kBlock * s + 8 * kk, vdesc + 128 * kk, idesc,
-                        x.seg == seg || kk > 0 ? 1u : 0u);
+          mma_f16_tmemA(tbase + kColO, pcol + 8 * kk, vdesc + 128 * kk, idesc, x.seg == seg || kk > 0 ? 1u : 0u);
         seg = x.seg;
-        mma_commit(smem_u32(&sm.pv_done[s]));
+        mma_commit(smem_u32(&sm.pv_done[t % kBars]));
       }
       if (seg >= 0) {
-        mma_commit(smem_u32(&sm.drain[1 + s]));
-        mbar_wait(smem_u32(&sm.drain[1 + s]), 0, p.flags);
+        mma_commit(smem_u32(&sm.drain[1]));
+        mbar_wait(smem_u32(&sm.drain[1]), 0, p.flags);
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp < kSoftWarps) {
     // ================= softmax warps of set s: TMEM lane l = query row m of copy c, which takes
     // tokens k0 .. k0 + kMpad - 1 of every tile
     const int s = warp / 4, quad = warp % 4;
     const int l = 32 * quad + lane, m = l % kMpad, c = l / kMpad, k0 = c * kMpad;
     const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
-    const uint32_t s_cols = tbase + lane_base + kColS + kBlock * s;
     const int row = m / G;
-    float mref = -INFINITY, lrun = 0.f, coef_q = 0.f;
-    int pos_max = 0, seg = 0, mine = 0, t_last = 0;  // mine: tiles of the segment that this set has done
+    float mref = -INFINITY, lrun = 0.f, coef_q = 0.f;  // this set's sum, relative to the last reference it used
+    int pos_max = 0, first = 0, seg = 0, mine = 0;              // mine: tiles of the segment that this set has done
     uint32_t met_all = 0, met_set = 0;               // phases of the meeting points
     // A meeting of warps, bounded like every other wait: after a timeout anywhere each warp leaves
     // by itself.
@@ -655,30 +698,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The segment's output or partial. Both sets take part: set s writes dims 64 s .. 64 s + 63.
     auto finish = [&](int k) -> bool {
       const Seg sg = sm.seg[k % kRing];
-      bool ok = true;
-      if (mine > 0) {
-        ok = __all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.pv_done[s]), (t_last >> 1) & 1, p.flags));
-        tc_fence_after();
-      }
-      const bool have = mine > 0 && ok;
-      sm.xm[s][l] = have ? mref : -INFINITY;
-      sm.xl[s][l] = have ? lrun : 0.f;
-      tc_fence_before();
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.pv_done[sg.last % kBars]), (sg.last / kBars) & 1, p.flags)))
+        return false;
+      sm.xm[s][l] = mref;
+      sm.xl[s][l] = lrun;
       if (!meet(&sm.sets_met, met_all)) return false;
-      tc_fence_after();  // the other set's O too: it has waited for its last P V
+      tc_fence_after();
+      // references only grow, so a lane's O is relative to the larger of the two sets' last ones
       float mt = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 2 * C; ++i) mt = fmaxf(mt, sm.xm[i & 1][(i >> 1) * kMpad + m]);
       const float ref = mt == -INFINITY ? 0.f : mt;
       float lt = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2 * C; ++i) {
-        const float mi = sm.xm[i & 1][(i >> 1) * kMpad + m];
-        lt += sm.xl[i & 1][(i >> 1) * kMpad + m] * ex2(mi - ref);
-      }
-      const float w0 = ex2(sm.xm[0][l] - ref), w1 = ex2(sm.xm[1][l] - ref);
-      // an O that no tile was added to is undefined: read only with a weight
-      const bool rd0 = __any_sync(0xFFFFFFFFu, w0 != 0.f), rd1 = __any_sync(0xFFFFFFFFu, w1 != 0.f);
+      for (int i = 0; i < 2 * C; ++i)
+        lt += sm.xl[i & 1][(i >> 1) * kMpad + m] * ex2(sm.xm[i & 1][(i >> 1) * kMpad + m] - ref);
+      const float w0 = ex2(fmaxf(sm.xm[0][l], sm.xm[1][l]) - ref);
       const bool real = m < G * sg.rows;
       const bool whole = sg.slot < 0;
       const float inv = !whole ? 1.f : (lt == 0.f ? 0.f : 1.f / lt);
@@ -690,16 +725,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int step = 0; step < 4; ++step) {
         const int d0 = 64 * s + 16 * step;
-        uint32_t a[16], b[16];
-#pragma unroll
-        for (int u = 0; u < 16; ++u) a[u] = b[u] = 0u;
-        if (rd0) tmem_ld16(tbase + lane_base + kColO + d0, a);
-        if (rd1) tmem_ld16(tbase + lane_base + kColO + kDim + d0, b);
+        uint32_t a[16];
+        tmem_ld16(tbase + lane_base + kColO + d0, a);
         tc_wait_ld();
         float o[16];
 #pragma unroll
-        for (int u = 0; u < 16; ++u)
-          o[u] = (w0 != 0.f ? w0 * __uint_as_float(a[u]) : 0.f) + (w1 != 0.f ? w1 * __uint_as_float(b[u]) : 0.f);
+        for (int u = 0; u < 16; ++u) o[u] = w0 * __uint_as_float(a[u]);
         float y[kW];
         if constexpr (C == 1) {
 #pragma unroll
@@ -752,18 +783,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       mref = -INFINITY;
       lrun = 0.f;
       mine = 0;
-      return ok;
+      return true;
     };
 
-    for (int t = s;; t += 2) {
-      if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.s_full[s]), (t >> 1) & 1, p.flags))) break;
-      const Tile x = sm.tile[t % kRing];
-      bool good = true;
-      while (good && seg < x.seg) good = finish(seg++);  // segments that had no (further) tile for this set
-      if (x.end || !good) break;
+    // one call of finish: after the set's last tile of a segment, or when its next tile shows that
+    // segments without one have passed
+    int t = s;
+    Tile x = {};
+    bool fresh = false, over = false;
+    for (;;) {
+      if (over || (fresh && seg < x.seg)) {
+        if (!finish(seg++)) break;
+        over = false;
+        continue;
+      }
+      if (!fresh) {
+        if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.s_full[t % kBars]), (t / kBars) & 1, p.flags))) break;
+        x = sm.tile[t % kRing];
+        fresh = true;
+        continue;
+      }
+      if (x.end) break;
       tc_fence_after();
       if (mine == 0) {
         pos_max = sm.seg[seg % kRing].pos + row;
+        first = sm.seg[seg % kRing].first;
         coef_q = p.sm_scale_log2 * (NP == 1 ? 1.f : sm.qscale[seg % kRows][l]);
       }
       const bool full_vis = x.pos0 + kBlock - 1 <= pos_max - row;  // every token visible to every row
@@ -771,10 +815,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the floor keeps a masked score at -inf when a scale is 0
       const float coef = fmaxf(coef_q * x.kscale, 1e-30f);
       const float lv = log2f(x.vscale);
+      const uint32_t s_cols = tbase + lane_base + kColS + kBlock * (t % kSBufs);
       constexpr int kCh = kMpad / 32;
       constexpr bool kHold = kCh <= 2;  // all of the thread's scores in registers
-      uint32_t v[kHold ? kMpad : 32];
+      uint32_t v[kHold ? kMpad : 64];
       float mx = -INFINITY;
+      auto load_masked = [&](int half) {  // 64 scores of a row that one thread takes whole
+        tmem_ld32(s_cols + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(v));
+        tmem_ld32(s_cols + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+        tc_wait_ld();
+        if (!full_vis) {
+#pragma unroll
+          for (int u = 0; u < 64; ++u) v[u] = 64 * half + u <= lim ? v[u] : __float_as_uint(-INFINITY);
+        }
+      };
       if constexpr (kHold) {
 #pragma unroll
         for (int ch = 0; ch < kCh; ++ch) tmem_ld32(s_cols + k0 + 32 * ch, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * ch));
@@ -785,27 +839,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int u = 0; u < kMpad; u += 2) mx = fmax3(mx, __uint_as_float(v[u]), __uint_as_float(v[u + 1]));
+      } else if (full_vis) {  // the TMEM load reduces
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          float m0 = tmem_ld32_max(s_cols + 64 * half), m1 = tmem_ld32_max(s_cols + 64 * half + 32);
+          tc_wait_ld();
+          asm volatile("" : "+f"(m0), "+f"(m1));  // no use moves above the wait
+          mx = fmax3(mx, m0, m1);
+        }
       } else {
 #pragma unroll 1
-        for (int ch = 0; ch < kCh; ++ch) {
-          tmem_ld32(s_cols + 32 * ch, *reinterpret_cast<uint32_t(*)[32]>(v));
-          tc_wait_ld();
-          if (!full_vis) {
+        for (int half = 0; half < 2; ++half) {
+          load_masked(half);
 #pragma unroll
-            for (int u = 0; u < 32; ++u) v[u] = 32 * ch + u <= lim ? v[u] : __float_as_uint(-INFINITY);
-          }
-#pragma unroll
-          for (int u = 0; u < 32; u += 2) mx = fmax3(mx, __uint_as_float(v[u]), __uint_as_float(v[u + 1]));
+          for (int u = 0; u < 64; u += 2) mx = fmax3(mx, __uint_as_float(v[u]), __uint_as_float(v[u + 1]));
         }
       }
       // P is taken relative to a reference that moves only when the maximum passes it by more
-      // than kRescaleLog2 (P stays within FP16); O / l does not depend on it
+      // than kRescaleLog2 (P stays within FP16); O / l does not depend on it. The tile before
+      // (the other set's) has decided on it first.
+      if (t > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.decided[s ^ 1][quad]), ((t - 1) >> 1) & 1, p.flags))) break;
+      const float r_old = t == first ? -INFINITY : sm.ref[l];
       const float bmax = fmaf(mx, coef, lv);
-      const bool move = bmax > mref + kRescaleLog2 || (mref == -INFINITY && bmax != -INFINITY);
-      const float m_new = move ? bmax : mref;
+      const bool move = bmax > r_old + kRescaleLog2 || (r_old == -INFINITY && bmax != -INFINITY);
+      const float m_new = move ? bmax : r_old;
+      if (move || t == first) sm.ref[l] = m_new;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.decided[s][quad]));
       const float ref = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = ex2(mref - ref);  // 0 while nothing was seen yet
-      const bool rescale = move && mref != -INFINITY;
+      const bool rescale = move && r_old != -INFINITY;
       const float off = lv - ref;
       const float2 coef2 = make_float2(coef, coef), off2 = make_float2(off, off);
       float lsum = 0.f;
@@ -830,40 +892,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (z < c * kCh || z >= (c + 1) * kCh) tmem_zero16(s_cols + 16 * z);
       } else {
 #pragma unroll 1
-        for (int ch = 0; ch < kCh; ++ch) {
-          tmem_ld32(s_cols + 32 * ch, *reinterpret_cast<uint32_t(*)[32]>(v));
-          tc_wait_ld();
-          if (!full_vis) {
-#pragma unroll
-            for (int u = 0; u < 32; ++u) v[u] = 32 * ch + u <= lim ? v[u] : __float_as_uint(-INFINITY);
-          }
-          weights(v, s_cols + 16 * ch);
+        for (int half = 0; half < 2; ++half) {
+          load_masked(half);
+          weights(v, s_cols + 32 * half);
+          weights(v + 32, s_cols + 32 * half + 16);
         }
       }
-      if (mine > 0 && __any_sync(0xFFFFFFFFu, rescale)) {
-        // O holds the set's earlier tiles of the segment once their P V is done
-        if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.pv_done[s]), ((t >> 1) - 1) & 1, p.flags))) break;
+      if (__any_sync(0xFFFFFFFFu, rescale)) {
+        // O holds the segment's earlier tiles once the P V before is done; this tile's waits for the
+        // arrival below
+        if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.pv_done[(t - 1) % kBars]), ((t - 1) / kBars) & 1, p.flags))) break;
         tc_fence_after();
-        const float a = rescale ? alpha : 1.f;
+        const float a = rescale ? ex2(r_old - ref) : 1.f;
 #pragma unroll 1
         for (int qc = 0; qc < 4; ++qc) {
           uint32_t o[32];
-          tmem_ld32(tbase + lane_base + kColO + kDim * s + 32 * qc, o);
+          tmem_ld32(tbase + lane_base + kColO + 32 * qc, o);
           tc_wait_ld();
 #pragma unroll
           for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * a);
-          tmem_st32(tbase + lane_base + kColO + kDim * s + 32 * qc, o);
+          tmem_st32(tbase + lane_base + kColO + 32 * qc, o);
         }
       }
-      lrun = lrun * alpha + lsum * (1.f / x.vscale);
+      lrun = lrun * ex2(mref - ref) + lsum * (1.f / x.vscale);  // mref -inf: nothing summed yet
       mref = m_new;
       ++mine;
-      t_last = t;
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[s]));
-      if (t + 2 > x.last && !finish(seg++)) break;
+      if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[t % kBars]));
+      over = t + 2 > x.last;
+      fresh = false;
+      t += 2;
     }
   }
   tc_fence_before();
@@ -925,11 +985,11 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnP
 }
 
 template <int C, int NP>
-cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8AttnParams& prm, int grid, cudaStream_t st) {
+cudaError_t launch(const CUtensorMap& kmap, const Kv8AttnParams& prm, int grid, cudaStream_t st) {
   const int smem = static_cast<int>(sizeof(Smem<NP>)) + 1024;
   cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<C, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kv8_attn_kernel<C, NP><<<grid, kThreads, smem, st>>>(kmap, vmap, prm);
+  kv8_attn_kernel<C, NP><<<grid, kThreads, smem, st>>>(kmap, prm);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, (128 / C) / (kMergeThreads / 32));
@@ -971,14 +1031,14 @@ msa_status check_args(const msa_kv8_attn_args* a) {
 
 }  // namespace
 
-cudaError_t launch_kv8_attn(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8AttnParams& prm, bool q_bf16,
-                            int grid, cudaStream_t st) {
+cudaError_t launch_kv8_attn(const CUtensorMap& kmap, const Kv8AttnParams& prm, bool q_bf16, int grid,
+                            cudaStream_t st) {
   const int c = copies_for(prm.max_rows, prm.q_per_kv);
   if (q_bf16)
-    return c == 4 ? launch<4, 2>(kmap, vmap, prm, grid, st)
-           : c == 2 ? launch<2, 2>(kmap, vmap, prm, grid, st) : launch<1, 2>(kmap, vmap, prm, grid, st);
-  return c == 4 ? launch<4, 1>(kmap, vmap, prm, grid, st)
-         : c == 2 ? launch<2, 1>(kmap, vmap, prm, grid, st) : launch<1, 1>(kmap, vmap, prm, grid, st);
+    return c == 4 ? launch<4, 2>(kmap, prm, grid, st)
+           : c == 2 ? launch<2, 2>(kmap, prm, grid, st) : launch<1, 2>(kmap, prm, grid, st);
+  return c == 4 ? launch<4, 1>(kmap, prm, grid, st)
+         : c == 2 ? launch<2, 1>(kmap, prm, grid, st) : launch<1, 1>(kmap, prm, grid, st);
 }
 
 }  // namespace msa
@@ -1049,11 +1109,10 @@ msa_status msa_kv8_attn(const msa_kv8_attn_args* a, void* ws, size_t ws_bytes, v
   const int room = 128 / copies_for(p.max_rows, p.q_per_kv) / p.q_per_kv;
   p.chunk = 1;
   while (2 * p.chunk <= room) p.chunk *= 2, ++p.chunk_log2;
-  CUtensorMap kmap, vmap;
+  CUtensorMap kmap;
   const long long token_rows = static_cast<long long>(a->num_pages) * a->num_kv_heads * kBlock;
   if ((s = encode_kv8_map(&kmap, a->k_data, token_rows)) != MSA_OK) return s;
-  if ((s = encode_kv8_map(&vmap, a->v_data, token_rows)) != MSA_OK) return s;
-  return launch_kv8_attn(kmap, vmap, p, a->q_type == MSA_TYPE_BF16, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_kv8_attn(kmap, p, a->q_type == MSA_TYPE_BF16, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MSA_OK
              : MSA_ERR_CUDA;
 }

@@ -25,31 +25,41 @@ def _need(ok: bool, what: str):
 def _plain(t: torch.Tensor, dtype, shape, dev, name: str) -> int:
     """The address of a contiguous tensor of the given type and shape on `dev`."""
     dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
-    _need(t.is_cuda and t.device == dev, f"{name}: expected a tensor on {dev}, got {t.device}")
-    _need(t.dtype in dtypes, f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    _need(tuple(t.shape) == tuple(shape), f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    _need(t.is_contiguous(), f"{name}: expected a contiguous tensor")
+    if not (t.dtype in dtypes and t.device == dev and t.is_cuda and t.shape == tuple(shape) and t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous {' or '.join(map(str, dtypes))} tensor {tuple(shape)} on {dev} "
+                         f"(a GPU), got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
     return t.data_ptr()
 
 
 def _rows(t: torch.Tensor, heads: int, name: str) -> int:
     """The stride between the rows of [rows, heads, 128] whose heads are contiguous."""
-    _need(t.stride(2) == 1 and (heads == 1 or t.stride(1) == DIM),
-          f"{name}: the heads of a row must be contiguous, got strides {t.stride()}")
-    return t.stride(0) if t.shape[0] > 1 else heads * DIM
+    row, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != DIM):
+        raise ValueError(f"{name}: the heads of a row must be contiguous, got strides {t.stride()}")
+    return row if t.shape[0] > 1 else heads * DIM
 
 
 def _call(dev, stream, fn, what, *args):
     """fn(*args, stream) on the tensors' device; the stream is that device's current one unless given."""
-    if torch.cuda.current_device() == dev.index:
-        _lib._check(fn(*args, _lib._stream(stream)), what)
-    else:
+    if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
-            _lib._check(fn(*args, _lib._stream(stream)), what)
+            return _call(dev, stream, fn, what, *args)
+    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
+    code = fn(*args, s)
+    if code != _lib.MSA_OK:
+        raise _lib.MSAError(code, what)
+
+
+class _Handle:
+    """Tensors that are checked and marshalled once: setting an attribute marshals again."""
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_marshalled", None)
 
 
 @dataclasses.dataclass
-class KV8Batch:
+class KV8Batch(_Handle):
     """One step's per-request metadata on the GPU, and its queries: request b owns rows
     q_indptr[b] .. q_indptr[b+1] - 1, at positions context_lens[b] - R .. context_lens[b] - 1."""
     context_lens: torch.Tensor          # int32 [B], this step's rows included
@@ -64,18 +74,22 @@ class KV8Batch:
         return int(self.context_lens.shape[0])
 
 
-def _geometry(a, cache: "KV8Cache", batch, dev):
-    B = batch.num_reqs
-    a.num_reqs, a.total_rows, a.max_rows_per_req = B, int(batch.total_rows), int(batch.max_rows_per_req)
-    a.num_pages, a.num_kv_heads = cache.num_pages, cache.num_kv_heads
-    a.max_pages_per_req = int(batch.block_table.shape[1])
-    a.context_lens = _plain(batch.context_lens, torch.int32, (B,), dev, "context_lens")
-    a.q_indptr = _plain(batch.q_indptr, torch.int32, (B + 1,), dev, "q_indptr")
-    a.block_table = _plain(batch.block_table, torch.int32, (B, a.max_pages_per_req), dev, "block_table")
+def _geometry(batch, dev):
+    """(B, rows, most rows per request, row length of the table, the three tensors' addresses)."""
+    got = batch.__dict__.get("_marshalled")
+    if got is None or got[0] != dev:
+        B, M = batch.num_reqs, int(batch.block_table.shape[1])
+        got = (dev, (B, int(batch.total_rows), int(batch.max_rows_per_req), M,
+                     _plain(batch.context_lens, torch.int32, (B,), dev, "context_lens"),
+                     _plain(batch.q_indptr, torch.int32, (B + 1,), dev, "q_indptr"),
+                     _plain(batch.block_table, torch.int32, (B, M), dev, "block_table")))
+        if isinstance(batch, KV8Batch):
+            batch.__dict__["_marshalled"] = got
+    return got[1]
 
 
 @dataclasses.dataclass
-class KV8Cache:
+class KV8Cache(_Handle):
     """Paged 8-bit K and V: data [P, H, 128, 128] uint8 (E4M3 codes), scale [P, H] float32; the
     value of a slot is E4M3(code) * scale."""
     k_data: torch.Tensor
@@ -97,36 +111,41 @@ class KV8Cache:
         scale = lambda: torch.zeros((num_pages, num_kv_heads), dtype=torch.float32, device=device)  # noqa: E731
         return KV8Cache(data(), scale(), data(), scale())
 
-    def _pointers(self, a, dev):
-        P, H = self.num_pages, self.num_kv_heads
-        for n in ("k", "v"):
-            data, scale = getattr(self, n + "_data"), getattr(self, n + "_scale")
-            setattr(a, n + "_data", _plain(data, (torch.uint8, torch.float8_e4m3fn), (P, H, BLOCK, DIM), dev, n + "_data"))
-            setattr(a, n + "_scale", _plain(scale, torch.float32, (P, H), dev, n + "_scale"))
+    def _pointers(self):
+        """(device, pages, KV heads, addresses of k_data, k_scale, v_data, v_scale)."""
+        got = self.__dict__.get("_marshalled")
+        if got is None:
+            P, H, dev = self.num_pages, self.num_kv_heads, self.k_data.device
+            codes = (torch.uint8, torch.float8_e4m3fn)
+            got = (dev, P, H, _plain(self.k_data, codes, (P, H, BLOCK, DIM), dev, "k_data"),
+                   _plain(self.k_scale, torch.float32, (P, H), dev, "k_scale"),
+                   _plain(self.v_data, codes, (P, H, BLOCK, DIM), dev, "v_data"),
+                   _plain(self.v_scale, torch.float32, (P, H), dev, "v_scale"))
+            self.__dict__["_marshalled"] = got
+        return got
 
     def append(self, batch, k: Optional[torch.Tensor], v: Optional[torch.Tensor], ws: torch.Tensor, stream=None):
         """Quantise the batch's new tokens into their pages (msa_kv8_append): k and v
         [rows, H, 128] in bfloat16, float16 or float32 (one type for both; rows may be strided, as
         the parts of a fused projection are), either of them None; ws a zero-filled workspace
         of >= 256 bytes (error flags). `batch` is a KV8Batch or a DecodeBatch; its q is not read."""
-        a = _lib.Kv8AppendArgs()
-        dev = self.k_data.device
-        _geometry(a, self, batch, dev)
-        self._pointers(a, dev)
-        types = {t.dtype for t in (k, v) if t is not None}
-        _need(len(types) <= 1 and types <= _SRC_TYPES.keys(),
-              f"k and v: expected one of bfloat16, float16, float32 for both, got {types}")
-        a.src_type = _SRC_TYPES[types.pop()] if types else _lib.TYPE_BF16
-        for name, t in (("k", k), ("v", v)):
+        dev, P, H, kd, ks, vd, vs = self._pointers()
+        B, total, most, M, lens, indptr, table = _geometry(batch, dev)
+        dtype, shape, src, strides = None, (total, H, DIM), [None, None], [0, 0]
+        for i, t in enumerate((k, v)):
             if t is None:
                 continue
-            _need(t.is_cuda and t.device == dev and tuple(t.shape) == (a.total_rows, a.num_kv_heads, DIM),
-                  f"{name}: expected [{a.total_rows}, {a.num_kv_heads}, {DIM}] on {dev}, got {tuple(t.shape)} on {t.device}")
-            setattr(a, name + "_token_stride", _rows(t, a.num_kv_heads, name))
-            setattr(a, name, t.data_ptr())
-        _need(ws.is_cuda and ws.device == dev and ws.is_contiguous(), f"ws: expected a contiguous tensor on {dev}")
-        _call(dev, stream, _lib.load().msa_kv8_append, "msa_kv8_append", ctypes.byref(a),
-              ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size())
+            if t.shape != shape or t.device != dev or (dtype is not None and t.dtype is not dtype) or \
+                    t.dtype not in _SRC_TYPES:
+                raise ValueError(f"{'kv'[i]}: expected {shape} on {dev} in one of {list(_SRC_TYPES)}, one type for k and "
+                                 f"v, got {tuple(t.shape)} {t.dtype} on {t.device}")
+            dtype, src[i], strides[i] = t.dtype, t.data_ptr(), _rows(t, H, "kv"[i])
+        if ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws: expected a contiguous tensor on {dev}")
+        a = _lib.Kv8AppendArgs(B, total, most, P, M, H, _SRC_TYPES.get(dtype, _lib.TYPE_BF16), strides[0], strides[1],
+                               lens, indptr, table, src[0], src[1], kd, ks, vd, vs)
+        _call(dev, stream, _lib.load().msa_kv8_append, "msa_kv8_append", ctypes.byref(a), ws.data_ptr(),
+              ws.numel() * ws.element_size())
 
 
 class KV8Attention:
@@ -150,28 +169,26 @@ class KV8Attention:
                         "msa_kv8_attn_workspace_size")
             self.ws = torch.empty(n.value, dtype=torch.uint8, device=self.device)
             _lib.msa_workspace_init(self.ws)
+        self._ws = (self.ws.data_ptr(), self.ws.numel())
 
     def rebind(self, batch: KV8Batch):
         """Point at another batch of the same sizes."""
-        a = _lib.Kv8AttnArgs()
-        _geometry(a, self.cache, batch, self.device)
-        self.cache._pointers(a, self.device)
+        dev, P, H, kd, ks, vd, vs = self.cache._pointers()
+        B, total, most, M, lens, indptr, table = _geometry(batch, dev)
         rows, heads = self.out.shape[:2]
         q = batch.q
-        _need(q is not None and q.is_cuda and q.device == self.device and tuple(q.shape) == (rows, heads, DIM) and
-              rows == a.total_rows, f"q: expected [{rows}, {heads}, {DIM}] on {self.device}")
+        _need(q is not None and q.device == dev and q.shape == (rows, heads, DIM) and rows == total,
+              f"q: expected [{rows}, {heads}, {DIM}] on {dev}")
         _need(q.dtype in _Q_TYPES, f"q: expected bfloat16 or E4M3 (uint8, float8_e4m3fn), got {q.dtype}")
-        _need(heads % a.num_kv_heads == 0, f"q: {heads} heads do not divide among {a.num_kv_heads} KV heads")
-        if getattr(self, "args", None) is not None:
-            old = self.args
-            _need((old.num_reqs, old.max_rows_per_req, old.max_pages_per_req) ==
-                  (a.num_reqs, a.max_rows_per_req, a.max_pages_per_req), "rebind: expected a batch of the same sizes")
-        a.q_per_kv = heads // a.num_kv_heads
-        a.q_type, a.q_row_stride, a.q = _Q_TYPES[q.dtype], _rows(q, heads, "q"), q.data_ptr()
-        a.sm_scale = float(self.sm_scale)
-        a.out = self.out.data_ptr()
-        a.lse = self.lse.data_ptr() if self.lse is not None else None
-        self.batch, self.args = batch, a
+        _need(heads % H == 0, f"q: {heads} heads do not divide among {H} KV heads")
+        old = getattr(self, "args", None)
+        _need(old is None or (old.num_reqs, old.max_rows_per_req, old.max_pages_per_req) == (B, most, M),
+              "rebind: expected a batch of the same sizes")
+        self.batch = batch
+        self.args = _lib.Kv8AttnArgs(B, total, most, P, M, H, heads // H, 0, _Q_TYPES[q.dtype], float(self.sm_scale),
+                                     _rows(q, heads, "q"), lens, indptr, table, None, q.data_ptr(), kd, ks, vd, vs,
+                                     self.out.data_ptr(), self.lse.data_ptr() if self.lse is not None else None)
+        self._ref = ctypes.byref(self.args)
 
     def attend(self, block_ids: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """softmax(sm_scale q k) v of every row over the keys it may see: of all blocks, or of
@@ -184,8 +201,7 @@ class KV8Attention:
             n = int(block_ids.shape[-1])
             a.block_ids = _plain(block_ids, torch.int32, (a.num_reqs, a.num_kv_heads, n), self.device, "block_ids")
             a.n_block_ids = n
-        _call(self.device, stream, _lib.load().msa_kv8_attn, "msa_kv8_attn", ctypes.byref(a),
-              ctypes.c_void_p(self.ws.data_ptr()), self.ws.numel())
+        _call(self.device, stream, _lib.load().msa_kv8_attn, "msa_kv8_attn", self._ref, self._ws[0], self._ws[1])
         return self.out
 
     def errors(self, stream=None) -> int:

@@ -56,6 +56,7 @@ class PagePool:
         with torch.cuda.device(dev):
             self.ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
             _lib.msa_workspace_init(self.ws)
+        self._ref, self._ws = ctypes.byref(a), (self.ws.data_ptr(), self.ws.numel())
 
     @staticmethod
     def empty(caches: Sequence[Union[KVCache, KV8Cache]], num_seqs: int, max_pages: int) -> "PagePool":
@@ -64,46 +65,50 @@ class PagePool:
         z = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=ref.device)  # noqa: E731
         return PagePool(caches, z(num_seqs), z(num_seqs, max_pages).fill_(-1), z(ref.shape[0]))
 
-    def _list(self, t: torch.Tensor, n: int, name: str):
-        return ctypes.c_void_p(_plain(t, torch.int32, (n,), self.device, name))
+    def _list(self, t: torch.Tensor, n: int, name: str) -> int:
+        if t.dtype is not torch.int32 or t.shape != (n,) or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous int32 list of {n} on {self.device}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
 
     def _run(self, name: str, stream, *args):
-        _call(self.device, stream, getattr(_lib.load(), name), name, ctypes.byref(self.args), *args,
-              ctypes.c_void_p(self.ws.data_ptr()), self.ws.numel())
+        _call(self.device, stream, getattr(_lib.load(), name), name, self._ref, *args, *self._ws)
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor, tokens: Optional[torch.Tensor] = None, stream=None):
         """Copy page src[i] to dst[i] in every plane: the first tokens[i] slots, or all."""
-        n = int(src.shape[0])
+        n = src.numel()
         self._run("msa_pages_copy", stream, n, self._list(src, n, "src"), self._list(dst, n, "dst"),
                   None if tokens is None else self._list(tokens, n, "tokens"))
 
     def fork(self, parents: torch.Tensor, children: torch.Tensor, stream=None):
         """Make the empty sequences children[i] copies of parents[i]: full pages shared, a partly
         filled last page copied to a free page."""
-        n = int(children.shape[0])
+        n = children.numel()
         self._run("msa_pages_fork", stream, n, self._list(parents, n, "parents"), self._list(children, n, "children"))
 
     def reserve(self, seqs: torch.Tensor, new_lens: torch.Tensor, stream=None):
         """Grow sequences to new_lens tokens, with free pages behind theirs as needed."""
-        n = int(seqs.shape[0])
+        n = seqs.numel()
         self._run("msa_pages_reserve", stream, n, self._list(seqs, n, "seqs"), self._list(new_lens, n, "new_lens"))
 
     def free(self, seqs: torch.Tensor, stream=None):
         """End sequences: their pages' counts fall by one, their lengths become 0."""
-        n = int(seqs.shape[0])
+        n = seqs.numel()
         self._run("msa_pages_free", stream, n, self._list(seqs, n, "seqs"))
 
     def compact(self, block_table: Optional[torch.Tensor] = None, ref_counts: Optional[torch.Tensor] = None,
                 num_live: Optional[torch.Tensor] = None, stream=None):
         """Move the live pages to the ids 0 .. L - 1, in place or with the new tables written to the
         given tensors (both or neither); num_live (int32 [1]) gets L."""
-        _need((block_table is None) == (ref_counts is None), "compact: give both tables or neither")
-        t = self.block_table if block_table is None else block_table
-        r = self.ref_counts if ref_counts is None else ref_counts
-        self._run("msa_pages_compact", stream,
-                  ctypes.c_void_p(_plain(t, torch.int32, self.block_table.shape, self.device, "block_table")),
-                  ctypes.c_void_p(_plain(r, torch.int32, self.ref_counts.shape, self.device, "ref_counts")),
-                  None if num_live is None else self._list(num_live, 1, "num_live"))
+        if (block_table is None) != (ref_counts is None):
+            raise ValueError("compact: give both tables or neither")
+        a = self.args
+        if block_table is None:
+            t, r = a.block_table, a.ref_counts
+        else:
+            t = _plain(block_table, torch.int32, (a.num_seqs, a.max_pages_per_seq), self.device, "block_table")
+            r = self._list(ref_counts, a.num_pages, "ref_counts")
+        self._run("msa_pages_compact", stream, t, r, None if num_live is None else self._list(num_live, 1, "num_live"))
 
     def errors(self, stream=None) -> int:
         """Device error flags since the last read (synchronises the stream)."""
