@@ -32,8 +32,9 @@
 //     copies their K (16 KB) into a ring; what the others need of a tile or segment goes into
 //     small rings beside it. V warp: copies their V. Each runs ahead as its own ring allows: a
 //     K stage is held until its S is computed, a V stage only until it is in registers;
-//   * 4 converting warps: V to FP16, rows past the context to zero; at a segment's first tile
-//     they also lay out its queries;
+//   * 8 converting warps, four for each 64-token half of a tile: V to FP16 (a half's buffer is
+//     written while the other half is multiplied), rows past the context to zero; at a
+//     segment's first tile they also lay out its queries;
 //   * S warp (three score buffers in tensor memory) and P V warp (one O);
 //   * 8 softmax warps in two sets taking alternate tiles. A lane of the O belongs to one thread
 //     of each set; the reference its weights are relative to goes from tile to tile through
@@ -55,17 +56,17 @@ namespace {
 
 constexpr int kSoftWarps = 8;                        // warps 0..7: two sets of 4, one per TMEM lane quadrant
 constexpr int kMmaWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11;
-constexpr int kCvWarp0 = 12, kCvWarps = 4;
+constexpr int kCvWarp0 = 12, kCvWarps = 8;           // two groups of 4
 constexpr int kThreads = (kCvWarp0 + kCvWarps) * 32;
-constexpr int kVStages = 3;
+constexpr int kVStages = 4;
 // A wait on a barrier's parity has to be for its current phase or the one before. Waiters that
 // skip tiles, or fall behind, therefore have barriers that go round 6 tiles (even: each serves one
-// softmax set; no wait is 6 tiles behind), or 12 for a tile's description (up to 8 ahead).
+// softmax set; no wait is 6 tiles behind), or 12 for a tile's description (up to 9 ahead).
 constexpr int kBars = 6, kTold = 12;
 constexpr int kRing = 16;                            // tiles and segments whose description is kept
 constexpr int kRows = 8;                             // segments whose query scales and NaN marks are kept
 constexpr uint32_t kTileBytes = kBlock * kDim;       // K or V of a tile
-constexpr uint32_t kHalfBytes = kBlock * 128;        // FP16 V: 128 tokens x 64 dims
+constexpr uint32_t kHalfBytes = 64 * 128;            // FP16 V: 64 tokens x 64 dims
 // TMEM columns: three score buffers (128 FP32; the weights, FP16 pairs, go over the first 64), O.
 constexpr int kSBufs = 3;
 constexpr uint32_t kColS = 0, kColO = kSBufs * kBlock, kTmemCols = 512;
@@ -98,11 +99,11 @@ struct Seg {
 
 template <int NP>
 struct Smem {
-  static constexpr int kKStages = NP == 1 ? 4 : 3;
+  static constexpr int kKStages = NP == 1 ? 5 : 4;
   uint8_t q[NP][kTileBytes];                         // A of S: copies of the query rows, by part
   uint8_t k[kKStages][kTileBytes];                   // B of S (K-major), 128-byte swizzle
   uint8_t v[kVStages][kTileBytes];                   // V codes as they are in the page
-  uint8_t v16[2][2][kHalfBytes];                     // B of O (MN-major): [set][half][token][64 dims]
+  uint8_t v16[2][2][kHalfBytes];                     // B of O (MN-major): [token half][dim half][token][64 dims]
   float red[2][128 * kRedStride];                    // copies of a row joined, 16 dims at a time
   float qscale[kRows][128];                          // 2^e of each tile row (BF16 queries)
   int nanpos[kRows][kDim];                           // first position with a NaN value in a dim, of partly seen tokens
@@ -112,7 +113,7 @@ struct Smem {
   Tile tile[kRing];
   Seg seg[kRing];
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], told[kTold];
-  uint64_t q_full, q_free, s_full[kBars], p_full[kBars], v16_full[2], pv_done[kBars], drain[2];
+  uint64_t q_full, q_free, s_full[kBars], p_full[kBars], v16_full[2], v16_free[2], pv_done[kBars], drain[2];
   uint64_t decided[2][4];                            // by set and quadrant: the tile's reference stands
   uint64_t sets_met, set_met[2];                     // the softmax warps of both sets, or of one, have come here
   long long part[kThreads / 32];
@@ -235,7 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sm.pv_done[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&sm.v16_full[s]), kCvWarps);
+      mbar_init(smem_u32(&sm.v16_full[s]), kCvWarps / 2);
+      mbar_init(smem_u32(&sm.v16_free[s]), 1);
       for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sm.decided[s][w]), 1);
     }
     for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&sm.drain[s]), 1);
@@ -444,51 +446,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) reinterpret_cast<Header*>(p.parts)[blockIdx.x] = hd;
     __syncwarp();
   } else if (warp >= kCvWarp0) {
-    // ================= converting warps; thread = one 16-byte piece of every 16th row
-    const int r = tid - kCvWarp0 * 32, r7 = r & 7;                             // r: the query row it lays out
-    const int vr = r >> 3, vc = r & 7;                                         // V row (mod 16) and 16-byte piece
+    // ================= converting warps: group h has tokens 64 h .. 64 h + 63 of every tile; thread =
+    // one 16-byte piece of every 16th row
+    const int h = (warp - kCvWarp0) / 4, r = (tid - kCvWarp0 * 32) & 127;
+    const int vr = r >> 3, vc = r & 7;  // V row (mod 16) and 16-byte piece
+    // 16 codes -> two 16-byte pieces of dim half vc / 4; the second half's threads store theirs the
+    // other way round, so that a row's 8 threads meet 8 different banks
+    const int flip = vc >> 2, ch = 2 * (vc & 3);
+    const uint32_t o0 = static_cast<uint32_t>((ch + flip) ^ (vr & 7)) << 4, o1 = o0 ^ 16u;
+    const uint32_t dst = smem_u32(sm.v16[h][flip]) + static_cast<uint32_t>(vr) * 128u;
     for (int t = 0;; ++t) {
       const int st = t % kVStages;
       if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.v_full[st]), (t / kVStages) & 1, p.flags))) break;
       const Tile x = sm.tile[t % kRing];
       const Seg& sg = sm.seg[x.seg % kRing];
       if (!x.end && sg.first == t) {
-        // the segment's queries, once the last segment's scores are computed
+        // the segment's queries, once the last segment's scores are computed: two threads per row
         const int k = x.seg;
         if (k > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.q_free), (k - 1) & 1, p.flags))) break;
-        const int m = r % kMpad;
+        const int rr = 64 * h + (r >> 1), half = r & 1, m = rr % kMpad;
         const bool real = m < G * sg.rows;
         const long long at = real ? static_cast<long long>(sg.row0 + m / G) * p.q_stride + (sg.head * G + m % G) * kDim : 0;
-        const uint32_t row = smem_u32(sm.q[0]) + static_cast<uint32_t>(r) * 128u;
+        const uint32_t row = smem_u32(sm.q[0]) + static_cast<uint32_t>(rr) * 128u;
         if constexpr (NP == 1) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) + at);
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) + at) + 4 * half;
+          uint4 v[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[c] = real ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            st_shared_v4(row + (static_cast<uint32_t>((4 * half + c) ^ (rr & 7)) << 4), v[c].x, v[c].y, v[c].z, v[c].w);
+        } else {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at) + 8 * half;
           uint4 v[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c) v[c] = real ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            st_shared_v4(row + (static_cast<uint32_t>(c ^ r7) << 4), v[c].x, v[c].y, v[c].z, v[c].w);
-        } else {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at);
           // largest magnitude by its bits: BF16 pairs, both halves at once
-          uint4 v[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) v[c] = real ? src[c] : make_uint4(0u, 0u, 0u, 0u);
           uint32_t big = 0u;
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
+          for (int c = 0; c < 8; ++c)
             big = __vmaxu2(big, __vmaxu2(__vmaxu2(v[c].x & 0x7FFF7FFFu, v[c].y & 0x7FFF7FFFu),
                                          __vmaxu2(v[c].z & 0x7FFF7FFFu, v[c].w & 0x7FFF7FFFu)));
+          big = __vmaxu2(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
           const uint32_t amax = max(big & 0xFFFFu, big >> 16);
           const bool odd = amax >= 0x7F80u;  // an infinity or a NaN: the whole row becomes NaN
           // smallest 2^e with amax <= 448 2^e; below 2^-120 nothing a score could show is left
           int e = static_cast<int>(amax >> 7) - 127 - 8 + ((amax & 0x7Fu) > 0x60u ? 1 : 0);
           e = e < -120 ? -120 : e;
           const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          sm.qscale[k % kRows][r] = odd ? 1.f : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-          const uint32_t row2 = row + kTileBytes;
+          if (half == 0) sm.qscale[k % kRows][rr] = odd ? 1.f : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {  // 16 elements: 16 code bytes of each part
+          for (int c = 0; c < 4; ++c) {  // 16 elements: 16 code bytes of each part
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -515,78 +523,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                 hi[i] = 0x7F7F7F7Fu;
                 lo[i] = 0u;
               }
-            const uint32_t o = static_cast<uint32_t>(c ^ r7) << 4;
+            const uint32_t o = static_cast<uint32_t>((4 * half + c) ^ (rr & 7)) << 4;
             st_shared_v4(row + o, hi[0], hi[1], hi[2], hi[3]);
-            st_shared_v4(row2 + o, lo[0], lo[1], lo[2], lo[3]);
+            st_shared_v4(row + kTileBytes + o, lo[0], lo[1], lo[2], lo[3]);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
       }
-      // the tile's codes to registers, and the stage back to the V warp
-      const int rows = x.vzero ? 0 : x.nvalid;
-      uint4 v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = 16 * i + vr < rows ? lds_u4(smem_u32(sm.v[st]) + static_cast<uint32_t>(r + 128 * i) * 16u)
-                                  : make_uint4(0u, 0u, 0u, 0u);
-      __threadfence_block();  // the loads are over, not only issued, when the stage is given back
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.v_empty[st]));
+      const uint32_t raw = smem_u32(sm.v[st]) + static_cast<uint32_t>(64 * kDim * h + 16 * r);
+      const int rows = (x.vzero ? 0 : x.nvalid) - 64 * h;  // of this half
       // a token that some rows of the segment do not see: its weight is 0 there, but 0 x NaN is
       // NaN, so its NaN codes become 0 here and are put back for the rows that see it
       if (x.nvalid > 0 && x.pos0 + x.nvalid - 1 > sg.pos) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (x.pos0 + 16 * i + vr <= sg.pos) continue;
-          uint32_t* w = reinterpret_cast<uint32_t*>(&v[i]);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint32_t nan = __vcmpeq4(w[y] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            if (nan) {
-              for (int z = 0; z < 4; ++z)
-                if ((nan >> (8 * z)) & 1u)
-                  atomicMin(&sm.nanpos[x.seg % kRows][16 * vc + 4 * y + z], x.pos0 + 16 * i + vr);
-              sm.nanany[x.seg % kRows] = 1;
-              w[y] &= ~nan;
-            }
-          }
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {  // word i % 4 of the piece of row 16 (i / 4) + vr
+          const int token = 64 * h + 16 * (i >> 2) + vr;
+          const uint32_t at = raw + 2048u * (i >> 2) + 4u * (i & 3);
+          const uint32_t w = lds_u1(at), nan = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          if (nan == 0u || token >= x.nvalid || x.pos0 + token <= sg.pos) continue;
+          for (int z = 0; z < 4; ++z)
+            if ((nan >> (8 * z)) & 1u) atomicMin(&sm.nanpos[x.seg % kRows][16 * vc + 4 * (i & 3) + z], x.pos0 + token);
+          sm.nanany[x.seg % kRows] = 1;
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(w & ~nan) : "memory");
         }
       }
-      // the P V two tiles before has read the FP16 tile
-      if (t >= 2 && !__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.pv_done[(t - 2) % kBars]), ((t - 2) / kBars) & 1, p.flags)))
+      // the P V of the tile before has read this half's buffer
+      if (t > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.v16_free[h]), (t - 1) & 1, p.flags))) break;
+      if (x.end) {
+        if (h == 0 && lane == 0) mbar_arrive(smem_u32(&sm.v16_full[0]));
         break;
-      if (!x.end) {
-        // 16 codes -> two 16-byte pieces of half vc / 4; the second half's threads store theirs the
-        // other way round, so that a row's 8 threads meet 8 different banks
-        const int flip = vc >> 2, ch = 2 * (vc & 3);
-        const uint32_t dst = smem_u32(sm.v16[t & 1][flip]) + static_cast<uint32_t>(vr) * 128u;
-        const uint32_t o0 = static_cast<uint32_t>((ch + flip) ^ (vr & 7)) << 4, o1 = o0 ^ 16u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-          uint32_t f[8];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            f[2 * y] = e4m3x2_f16x2(w[y] & 0xFFFFu);
-            f[2 * y + 1] = e4m3x2_f16x2(w[y] >> 16);
-          }
-          const uint32_t row = dst + 16u * 128u * i;
-          st_shared_v4(row + o0, flip ? f[4] : f[0], flip ? f[5] : f[1], flip ? f[6] : f[2], flip ? f[7] : f[3]);
-          st_shared_v4(row + o1, flip ? f[0] : f[4], flip ? f[1] : f[5], flip ? f[2] : f[6], flip ? f[3] : f[7]);
-        }
-        fence_proxy_async_smem();
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (16 * i + vr < rows) w = lds_u4(raw + 2048u * i);
+        const uint32_t f[8] = {e4m3x2_f16x2(w.x & 0xFFFFu), e4m3x2_f16x2(w.x >> 16), e4m3x2_f16x2(w.y & 0xFFFFu),
+                               e4m3x2_f16x2(w.y >> 16),     e4m3x2_f16x2(w.z & 0xFFFFu), e4m3x2_f16x2(w.z >> 16),
+                               e4m3x2_f16x2(w.w & 0xFFFFu), e4m3x2_f16x2(w.w >> 16)};
+        st_shared_v4(dst + 2048u * i + o0, flip ? f[4] : f[0], flip ? f[5] : f[1], flip ? f[6] : f[2], flip ? f[7] : f[3]);
+        st_shared_v4(dst + 2048u * i + o1, flip ? f[0] : f[4], flip ? f[1] : f[5], flip ? f[2] : f[6], flip ? f[3] : f[7]);
+      }
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.v16_full[t & 1]));
-      if (x.end) break;
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&sm.v16_full[h]));
+        // the codes are in the stores above, not only asked for: the stage may be refilled
+        mbar_arrive(smem_u32(&sm.v_empty[st]));
+      }
     }
   } else if (warp == kVWarp) {
     // ================= V warp
     if (lane == 0) {
       int t = 0;
-      for (;; ++t) {
+      for (bool end = false; !end; ++t) {
         const int st = t % kVStages;
         if (!wait_bar(smem_u32(&sm.told[t % kTold]), (t / kTold) & 1, p.flags)) break;
         const Tile x = sm.tile[t % kRing];
@@ -598,10 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           mbar_arrive(bar);
         }
-        if (x.end) {
-          ++t;
-          break;
-        }
+        end = x.end;
       }
       // no copy may still be landing when the CTA leaves
       for (int j = t - kVStages < 0 ? 0 : t - kVStages; j < t; ++j)
@@ -656,18 +644,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc = idesc_f16_f32(128, kDim, true);
       int seg = -1;
       for (int t = 0;; ++t) {
-        const int s = t & 1;
-        if (!wait_bar(smem_u32(&sm.v16_full[s]), (t >> 1) & 1, p.flags)) break;
+        if (!wait_bar(smem_u32(&sm.v16_full[0]), t & 1, p.flags)) break;
         const Tile x = sm.tile[t % kRing];
         if (x.end) break;
         if (!wait_bar(smem_u32(&sm.p_full[t % kBars]), (t / kBars) & 1, p.flags)) break;
-        tc_fence_after();
-        // 128 dims = two 64-dim halves (the leading offset), 8-token groups 1 KB apart, 16 tokens = 2 KB
-        const uint64_t vdesc = sdesc_mn_sw128(smem_u32(sm.v16[s][0]), kHalfBytes);
         const uint32_t pcol = tbase + kColS + kBlock * (t % kSBufs);
+        bool good = true;
 #pragma unroll
-        for (int kk = 0; kk < kBlock / 16; ++kk)
-          mma_f16_tmemA(tbase + kColO, pcol + 8 * kk, vdesc + 128 * kk, idesc, x.seg == seg || kk > 0 ? 1u : 0u);
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && !wait_bar(smem_u32(&sm.v16_full[1]), t & 1, p.flags)) {
+            good = false;
+            break;
+          }
+          tc_fence_after();
+          // 128 dims = two 64-dim halves (the leading offset), 8-token groups 1 KB apart, 16 tokens = 2 KB
+          const uint64_t vdesc = sdesc_mn_sw128(smem_u32(sm.v16[h][0]), kHalfBytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_tmemA(tbase + kColO, pcol + 32 * h + 8 * kk, vdesc + 128 * kk, idesc,
+                          x.seg == seg || h > 0 || kk > 0 ? 1u : 0u);
+          mma_commit(smem_u32(&sm.v16_free[h]));
+        }
+        if (!good) break;
         seg = x.seg;
         mma_commit(smem_u32(&sm.pv_done[t % kBars]));
       }
@@ -737,6 +735,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 0; u < 16; ++u) y[u] = o[u];
         } else {
           float* red = sm.red[s];
+          // (sums read from it have been stored, so their loads are over)
+          if (step > 0 && !meet(&sm.set_met[s], met_set)) return false;
 #pragma unroll
           for (int u = 0; u < 16; ++u) red[l * kRedStride + u] = o[u];
           if (!meet(&sm.set_met[s], met_set)) return false;
@@ -746,7 +746,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < C; ++i) y[u] += red[(i * kMpad + m) * kRedStride + c * kW + u];
           }
-          if (!meet(&sm.set_met[s], met_set)) return false;
         }
         const int d = d0 + c * kW;
 #pragma unroll
@@ -817,42 +816,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float lv = log2f(x.vscale);
       const uint32_t s_cols = tbase + lane_base + kColS + kBlock * (t % kSBufs);
       constexpr int kCh = kMpad / 32;
-      constexpr bool kHold = kCh <= 2;  // all of the thread's scores in registers
-      uint32_t v[kHold ? kMpad : 64];
+      uint32_t v[32];  // 32 scores at a time: 20 warps share the registers, and short code stays cached
       float mx = -INFINITY;
-      auto load_masked = [&](int half) {  // 64 scores of a row that one thread takes whole
-        tmem_ld32(s_cols + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(v));
-        tmem_ld32(s_cols + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+      auto load = [&](int ch) {  // scores of tokens k0 + 32 ch .., -inf where the row does not see them
+        tmem_ld32(s_cols + k0 + 32 * ch, v);
         tc_wait_ld();
         if (!full_vis) {
 #pragma unroll
-          for (int u = 0; u < 64; ++u) v[u] = 64 * half + u <= lim ? v[u] : __float_as_uint(-INFINITY);
+          for (int u = 0; u < 32; ++u) v[u] = 32 * ch + u <= lim ? v[u] : __float_as_uint(-INFINITY);
         }
       };
-      if constexpr (kHold) {
-#pragma unroll
-        for (int ch = 0; ch < kCh; ++ch) tmem_ld32(s_cols + k0 + 32 * ch, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * ch));
-        tc_wait_ld();
-        if (!full_vis) {
-#pragma unroll
-          for (int u = 0; u < kMpad; ++u) v[u] = u <= lim ? v[u] : __float_as_uint(-INFINITY);
-        }
-#pragma unroll
-        for (int u = 0; u < kMpad; u += 2) mx = fmax3(mx, __uint_as_float(v[u]), __uint_as_float(v[u + 1]));
-      } else if (full_vis) {  // the TMEM load reduces
+      if (kCh > 1 && full_vis) {  // the TMEM load reduces
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          float m0 = tmem_ld32_max(s_cols + 64 * half), m1 = tmem_ld32_max(s_cols + 64 * half + 32);
+        for (int ch = 0; ch < kCh; ++ch) {
+          float m1 = tmem_ld32_max(s_cols + k0 + 32 * ch);
           tc_wait_ld();
-          asm volatile("" : "+f"(m0), "+f"(m1));  // no use moves above the wait
-          mx = fmax3(mx, m0, m1);
+          asm volatile("" : "+f"(m1));  // no use moves above the wait
+          mx = fmaxf(mx, m1);
         }
       } else {
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          load_masked(half);
+        for (int ch = 0; ch < kCh; ++ch) {
+          load(ch);
+          float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-          for (int u = 0; u < 64; u += 2) mx = fmax3(mx, __uint_as_float(v[u]), __uint_as_float(v[u + 1]));
+          for (int u = 0; u < 32; u += 4) {
+            m0 = fmax3(m0, __uint_as_float(v[u]), __uint_as_float(v[u + 1]));
+            m1 = fmax3(m1, __uint_as_float(v[u + 2]), __uint_as_float(v[u + 3]));
+          }
+          mx = fmax3(mx, m0, m1);
         }
       }
       // P is taken relative to a reference that moves only when the maximum passes it by more
@@ -871,32 +863,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float off = lv - ref;
       const float2 coef2 = make_float2(coef, coef), off2 = make_float2(off, off);
       float lsum = 0.f;
-      auto weights = [&](uint32_t* w, uint32_t col) {  // 32 scores -> 16 columns of FP16 pairs
+#pragma unroll 1
+      for (int ch = 0; ch < kCh; ++ch) {
+        if (kCh > 1) load(ch);  // again; a single chunk is still in v
         float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
-          const float2 d = __ffma2_rn(make_float2(__uint_as_float(w[2 * u]), __uint_as_float(w[2 * u + 1])), coef2, off2);
+        for (int u = 0; u < 16; ++u) {  // 32 scores -> 16 columns of FP16 pairs
+          const float2 d = __ffma2_rn(make_float2(__uint_as_float(v[2 * u]), __uint_as_float(v[2 * u + 1])), coef2, off2);
           const float2 e = make_float2(ex2(d.x), ex2(d.y));
           acc = __fadd2_rn(acc, e);
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[u]) : "f"(e.y), "f"(e.x));
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v[u]) : "f"(e.y), "f"(e.x));
         }
         lsum += acc.x + acc.y;
-        tmem_st16(col, w);
-      };
-      if constexpr (kHold) {
-#pragma unroll
-        for (int ch = 0; ch < kCh; ++ch) weights(v + 32 * ch, s_cols + (k0 + 32 * ch) / 2);
-        // the columns of the other copies' tokens (their scores were there)
+        tmem_st16(s_cols + (k0 + 32 * ch) / 2, v);
+      }
+      // the weights' columns of the other copies' tokens (scores were there)
+      if constexpr (C > 1) {
 #pragma unroll
         for (int z = 0; z < 4; ++z)
           if (z < c * kCh || z >= (c + 1) * kCh) tmem_zero16(s_cols + 16 * z);
-      } else {
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          load_masked(half);
-          weights(v, s_cols + 32 * half);
-          weights(v + 32, s_cols + 32 * half + 16);
-        }
       }
       if (__any_sync(0xFFFFFFFFu, rescale)) {
         // O holds the segment's earlier tiles once the P V before is done; this tile's waits for the
