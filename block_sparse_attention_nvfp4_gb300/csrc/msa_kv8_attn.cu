@@ -32,9 +32,9 @@
 //     copies their K (16 KB) into a ring; what the others need of a tile or segment goes into
 //     small rings beside it. V warp: copies their V. Each runs ahead as its own ring allows: a
 //     K stage is held until its S is computed, a V stage only until it is in registers;
-//   * 8 converting warps, four for each 64-token half of a tile: V to FP16 (a half's buffer is
-//     written while the other half is multiplied), rows past the context to zero; at a
-//     segment's first tile they also lay out its queries;
+//   * 8 converting warps, four for each 64-token half of a tile: V to FP16 in three buffers that
+//     the halves take in turn, rows past the context to zero; at a segment's first tile they
+//     also lay out its queries;
 //   * S warp (three score buffers in tensor memory) and P V warp (one O);
 //   * 8 softmax warps in two sets taking alternate tiles. A lane of the O belongs to one thread
 //     of each set; the reference its weights are relative to goes from tile to tile through
@@ -58,7 +58,7 @@ constexpr int kSoftWarps = 8;                        // warps 0..7: two sets of 
 constexpr int kMmaWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11;
 constexpr int kCvWarp0 = 12, kCvWarps = 8;           // two groups of 4
 constexpr int kThreads = (kCvWarp0 + kCvWarps) * 32;
-constexpr int kVStages = 4;
+constexpr int kVBufs = 3;                            // FP16 halves of V
 // A wait on a barrier's parity has to be for its current phase or the one before. Waiters that
 // skip tiles, or fall behind, therefore have barriers that go round 6 tiles (even: each serves one
 // softmax set; no wait is 6 tiles behind), or 12 for a tile's description (up to 9 ahead).
@@ -99,11 +99,11 @@ struct Seg {
 
 template <int NP>
 struct Smem {
-  static constexpr int kKStages = NP == 1 ? 5 : 4;
+  static constexpr int kKStages = 4, kVStages = NP == 1 ? 4 : 3;
   uint8_t q[NP][kTileBytes];                         // A of S: copies of the query rows, by part
   uint8_t k[kKStages][kTileBytes];                   // B of S (K-major), 128-byte swizzle
   uint8_t v[kVStages][kTileBytes];                   // V codes as they are in the page
-  uint8_t v16[2][2][kHalfBytes];                     // B of O (MN-major): [token half][dim half][token][64 dims]
+  uint8_t v16[kVBufs][2][kHalfBytes];                // B of O (MN-major): [dim half][token][64 dims]
   float red[2][128 * kRedStride];                    // copies of a row joined, 16 dims at a time
   float qscale[kRows][128];                          // 2^e of each tile row (BF16 queries)
   int nanpos[kRows][kDim];                           // first position with a NaN value in a dim, of partly seen tokens
@@ -113,7 +113,7 @@ struct Smem {
   Tile tile[kRing];
   Seg seg[kRing];
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], told[kTold];
-  uint64_t q_full, q_free, s_full[kBars], p_full[kBars], v16_full[2], v16_free[2], pv_done[kBars], drain[2];
+  uint64_t q_full, q_free, s_full[kBars], p_full[kBars], v16_full[kVBufs], v16_free[kBars], pv_done[kBars], drain[2];
   uint64_t decided[2][4];                            // by set and quadrant: the tile's reference stands
   uint64_t sets_met, set_met[2];                     // the softmax warps of both sets, or of one, have come here
   long long part[kThreads / 32];
@@ -137,8 +137,24 @@ struct Header {
 constexpr long long kPartFloats = 128LL * kDim + 256;  // O, m, l
 __host__ __device__ inline size_t headers_bytes(int grid) { return (grid * sizeof(Header) + 255) / 256 * 256; }
 
+// A bounded wait (kWaitLimitNs) that reads the timer once in 256 tries: the timer's latency would
+// otherwise be part of every hand-over between the roles.
+static __device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, uint32_t* flags) {
+  long long t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try(bar, parity)) return true;
+    if ((i & 255u) == 0u) {
+      const long long now = global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) {
+        set_flag(flags, kFlagTimeout);
+        return false;
+      }
+    }
+  }
+}
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t* flags) {
-  return mbar_try(bar, parity) || mbar_wait(bar, parity, flags);
+  return mbar_try(bar, parity) || wait_bar_slow(bar, parity, flags);
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -211,7 +227,7 @@ template <int C, int NP>
 __global__ void __launch_bounds__(kThreads, 1)
     kv8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const Kv8AttnParams p) {
   constexpr int kMpad = 128 / C;
-  constexpr int kStages = Smem<NP>::kKStages;
+  constexpr int kStages = Smem<NP>::kKStages, kVStages = Smem<NP>::kVStages;
   extern __shared__ uint8_t smem_raw[];
   Smem<NP>& sm = *reinterpret_cast<Smem<NP>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -223,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sm.k_full[s]), 1);
       mbar_init(smem_u32(&sm.k_empty[s]), 1);
     }
+    for (int s = 0; s < kVBufs; ++s) mbar_init(smem_u32(&sm.v16_full[s]), kCvWarps / 2);
     for (int s = 0; s < kVStages; ++s) {
       mbar_init(smem_u32(&sm.v_full[s]), 1);
       mbar_init(smem_u32(&sm.v_empty[s]), kCvWarps);
@@ -232,12 +249,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&sm.q_free), 1);
     for (int s = 0; s < kBars; ++s) {
       mbar_init(smem_u32(&sm.s_full[s]), 1);
+      mbar_init(smem_u32(&sm.v16_free[s]), 1);
       mbar_init(smem_u32(&sm.p_full[s]), kSoftWarps / 2);
       mbar_init(smem_u32(&sm.pv_done[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&sm.v16_full[s]), kCvWarps / 2);
-      mbar_init(smem_u32(&sm.v16_free[s]), 1);
       for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sm.decided[s][w]), 1);
     }
     for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&sm.drain[s]), 1);
@@ -454,7 +470,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // other way round, so that a row's 8 threads meet 8 different banks
     const int flip = vc >> 2, ch = 2 * (vc & 3);
     const uint32_t o0 = static_cast<uint32_t>((ch + flip) ^ (vr & 7)) << 4, o1 = o0 ^ 16u;
-    const uint32_t dst = smem_u32(sm.v16[h][flip]) + static_cast<uint32_t>(vr) * 128u;
     for (int t = 0;; ++t) {
       const int st = t % kVStages;
       if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.v_full[st]), (t / kVStages) & 1, p.flags))) break;
@@ -549,26 +564,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(w & ~nan) : "memory");
         }
       }
-      // the P V of the tile before has read this half's buffer
-      if (t > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.v16_free[h]), (t - 1) & 1, p.flags))) break;
+      // the half that was in this buffer (three halves ago) has been multiplied
+      const int u = 2 * t + h;
+      if (u >= kVBufs &&
+          !__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.v16_free[(u - kVBufs) % kBars]), ((u - kVBufs) / kBars) & 1, p.flags)))
+        break;
       if (x.end) {
-        if (h == 0 && lane == 0) mbar_arrive(smem_u32(&sm.v16_full[0]));
+        if (h == 0 && lane == 0) mbar_arrive(smem_u32(&sm.v16_full[u % kVBufs]));
         break;
       }
-#pragma unroll
+      const uint32_t dst = smem_u32(sm.v16[u % kVBufs][flip]) + static_cast<uint32_t>(vr) * 128u;
+#pragma unroll 2
       for (int i = 0; i < 4; ++i) {
         uint4 w = make_uint4(0u, 0u, 0u, 0u);
         if (16 * i + vr < rows) w = lds_u4(raw + 2048u * i);
-        const uint32_t f[8] = {e4m3x2_f16x2(w.x & 0xFFFFu), e4m3x2_f16x2(w.x >> 16), e4m3x2_f16x2(w.y & 0xFFFFu),
-                               e4m3x2_f16x2(w.y >> 16),     e4m3x2_f16x2(w.z & 0xFFFFu), e4m3x2_f16x2(w.z >> 16),
-                               e4m3x2_f16x2(w.w & 0xFFFFu), e4m3x2_f16x2(w.w >> 16)};
-        st_shared_v4(dst + 2048u * i + o0, flip ? f[4] : f[0], flip ? f[5] : f[1], flip ? f[6] : f[2], flip ? f[7] : f[3]);
-        st_shared_v4(dst + 2048u * i + o1, flip ? f[0] : f[4], flip ? f[1] : f[5], flip ? f[2] : f[6], flip ? f[3] : f[7]);
+        const uint32_t a0 = flip ? w.z : w.x, a1 = flip ? w.w : w.y, b0 = flip ? w.x : w.z, b1 = flip ? w.y : w.w;
+        st_shared_v4(dst + 2048u * i + o0, e4m3x2_f16x2(a0), e4m3x2_f16x2(a0 >> 16), e4m3x2_f16x2(a1), e4m3x2_f16x2(a1 >> 16));
+        st_shared_v4(dst + 2048u * i + o1, e4m3x2_f16x2(b0), e4m3x2_f16x2(b0 >> 16), e4m3x2_f16x2(b1), e4m3x2_f16x2(b1 >> 16));
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(smem_u32(&sm.v16_full[h]));
+        mbar_arrive(smem_u32(&sm.v16_full[u % kVBufs]));
         // the codes are in the stores above, not only asked for: the stage may be refilled
         mbar_arrive(smem_u32(&sm.v_empty[st]));
       }
@@ -644,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc = idesc_f16_f32(128, kDim, true);
       int seg = -1;
       for (int t = 0;; ++t) {
-        if (!wait_bar(smem_u32(&sm.v16_full[0]), t & 1, p.flags)) break;
+        if (!wait_bar(smem_u32(&sm.v16_full[(2 * t) % kVBufs]), (2 * t / kVBufs) & 1, p.flags)) break;
         const Tile x = sm.tile[t % kRing];
         if (x.end) break;
         if (!wait_bar(smem_u32(&sm.p_full[t % kBars]), (t / kBars) & 1, p.flags)) break;
@@ -652,18 +669,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool good = true;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (h == 1 && !wait_bar(smem_u32(&sm.v16_full[1]), t & 1, p.flags)) {
+          const int u = 2 * t + h;
+          if (h == 1 && !wait_bar(smem_u32(&sm.v16_full[u % kVBufs]), (u / kVBufs) & 1, p.flags)) {
             good = false;
             break;
           }
           tc_fence_after();
           // 128 dims = two 64-dim halves (the leading offset), 8-token groups 1 KB apart, 16 tokens = 2 KB
-          const uint64_t vdesc = sdesc_mn_sw128(smem_u32(sm.v16[h][0]), kHalfBytes);
+          const uint64_t vdesc = sdesc_mn_sw128(smem_u32(sm.v16[u % kVBufs][0]), kHalfBytes);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_f16_tmemA(tbase + kColO, pcol + 32 * h + 8 * kk, vdesc + 128 * kk, idesc,
                           x.seg == seg || h > 0 || kk > 0 ? 1u : 0u);
-          mma_commit(smem_u32(&sm.v16_free[h]));
+          mma_commit(smem_u32(&sm.v16_free[u % kBars]));
         }
         if (!good) break;
         seg = x.seg;
@@ -682,8 +700,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int l = 32 * quad + lane, m = l % kMpad, c = l / kMpad, k0 = c * kMpad;
     const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
     const int row = m / G;
-    float mref = -INFINITY, lrun = 0.f, coef_q = 0.f;  // this set's sum, relative to the last reference it used
-    int pos_max = 0, first = 0, seg = 0, mine = 0;              // mine: tiles of the segment that this set has done
+    float mref = -INFINITY, lrun = 0.f;  // this set's sum, relative to the last reference it used
+    int seg = 0;
     uint32_t met_all = 0, met_set = 0;               // phases of the meeting points
     // A meeting of warps, bounded like every other wait: after a timeout anywhere each warp leaves
     // by itself.
@@ -781,7 +799,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mref = -INFINITY;
       lrun = 0.f;
-      mine = 0;
       return true;
     };
 
@@ -804,46 +821,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (x.end) break;
       tc_fence_after();
-      if (mine == 0) {
-        pos_max = sm.seg[seg % kRing].pos + row;
-        first = sm.seg[seg % kRing].first;
-        coef_q = p.sm_scale_log2 * (NP == 1 ? 1.f : sm.qscale[seg % kRows][l]);
-      }
+      const int pos_max = sm.seg[seg % kRing].pos + row, first = sm.seg[seg % kRing].first;
+      const float coef_q = p.sm_scale_log2 * (NP == 1 ? 1.f : sm.qscale[seg % kRows][l]);
       const bool full_vis = x.pos0 + kBlock - 1 <= pos_max - row;  // every token visible to every row
       const int lim = pos_max - x.pos0 - k0;                        // token k0 + n visible iff n <= lim
       // the floor keeps a masked score at -inf when a scale is 0
       const float coef = fmaxf(coef_q * x.kscale, 1e-30f);
       const float lv = log2f(x.vscale);
       const uint32_t s_cols = tbase + lane_base + kColS + kBlock * (t % kSBufs);
+      // The loop bodies are short and run several times on purpose: the roles' code together is what
+      // an SM's instruction cache has to hold, and fetching it was the bound when they were unrolled.
       constexpr int kCh = kMpad / 32;
-      uint32_t v[32];  // 32 scores at a time: 20 warps share the registers, and short code stays cached
-      float mx = -INFINITY;
-      auto load = [&](int ch) {  // scores of tokens k0 + 32 ch .., -inf where the row does not see them
-        tmem_ld32(s_cols + k0 + 32 * ch, v);
-        tc_wait_ld();
-        if (!full_vis) {
+      uint32_t v[32];
+      if (!full_vis) {  // scores of tokens that the row does not see become -inf in place
+#pragma unroll 1
+        for (int ch = 0; ch < kCh; ++ch) {
+          tmem_ld32(s_cols + k0 + 32 * ch, v);
+          tc_wait_ld();
 #pragma unroll
           for (int u = 0; u < 32; ++u) v[u] = 32 * ch + u <= lim ? v[u] : __float_as_uint(-INFINITY);
+          tmem_st32(s_cols + k0 + 32 * ch, v);
         }
-      };
-      if (kCh > 1 && full_vis) {  // the TMEM load reduces
-#pragma unroll 1
-        for (int ch = 0; ch < kCh; ++ch) {
-          float m1 = tmem_ld32_max(s_cols + k0 + 32 * ch);
-          tc_wait_ld();
-          asm volatile("" : "+f"(m1));  // no use moves above the wait
-          mx = fmaxf(mx, m1);
-        }
+        tc_wait_st();
+      }
+      float mx = -INFINITY;
+      if constexpr (kCh == 1) {
+        tmem_ld32(s_cols + k0, v);
+        tc_wait_ld();
+#pragma unroll
+        for (int u = 0; u < 32; u += 2) mx = fmax3(mx, __uint_as_float(v[u]), __uint_as_float(v[u + 1]));
       } else {
 #pragma unroll 1
-        for (int ch = 0; ch < kCh; ++ch) {
-          load(ch);
-          float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-          for (int u = 0; u < 32; u += 4) {
-            m0 = fmax3(m0, __uint_as_float(v[u]), __uint_as_float(v[u + 1]));
-            m1 = fmax3(m1, __uint_as_float(v[u + 2]), __uint_as_float(v[u + 3]));
-          }
+        for (int ch = 0; ch < kCh; ch += 2) {  // the TMEM load reduces
+          float m0 = tmem_ld32_max(s_cols + k0 + 32 * ch), m1 = tmem_ld32_max(s_cols + k0 + 32 * ch + 32);
+          tc_wait_ld();
+          asm volatile("" : "+f"(m0), "+f"(m1));  // no use moves above the wait
           mx = fmax3(mx, m0, m1);
         }
       }
@@ -865,7 +877,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       float lsum = 0.f;
 #pragma unroll 1
       for (int ch = 0; ch < kCh; ++ch) {
-        if (kCh > 1) load(ch);  // again; a single chunk is still in v
+        if (kCh > 1) {
+          tmem_ld32(s_cols + k0 + 32 * ch, v);
+          tc_wait_ld();
+        }
         float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < 16; ++u) {  // 32 scores -> 16 columns of FP16 pairs
@@ -901,7 +916,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       lrun = lrun * ex2(mref - ref) + lsum * (1.f / x.vscale);  // mref -inf: nothing summed yet
       mref = m_new;
-      ++mine;
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
