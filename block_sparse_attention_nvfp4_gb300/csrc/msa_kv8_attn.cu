@@ -29,12 +29,14 @@
 // that few rows still spread the exponentials over all four SM sub-partitions (P is zero in the
 // other copies' columns). Roles, as in the sparse attention over the NVFP4 cache (msa_attn.cu):
 //   * K warp: finds the tiles (32 block-table entries and scales at a time, one per lane) and
-//     copies their K (16 KB) into a ring; what the others need of a tile or segment goes into
-//     small rings beside it. V warp: copies their V. Each runs ahead as its own ring allows: a
-//     K stage is held until its S is computed, a V stage only until it is in registers;
+//     copies their K (16 KB, tensor copies) into a ring; what the others need of a tile or
+//     segment goes into small rings beside it;
 //   * 8 converting warps, four for each 64-token half of a tile: V to FP16 in three buffers that
 //     the halves take in turn, rows past the context to zero; at a segment's first tile they
-//     also lay out its queries;
+//     also lay out its queries. Each thread copies the codes that it will convert itself (16-byte
+//     asynchronous copies, 2 or 3 tiles ahead), so V needs no hand-over, and K and V come by
+//     different paths: tensor and bulk copies alone measured 20-23 bytes a cycle and SM whatever
+//     is in flight, a tile's 32 KB then 1,400 cycles even from L2; both paths together 50;
 //   * S warp (three score buffers in tensor memory) and P V warp (one O);
 //   * 8 softmax warps in two sets taking alternate tiles. A lane of the O belongs to one thread
 //     of each set; the reference its weights are relative to goes from tile to tile through
@@ -55,7 +57,7 @@ namespace msa {
 namespace {
 
 constexpr int kSoftWarps = 8;                        // warps 0..7: two sets of 4, one per TMEM lane quadrant
-constexpr int kMmaWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11;
+constexpr int kMmaWarp = 8, kPvWarp = 9, kKWarp = 10;  // (warp 11 has no part: warps come in fours)
 constexpr int kCvWarp0 = 12, kCvWarps = 8;           // two groups of 4
 constexpr int kThreads = (kCvWarp0 + kCvWarps) * 32;
 constexpr int kVBufs = 3;                            // FP16 halves of V
@@ -102,7 +104,7 @@ struct Smem {
   static constexpr int kKStages = 4, kVStages = NP == 1 ? 4 : 3;
   uint8_t q[NP][kTileBytes];                         // A of S: copies of the query rows, by part
   uint8_t k[kKStages][kTileBytes];                   // B of S (K-major), 128-byte swizzle
-  uint8_t v[kVStages][kTileBytes];                   // V codes as they are in the page
+  uint8_t v[kVStages][kTileBytes];                   // V codes as they are in the page, a slot of each thread
   uint8_t v16[kVBufs][2][kHalfBytes];                // B of O (MN-major): [dim half][token][64 dims]
   float red[2][128 * kRedStride];                    // copies of a row joined, 16 dims at a time
   float qscale[kRows][128];                          // 2^e of each tile row (BF16 queries)
@@ -112,7 +114,7 @@ struct Smem {
   float xm[2][128], xl[2][128];
   Tile tile[kRing];
   Seg seg[kRing];
-  uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], told[kTold];
+  uint64_t k_full[kKStages], k_empty[kKStages], told[kTold];
   uint64_t q_full, q_free, s_full[kBars], p_full[kBars], v16_full[kVBufs], v16_free[kBars], pv_done[kBars], drain[2];
   uint64_t decided[2][4];                            // by set and quadrant: the tile's reference stands
   uint64_t sets_met, set_met[2];                     // the softmax warps of both sets, or of one, have come here
@@ -137,13 +139,23 @@ struct Header {
 constexpr long long kPartFloats = 128LL * kDim + 256;  // O, m, l
 __host__ __device__ inline size_t headers_bytes(int grid) { return (grid * sizeof(Header) + 255) / 256 * 256; }
 
-// A bounded wait (kWaitLimitNs) that reads the timer once in 256 tries: the timer's latency would
-// otherwise be part of every hand-over between the roles.
+// A bounded wait (kWaitLimitNs). A try suspends the warp for up to 20 us, so that waiting roles
+// leave the issue slots to the others; the timer is read once in 64 tries, because its latency
+// would otherwise be part of every hand-over.
+__device__ __forceinline__ bool try_bar(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
 static __device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, uint32_t* flags) {
   long long t0 = 0;
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try(bar, parity)) return true;
-    if ((i & 255u) == 0u) {
+    if (try_bar(bar, parity)) return true;
+    if ((i & 63u) == 0u) {
       const long long now = global_ns();
       if (t0 == 0) t0 = now;
       if (now - t0 > kWaitLimitNs) {
@@ -154,7 +166,43 @@ static __device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity,
   }
 }
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t* flags) {
-  return mbar_try(bar, parity) || wait_bar_slow(bar, parity, flags);
+  return try_bar(bar, parity) || wait_bar_slow(bar, parity, flags);
+}
+// The whole warp waits, converged (one lane asking for all leaves the others to a divergent
+// barrier, which wakes ~1,500 cycles late).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t* flags) {
+  return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, flags));
+}
+// The MMAs and commits with the election inside: the issuing warp stays converged, so that its
+// descriptors live in uniform registers (8 products issue in 260 cycles against 450 from a
+// one-lane branch).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void mma_f8_ss_elect(uint32_t elected, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; "
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_tmemA_elect(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                    uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; "
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elect(uint32_t elected, uint32_t bar) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %1, 0; "
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar),
+      "r"(elected)
+      : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -168,6 +216,10 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
         "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(taddr)
       : "memory");
+}
+// 16 bytes to shared memory, asynchronously; the first `bytes` (0 or 16) are copied, the others zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
   const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
@@ -240,10 +292,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sm.k_empty[s]), 1);
     }
     for (int s = 0; s < kVBufs; ++s) mbar_init(smem_u32(&sm.v16_full[s]), kCvWarps / 2);
-    for (int s = 0; s < kVStages; ++s) {
-      mbar_init(smem_u32(&sm.v_full[s]), 1);
-      mbar_init(smem_u32(&sm.v_empty[s]), kCvWarps);
-    }
     for (int s = 0; s < kTold; ++s) mbar_init(smem_u32(&sm.told[s]), 1);
     mbar_init(smem_u32(&sm.q_full), kCvWarps);
     mbar_init(smem_u32(&sm.q_free), 1);
@@ -327,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto emit = [&](int pos0, int nvalid, int last, int end, int page, float ks, float vs) {
       const int st = t % kStages;
       if (t >= kStages) {
-        good = __all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.k_empty[st]), ((t / kStages) - 1) & 1, p.flags));
+        good = warp_wait(smem_u32(&sm.k_empty[st]), ((t / kStages) - 1) & 1, p.flags);
         if (!good) return;
       }
       if (lane == 0) {
@@ -470,15 +518,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     // other way round, so that a row's 8 threads meet 8 different banks
     const int flip = vc >> 2, ch = 2 * (vc & 3);
     const uint32_t o0 = static_cast<uint32_t>((ch + flip) ^ (vr & 7)) << 4, o1 = o0 ^ 16u;
-    for (int t = 0;; ++t) {
-      const int st = t % kVStages;
-      if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.v_full[st]), (t / kVStages) & 1, p.flags))) break;
-      const Tile x = sm.tile[t % kRing];
+    const uint32_t slot0 = smem_u32(sm.v[0]) + static_cast<uint32_t>(64 * kDim * h + 16 * r);
+    // Starts the copies of this thread's pieces of tile t (zeros for rows past the context).
+    bool more = true;  // no end mark fetched yet
+    auto fetch = [&](int t) -> bool {
+      if (more) {
+        if (!warp_wait(smem_u32(&sm.told[t % kTold]), (t / kTold) & 1, p.flags)) return false;
+        const Tile& x = sm.tile[t % kRing];
+        more = !x.end;
+        const int rows = (x.vzero ? 0 : x.nvalid) - 64 * h - vr;  // > 16 i: row 16 i + vr of this half counts
+        const uint8_t* src = p.v_data + static_cast<long long>(x.page) * kTileBytes + 64 * kDim * h + 16 * r;
+        const uint32_t to = slot0 + static_cast<uint32_t>(t % kVStages) * kTileBytes;
+        if (more)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) cp_async16(to + 2048u * i, src + 2048 * i, rows > 16 * i ? 16u : 0u);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      return true;
+    };
+    bool ok = true;
+    for (int t = 0; t < kVStages - 1 && ok; ++t) ok = fetch(t);
+    for (int t = 0; ok; ++t) {
+      const Tile& x = sm.tile[t % kRing];
+      const bool end = x.end;
       const Seg& sg = sm.seg[x.seg % kRing];
-      if (!x.end && sg.first == t) {
+      if (!end && sg.first == t) {
         // the segment's queries, once the last segment's scores are computed: two threads per row
         const int k = x.seg;
-        if (k > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.q_free), (k - 1) & 1, p.flags))) break;
+        if (k > 0 && !warp_wait(smem_u32(&sm.q_free), (k - 1) & 1, p.flags)) break;
         const int rr = 64 * h + (r >> 1), half = r & 1, m = rr % kMpad;
         const bool real = m < G * sg.rows;
         const long long at = real ? static_cast<long long>(sg.row0 + m / G) * p.q_stride + (sg.head * G + m % G) * kDim : 0;
@@ -547,8 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
       }
-      const uint32_t raw = smem_u32(sm.v[st]) + static_cast<uint32_t>(64 * kDim * h + 16 * r);
-      const int rows = (x.vzero ? 0 : x.nvalid) - 64 * h;  // of this half
+      asm volatile("cp.async.wait_group %0;" ::"n"(kVStages - 2) : "memory");  // this thread's pieces of tile t
+      const uint32_t raw = slot0 + static_cast<uint32_t>(t % kVStages) * kTileBytes;
       // a token that some rows of the segment do not see: its weight is 0 there, but 0 x NaN is
       // NaN, so its NaN codes become 0 here and are put back for the rows that see it
       if (x.nvalid > 0 && x.pos0 + x.nvalid - 1 > sg.pos) {
@@ -564,133 +631,115 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(w & ~nan) : "memory");
         }
       }
+      uint32_t f[4][8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 w = lds_u4(raw + 2048u * i);
+        const uint32_t a0 = flip ? w.z : w.x, a1 = flip ? w.w : w.y, b0 = flip ? w.x : w.z, b1 = flip ? w.y : w.w;
+        f[i][0] = e4m3x2_f16x2(a0), f[i][1] = e4m3x2_f16x2(a0 >> 16);
+        f[i][2] = e4m3x2_f16x2(a1), f[i][3] = e4m3x2_f16x2(a1 >> 16);
+        f[i][4] = e4m3x2_f16x2(b0), f[i][5] = e4m3x2_f16x2(b0 >> 16);
+        f[i][6] = e4m3x2_f16x2(b1), f[i][7] = e4m3x2_f16x2(b1 >> 16);
+      }
       // the half that was in this buffer (three halves ago) has been multiplied
       const int u = 2 * t + h;
-      if (u >= kVBufs &&
-          !__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.v16_free[(u - kVBufs) % kBars]), ((u - kVBufs) / kBars) & 1, p.flags)))
-        break;
-      if (x.end) {
+      if (u >= kVBufs && !warp_wait(smem_u32(&sm.v16_free[(u - kVBufs) % kBars]), ((u - kVBufs) / kBars) & 1, p.flags)) break;
+      if (end) {
         if (h == 0 && lane == 0) mbar_arrive(smem_u32(&sm.v16_full[u % kVBufs]));
         break;
       }
       const uint32_t dst = smem_u32(sm.v16[u % kVBufs][flip]) + static_cast<uint32_t>(vr) * 128u;
-#pragma unroll 2
+#pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (16 * i + vr < rows) w = lds_u4(raw + 2048u * i);
-        const uint32_t a0 = flip ? w.z : w.x, a1 = flip ? w.w : w.y, b0 = flip ? w.x : w.z, b1 = flip ? w.y : w.w;
-        st_shared_v4(dst + 2048u * i + o0, e4m3x2_f16x2(a0), e4m3x2_f16x2(a0 >> 16), e4m3x2_f16x2(a1), e4m3x2_f16x2(a1 >> 16));
-        st_shared_v4(dst + 2048u * i + o1, e4m3x2_f16x2(b0), e4m3x2_f16x2(b0 >> 16), e4m3x2_f16x2(b1), e4m3x2_f16x2(b1 >> 16));
+        st_shared_v4(dst + 2048u * i + o0, f[i][0], f[i][1], f[i][2], f[i][3]);
+        st_shared_v4(dst + 2048u * i + o1, f[i][4], f[i][5], f[i][6], f[i][7]);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&sm.v16_full[u % kVBufs]));
-        // the codes are in the stores above, not only asked for: the stage may be refilled
-        mbar_arrive(smem_u32(&sm.v_empty[st]));
-      }
+      if (lane == 0) mbar_arrive(smem_u32(&sm.v16_full[u % kVBufs]));
+      if (!fetch(t + kVStages - 1)) break;  // into the slots that tile t - 1 had
     }
-  } else if (warp == kVWarp) {
-    // ================= V warp
-    if (lane == 0) {
-      int t = 0;
-      for (bool end = false; !end; ++t) {
-        const int st = t % kVStages;
-        if (!wait_bar(smem_u32(&sm.told[t % kTold]), (t / kTold) & 1, p.flags)) break;
-        const Tile x = sm.tile[t % kRing];
-        if (t >= kVStages && !wait_bar(smem_u32(&sm.v_empty[st]), ((t / kVStages) - 1) & 1, p.flags)) break;
-        const uint32_t bar = smem_u32(&sm.v_full[st]);
-        if (x.nvalid > 0 && !x.vzero) {
-          mbar_arrive_expect_tx(bar, kTileBytes);
-          bulk_load(smem_u32(sm.v[st]), p.v_data + static_cast<long long>(x.page) * kTileBytes, kTileBytes, bar);
-        } else {
-          mbar_arrive(bar);
-        }
-        end = x.end;
-      }
-      // no copy may still be landing when the CTA leaves
-      for (int j = t - kVStages < 0 ? 0 : t - kVStages; j < t; ++j)
-        if (!wait_bar(smem_u32(&sm.v_full[j % kVStages]), (j / kVStages) & 1, p.flags)) break;
-    }
-    __syncwarp();
+    asm volatile("cp.async.wait_all;" ::: "memory");  // none may still be landing when the CTA leaves
   } else if (warp == kMmaWarp) {
     // ================= S warp: S_t = Q K_t^T into buffer t % 3
-    if (lane == 0) {
-      const uint64_t qdesc = sdesc_kmajor_sw128(smem_u32(sm.q[0]));
-      const uint32_t idesc = idesc_e4m3_f32(128, kBlock, false, false);
-      int seg = -1;
-      bool any = false;
-      for (int t = 0;; ++t) {
-        const int st = t % kStages, sb = t % kSBufs;
-        if (!wait_bar(smem_u32(&sm.k_full[st]), (t / kStages) & 1, p.flags)) break;
-        const Tile x = sm.tile[t % kRing];
-        // the buffer's previous weights have been used
-        if (t >= kSBufs && !wait_bar(smem_u32(&sm.pv_done[(t - kSBufs) % kBars]), ((t - kSBufs) / kBars) & 1, p.flags)) break;
-        if (x.end) {
+    const uint32_t el = elect_one();
+    const uint64_t qdesc = sdesc_kmajor_sw128(smem_u32(sm.q[0])), kdesc0 = sdesc_kmajor_sw128(smem_u32(sm.k[0]));
+    const uint32_t idesc = idesc_e4m3_f32(128, kBlock, false, false);
+    int seg = -1, ends = 0;
+    bool good = true;
+    for (int t = 0; ends < 2; ++t) {  // each softmax set sees one of the two end marks
+      const int st = t % kStages, sb = t % kSBufs;
+      // the buffer's previous weights have been used
+      if (t >= kSBufs) good = warp_wait(smem_u32(&sm.pv_done[(t - kSBufs) % kBars]), ((t - kSBufs) / kBars) & 1, p.flags);
+      if (!good || !warp_wait(smem_u32(&sm.k_full[st]), (t / kStages) & 1, p.flags)) break;
+      const Tile& x = sm.tile[t % kRing];
+      if (x.end) {
+        ++ends;
+        if (lane == 0) {
           mbar_arrive(smem_u32(&sm.s_full[t % kBars]));
           mbar_arrive(smem_u32(&sm.k_empty[st]));
-          if (t > 0 && sm.tile[(t - 1) % kRing].end) break;  // both sets know
-          continue;
         }
-        if (x.seg != seg) {
-          seg = x.seg;
-          if (!wait_bar(smem_u32(&sm.q_full), seg & 1, p.flags)) break;
-        }
-        tc_fence_after();
-        any = true;
-        const uint64_t kdesc = sdesc_kmajor_sw128(smem_u32(sm.k[st]));
-#pragma unroll
-        for (int part = 0; part < NP; ++part)
-#pragma unroll
-          for (int kk = 0; kk < kDim / 32; ++kk)  // 32 bytes along the rows: + 2 in the address field
-            mma_f8_ss(tbase + kColS + kBlock * sb, qdesc + part * (kTileBytes >> 4) + 2 * kk, kdesc + 2 * kk, idesc,
-                      part > 0 || kk > 0);
-        mma_commit(smem_u32(&sm.s_full[t % kBars]));
-        mma_commit(smem_u32(&sm.k_empty[st]));
-        if (t == x.last) mma_commit(smem_u32(&sm.q_free));
+        continue;
       }
-      if (any) {  // every MMA of this thread has finished before the tensor memory is released
-        mma_commit(smem_u32(&sm.drain[0]));
-        mbar_wait(smem_u32(&sm.drain[0]), 0, p.flags);
+      const int last = x.last;
+      if (x.seg != seg) {
+        seg = x.seg;
+        if (!warp_wait(smem_u32(&sm.q_full), seg & 1, p.flags)) break;
       }
+      tc_fence_after();
+      const uint64_t kdesc = kdesc0 + static_cast<uint32_t>(st) * (kTileBytes >> 4);
+#pragma unroll
+      for (int part = 0; part < NP; ++part)
+#pragma unroll
+        for (int kk = 0; kk < kDim / 32; ++kk)  // 32 bytes along the rows: + 2 in the address field
+          mma_f8_ss_elect(el, tbase + kColS + kBlock * sb, qdesc + part * (kTileBytes >> 4) + 2 * kk, kdesc + 2 * kk, idesc,
+                          part > 0 || kk > 0);
+      commit_elect(el, smem_u32(&sm.s_full[t % kBars]));
+      commit_elect(el, smem_u32(&sm.k_empty[st]));
+      if (t == last) commit_elect(el, smem_u32(&sm.q_free));
+    }
+    if (seg >= 0) {  // every MMA of this thread has finished before the tensor memory is released
+      commit_elect(el, smem_u32(&sm.drain[0]));
+      warp_wait(smem_u32(&sm.drain[0]), 0, p.flags);
     }
     __syncwarp();
   } else if (warp == kPvWarp) {
-    // ================= P V warp: O (+)= P_t V_t
-    if (lane == 0) {
-      const uint32_t idesc = idesc_f16_f32(128, kDim, true);
-      int seg = -1;
-      for (int t = 0;; ++t) {
-        if (!wait_bar(smem_u32(&sm.v16_full[(2 * t) % kVBufs]), (2 * t / kVBufs) & 1, p.flags)) break;
-        const Tile x = sm.tile[t % kRing];
-        if (x.end) break;
-        if (!wait_bar(smem_u32(&sm.p_full[t % kBars]), (t / kBars) & 1, p.flags)) break;
-        const uint32_t pcol = tbase + kColS + kBlock * (t % kSBufs);
-        bool good = true;
+    // ================= P V warp: O (+)= P_t V_t, a half of the tokens at a time
+    const uint32_t el = elect_one();
+    const uint32_t idesc = idesc_f16_f32(128, kDim, true);
+    // 128 dims = two 64-dim halves (the leading offset), 8-token groups 1 KB apart, 16 tokens = 2 KB
+    const uint64_t vdesc0 = sdesc_mn_sw128(smem_u32(sm.v16[0][0]), kHalfBytes);
+    int seg = -1;
+    bool good = true;
+    for (int t = 0; good; ++t) {
+      if (!warp_wait(smem_u32(&sm.v16_full[(2 * t) % kVBufs]), (2 * t / kVBufs) & 1, p.flags)) break;
+      const Tile& x = sm.tile[t % kRing];
+      if (x.end) break;
+      const int seg_t = x.seg;
+      if (!warp_wait(smem_u32(&sm.p_full[t % kBars]), (t / kBars) & 1, p.flags)) break;
+      const uint32_t pcol = tbase + kColS + kBlock * (t % kSBufs);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int u = 2 * t + h;
-          if (h == 1 && !wait_bar(smem_u32(&sm.v16_full[u % kVBufs]), (u / kVBufs) & 1, p.flags)) {
-            good = false;
-            break;
-          }
-          tc_fence_after();
-          // 128 dims = two 64-dim halves (the leading offset), 8-token groups 1 KB apart, 16 tokens = 2 KB
-          const uint64_t vdesc = sdesc_mn_sw128(smem_u32(sm.v16[u % kVBufs][0]), kHalfBytes);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_tmemA(tbase + kColO, pcol + 32 * h + 8 * kk, vdesc + 128 * kk, idesc,
-                          x.seg == seg || h > 0 || kk > 0 ? 1u : 0u);
-          mma_commit(smem_u32(&sm.v16_free[u % kBars]));
+      for (int h = 0; h < 2; ++h) {
+        const int u = 2 * t + h;
+        if (h == 1) {
+          good = warp_wait(smem_u32(&sm.v16_full[u % kVBufs]), (u / kVBufs) & 1, p.flags);
+          if (!good) break;
         }
-        if (!good) break;
-        seg = x.seg;
-        mma_commit(smem_u32(&sm.pv_done[t % kBars]));
+        tc_fence_after();
+        const uint64_t vdesc = vdesc0 + static_cast<uint32_t>(u % kVBufs) * (2 * kHalfBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f16_tmemA_elect(el, tbase + kColO, pcol + 32 * h + 8 * kk, vdesc + 128 * kk, idesc,
+                              seg_t == seg || h > 0 || kk > 0 ? 1u : 0u);
+        commit_elect(el, smem_u32(&sm.v16_free[u % kBars]));
       }
-      if (seg >= 0) {
-        mma_commit(smem_u32(&sm.drain[1]));
-        mbar_wait(smem_u32(&sm.drain[1]), 0, p.flags);
-      }
+      if (!good) break;
+      seg = seg_t;
+      commit_elect(el, smem_u32(&sm.pv_done[t % kBars]));
+    }
+    if (seg >= 0) {
+      commit_elect(el, smem_u32(&sm.drain[1]));
+      warp_wait(smem_u32(&sm.drain[1]), 0, p.flags);
     }
     __syncwarp();
   } else if (warp < kSoftWarps) {
@@ -708,13 +757,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto meet = [&](uint64_t* bar, uint32_t& phase) -> bool {
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(bar));
-      return __all_sync(0xFFFFFFFFu, wait_bar(smem_u32(bar), phase++ & 1u, p.flags));
+      return warp_wait(smem_u32(bar), phase++ & 1u, p.flags);
     };
 
     // The segment's output or partial. Both sets take part: set s writes dims 64 s .. 64 s + 63.
     auto finish = [&](int k) -> bool {
       const Seg sg = sm.seg[k % kRing];
-      if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.pv_done[sg.last % kBars]), (sg.last / kBars) & 1, p.flags)))
+      if (!warp_wait(smem_u32(&sm.pv_done[sg.last % kBars]), (sg.last / kBars) & 1, p.flags))
         return false;
       sm.xm[s][l] = mref;
       sm.xl[s][l] = lrun;
@@ -814,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       if (!fresh) {
-        if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.s_full[t % kBars]), (t / kBars) & 1, p.flags))) break;
+        if (!warp_wait(smem_u32(&sm.s_full[t % kBars]), (t / kBars) & 1, p.flags)) break;
         x = sm.tile[t % kRing];
         fresh = true;
         continue;
@@ -862,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // P is taken relative to a reference that moves only when the maximum passes it by more
       // than kRescaleLog2 (P stays within FP16); O / l does not depend on it. The tile before
       // (the other set's) has decided on it first.
-      if (t > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.decided[s ^ 1][quad]), ((t - 1) >> 1) & 1, p.flags))) break;
+      if (t > 0 && !warp_wait(smem_u32(&sm.decided[s ^ 1][quad]), ((t - 1) >> 1) & 1, p.flags)) break;
       const float r_old = t == first ? -INFINITY : sm.ref[l];
       const float bmax = fmaf(mx, coef, lv);
       const bool move = bmax > r_old + kRescaleLog2 || (r_old == -INFINITY && bmax != -INFINITY);
@@ -901,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (__any_sync(0xFFFFFFFFu, rescale)) {
         // O holds the segment's earlier tiles once the P V before is done; this tile's waits for the
         // arrival below
-        if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&sm.pv_done[(t - 1) % kBars]), ((t - 1) / kBars) & 1, p.flags))) break;
+        if (!warp_wait(smem_u32(&sm.pv_done[(t - 1) % kBars]), ((t - 1) / kBars) & 1, p.flags)) break;
         tc_fence_after();
         const float a = rescale ? ex2(r_old - ref) : 1.f;
 #pragma unroll 1
