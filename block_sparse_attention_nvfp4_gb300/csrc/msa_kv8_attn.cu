@@ -38,9 +38,11 @@
 //     different paths: tensor and bulk copies alone measured 20-23 bytes a cycle and SM whatever
 //     is in flight, a tile's 32 KB then 1,400 cycles even from L2; both paths together 50;
 //   * S warp (three score buffers in tensor memory) and P V warp (one O);
-//   * 8 softmax warps in two sets taking alternate tiles. A lane of the O belongs to one thread
-//     of each set; the reference its weights are relative to goes from tile to tile through
-//     shared memory, and a set waits only for the other's decision on it, not for its weights.
+//   * 8 softmax warps in two sets that share every tile: of the tokens that a copy of a row takes,
+//     set 0 has the first half and set 1 the second. The two threads of a row exchange their
+//     maxima through shared memory, so both know its reference without asking again. (Sets that
+//     take alternate tiles make the chain scores -> weights -> P V longer than three score
+//     buffers cover: 2,050 cycles a prompt tile.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -62,14 +64,15 @@ constexpr int kCvWarp0 = 12, kCvWarps = 8;           // two groups of 4
 constexpr int kThreads = (kCvWarp0 + kCvWarps) * 32;
 constexpr int kVBufs = 3;                            // FP16 halves of V
 // A wait on a barrier's parity has to be for its current phase or the one before. Waiters that
-// skip tiles, or fall behind, therefore have barriers that go round 6 tiles (even: each serves one
-// softmax set; no wait is 6 tiles behind), or 12 for a tile's description (up to 9 ahead).
+// fall behind therefore have barriers that go round 6 tiles (no wait is 6 tiles behind), or 12 for a
+// tile's description (up to 9 ahead).
 constexpr int kBars = 6, kTold = 12;
 constexpr int kRing = 16;                            // tiles and segments whose description is kept
 constexpr int kRows = 8;                             // segments whose query scales and NaN marks are kept
 constexpr uint32_t kTileBytes = kBlock * kDim;       // K or V of a tile
 constexpr uint32_t kHalfBytes = 64 * 128;            // FP16 V: 64 tokens x 64 dims
-// TMEM columns: three score buffers (128 FP32; the weights, FP16 pairs, go over the first 64), O.
+// TMEM columns: three score buffers (128 FP32), O. The weights (FP16 pairs) go over the scores: tokens
+// 0 .. 63 of a tile over columns 0 .. 31 of its buffer, tokens 64 .. 127 over columns 64 .. 95.
 constexpr int kSBufs = 3;
 constexpr uint32_t kColS = 0, kColO = kSBufs * kBlock, kTmemCols = 512;
 static_assert(kColO + kDim <= kTmemCols, "TMEM");
@@ -86,7 +89,8 @@ struct Tile {
   int last;      // last tile of that segment
   int end;       // no tile: the CTA's work is over
   int vzero;     // the page's value scale is 0
-  float kscale, vscale;
+  float kscale;
+  float lv, iv;  // log2 of the value scale, and its inverse
 };
 
 struct Seg {
@@ -97,6 +101,15 @@ struct Seg {
   int head;      // KV head
   int pos;       // position of row0
   int slot;      // -1: a whole item, else the CTA's partial 0 or 1
+};
+
+// Counts round N places; `phase` flips every time round (a barrier's parity), without divisions.
+template <int N>
+struct Ring {
+  uint32_t at = 0, phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++at == N) at = 0, phase ^= 1u;
+  }
 };
 
 template <int NP>
@@ -110,13 +123,13 @@ struct Smem {
   float qscale[kRows][128];                          // 2^e of each tile row (BF16 queries)
   int nanpos[kRows][kDim];                           // first position with a NaN value in a dim, of partly seen tokens
   int nanany[kRows];
-  float ref[128];                                    // what the weights of a lane are relative to now
-  float xm[2][128], xl[2][128];
+  float half_max[2][2][128];                         // by tile parity and set
+  float xm[128], xl[2][128];
   Tile tile[kRing];
   Seg seg[kRing];
   uint64_t k_full[kKStages], k_empty[kKStages], told[kTold];
   uint64_t q_full, q_free, s_full[kBars], p_full[kBars], v16_full[kVBufs], v16_free[kBars], pv_done[kBars], drain[2];
-  uint64_t decided[2][4];                            // by set and quadrant: the tile's reference stands
+  uint64_t pair_met[4];                              // by quadrant: both sets' warps have the tile's maxima
   uint64_t sets_met, set_met[2];                     // the softmax warps of both sets, or of one, have come here
   long long part[kThreads / 32];
   long long lo, hi;
@@ -221,6 +234,20 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+// 32 columns of the warp's lanes times a factor per lane.
+__device__ __forceinline__ void tmem_scale32(uint32_t taddr, float a) {
+  uint32_t o[32];
+  tmem_ld32(taddr, o);
+  tc_wait_ld();
+#pragma unroll
+  for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * a);
+  tmem_st32(taddr, o);
+}
 __device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
   const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&x);
@@ -298,14 +325,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kBars; ++s) {
       mbar_init(smem_u32(&sm.s_full[s]), 1);
       mbar_init(smem_u32(&sm.v16_free[s]), 1);
-      mbar_init(smem_u32(&sm.p_full[s]), kSoftWarps / 2);
+      mbar_init(smem_u32(&sm.p_full[s]), kSoftWarps);
       mbar_init(smem_u32(&sm.pv_done[s]), 1);
-    }
-    for (int s = 0; s < 2; ++s) {
-      for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sm.decided[s][w]), 1);
     }
     for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&sm.drain[s]), 1);
     mbar_init(smem_u32(&sm.sets_met), kSoftWarps);
+    for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sm.pair_met[w]), 2);
     for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&sm.set_met[s]), kSoftWarps / 2);
     mbar_fence_init();
     sm.lo = sm.hi = 0;
@@ -388,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.end = end;
         x.vzero = vs == 0.f;
         x.kscale = ks;
-        x.vscale = vs == 0.f ? 1.f : vs;
+        x.lv = vs == 0.f ? 0.f : log2f(vs);
+        x.iv = vs == 0.f ? 1.f : 1.f / vs;
         mbar_arrive(smem_u32(&sm.told[t % kTold]));
         const uint32_t kb = smem_u32(&sm.k_full[st]);
         if (nvalid > 0) {
@@ -503,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    for (int e = 0; e < 2 && good; ++e) emit(kNoPos, 0, INT_MAX, 1, 0, 1.f, 1.f);
+    if (good) emit(kNoPos, 0, INT_MAX, 1, 0, 1.f, 1.f);
     // no copy may still be landing when the CTA leaves
     for (int j = t - kStages < 0 ? 0 : t - kStages; j < t; ++j)
       if (!wait_bar(smem_u32(&sm.k_full[j % kStages]), (j / kStages) & 1, p.flags)) break;
@@ -521,14 +547,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t slot0 = smem_u32(sm.v[0]) + static_cast<uint32_t>(64 * kDim * h + 16 * r);
     // Starts the copies of this thread's pieces of tile t (zeros for rows past the context).
     bool more = true;  // no end mark fetched yet
+    Ring<kTold> rt;
+    Ring<kVStages> rf, rs;  // slots fetched into, slots converted
     auto fetch = [&](int t) -> bool {
       if (more) {
-        if (!warp_wait(smem_u32(&sm.told[t % kTold]), (t / kTold) & 1, p.flags)) return false;
+        if (!warp_wait(smem_u32(&sm.told[rt.at]), rt.phase, p.flags)) return false;
+        rt.step();
         const Tile& x = sm.tile[t % kRing];
         more = !x.end;
         const int rows = (x.vzero ? 0 : x.nvalid) - 64 * h - vr;  // > 16 i: row 16 i + vr of this half counts
         const uint8_t* src = p.v_data + static_cast<long long>(x.page) * kTileBytes + 64 * kDim * h + 16 * r;
-        const uint32_t to = slot0 + static_cast<uint32_t>(t % kVStages) * kTileBytes;
+        const uint32_t to = slot0 + rf.at * kTileBytes;
+        rf.step();
         if (more)
 #pragma unroll
           for (int i = 0; i < 4; ++i) cp_async16(to + 2048u * i, src + 2048 * i, rows > 16 * i ? 16u : 0u);
@@ -538,7 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool ok = true;
     for (int t = 0; t < kVStages - 1 && ok; ++t) ok = fetch(t);
-    for (int t = 0; ok; ++t) {
+    uint32_t uv = h, ub = h, uph = 0;  // half u = 2 t + h: u % 3, u % 6, (u / 6) % 2
+    for (int t = 0; ok; ++t, rs.step()) {
       const Tile& x = sm.tile[t % kRing];
       const bool end = x.end;
       const Seg& sg = sm.seg[x.seg % kRing];
@@ -615,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
       }
       asm volatile("cp.async.wait_group %0;" ::"n"(kVStages - 2) : "memory");  // this thread's pieces of tile t
-      const uint32_t raw = slot0 + static_cast<uint32_t>(t % kVStages) * kTileBytes;
+      const uint32_t raw = slot0 + rs.at * kTileBytes;
       // a token that some rows of the segment do not see: its weight is 0 there, but 0 x NaN is
       // NaN, so its NaN codes become 0 here and are put back for the rows that see it
       if (x.nvalid > 0 && x.pos0 + x.nvalid - 1 > sg.pos) {
@@ -642,13 +673,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         f[i][6] = e4m3x2_f16x2(b1), f[i][7] = e4m3x2_f16x2(b1 >> 16);
       }
       // the half that was in this buffer (three halves ago) has been multiplied
-      const int u = 2 * t + h;
-      if (u >= kVBufs && !warp_wait(smem_u32(&sm.v16_free[(u - kVBufs) % kBars]), ((u - kVBufs) / kBars) & 1, p.flags)) break;
+      if (2 * t + h >= kVBufs && !(ub < 3u ? warp_wait(smem_u32(&sm.v16_free[ub + 3u]), uph ^ 1u, p.flags)
+                                           : warp_wait(smem_u32(&sm.v16_free[ub - 3u]), uph, p.flags)))
+        break;
       if (end) {
-        if (h == 0 && lane == 0) mbar_arrive(smem_u32(&sm.v16_full[u % kVBufs]));
+        if (h == 0 && lane == 0) mbar_arrive(smem_u32(&sm.v16_full[uv]));
         break;
       }
-      const uint32_t dst = smem_u32(sm.v16[u % kVBufs][flip]) + static_cast<uint32_t>(vr) * 128u;
+      const uint32_t dst = smem_u32(sm.v16[uv][flip]) + static_cast<uint32_t>(vr) * 128u;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         st_shared_v4(dst + 2048u * i + o0, f[i][0], f[i][1], f[i][2], f[i][3]);
@@ -656,7 +688,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.v16_full[u % kVBufs]));
+      if (lane == 0) mbar_arrive(smem_u32(&sm.v16_full[uv]));
+      uv = uv == 0u ? 2u : uv - 1u;  // + 2 mod 3
+      ub += 2u;
+      if (ub >= 6u) ub -= 6u, uph ^= 1u;
       if (!fetch(t + kVStages - 1)) break;  // into the slots that tile t - 1 had
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // none may still be landing when the CTA leaves
@@ -665,21 +700,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t el = elect_one();
     const uint64_t qdesc = sdesc_kmajor_sw128(smem_u32(sm.q[0])), kdesc0 = sdesc_kmajor_sw128(smem_u32(sm.k[0]));
     const uint32_t idesc = idesc_e4m3_f32(128, kBlock, false, false);
-    int seg = -1, ends = 0;
+    int seg = -1;
     bool good = true;
-    for (int t = 0; ends < 2; ++t) {  // each softmax set sees one of the two end marks
-      const int st = t % kStages, sb = t % kSBufs;
-      // the buffer's previous weights have been used
-      if (t >= kSBufs) good = warp_wait(smem_u32(&sm.pv_done[(t - kSBufs) % kBars]), ((t - kSBufs) / kBars) & 1, p.flags);
-      if (!good || !warp_wait(smem_u32(&sm.k_full[st]), (t / kStages) & 1, p.flags)) break;
+    Ring<kBars> rb;
+    Ring<kStages> rk;
+    for (int t = 0;; ++t, rb.step(), rk.step()) {
+      const uint32_t sb = rb.at < 3u ? rb.at : rb.at - 3u;
+      // the buffer's previous weights (of tile t - 3) have been used
+      static_assert(kBars == 2 * kSBufs, "");
+      if (t >= kSBufs)
+        good = rb.at < 3u ? warp_wait(smem_u32(&sm.pv_done[rb.at + 3u]), rb.phase ^ 1u, p.flags)
+                          : warp_wait(smem_u32(&sm.pv_done[rb.at - 3u]), rb.phase, p.flags);
+      if (!good || !warp_wait(smem_u32(&sm.k_full[rk.at]), rk.phase, p.flags)) break;
       const Tile& x = sm.tile[t % kRing];
       if (x.end) {
-        ++ends;
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&sm.s_full[t % kBars]));
-          mbar_arrive(smem_u32(&sm.k_empty[st]));
-        }
-        continue;
+        if (lane == 0) mbar_arrive(smem_u32(&sm.s_full[rb.at]));
+        break;
       }
       const int last = x.last;
       if (x.seg != seg) {
@@ -687,15 +723,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(smem_u32(&sm.q_full), seg & 1, p.flags)) break;
       }
       tc_fence_after();
-      const uint64_t kdesc = kdesc0 + static_cast<uint32_t>(st) * (kTileBytes >> 4);
+      const uint64_t kdesc = kdesc0 + rk.at * (kTileBytes >> 4);
 #pragma unroll
       for (int part = 0; part < NP; ++part)
 #pragma unroll
         for (int kk = 0; kk < kDim / 32; ++kk)  // 32 bytes along the rows: + 2 in the address field
           mma_f8_ss_elect(el, tbase + kColS + kBlock * sb, qdesc + part * (kTileBytes >> 4) + 2 * kk, kdesc + 2 * kk, idesc,
                           part > 0 || kk > 0);
-      commit_elect(el, smem_u32(&sm.s_full[t % kBars]));
-      commit_elect(el, smem_u32(&sm.k_empty[st]));
+      commit_elect(el, smem_u32(&sm.s_full[rb.at]));
+      commit_elect(el, smem_u32(&sm.k_empty[rk.at]));
       if (t == last) commit_elect(el, smem_u32(&sm.q_free));
     }
     if (seg >= 0) {  // every MMA of this thread has finished before the tensor memory is released
@@ -711,31 +747,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t vdesc0 = sdesc_mn_sw128(smem_u32(sm.v16[0][0]), kHalfBytes);
     int seg = -1;
     bool good = true;
-    for (int t = 0; good; ++t) {
-      if (!warp_wait(smem_u32(&sm.v16_full[(2 * t) % kVBufs]), (2 * t / kVBufs) & 1, p.flags)) break;
+    Ring<kBars> rb, ru;    // tiles, halves
+    Ring<kVBufs> rv;       // the halves' buffers
+    for (int t = 0; good; ++t, rb.step()) {
+      if (!warp_wait(smem_u32(&sm.v16_full[rv.at]), rv.phase, p.flags)) break;
       const Tile& x = sm.tile[t % kRing];
       if (x.end) break;
       const int seg_t = x.seg;
-      if (!warp_wait(smem_u32(&sm.p_full[t % kBars]), (t / kBars) & 1, p.flags)) break;
-      const uint32_t pcol = tbase + kColS + kBlock * (t % kSBufs);
+      if (!warp_wait(smem_u32(&sm.p_full[rb.at]), rb.phase, p.flags)) break;
+      const uint32_t pcol = tbase + kColS + kBlock * (rb.at < 3u ? rb.at : rb.at - 3u);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int u = 2 * t + h;
+      for (int h = 0; h < 2; ++h, rv.step(), ru.step()) {
         if (h == 1) {
-          good = warp_wait(smem_u32(&sm.v16_full[u % kVBufs]), (u / kVBufs) & 1, p.flags);
+          good = warp_wait(smem_u32(&sm.v16_full[rv.at]), rv.phase, p.flags);
           if (!good) break;
         }
         tc_fence_after();
-        const uint64_t vdesc = vdesc0 + static_cast<uint32_t>(u % kVBufs) * (2 * kHalfBytes >> 4);
+        const uint64_t vdesc = vdesc0 + rv.at * (2 * kHalfBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_f16_tmemA_elect(el, tbase + kColO, pcol + 32 * h + 8 * kk, vdesc + 128 * kk, idesc,
+          mma_f16_tmemA_elect(el, tbase + kColO, pcol + 64 * h + 8 * kk, vdesc + 128 * kk, idesc,
                               seg_t == seg || h > 0 || kk > 0 ? 1u : 0u);
-        commit_elect(el, smem_u32(&sm.v16_free[u % kBars]));
+        commit_elect(el, smem_u32(&sm.v16_free[ru.at]));
       }
       if (!good) break;
       seg = seg_t;
-      commit_elect(el, smem_u32(&sm.pv_done[t % kBars]));
+      commit_elect(el, smem_u32(&sm.pv_done[rb.at]));
     }
     if (seg >= 0) {
       commit_elect(el, smem_u32(&sm.drain[1]));
@@ -744,12 +781,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < kSoftWarps) {
     // ================= softmax warps of set s: TMEM lane l = query row m of copy c, which takes
-    // tokens k0 .. k0 + kMpad - 1 of every tile
+    // tokens 128 c / C .. of every tile; this set's kN of them start at token k0
+    constexpr int kN = kMpad / 2;
     const int s = warp / 4, quad = warp % 4;
-    const int l = 32 * quad + lane, m = l % kMpad, c = l / kMpad, k0 = c * kMpad;
+    const int l = 32 * quad + lane, m = l % kMpad, c = l / kMpad, k0 = c * kMpad + s * kN;
     const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
+    const uint32_t p_off = 64u * (k0 / 64) + (k0 % 64) / 2;  // the weights' first column
     const int row = m / G;
-    float mref = -INFINITY, lrun = 0.f;  // this set's sum, relative to the last reference it used
+    float mref = -INFINITY, lrun = 0.f;  // the row's reference (both sets'), this set's sum
     int seg = 0;
     uint32_t met_all = 0, met_set = 0;               // phases of the meeting points
     // A meeting of warps, bounded like every other wait: after a timeout anywhere each warp leaves
@@ -765,20 +804,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Seg sg = sm.seg[k % kRing];
       if (!warp_wait(smem_u32(&sm.pv_done[sg.last % kBars]), (sg.last / kBars) & 1, p.flags))
         return false;
-      sm.xm[s][l] = mref;
+      if (s == 0) sm.xm[l] = mref;
       sm.xl[s][l] = lrun;
       if (!meet(&sm.sets_met, met_all)) return false;
       tc_fence_after();
-      // references only grow, so a lane's O is relative to the larger of the two sets' last ones
       float mt = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 2 * C; ++i) mt = fmaxf(mt, sm.xm[i & 1][(i >> 1) * kMpad + m]);
+      for (int i = 0; i < C; ++i) mt = fmaxf(mt, sm.xm[i * kMpad + m]);
       const float ref = mt == -INFINITY ? 0.f : mt;
       float lt = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2 * C; ++i)
-        lt += sm.xl[i & 1][(i >> 1) * kMpad + m] * ex2(sm.xm[i & 1][(i >> 1) * kMpad + m] - ref);
-      const float w0 = ex2(fmaxf(sm.xm[0][l], sm.xm[1][l]) - ref);
+      for (int i = 0; i < C; ++i)
+        lt += (sm.xl[0][i * kMpad + m] + sm.xl[1][i * kMpad + m]) * ex2(sm.xm[i * kMpad + m] - ref);
+      const float w0 = ex2(mref - ref);
       const bool real = m < G * sg.rows;
       const bool whole = sg.slot < 0;
       const float inv = !whole ? 1.f : (lt == 0.f ? 0.f : 1.f / lt);
@@ -851,74 +889,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
 
-    // one call of finish: after the set's last tile of a segment, or when its next tile shows that
-    // segments without one have passed
-    int t = s;
-    Tile x = {};
-    bool fresh = false, over = false;
-    for (;;) {
-      if (over || (fresh && seg < x.seg)) {
-        if (!finish(seg++)) break;
-        over = false;
-        continue;
-      }
-      if (!fresh) {
-        if (!warp_wait(smem_u32(&sm.s_full[t % kBars]), (t / kBars) & 1, p.flags)) break;
-        x = sm.tile[t % kRing];
-        fresh = true;
-        continue;
-      }
+    Ring<kBars> rb;
+    for (int t = 0;; ++t, rb.step()) {
+      if (!warp_wait(smem_u32(&sm.s_full[rb.at]), rb.phase, p.flags)) break;
+      const Tile& x = sm.tile[t % kRing];
       if (x.end) break;
       tc_fence_after();
-      const int pos_max = sm.seg[seg % kRing].pos + row, first = sm.seg[seg % kRing].first;
-      const float coef_q = p.sm_scale_log2 * (NP == 1 ? 1.f : sm.qscale[seg % kRows][l]);
+      const int pos_max = sm.seg[seg % kRing].pos + row, last = x.last;
+      const float coef_q = p.sm_scale_log2 * (NP == 1 ? 1.f : sm.qscale[seg % kRows][l]), lv = x.lv, iv = x.iv;
       const bool full_vis = x.pos0 + kBlock - 1 <= pos_max - row;  // every token visible to every row
       const int lim = pos_max - x.pos0 - k0;                        // token k0 + n visible iff n <= lim
       // the floor keeps a masked score at -inf when a scale is 0
       const float coef = fmaxf(coef_q * x.kscale, 1e-30f);
-      const float lv = log2f(x.vscale);
-      const uint32_t s_cols = tbase + lane_base + kColS + kBlock * (t % kSBufs);
+      const uint32_t s_cols = tbase + lane_base + kColS + kBlock * (rb.at < 3u ? rb.at : rb.at - 3u);
       // The loop bodies are short and run several times on purpose: the roles' code together is what
       // an SM's instruction cache has to hold, and fetching it was the bound when they were unrolled.
-      constexpr int kCh = kMpad / 32;
-      uint32_t v[32];
-      if (!full_vis) {  // scores of tokens that the row does not see become -inf in place
-#pragma unroll 1
-        for (int ch = 0; ch < kCh; ++ch) {
-          tmem_ld32(s_cols + k0 + 32 * ch, v);
-          tc_wait_ld();
-#pragma unroll
-          for (int u = 0; u < 32; ++u) v[u] = 32 * ch + u <= lim ? v[u] : __float_as_uint(-INFINITY);
-          tmem_st32(s_cols + k0 + 32 * ch, v);
-        }
-        tc_wait_st();
-      }
-      float mx = -INFINITY;
-      if constexpr (kCh == 1) {
-        tmem_ld32(s_cols + k0, v);
+      constexpr int kStep = kN < 32 ? kN : 32, kCh = kN / kStep;
+      uint32_t v[kStep];
+      auto load = [&](int ch) {
+        if constexpr (kStep == 32) tmem_ld32(s_cols + k0 + 32 * ch, v);
+        else tmem_ld16(s_cols + k0, v);
         tc_wait_ld();
-#pragma unroll
-        for (int u = 0; u < 32; u += 2) mx = fmax3(mx, __uint_as_float(v[u]), __uint_as_float(v[u + 1]));
+      };
+      float mx = -INFINITY;
+      if (kCh > 1 && full_vis) {
+        float m0 = tmem_ld32_max(s_cols + k0), m1 = tmem_ld32_max(s_cols + k0 + 32);  // the TMEM load reduces
+        tc_wait_ld();
+        asm volatile("" : "+f"(m0), "+f"(m1));  // no use moves above the wait
+        mx = fmaxf(m0, m1);
       } else {
 #pragma unroll 1
-        for (int ch = 0; ch < kCh; ch += 2) {  // the TMEM load reduces
-          float m0 = tmem_ld32_max(s_cols + k0 + 32 * ch), m1 = tmem_ld32_max(s_cols + k0 + 32 * ch + 32);
-          tc_wait_ld();
-          asm volatile("" : "+f"(m0), "+f"(m1));  // no use moves above the wait
-          mx = fmax3(mx, m0, m1);
+        for (int ch = 0; ch < kCh; ++ch) {
+          load(ch);
+          if (!full_vis) {  // scores of tokens that the row does not see become -inf
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) v[u] = kStep * ch + u <= lim ? v[u] : __float_as_uint(-INFINITY);
+            if constexpr (kCh > 1) tmem_st32(s_cols + k0 + 32 * ch, v);  // in place: they are read again
+          }
+#pragma unroll
+          for (int u = 0; u < kStep; u += 2) mx = fmax3(mx, __uint_as_float(v[u]), __uint_as_float(v[u + 1]));
         }
+        if (kCh > 1) tc_wait_st();
       }
+      // the row's maximum over both sets; after the meeting nobody needs the scores that the weights of
+      // the other set go over
+      float* hm = &sm.half_max[t & 1][0][0];
+      hm[128 * s + l] = mx;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.pair_met[quad]));
+      if (!warp_wait(smem_u32(&sm.pair_met[quad]), t & 1, p.flags)) break;
+      mx = fmaxf(mx, hm[128 * (s ^ 1) + l]);
       // P is taken relative to a reference that moves only when the maximum passes it by more
-      // than kRescaleLog2 (P stays within FP16); O / l does not depend on it. The tile before
-      // (the other set's) has decided on it first.
-      if (t > 0 && !warp_wait(smem_u32(&sm.decided[s ^ 1][quad]), ((t - 1) >> 1) & 1, p.flags)) break;
-      const float r_old = t == first ? -INFINITY : sm.ref[l];
-      const float bmax = fmaf(mx, coef, lv);
+      // than kRescaleLog2 (P stays within FP16); O / l does not depend on it
+      const float bmax = fmaf(mx, coef, lv), r_old = mref;
       const bool move = bmax > r_old + kRescaleLog2 || (r_old == -INFINITY && bmax != -INFINITY);
       const float m_new = move ? bmax : r_old;
-      if (move || t == first) sm.ref[l] = m_new;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.decided[s][quad]));
       const float ref = m_new == -INFINITY ? 0.f : m_new;
       const bool rescale = move && r_old != -INFINITY;
       const float off = lv - ref;
@@ -926,26 +951,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       float lsum = 0.f;
 #pragma unroll 1
       for (int ch = 0; ch < kCh; ++ch) {
-        if (kCh > 1) {
-          tmem_ld32(s_cols + k0 + 32 * ch, v);
-          tc_wait_ld();
-        }
+        if (kCh > 1) load(ch);
         float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {  // 32 scores -> 16 columns of FP16 pairs
+        for (int u = 0; u < kStep / 2; ++u) {  // scores -> columns of FP16 pairs
           const float2 d = __ffma2_rn(make_float2(__uint_as_float(v[2 * u]), __uint_as_float(v[2 * u + 1])), coef2, off2);
           const float2 e = make_float2(ex2(d.x), ex2(d.y));
           acc = __fadd2_rn(acc, e);
           asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v[u]) : "f"(e.y), "f"(e.x));
         }
         lsum += acc.x + acc.y;
-        tmem_st16(s_cols + (k0 + 32 * ch) / 2, v);
+        if constexpr (kStep == 32) tmem_st16(s_cols + p_off + 16 * ch, v);
+        else tmem_st8(s_cols + p_off, v);
       }
-      // the weights' columns of the other copies' tokens (scores were there)
-      if constexpr (C > 1) {
+      // the weights of the tokens of other copies are 0: 16-column blocks (32 tokens each, block z at
+      // column 64 (z / 2) + 16 (z % 2)), shared out between the sets
+      if constexpr (C == 2) tmem_zero16(s_cols + 64 * (c ^ 1) + 16 * s);
+      if constexpr (C == 4) {
 #pragma unroll
-        for (int z = 0; z < 4; ++z)
-          if (z < c * kCh || z >= (c + 1) * kCh) tmem_zero16(s_cols + 16 * z);
+        for (int i = 1 + s; i < 2 + 2 * s; ++i) tmem_zero16(s_cols + 64 * (((c + i) & 3) >> 1) + 16 * ((c + i) & 1));
       }
       if (__any_sync(0xFFFFFFFFu, rescale)) {
         // O holds the segment's earlier tiles once the P V before is done; this tile's waits for the
@@ -954,24 +978,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float a = rescale ? ex2(r_old - ref) : 1.f;
 #pragma unroll 1
-        for (int qc = 0; qc < 4; ++qc) {
-          uint32_t o[32];
-          tmem_ld32(tbase + lane_base + kColO + 32 * qc, o);
-          tc_wait_ld();
-#pragma unroll
-          for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * a);
-          tmem_st32(tbase + lane_base + kColO + 32 * qc, o);
+        for (int qc = 2 * s; qc < 2 * s + 2; ++qc) {  // this set's half of the dims
+          tmem_scale32(tbase + lane_base + kColO + 32 * qc, a);
         }
       }
-      lrun = lrun * ex2(mref - ref) + lsum * (1.f / x.vscale);  // mref -inf: nothing summed yet
+      lrun = lrun * ex2(r_old - ref) + lsum * iv;  // r_old -inf: nothing summed yet
       mref = m_new;
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[t % kBars]));
-      over = t + 2 > x.last;
-      fresh = false;
-      t += 2;
+      if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[rb.at]));
+      if (t == last && !finish(seg++)) break;
     }
   }
   tc_fence_before();
