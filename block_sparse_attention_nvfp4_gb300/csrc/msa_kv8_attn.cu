@@ -78,7 +78,7 @@ constexpr uint32_t kColS = 0, kColO = kSBufs * kBlock, kTmemCols = 512;
 static_assert(kColO + kDim <= kTmemCols, "TMEM");
 constexpr float kRescaleLog2 = 8.f;                  // O is rescaled when the maximum grows by more than 2^8
 constexpr int kNoPos = 1 << 30;                      // position of a tile that nobody sees
-constexpr int kRedStride = 17;
+constexpr int kRedStride = 17;                       // floats of a lane's 16 dims in the copies' exchange
 constexpr int kMergeThreads = 256;
 
 struct Tile {
@@ -119,12 +119,12 @@ struct Smem {
   uint8_t k[kKStages][kTileBytes];                   // B of S (K-major), 128-byte swizzle
   uint8_t v[kVStages][kTileBytes];                   // V codes as they are in the page, a slot of each thread
   uint8_t v16[kVBufs][2][kHalfBytes];                // B of O (MN-major): [dim half][token][64 dims]
-  float red[2][128 * kRedStride];                    // copies of a row joined, 16 dims at a time
+  float red[2][128 * kRedStride];                    // by set: what the lanes hand to another copy
   float qscale[kRows][128];                          // 2^e of each tile row (BF16 queries)
   int nanpos[kRows][kDim];                           // first position with a NaN value in a dim, of partly seen tokens
   int nanany[kRows];
   float half_max[2][2][128];                         // by tile parity and set
-  float xm[128], xl[2][128];
+  float xm[128], xl[2][128], xm2[2][128];
   Tile tile[kRing];
   Seg seg[kRing];
   uint64_t k_full[kKStages], k_empty[kKStages], told[kTold];
@@ -298,7 +298,7 @@ __device__ __forceinline__ long long tiles_before(const Kv8AttnParams& p, const 
 __device__ __forceinline__ long long head_tiles(const Kv8AttnParams& p, const Req& q) {
   if (q.R == 0) return 0;
   const int n = chunks_of(p, q.R);
-  return tiles_before(p, q, n - 1) + tiles_of(p, q, n - 1);
+  return (n > 1 ? tiles_before(p, q, n - 1) : 0) + tiles_of(p, q, n - 1);
 }
 
 // C copies of the query rows down the MMA tile (128 / C rows each); NP = E4M3 parts of a query.
@@ -313,27 +313,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = p.q_per_kv;
 
   pdl_launch_dependents();  // the merge waits for this grid's end; its CTAs may be set up before
-  if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_u32(&sm.k_full[s]), 1);
-      mbar_init(smem_u32(&sm.k_empty[s]), 1);
-    }
-    for (int s = 0; s < kVBufs; ++s) mbar_init(smem_u32(&sm.v16_full[s]), kCvWarps / 2);
-    for (int s = 0; s < kTold; ++s) mbar_init(smem_u32(&sm.told[s]), 1);
-    mbar_init(smem_u32(&sm.q_full), kCvWarps);
-    mbar_init(smem_u32(&sm.q_free), 1);
-    for (int s = 0; s < kBars; ++s) {
-      mbar_init(smem_u32(&sm.s_full[s]), 1);
-      mbar_init(smem_u32(&sm.v16_free[s]), 1);
-      mbar_init(smem_u32(&sm.p_full[s]), kSoftWarps);
-      mbar_init(smem_u32(&sm.pv_done[s]), 1);
-    }
-    for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&sm.drain[s]), 1);
-    mbar_init(smem_u32(&sm.sets_met), kSoftWarps);
-    for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sm.pair_met[w]), 2);
-    for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&sm.set_met[s]), kSoftWarps / 2);
-    mbar_fence_init();
-    sm.lo = sm.hi = 0;
+  {  // a thread per barrier
+    auto init = [&](uint64_t* bar, int n, int first, uint32_t count) {
+      if (tid >= first && tid < first + n) mbar_init(smem_u32(bar + (tid - first)), count);
+    };
+    init(sm.k_full, kStages, 0, 1);
+    init(sm.k_empty, kStages, 8, 1);
+    init(sm.told, kTold, 16, 1);
+    init(sm.s_full, kBars, 32, 1);
+    init(sm.p_full, kBars, 40, kSoftWarps);
+    init(sm.v16_full, kVBufs, 48, kCvWarps / 2);
+    init(sm.v16_free, kBars, 56, 1);
+    init(sm.pv_done, kBars, 64, 1);
+    init(sm.drain, 2, 72, 1);
+    init(&sm.q_full, 1, 74, kCvWarps);
+    init(&sm.q_free, 1, 75, 1);
+    init(&sm.sets_met, 1, 76, kSoftWarps);
+    init(sm.set_met, 2, 78, kSoftWarps / 2);
+    init(sm.pair_met, 4, 80, 2);
+    if (tid < 96) mbar_fence_init();
+    if (tid == 0) sm.lo = sm.hi = 0;
   }
   for (int i = tid; i < kRows * kDim; i += kThreads) (&sm.nanpos[0][0])[i] = INT_MAX;
   if (tid < kRows) sm.nanany[tid] = 0;
@@ -366,9 +365,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       total += sm.part[w];
     }
     // fewer tiles than CTAs: the last CTAs have none (a partial's continuation is in the next CTA)
-    const long long use = total < gridDim.x ? total : gridDim.x;
-    const long long lo = blockIdx.x < use ? total * blockIdx.x / use : 0;
-    const long long hi = blockIdx.x < use ? total * (blockIdx.x + 1) / use : 0;
+    long long lo = 0, hi = 0;
+    if (total < (1LL << 31)) {  // 32-bit division: this is on the way of the first copy
+      const uint32_t tot = static_cast<uint32_t>(total), use = tot < gridDim.x ? tot : gridDim.x;
+      if (blockIdx.x < use) {
+        const uint32_t per = tot / use, more = tot - per * use;  // the first `more` CTAs take one more
+        lo = per * blockIdx.x + (blockIdx.x < more ? blockIdx.x : more);
+        hi = lo + per + (blockIdx.x < more ? 1 : 0);
+      }
+    } else {
+      lo = total * blockIdx.x / gridDim.x;
+      hi = total * (blockIdx.x + 1) / gridDim.x;
+    }
     long long at = before + incl - mine;
     if (lo < hi && at <= lo && lo < at + mine) {  // the range starts among this thread's requests
       for (int b = b0; b < b1; ++b) {
@@ -435,9 +443,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_req(p, b, &q);
       int h, ch, j0, n_ch = chunks_of(p, q.R);
       {
-        const long long ht = head_tiles(p, q);
-        h = static_cast<int>(sm.start_off / ht);
-        const long long off = sm.start_off % ht;
+        const long long ht = head_tiles(p, q), start = sm.start_off;
+        h = start < (1LL << 31) && ht < (1LL << 31)
+                ? static_cast<int>(static_cast<uint32_t>(start) / static_cast<uint32_t>(ht))
+                : static_cast<int>(start / ht);
+        const long long off = start - h * ht;
         int a = 0, e = n_ch;  // tiles_before(a) <= off < tiles_before(e)
         while (e - a > 1) {
           const int mid = (a + e) / 2;
@@ -445,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           else e = mid;
         }
         ch = a;
-        j0 = static_cast<int>(off - tiles_before(p, q, a));
+        j0 = static_cast<int>(off - (a > 0 ? tiles_before(p, q, a) : 0));
       }
       while (left > 0 && good) {
         const int nt = tiles_of(p, q, ch);
@@ -808,73 +818,97 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm.xl[s][l] = lrun;
       if (!meet(&sm.sets_met, met_all)) return false;
       tc_fence_after();
-      float mt = -INFINITY;
+      // reference and sum of row mm over its copies
+      auto stats = [&](int mm, float& ref, float& sum) {
+        ref = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < C; ++i) mt = fmaxf(mt, sm.xm[i * kMpad + m]);
-      const float ref = mt == -INFINITY ? 0.f : mt;
-      float lt = 0.f;
+        for (int i = 0; i < C; ++i) ref = fmaxf(ref, sm.xm[i * kMpad + mm]);
+        const float r0 = ref == -INFINITY ? 0.f : ref;
+        sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < C; ++i)
-        lt += (sm.xl[0][i * kMpad + m] + sm.xl[1][i * kMpad + m]) * ex2(sm.xm[i * kMpad + m] - ref);
-      const float w0 = ex2(mref - ref);
-      const bool real = m < G * sg.rows;
+        for (int i = 0; i < C; ++i)
+          sum += (sm.xl[0][i * kMpad + mm] + sm.xl[1][i * kMpad + mm]) * ex2(sm.xm[i * kMpad + mm] - r0);
+      };
       const bool whole = sg.slot < 0;
-      const float inv = !whole ? 1.f : (lt == 0.f ? 0.f : 1.f / lt);
       const bool nans = sm.nanany[k % kRows] != 0;
-      const long long orow = static_cast<long long>(sg.row0 + row) * (p.num_kv_heads * G) + sg.head * G + m % G;
+      const int M = G * sg.rows;
       float* part = reinterpret_cast<float*>(p.parts + headers_bytes(gridDim.x)) +
                     (2LL * blockIdx.x + (whole ? 0 : sg.slot)) * kPartFloats;
-      constexpr int kW = 16 / C;  // dims of its row that a thread writes of every 16
-#pragma unroll 1
-      for (int step = 0; step < 4; ++step) {
-        const int d0 = 64 * s + 16 * step;
-        uint32_t a[16];
-        tmem_ld16(tbase + lane_base + kColO + d0, a);
-        tc_wait_ld();
-        float o[16];
+      // Four dims from d on of row mm, not yet divided by the sum.
+      auto put = [&](int mm, int d, float4 y, float sum) {
+        const float inv = !whole ? 1.f : (sum == 0.f ? 0.f : 1.f / sum);
+        float* f = reinterpret_cast<float*>(&y);
 #pragma unroll
-        for (int u = 0; u < 16; ++u) o[u] = w0 * __uint_as_float(a[u]);
-        float y[kW];
-        if constexpr (C == 1) {
-#pragma unroll
-          for (int u = 0; u < 16; ++u) y[u] = o[u];
+        for (int u = 0; u < 4; ++u) {
+          f[u] *= inv;
+          if (nans && sm.nanpos[k % kRows][d + u] <= sg.pos + mm / G) f[u] = __int_as_float(0x7FFFFFFF);
+        }
+        if (whole) {
+          const long long orow = static_cast<long long>(sg.row0 + mm / G) * (p.num_kv_heads * G) + sg.head * G + mm % G;
+          *reinterpret_cast<uint2*>(p.out + orow * kDim + d) = make_uint2(bf16x2_bits(y.x, y.y), bf16x2_bits(y.z, y.w));
         } else {
-          float* red = sm.red[s];
-          // (sums read from it have been stored, so their loads are over)
-          if (step > 0 && !meet(&sm.set_met[s], met_set)) return false;
+          *reinterpret_cast<float4*>(part + mm * kDim + d) = y;
+        }
+      };
+      float my_ref, my_sum;
+      stats(m, my_ref, my_sum);
+      const float w0 = ex2(mref - (my_ref == -INFINITY ? 0.f : my_ref));
+      if constexpr (C == 1) {  // a thread has its row's 64 dims of this set
+#pragma unroll 1
+        for (int d = 64 * s; d < 64 * s + 64; d += 16) {
+          uint32_t a[16];
+          tmem_ld16(tbase + lane_base + kColO + d, a);
+          tc_wait_ld();
+          if (m < M)
 #pragma unroll
-          for (int u = 0; u < 16; ++u) red[l * kRedStride + u] = o[u];
+            for (int u = 0; u < 16; u += 4)
+              put(m, d + u, make_float4(w0 * __uint_as_float(a[u]), w0 * __uint_as_float(a[u + 1]),
+                                        w0 * __uint_as_float(a[u + 2]), w0 * __uint_as_float(a[u + 3])), my_sum);
+        }
+      } else {
+        // Copy c finishes dims kD c .. of this set's 64: in round r every lane hands 16 dims to copy
+        // c + r and takes 16 from copy c - r, in a fixed order.
+        constexpr int kD = 64 / C;
+        float* red = sm.red[s];
+        float y[kD];
+#pragma unroll
+        for (int ch = 0; ch < kD / 16; ++ch) {
+          uint32_t a[16];
+          tmem_ld16(tbase + lane_base + kColO + 64 * s + kD * c + 16 * ch, a);
+          tc_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 16; ++u) y[16 * ch + u] = w0 * __uint_as_float(a[u]);
+        }
+#pragma unroll
+        for (int step = 0; step < (C - 1) * (kD / 16); ++step) {
+          const int r = 1 + step / (kD / 16), ch = step % (kD / 16), to = (c + r) % C, from = (c + C - r) % C;
+          uint32_t a[16];
+          tmem_ld16(tbase + lane_base + kColO + 64 * s + kD * to + 16 * ch, a);
+          tc_wait_ld();
+          if (step > 0 && !meet(&sm.set_met[s], met_set)) return false;  // the last round's values are in y
+#pragma unroll
+          for (int u = 0; u < 16; ++u) red[l * kRedStride + u] = w0 * __uint_as_float(a[u]);
           if (!meet(&sm.set_met[s], met_set)) return false;
+          float z = 0.f;
 #pragma unroll
-          for (int u = 0; u < kW; ++u) {
-            y[u] = 0.f;
-#pragma unroll
-            for (int i = 0; i < C; ++i) y[u] += red[(i * kMpad + m) * kRedStride + c * kW + u];
+          for (int u = 0; u < 16; ++u) {
+            y[16 * ch + u] += red[(from * kMpad + m) * kRedStride + u];
+            z = fmaxf(z, y[16 * ch + u]);
           }
+          sm.xm2[s][l] = z;  // (a store of what was read: the loads are over when the next meeting is reached)
         }
-        const int d = d0 + c * kW;
+        if (m < M)
 #pragma unroll
-        for (int u = 0; u < kW; ++u) {
-          y[u] *= inv;
-          if (nans && sm.nanpos[k % kRows][d + u] <= sg.pos + row) y[u] = __int_as_float(0x7FFFFFFF);
-        }
-        if (real && whole) {
-          uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * kDim + d);
-#pragma unroll
-          for (int u = 0; u < kW; u += 4)
-            *reinterpret_cast<uint2*>(dst + u / 2) = make_uint2(bf16x2_bits(y[u], y[u + 1]), bf16x2_bits(y[u + 2], y[u + 3]));
-        } else if (real) {
-#pragma unroll
-          for (int u = 0; u < kW; u += 4)
-            *reinterpret_cast<float4*>(part + m * kDim + d + u) = make_float4(y[u], y[u + 1], y[u + 2], y[u + 3]);
-        }
+          for (int u = 0; u < kD; u += 4)
+            put(m, 64 * s + kD * c + u, make_float4(y[u], y[u + 1], y[u + 2], y[u + 3]), my_sum);
       }
-      if (real && s == 0 && c == 0) {
+      if (m < M && s == 0 && c == 0) {
         if (!whole) {
-          part[128 * kDim + m] = mt;
-          part[128 * kDim + 128 + m] = lt;
+          part[128 * kDim + m] = my_ref;
+          part[128 * kDim + 128 + m] = my_sum;
         } else if (p.lse != nullptr) {
-          p.lse[orow] = lt == 0.f ? -INFINITY : (ref + log2f(lt)) * 0.69314718055994531f;
+          p.lse[static_cast<long long>(sg.row0 + row) * (p.num_kv_heads * G) + sg.head * G + m % G] =
+              my_sum == 0.f ? -INFINITY : ((my_ref == -INFINITY ? 0.f : my_ref) + log2f(my_sum)) * 0.69314718055994531f;
         }
       }
       // O, the exchange and the NaN marks are free again
@@ -999,54 +1033,80 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the partials of an item that starts in CTA blockIdx.x's range and ends in a later one's.
-// A warp takes one query row: the partials' maxima and sums by lanes, then 4 dims per lane.
+// Joins the partials of an item that starts in CTA blockIdx.x's range and ends in a later one's
+// (log-sum-exp, partials in tile order). A warp takes a query row, 4 dims per lane; with more than
+// 8 partials four warps share a row, every fourth partial each, and the first adds their sums.
 __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnParams p, int grid) {
+  constexpr int kWarps = kMergeThreads / 32;
+  __shared__ float4 part_o[kWarps][32];
+  __shared__ float part_l[kWarps];
   pdl_wait_primary();
   const Header* hd = reinterpret_cast<const Header*>(p.parts);
-  const int cta = blockIdx.x, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Header me = hd[cta];
+  // partials: this CTA's, then those of the next ones up to the item's last
+  auto middle = [&](int i) { return i < grid && hd[i].cont && !hd[i].cont_end; };
+  unsigned ends = __ballot_sync(0xFFFFFFFFu, !middle(cta + 1 + lane));
   if (!me.tail) return;
-  const int m = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
-  if (m >= me.rows * p.q_per_kv) return;
-  int end = cta + 1;  // the last CTA with a part of the item
-  while (end < grid && hd[end].cont && !hd[end].cont_end) ++end;
-  const int n = end - cta + 1;
+  int n = 1 + (ends ? __ffs(ends) : 32);
+  for (int base = cta + 33; ends == 0u && base < grid; base += 32) {
+    ends = __ballot_sync(0xFFFFFFFFu, !middle(base + lane));
+    n += ends ? __ffs(ends) : 32;
+  }
+  if (cta + n > grid) n = grid - cta;
   const float* parts = reinterpret_cast<const float*>(p.parts + headers_bytes(grid));
   auto part = [&](int i) { return parts + (i == 0 ? 2LL * cta + 1 : 2LL * (cta + i)) * kPartFloats; };
-  float mt = -INFINITY;
-  for (int i = lane; i < n; i += 32) mt = fmaxf(mt, part(i)[128 * kDim + m]);
+  const int rows = me.rows * p.q_per_kv;
+  const int share = n > 8 ? 4 : 1, per = kWarps / share;  // warps of a row, rows at a time
+  for (int m0 = per * blockIdx.y; m0 < rows; m0 += per * gridDim.y) {
+    const int m = m0 + warp / share, first = warp % share;
+    float lt = 0.f, ref = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m < rows) {
+      float mt = -INFINITY;
+      for (int i = lane; i < n; i += 32) mt = fmaxf(mt, part(i)[128 * kDim + m]);
 #pragma unroll
-  for (int d = 16; d; d /= 2) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, d));
-  const float ref = mt == -INFINITY ? 0.f : mt;
-  float lt = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float w = 0.f, l = 0.f;
-    if (i0 + lane < n) {
-      w = ex2(part(i0 + lane)[128 * kDim + m] - ref);
-      l = part(i0 + lane)[128 * kDim + 128 + m] * w;
-    }
-    const int k = n - i0 < 32 ? n - i0 : 32;
-#pragma unroll 4
-    for (int i = 0; i < k; ++i) {
-      const float wi = __shfl_sync(0xFFFFFFFFu, w, i);
-      lt += __shfl_sync(0xFFFFFFFFu, l, i);
-      const float4 x = *reinterpret_cast<const float4*>(part(i0 + i) + m * kDim + 4 * lane);
-      if (wi != 0.f) {
-        o.x += wi * x.x;
-        o.y += wi * x.y;
-        o.z += wi * x.z;
-        o.w += wi * x.w;
+      for (int d = 16; d; d /= 2) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, d));
+      ref = mt == -INFINITY ? 0.f : mt;
+#pragma unroll 8
+      for (int i = first; i < n; i += share) {
+        const float* q = part(i);
+        const float w = ex2(q[128 * kDim + m] - ref);
+        const float4 x = *reinterpret_cast<const float4*>(q + m * kDim + 4 * lane);
+        lt += w * q[128 * kDim + 128 + m];
+        if (w != 0.f) {
+          o.x += w * x.x;
+          o.y += w * x.y;
+          o.z += w * x.z;
+          o.w += w * x.w;
+        }
       }
     }
+    if (share > 1) {
+      part_o[warp][lane] = o;
+      if (lane == 0) part_l[warp] = lt;
+      __syncthreads();
+      if (first == 0)
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+          const float4 x = part_o[warp + i][lane];
+          o.x += x.x;
+          o.y += x.y;
+          o.z += x.z;
+          o.w += x.w;
+          lt += part_l[warp + i];
+        }
+    }
+    if (first == 0 && m < rows) {
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      const long long orow = static_cast<long long>(me.row0 + m / p.q_per_kv) * (p.num_kv_heads * p.q_per_kv) +
+                             me.head * p.q_per_kv + m % p.q_per_kv;
+      *reinterpret_cast<uint2*>(p.out + orow * kDim + 4 * lane) =
+          make_uint2(bf16x2_bits(o.x * inv, o.y * inv), bf16x2_bits(o.z * inv, o.w * inv));
+      if (lane == 0 && p.lse != nullptr) p.lse[orow] = lt == 0.f ? -INFINITY : (ref + log2f(lt)) * 0.69314718055994531f;
+    }
+    if (share > 1) __syncthreads();
   }
-  const float inv = lt == 0.f ? 0.f : 1.f / lt;
-  const long long orow = static_cast<long long>(me.row0 + m / p.q_per_kv) * (p.num_kv_heads * p.q_per_kv) +
-                         me.head * p.q_per_kv + m % p.q_per_kv;
-  *reinterpret_cast<uint2*>(p.out + orow * kDim + 4 * lane) =
-      make_uint2(bf16x2_bits(o.x * inv, o.y * inv), bf16x2_bits(o.z * inv, o.w * inv));
-  if (lane == 0 && p.lse != nullptr) p.lse[orow] = lt == 0.f ? -INFINITY : (ref + log2f(lt)) * 0.69314718055994531f;
 }
 
 template <int C, int NP>
@@ -1057,7 +1117,7 @@ cudaError_t launch(const CUtensorMap& kmap, const Kv8AttnParams& prm, int grid, 
   kv8_attn_kernel<C, NP><<<grid, kThreads, smem, st>>>(kmap, prm);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, (128 / C) / (kMergeThreads / 32));
+  cfg.gridDim = dim3(grid, 16 / C);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr;
