@@ -20,7 +20,8 @@
 // Work. An item is a (request, KV head, chunk of query rows); its tiles are the pages its
 // last row sees, or its block ids. All items' tiles form one line that the CTAs (one per SM)
 // take in equal contiguous ranges, so ragged lengths balance and one long request uses the whole
-// GPU. A CTA's part of an item is a segment; segments that are not whole items leave (O, m, l)
+// GPU; an item has kItemCost places on the line before its tiles, because starting and finishing
+// a part costs a CTA as much as that many tiles. A CTA's part of an item is a segment; segments that are not whole items leave (O, m, l)
 // in the workspace and kv8_merge_kernel joins them (log-sum-exp), in tile order: no atomics,
 // the same bits every time.
 //
@@ -264,6 +265,7 @@ __device__ __forceinline__ uint32_t f32x2_e4m3x2(float a, float b) {  // a in th
 }
 
 // ---- the line of tiles
+constexpr int kItemCost = 4;
 struct Req {
   int N, R, r0;
 };
@@ -294,11 +296,14 @@ __device__ __forceinline__ long long tiles_before(const Kv8AttnParams& p, const 
   };
   return static_cast<long long>(i) * (1 + a) + floors(c0 + i + 1LL) - floors(c0 + 1LL);
 }
-// Tiles of one KV head of the request.
-__device__ __forceinline__ long long head_tiles(const Kv8AttnParams& p, const Req& q) {
+// Places on the line before row chunk i (at most the last one), and of one KV head of the request.
+__device__ __forceinline__ long long cost_before(const Kv8AttnParams& p, const Req& q, int i) {
+  return i > 0 ? tiles_before(p, q, i) + static_cast<long long>(i) * kItemCost : 0;
+}
+__device__ __forceinline__ long long head_cost(const Kv8AttnParams& p, const Req& q) {
   if (q.R == 0) return 0;
   const int n = chunks_of(p, q.R);
-  return (n > 1 ? tiles_before(p, q, n - 1) : 0) + tiles_of(p, q, n - 1);
+  return cost_before(p, q, n - 1) + kItemCost + tiles_of(p, q, n - 1);
 }
 
 // C copies of the query rows down the MMA tile (128 / C rows each); NP = E4M3 parts of a query.
@@ -348,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long mine = 0;
     for (int b = b0; b < b1; ++b) {
       Req q;
-      if (load_req(p, b, &q)) mine += p.num_kv_heads * head_tiles(p, q);
+      if (load_req(p, b, &q)) mine += p.num_kv_heads * head_cost(p, q);
       else if (blockIdx.x == 0) set_flag(p.flags, kFlagBadLength);
     }
     long long incl = mine;
@@ -381,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lo < hi && at <= lo && lo < at + mine) {  // the range starts among this thread's requests
       for (int b = b0; b < b1; ++b) {
         Req q;
-        const long long n = load_req(p, b, &q) ? p.num_kv_heads * head_tiles(p, q) : 0;
+        const long long n = load_req(p, b, &q) ? p.num_kv_heads * head_cost(p, q) : 0;
         if (lo < at + n) {
           sm.start_b = b;
           sm.start_off = lo - at;
@@ -441,25 +446,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       int b = sm.start_b;
       Req q;
       load_req(p, b, &q);
-      int h, ch, j0, n_ch = chunks_of(p, q.R);
+      int h, ch, at, n_ch = chunks_of(p, q.R);  // at: the CTA's place in the item
       {
-        const long long ht = head_tiles(p, q), start = sm.start_off;
-        h = start < (1LL << 31) && ht < (1LL << 31)
-                ? static_cast<int>(static_cast<uint32_t>(start) / static_cast<uint32_t>(ht))
-                : static_cast<int>(start / ht);
-        const long long off = start - h * ht;
-        int a = 0, e = n_ch;  // tiles_before(a) <= off < tiles_before(e)
+        const long long hc = head_cost(p, q), start = sm.start_off;
+        h = start < (1LL << 31) && hc < (1LL << 31)
+                ? static_cast<int>(static_cast<uint32_t>(start) / static_cast<uint32_t>(hc))
+                : static_cast<int>(start / hc);
+        const long long off = start - h * hc;
+        int a = 0, e = n_ch;  // cost_before(a) <= off < cost_before(e)
         while (e - a > 1) {
           const int mid = (a + e) / 2;
-          if (tiles_before(p, q, mid) <= off) a = mid;
+          if (cost_before(p, q, mid) <= off) a = mid;
           else e = mid;
         }
         ch = a;
-        j0 = static_cast<int>(off - (a > 0 ? tiles_before(p, q, a) : 0));
+        at = static_cast<int>(off - cost_before(p, q, a));
       }
       while (left > 0 && good) {
         const int nt = tiles_of(p, q, ch);
-        const int j1 = j0 + left < nt ? static_cast<int>(j0 + left) : nt;
+        const int j0 = at > kItemCost ? at - kItemCost : 0;
+        const long long to = at + left - kItemCost;
+        const int j1 = to < nt ? static_cast<int>(to) : nt;
+        if (j1 <= j0) break;  // the range ends before the item's first tile
         const int nb = (q.N + kBlock - 1) / kBlock;
         const bool begin = j0 == 0, end = j1 == nt;
         const int row0 = ch << p.chunk_log2, rows = q.R - row0 < p.chunk ? q.R - row0 : p.chunk;
@@ -525,9 +533,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (p.n_ids && use == 0u && good) emit(kNoPos, 0, last, 0, 0, 1.f, 1.f);
         ++nseg;
-        left -= j1 - j0;
+        left -= kItemCost + nt - at;
         // the next item
-        j0 = 0;
+        at = 0;
         if (left > 0 && ++ch == n_ch) {
           ch = 0;
           if (++h == p.num_kv_heads) {
