@@ -17,7 +17,7 @@
 //   * append_rows_kernel (at most 8 rows per request): CTA = (request, page), each warp whole
 //     (head, K or V) pairs; the pairs whose scale moved are rescaled by the whole CTA after.
 //   * append_tile_kernel: CTA = one (request, page, head, K or V), up to 128 x 128 values in
-//     registers (64 per thread).
+//     registers; the next unit is located while this one's rows are on their way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -143,7 +143,9 @@ __device__ __forceinline__ int touched(const Kv8AppendParams& p, int b) {
   return R == 0 ? 0 : (N - 1) / kBlock - (N - R) / kBlock + 1;
 }
 
+template <int kThreads>
 __device__ __forceinline__ int scan_units(const Kv8AppendParams& p, Units& un) {
+  constexpr int kWarps = kThreads / 32;
   __shared__ int part[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int per = (p.num_reqs + kThreads - 1) / kThreads;
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const Kv8AppendPa
   __shared__ float grown_ratio[2 * 64];
   __shared__ int n_grown;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int total = scan_units(p, un);
+  const int total = scan_units<kThreads>(p, un);
   for (int u = blockIdx.x; u < total; u += gridDim.x) {
     const Unit x = locate(p, un, u, tid == 0);
     if (x.phys < 0) continue;
@@ -290,46 +292,60 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const Kv8AppendPa
   }
 }
 
+// The largest finite magnitude among 16 loaded bytes of T, by its FP32 bits.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) append_tile_kernel(const Kv8AppendParams p) {
+__device__ __forceinline__ uint32_t amax_bits(const uint4& v) {
+  float f[16 / sizeof(T)];
+  widen<T>(v, f);
+  uint32_t m = 0u;
+#pragma unroll
+  for (int j = 0; j < static_cast<int>(16 / sizeof(T)); ++j) m = max(m, finite_abs_bits(f[j]));
+  return m;
+}
+
+// kThreads x 8 loads of 16 bytes cover a tile of 2-byte (256) or 4-byte (512) values: 64 registers a
+// thread keep four (two) CTAs on an SM, 128 KB of loads in flight.
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) append_tile_kernel(const Kv8AppendParams p) {
+  constexpr int kWarps = kThreads / 32;
   constexpr int kV = 16 / sizeof(T);
   constexpr int kLanes = kDim / kV;
   constexpr int kPer = kThreads / kLanes;  // rows the CTA loads at once
   constexpr int kIter = kBlock / kPer;
+  static_assert(kIter == 8, "registers");
   __shared__ Units un;
   __shared__ uint32_t wmax[2][kWarps];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int total = scan_units(p, un);
+  const int total = scan_units<kThreads>(p, un);
   const int pairs = 2 * p.num_kv_heads;
   const long long work = static_cast<long long>(total) * pairs;
+  const int r_lane = tid / kLanes, c_lane = tid % kLanes;
   int buf = 0;
-  for (long long t = blockIdx.x; t < work; t += gridDim.x) {
-    const int u = static_cast<int>(t / pairs), s = static_cast<int>(t % pairs);
-    const int h = s >> 1, kv = s & 1;
+  long long t = blockIdx.x;
+  Unit x = {};
+  if (t < work) x = locate(p, un, static_cast<int>(t / pairs), tid == 0);
+  while (t < work) {
+    const int s = static_cast<int>(t % pairs), h = s >> 1, kv = s & 1;
     const T* src = static_cast<const T*>(kv ? p.v : p.k);
-    if (src == nullptr) continue;
-    const Unit x = locate(p, un, u, tid == 0);
-    if (x.phys < 0) continue;
+    const bool on = src != nullptr && x.phys >= 0;
     const long long stride = kv ? p.v_stride : p.k_stride;
-    const int r_lane = tid / kLanes, c_lane = tid % kLanes;
     uint4 raw[kIter];
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
       const int r = i * kPer + r_lane;
       raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < x.m) raw[i] = __ldcs(reinterpret_cast<const uint4*>(src + (x.row + r) * stride + h * kDim) + c_lane);
+      if (on && r < x.m) raw[i] = __ldcs(reinterpret_cast<const uint4*>(src + (x.row + r) * stride + h * kDim) + c_lane);
     }
-    const long long ph = static_cast<long long>(x.phys) * p.num_kv_heads + h;
+    const long long ph = static_cast<long long>(on ? x.phys : 0) * p.num_kv_heads + h;
     float* scale = (kv ? p.v_scale : p.k_scale) + ph;
-    const float old = *scale;
+    const float old = on ? *scale : 1.f;
+    const Unit cur = x;
+    t += gridDim.x;
+    if (t < work) x = locate(p, un, static_cast<int>(t / pairs), tid == 0);  // while the loads are on their way
+    if (!on) continue;
     uint32_t amax = 0u;
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) {
-      float f[kV];
-      widen<T>(raw[i], f);
-#pragma unroll
-      for (int j = 0; j < kV; ++j) amax = max(amax, finite_abs_bits(f[j]));
-    }
+    for (int i = 0; i < kIter; ++i) amax = max(amax, amax_bits<T>(raw[i]));
     amax = __reduce_max_sync(0xFFFFFFFFu, amax);
     if (lane == 0) wmax[buf][w] = amax;
     __syncthreads();  // also: every thread has read the old scale
@@ -337,7 +353,7 @@ __global__ void __launch_bounds__(kThreads) append_tile_kernel(const Kv8AppendPa
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) amax = max(amax, wmax[buf][i]);
     buf ^= 1;  // the other half is free: its readers passed the barrier above
-    const Scale sc = new_scale(amax, old, x.f);
+    const Scale sc = new_scale(amax, old, cur.f);
     uint8_t* data = (kv ? p.v_data : p.k_data) + ph * (kBlock * kDim);
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
@@ -348,15 +364,16 @@ __global__ void __launch_bounds__(kThreads) append_tile_kernel(const Kv8AppendPa
 #pragma unroll
       for (int j = 0; j < kV / 4; ++j)
         c[j] = e4m3x4(f[4 * j] * sc.inv, f[4 * j + 1] * sc.inv, f[4 * j + 2] * sc.inv, f[4 * j + 3] * sc.inv);
-      if (r < x.m) {
-        uint8_t* dst = data + (x.f + r) * kDim + c_lane * kV;
+      if (r < cur.m) {
+        uint8_t* dst = data + (cur.f + r) * kDim + c_lane * kV;
         if constexpr (kV == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
         else *reinterpret_cast<uint32_t*>(dst) = c[0];
       }
     }
     if (tid == 0) *scale = sc.scale;
     if (sc.ratio != 1.f)
-      for (int c = tid; c < x.f * (kDim / 16); c += kThreads) rescale_chunk(reinterpret_cast<uint4*>(data) + c, sc.ratio);
+      for (int c = tid; c < cur.f * (kDim / 16); c += kThreads)
+        rescale_chunk(reinterpret_cast<uint4*>(data) + c, sc.ratio);
   }
 }
 
@@ -370,7 +387,8 @@ cudaError_t launch(const Kv8AppendParams& prm, int sm_count, cudaStream_t st) {
     append_rows_kernel<T><<<static_cast<int>(most < cap ? most : cap), kThreads, 0, st>>>(prm);
   } else {
     const long long cap = static_cast<long long>(sm_count) * 4, work = units * 2 * prm.num_kv_heads;
-    append_tile_kernel<T><<<static_cast<int>(work < cap ? work : cap), kThreads, 0, st>>>(prm);
+    constexpr int kTh = sizeof(T) == 2 ? 256 : 512;
+    append_tile_kernel<T, kTh><<<static_cast<int>(work < cap ? work : cap), kTh, 0, st>>>(prm);
   }
   return cudaGetLastError();
 }
