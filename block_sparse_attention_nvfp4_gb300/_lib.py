@@ -136,7 +136,7 @@ def load(path: str = LIB_PATH):
             lib.msa_dcp_local_topk.argtypes = [ap, i32, i32, vp, vp, sz, vp]
             lib.msa_dcp_merge_topk.argtypes = [ap, i32, i32, i32, vp, vp, vp, sz, vp]
             lib.msa_selftest_wait_timeout.argtypes = [vp, sz, vp]
-            lib.msa_kv8_append.argtypes = [ctypes.POINTER(Kv8AppendArgs), vp, sz, vp]
+            lib.msa_kv8_append.argtypes = [vp, vp, sz, vp]  # (the arguments also come as packed bytes)
             lib.msa_kv8_attn_workspace_size.argtypes = [ctypes.POINTER(Kv8AttnArgs), ctypes.POINTER(sz)]
             lib.msa_kv8_attn.argtypes = [ctypes.POINTER(Kv8AttnArgs), vp, sz, vp]
             pp = ctypes.POINTER(PagePoolArgs)

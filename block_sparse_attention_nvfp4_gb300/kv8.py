@@ -6,6 +6,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import math
+import struct
 from typing import Optional
 
 import torch
@@ -39,13 +40,19 @@ def _rows(t: torch.Tensor, heads: int, name: str) -> int:
     return row if t.shape[0] > 1 else heads * DIM
 
 
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+_append_args = struct.Struct("@7i2q9P")      # msa_kv8_append_args
+assert _append_args.size == ctypes.sizeof(_lib.Kv8AppendArgs)
+
+
 def _call(dev, stream, fn, what, *args):
     """fn(*args, stream) on the tensors' device; the stream is that device's current one unless given."""
-    if torch.cuda.current_device() != dev.index:
+    index = dev.index
+    if _current_device() != index:
         with torch.cuda.device(dev):
             return _call(dev, stream, fn, what, *args)
-    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
-    code = fn(*args, s)
+    code = fn(*args, _current_stream(index) if stream is None else stream.cuda_stream)
     if code != _lib.MSA_OK:
         raise _lib.MSAError(code, what)
 
@@ -131,21 +138,34 @@ class KV8Cache(_Handle):
         of >= 256 bytes (error flags). `batch` is a KV8Batch or a DecodeBatch; its q is not read."""
         dev, P, H, kd, ks, vd, vs = self._pointers()
         B, total, most, M, lens, indptr, table = _geometry(batch, dev)
-        dtype, shape, src, strides = None, (total, H, DIM), [None, None], [0, 0]
-        for i, t in enumerate((k, v)):
-            if t is None:
-                continue
-            if t.shape != shape or t.device != dev or (dtype is not None and t.dtype is not dtype) or \
-                    t.dtype not in _SRC_TYPES:
-                raise ValueError(f"{'kv'[i]}: expected {shape} on {dev} in one of {list(_SRC_TYPES)}, one type for k and "
-                                 f"v, got {tuple(t.shape)} {t.dtype} on {t.device}")
-            dtype, src[i], strides[i] = t.dtype, t.data_ptr(), _rows(t, H, "kv"[i])
+        if k is not None:
+            kp, kst, kt = self._source(k, total, H, dev, "k")
+        if v is not None:
+            vp, vst, vt = self._source(v, total, H, dev, "v")
+            if k is None:
+                kp, kst, kt = 0, 0, vt
+            elif vt != kt:
+                raise ValueError(f"k and v: expected one type for both, got {k.dtype} and {v.dtype}")
+        else:
+            vp = vst = 0
+            if k is None:
+                return
         if ws.device != dev or not ws.is_contiguous():
             raise ValueError(f"ws: expected a contiguous tensor on {dev}")
-        a = _lib.Kv8AppendArgs(B, total, most, P, M, H, _SRC_TYPES.get(dtype, _lib.TYPE_BF16), strides[0], strides[1],
-                               lens, indptr, table, src[0], src[1], kd, ks, vd, vs)
-        _call(dev, stream, _lib.load().msa_kv8_append, "msa_kv8_append", ctypes.byref(a), ws.data_ptr(),
-              ws.numel() * ws.element_size())
+        a = _append_args.pack(B, total, most, P, M, H, kt, kst, vst, lens, indptr, table, kp, vp, kd, ks, vd, vs)
+        _call(dev, stream, _lib.load().msa_kv8_append, "msa_kv8_append", a, ws.data_ptr(), ws.nbytes)
+
+    @staticmethod
+    def _source(t: torch.Tensor, rows: int, heads: int, dev, name: str):
+        """Address, row stride and type of new tokens' rows."""
+        kind = _SRC_TYPES.get(t.dtype)
+        if kind is None or t.shape != (rows, heads, DIM) or t.device != dev:
+            raise ValueError(f"{name}: expected [{rows}, {heads}, {DIM}] on {dev} in one of {list(_SRC_TYPES)}, got "
+                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
+        row, head, one = t.stride()
+        if one != 1 or (heads > 1 and head != DIM):
+            raise ValueError(f"{name}: the heads of a row must be contiguous, got strides {t.stride()}")
+        return t.data_ptr(), row if rows > 1 else heads * DIM, kind
 
 
 class KV8Attention:

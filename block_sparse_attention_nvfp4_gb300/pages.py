@@ -56,7 +56,7 @@ class PagePool:
         with torch.cuda.device(dev):
             self.ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
             _lib.msa_workspace_init(self.ws)
-        self._ref, self._ws = ctypes.byref(a), (self.ws.data_ptr(), self.ws.numel())
+        self._ref, self._ws, self._index = ctypes.byref(a), (self.ws.data_ptr(), self.ws.numel()), dev.index
 
     @staticmethod
     def empty(caches: Sequence[Union[KVCache, KV8Cache]], num_seqs: int, max_pages: int) -> "PagePool":
@@ -66,7 +66,8 @@ class PagePool:
         return PagePool(caches, z(num_seqs), z(num_seqs, max_pages).fill_(-1), z(ref.shape[0]))
 
     def _list(self, t: torch.Tensor, n: int, name: str) -> int:
-        if t.dtype is not torch.int32 or t.shape != (n,) or t.device != self.device or not t.is_contiguous():
+        if t.dtype is not torch.int32 or t.get_device() != self._index or t.dim() != 1 or t.numel() != n or \
+                not t.is_contiguous():
             raise ValueError(f"{name}: expected a contiguous int32 list of {n} on {self.device}, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
         return t.data_ptr()
