@@ -3,12 +3,14 @@
 //
 // Each operator is a plan over small integer state (lengths, counts, block tables), then the
 // movement of page bytes:
-//   * the plan runs in one CTA: list entries are checked, the pages that each one needs are
-//     summed in list order, and the free pages are found by one scan of the counts in id
-//     order. Ranks come from prefix sums, so ids do not depend on timing.
+//   * the plan runs in one CTA and is bound by its chain of dependent reads (0.6-0.8 us each):
+//     list entries are checked, the pages that each one needs are summed in list order, and the
+//     free pages are found by one scan of the counts in id order, whose first 4,096 are asked for
+//     before anything else. Ranks come from prefix sums, so ids do not depend on timing.
 //   * pages move in one grid-wide kernel over (pair, 16 KB chunk): bound by memory, 2 bytes
 //     moved for each byte of a page. Four 16-byte loads per thread are in flight before the first
-//     store. Block-table rows are copied or remapped by the same launch.
+//     store. Block-table rows are copied or remapped by the same launch, which is set up while
+//     the plan runs (programmatic dependent launch).
 // Sources are live pages and targets are free ones, so no order among the copies matters.
 #include <climits>
 #include <cstdint>
@@ -96,15 +98,37 @@ __device__ __forceinline__ int cta_exclusive_sum(int v, int* total) {
   return base + incl - v;
 }
 
+// Counts 4 t .. 4 t + 3 (t = thread) of ids base ..; ids past the pool count as held.
+__device__ __forceinline__ int4 load_counts(const Pool& p, int base) {
+  const int id = base + 4 * threadIdx.x;
+  int4 r = make_int4(1, 1, 1, 1);
+  if (id + 3 < p.num_pages && (reinterpret_cast<uintptr_t>(p.refs) & 15u) == 0) {
+    r = *reinterpret_cast<const int4*>(p.refs + id);
+  } else {
+    if (id < p.num_pages) r.x = p.refs[id];
+    if (id + 1 < p.num_pages) r.y = p.refs[id + 1];
+    if (id + 2 < p.num_pages) r.z = p.refs[id + 2];
+    if (id + 3 < p.num_pages) r.w = p.refs[id + 3];
+  }
+  return r;
+}
+
 // The first `want` free pages in id order into free_ids; returns how many there are (at most want).
-__device__ int find_free(const Pool& p, int want, int32_t* free_ids) {
+// `first`: load_counts(p, 0), asked for early.
+__device__ int find_free(const Pool& p, int want, int32_t* free_ids, int4 first) {
   int found = 0;
-  for (int base = 0; base < p.num_pages && found < want; base += kPlanThreads) {
-    const int id = base + threadIdx.x;
-    const int is = id < p.num_pages && p.refs[id] == 0 ? 1 : 0;
+  for (int base = 0; base < p.num_pages && found < want; base += 4 * kPlanThreads) {
+    const int4 r = base == 0 ? first : load_counts(p, base);
     int total;
-    const int at = found + cta_exclusive_sum(is, &total);
-    if (is && at < want) free_ids[at] = id;
+    int at = found + cta_exclusive_sum((r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0), &total);
+    const int id = base + 4 * threadIdx.x;
+    if (r.x == 0 && at < want) free_ids[at] = id;
+    at += r.x == 0;
+    if (r.y == 0 && at < want) free_ids[at] = id + 1;
+    at += r.y == 0;
+    if (r.z == 0 && at < want) free_ids[at] = id + 2;
+    at += r.z == 0;
+    if (r.w == 0 && at < want) free_ids[at] = id + 3;
     found += total;
   }
   __syncthreads();
@@ -117,20 +141,26 @@ __device__ __forceinline__ bool good_len(const Pool& p, int n) {
   return n >= 0 && n <= static_cast<long long>(p.max_pages) * kBlock;
 }
 
-// claim[s] = the first entry that lists sequence s, for every listed one.
-__device__ void claim_first(const Pool& p, const Lists& l, int n, const int32_t* seqs) {
+// claim[s] = the first entry that lists sequence s, for every listed one: in shared memory when the
+// pool's sequences fit there.
+constexpr int kSmemSeqs = 8192;
+__device__ void claim_first(const Pool& p, int32_t* claim, int n, const int32_t* seqs) {
   for (int i = threadIdx.x; i < n; i += kPlanThreads)
-    if (in(seqs[i], p.num_seqs)) l.claim[seqs[i]] = INT_MAX;
+    if (in(seqs[i], p.num_seqs)) claim[seqs[i]] = INT_MAX;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kPlanThreads)
-    if (in(seqs[i], p.num_seqs)) atomicMin(&l.claim[seqs[i]], i);
+    if (in(seqs[i], p.num_seqs)) atomicMin(&claim[seqs[i]], i);
   __syncthreads();
 }
 
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const Pool p, const Lists l, int n,
                                                                  const int32_t* parents, const int32_t* children) {
+  __shared__ int32_t claim_s[kSmemSeqs];
+  pdl_launch_dependents();
   const int tid = threadIdx.x;
-  claim_first(p, l, n, children);
+  const int4 counts = load_counts(p, 0);
+  int32_t* claim = p.num_seqs <= kSmemSeqs ? claim_s : l.claim;
+  claim_first(p, claim, n, children);
   // what each entry needs, in list order; len[i] = the parent's length, src[i] = its tail page
   int need_all = 0;
   for (int base = 0; base < n; base += kPlanThreads) {
@@ -139,7 +169,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const Pool p, c
     if (i < n) {
       const int par = parents[i], ch = children[i];
       int len = -1, tail = -1;
-      if (!in(par, p.num_seqs) || !in(ch, p.num_seqs) || l.claim[ch] != i || p.seq_lens[ch] != 0 || par == ch) {
+      if (!in(par, p.num_seqs) || !in(ch, p.num_seqs) || claim[ch] != i || p.seq_lens[ch] != 0 || par == ch) {
         set_flag(p.flags, kFlagBadSeq);
       } else {
         len = p.seq_lens[par];
@@ -166,7 +196,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const Pool p, c
     need_all += total;
   }
   __syncthreads();
-  const int have = find_free(p, need_all, l.free_ids);
+  const int have = find_free(p, need_all, l.free_ids, counts);
   // every length and tail has been read: the children may be written
   for (int i = tid; i < n; i += kPlanThreads) {
     const int rank = l.dst[i], len = l.len[i];
@@ -192,8 +222,11 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const Pool p, c
 
 __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const Pool p, const Lists l, int n, const int32_t* seqs,
                                                                const int32_t* new_lens) {
+  __shared__ int32_t claim_s[kSmemSeqs];
   const int tid = threadIdx.x;
-  claim_first(p, l, n, seqs);
+  const int4 counts = load_counts(p, 0);
+  int32_t* claim = p.num_seqs <= kSmemSeqs ? claim_s : l.claim;
+  claim_first(p, claim, n, seqs);
   // len[i] = the new length (-1: nothing to do), src[i] = pages needed, dst[i] = rank of the first
   int need_all = 0;
   for (int base = 0; base < n; base += kPlanThreads) {
@@ -201,7 +234,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const Pool p, con
     int need = 0, to = -1;
     if (i < n) {
       const int s = seqs[i];
-      if (!in(s, p.num_seqs) || l.claim[s] != i) {
+      if (!in(s, p.num_seqs) || claim[s] != i) {
         set_flag(p.flags, kFlagBadSeq);
       } else {
         const int len = p.seq_lens[s], want = new_lens[i];
@@ -227,23 +260,31 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const Pool p, con
     need_all = sum < INT_MAX / 2 ? static_cast<int>(sum) : INT_MAX / 2;
   }
   __syncthreads();
-  const int have = find_free(p, need_all < p.num_pages ? need_all : p.num_pages, l.free_ids);
-  const int w = tid >> 5, lane = tid & 31;
-  for (int i = w; i < n; i += kPlanWarps) {  // a warp per entry
+  const int have = find_free(p, need_all < p.num_pages ? need_all : p.num_pages, l.free_ids, counts);
+  // Entries that need a few pages take a thread, the others a warp.
+  constexpr int kFew = 4;
+  auto serve = [&](int i, int lane, int lanes) {
     const int to = l.len[i], need = l.src[i], at = l.dst[i];
-    if (to < 0) continue;
+    if (to < 0 || (lanes == 1) != (need <= kFew)) return;
     if (at + need > have && need > 0) {
       if (lane == 0) set_flag(p.flags, kFlagNoPage);
-      continue;
+      return;
     }
     const int s = seqs[i], c0 = pages_of(to) - need;
-    for (int k = lane; k < need; k += 32) {
+    for (int k = lane; k < need; k += lanes) {
       const int id = l.free_ids[at + k];
       p.refs[id] = 1;
       p.table[static_cast<long long>(s) * p.max_pages + c0 + k] = id;
     }
     if (lane == 0) p.seq_lens[s] = to;
+  };
+  bool many = false;
+  for (int i = tid; i < n; i += kPlanThreads) {
+    serve(i, 0, 1);
+    many |= l.src[i] > kFew;
   }
+  if (__syncthreads_or(many))
+    for (int i = tid >> 5; i < n; i += kPlanWarps) serve(i, tid & 31, 32);
 }
 
 // One CTA per list entry; the exchange of the length decides which of equal entries frees.
@@ -277,45 +318,68 @@ __global__ void __launch_bounds__(128) free_kernel(const Pool p, int n, const in
 
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Pool p, const Lists l, int32_t* new_refs,
                                                                     int32_t* num_live) {
+  pdl_launch_dependents();
   const int tid = threadIdx.x;
+  constexpr int kStep = 4 * kPlanThreads;
+  const int4 first = load_counts(p, 0);
+  auto live4 = [](const int4& r) { return (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0); };
+  auto get = [](const int4& r, int k) { return k == 0 ? r.x : k == 1 ? r.y : k == 2 ? r.z : r.w; };
   int mine = 0;
-  for (int id = tid; id < p.num_pages; id += kPlanThreads) mine += p.refs[id] > 0 ? 1 : 0;
+  for (int base = 0; base < p.num_pages; base += kStep) {
+    const int4 r = base == 0 ? first : load_counts(p, base);
+    const int past = base + 4 * tid + 4 - p.num_pages;  // ids past the pool, which count as held
+    mine += live4(r) - (past > 0 ? (past < 4 ? past : 4) : 0);
+  }
   int live;
   cta_exclusive_sum(mine, &live);
   // holes below `live` in id order
   int holes = 0;
-  for (int base = 0; base < live; base += kPlanThreads) {
-    const int id = base + tid;
-    const int is = id < live && p.refs[id] <= 0 ? 1 : 0;
-    int total;
-    const int at = holes + cta_exclusive_sum(is, &total);
-    if (id < live) {
-      if (is) l.free_ids[at] = id;
-      else {
+  for (int base = 0; base < live; base += kStep) {
+    const int4 r = base == 0 ? first : load_counts(p, base);
+    const int id0 = base + 4 * tid;
+    int n = 0, total;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) n += id0 + k < live && get(r, k) <= 0;
+    int at = holes + cta_exclusive_sum(n, &total);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int id = id0 + k;
+      if (id >= live) break;
+      if (get(r, k) <= 0) {
+        l.free_ids[at++] = id;
+      } else {
         l.map[id] = id;
-        if (new_refs != p.refs) new_refs[id] = p.refs[id];
+        if (new_refs != p.refs) new_refs[id] = get(r, k);
       }
     }
     holes += total;
   }
   __syncthreads();
-  // live pages from `live` on: as many as holes; k-th to the k-th
+  // live pages from `live` on: as many as holes; k-th to the k-th. In place this writes counts below
+  // `live`, which no later step reads, and a step's own, which its sum's barrier has seen read.
   int moved = 0;
-  for (int base = live; base < p.num_pages; base += kPlanThreads) {
-    const int id = base + tid;
-    const int ref = id < p.num_pages ? p.refs[id] : 0;
-    const int is = ref > 0 ? 1 : 0;
-    int total;
-    const int at = moved + cta_exclusive_sum(is, &total);
-    if (is) {
-      const int to = l.free_ids[at];
-      l.map[id] = to;
-      l.free_ids[live + at] = id;  // sources behind the targets: live + holes <= num_pages
-      new_refs[to] = ref;
-    } else if (id < p.num_pages) {
-      l.map[id] = id;
+  for (int base = live / kStep * kStep; base < p.num_pages; base += kStep) {
+    const int4 r = base == 0 ? first : load_counts(p, base);
+    const int id0 = base + 4 * tid;
+    int n = 0, total;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) n += id0 + k >= live && id0 + k < p.num_pages && get(r, k) > 0;
+    int at = moved + cta_exclusive_sum(n, &total);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int id = id0 + k, ref = get(r, k);
+      if (id < live || id >= p.num_pages) continue;
+      new_refs[id] = 0;
+      if (ref > 0) {
+        const int to = l.free_ids[at];
+        l.map[id] = to;
+        l.free_ids[live + at] = id;  // sources behind the targets: live + holes <= num_pages
+        new_refs[to] = ref;
+        ++at;
+      } else {
+        l.map[id] = id;
+      }
     }
-    if (id < p.num_pages) new_refs[id] = 0;
     moved += total;
   }
   if (tid == 0) {
@@ -382,6 +446,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Pool p, int n,
 __global__ void __launch_bounds__(kCopyThreads) fork_move_kernel(const Pool p, const Lists l, int n,
                                                                  const int32_t* parents, const int32_t* children,
                                                                  int row_units) {
+  pdl_wait_primary();
   const int per = p.chunks + row_units;
   const long long work = static_cast<long long>(n) * per;
   for (long long u = blockIdx.x; u < work; u += gridDim.x) {
@@ -407,6 +472,7 @@ __global__ void __launch_bounds__(kCopyThreads) fork_move_kernel(const Pool p, c
 
 __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const Pool p, const Lists l, int32_t* new_table,
                                                                     int row_units) {
+  pdl_wait_primary();
   const int moved = l.count[0], sources = l.count[1];
   const long long rows = static_cast<long long>(p.num_seqs) * row_units;
   const long long work = rows + static_cast<long long>(moved) * p.chunks;
@@ -485,6 +551,21 @@ int copy_grid(long long work, int sms) {
   return static_cast<int>(work < cap ? work : cap);
 }
 
+// Launch chained to the kernel before it in the stream: it waits for that kernel's end itself.
+template <typename... Args>
+msa_status launch_chained(void (*kernel)(Args...), int grid, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+}
+
 msa_status launched() { return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA; }
 
 }  // namespace
@@ -529,9 +610,8 @@ msa_status msa_pages_fork(const msa_page_pool* a, int32_t n, const int32_t* pare
   fork_plan_kernel<<<1, kPlanThreads, 0, st>>>(p, l, n, parents, children);
   if ((s = launched()) != MSA_OK) return s;
   const int row_units = (p.max_pages + kTableChunk - 1) / kTableChunk;
-  fork_move_kernel<<<copy_grid(static_cast<long long>(n) * (p.chunks + row_units), sms), kCopyThreads, 0, st>>>(
-      p, l, n, parents, children, row_units);
-  return launched();
+  return launch_chained(fork_move_kernel, copy_grid(static_cast<long long>(n) * (p.chunks + row_units), sms), st, p, l,
+                        static_cast<int>(n), parents, children, row_units);
 }
 
 msa_status msa_pages_reserve(const msa_page_pool* a, int32_t n, const int32_t* seqs, const int32_t* new_lens, void* ws,
@@ -576,8 +656,7 @@ msa_status msa_pages_compact(const msa_page_pool* a, int32_t* new_block_table, i
   const int row_units = (p.max_pages + kTableChunk - 1) / kTableChunk;
   const long long most = static_cast<long long>(p.num_seqs) * row_units +
                          static_cast<long long>(p.num_pages / 2 + 1) * p.chunks;
-  compact_move_kernel<<<copy_grid(most, sms), kCopyThreads, 0, st>>>(p, l, new_block_table, row_units);
-  return launched();
+  return launch_chained(compact_move_kernel, copy_grid(most, sms), st, p, l, new_block_table, row_units);
 }
 
 }  // extern "C"
