@@ -32,18 +32,22 @@
 //   * K warp: finds the tiles (32 block-table entries and scales at a time, one per lane) and
 //     copies their K (16 KB, tensor copies) into a ring; what the others need of a tile or
 //     segment goes into small rings beside it;
+//   * V warp: copies the tiles' V codes (16-byte asynchronous copies, zeros past the context). K and
+//     V come by different paths: tensor and bulk copies alone measured 20-23 bytes a cycle and SM
+//     whatever is in flight, a tile's 32 KB then 1,400 cycles even from L2; both paths together 50;
 //   * 8 converting warps, four for each 64-token half of a tile: V to FP16 in three buffers that
-//     the halves take in turn, rows past the context to zero; at a segment's first tile they
-//     also lay out its queries. Each thread copies the codes that it will convert itself (16-byte
-//     asynchronous copies, 2 or 3 tiles ahead), so V needs no hand-over, and K and V come by
-//     different paths: tensor and bulk copies alone measured 20-23 bytes a cycle and SM whatever
-//     is in flight, a tile's 32 KB then 1,400 cycles even from L2; both paths together 50;
+//     the halves take in turn; at a segment's first tile they also lay out its queries;
 //   * S warp (three score buffers in tensor memory) and P V warp (one O);
-//   * 8 softmax warps in two sets that share every tile: of the tokens that a copy of a row takes,
-//     set 0 has the first half and set 1 the second. The two threads of a row exchange their
-//     maxima through shared memory, so both know its reference without asking again. (Sets that
-//     take alternate tiles make the chain scores -> weights -> P V longer than three score
-//     buffers cover: 2,050 cycles a prompt tile.)
+//   * 8 softmax warps in two sets. With one copy (prompts) a set takes every other tile, and the
+//     rows' reference goes from set to set through shared memory. With more copies, where a row
+//     has few tokens, both sets share every tile: of the tokens that a copy takes, set 0 has the
+//     first half and set 1 the second, and the two threads of a row exchange their maxima.
+//     (One scheme for both: 2,053 rows on 16,421 tokens, 4 x 8 heads, BF16, take 488 us with shared
+//     tiles and 444 in turn; 64 ragged requests of up to 8 rows 202 us shared and 215 in turn.)
+//
+// What bounds it now: the roles' instruction streams. A tile costs a CTA 1,750 to 2,000 cycles
+// whether its bytes come from HBM or L2, most of them the dependent instructions of a single warp
+// between two hand-overs (about 6 cycles each with five warps a scheduler).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -60,13 +64,13 @@ namespace msa {
 namespace {
 
 constexpr int kSoftWarps = 8;                        // warps 0..7: two sets of 4, one per TMEM lane quadrant
-constexpr int kMmaWarp = 8, kPvWarp = 9, kKWarp = 10;  // (warp 11 has no part: warps come in fours)
+constexpr int kMmaWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11;
 constexpr int kCvWarp0 = 12, kCvWarps = 8;           // two groups of 4
 constexpr int kThreads = (kCvWarp0 + kCvWarps) * 32;
 constexpr int kVBufs = 3;                            // FP16 halves of V
 // A wait on a barrier's parity has to be for its current phase or the one before. Waiters that
-// fall behind therefore have barriers that go round 6 tiles (no wait is 6 tiles behind), or 12 for a
-// tile's description (up to 9 ahead).
+// fall behind therefore have barriers that go round 6 tiles or halves (no wait is 6 behind), or 12
+// tiles for a tile's description (up to 9 ahead).
 constexpr int kBars = 6, kTold = 12;
 constexpr int kRing = 16;                            // tiles and segments whose description is kept
 constexpr int kRows = 8;                             // segments whose query scales and NaN marks are kept
@@ -82,21 +86,20 @@ constexpr int kNoPos = 1 << 30;                      // position of a tile that 
 constexpr int kRedStride = 17;                       // floats of a lane's 16 dims in the copies' exchange
 constexpr int kMergeThreads = 256;
 
-struct Tile {
-  int pos0;      // position of its first token
-  int nvalid;    // tokens inside the context; 0: nothing to read
+enum : int { kEnd = 1, kFirst = 2, kLast = 4, kPart = 8 };
+struct alignas(16) Tile {
   int page;      // physical page x KV heads + head
-  int seg;       // the CTA's segment
-  int last;      // last tile of that segment
-  int end;       // no tile: the CTA's work is over
-  int vzero;     // the page's value scale is 0
+  int rows;      // V rows to read: tokens inside the context; 0 when its values count for nothing
+  int marks;     // kEnd: no tile, the work is over; kFirst, kLast of its segment; kPart: some rows do
+                 // not see all of its tokens
+  int pos0;      // position of its first token
   float kscale;
   float lv, iv;  // log2 of the value scale, and its inverse
+  int pad;
 };
 
 struct Seg {
-  int first;     // its first tile
-  int last;
+  int last;      // its last tile
   int row0;      // first query row
   int rows;
   int head;      // KV head
@@ -118,19 +121,20 @@ struct Smem {
   static constexpr int kKStages = 4, kVStages = NP == 1 ? 4 : 3;
   uint8_t q[NP][kTileBytes];                         // A of S: copies of the query rows, by part
   uint8_t k[kKStages][kTileBytes];                   // B of S (K-major), 128-byte swizzle
-  uint8_t v[kVStages][kTileBytes];                   // V codes as they are in the page, a slot of each thread
+  uint8_t v[kVStages][kTileBytes];                   // V codes as they are in the page
   uint8_t v16[kVBufs][2][kHalfBytes];                // B of O (MN-major): [dim half][token][64 dims]
   float red[2][128 * kRedStride];                    // by set: what the lanes hand to another copy
   float qscale[kRows][128];                          // 2^e of each tile row (BF16 queries)
   int nanpos[kRows][kDim];                           // first position with a NaN value in a dim, of partly seen tokens
   int nanany[kRows];
-  float half_max[2][2][128];                         // by tile parity and set
-  float xm[128], xl[2][128], xm2[2][128];
+  float half_max[2][2][128];                         // by tile parity: each set's maxima, or the reference
+  float xm[2][128], xl[2][128], xm2[2][128];
   Tile tile[kRing];
   Seg seg[kRing];
   uint64_t k_full[kKStages], k_empty[kKStages], told[kTold];
-  uint64_t q_full, q_free, s_full[kBars], p_full[kBars], v16_full[kVBufs], v16_free[kBars], pv_done[kBars], drain[2];
-  uint64_t pair_met[4];                              // by quadrant: both sets' warps have the tile's maxima
+  uint64_t v_full[kVStages], v_empty[kVStages];
+  uint64_t q_full, q_free, s_full[kBars], p_full[kBars], pv_done[kBars], v16_full[kVBufs], v16_free[kBars], drain[2];
+  uint64_t row_told[4];                              // by quadrant: a tile's maxima or reference are there
   uint64_t sets_met, set_met[2];                     // the softmax warps of both sets, or of one, have come here
   long long part[kThreads / 32];
   long long lo, hi;
@@ -258,6 +262,11 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t c) {  // the low two c
   asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(h) : "r"(c));
   return h;
 }
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t c, uint32_t& lo, uint32_t& hi) {
+  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+      : "=r"(lo), "=r"(hi)
+      : "r"(c));
+}
 __device__ __forceinline__ uint32_t f32x2_e4m3x2(float a, float b) {  // a in the low byte
   uint32_t r;
   asm("{ .reg .b16 t; cvt.rn.satfinite.e4m3x2.f32 t, %2, %1; cvt.u32.u16 %0, t; }" : "=r"(r) : "f"(a), "f"(b));
@@ -311,6 +320,7 @@ template <int C, int NP>
 __global__ void __launch_bounds__(kThreads, 1)
     kv8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const Kv8AttnParams p) {
   constexpr int kMpad = 128 / C;
+  constexpr bool kTurns = C == 1;  // the softmax sets take tiles in turn; otherwise they share every tile
   constexpr int kStages = Smem<NP>::kKStages, kVStages = Smem<NP>::kVStages;
   extern __shared__ uint8_t smem_raw[];
   Smem<NP>& sm = *reinterpret_cast<Smem<NP>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
@@ -325,17 +335,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     init(sm.k_full, kStages, 0, 1);
     init(sm.k_empty, kStages, 8, 1);
     init(sm.told, kTold, 16, 1);
-    init(sm.s_full, kBars, 32, 1);
-    init(sm.p_full, kBars, 40, kSoftWarps);
-    init(sm.v16_full, kVBufs, 48, kCvWarps / 2);
-    init(sm.v16_free, kBars, 56, 1);
-    init(sm.pv_done, kBars, 64, 1);
-    init(sm.drain, 2, 72, 1);
-    init(&sm.q_full, 1, 74, kCvWarps);
-    init(&sm.q_free, 1, 75, 1);
-    init(&sm.sets_met, 1, 76, kSoftWarps);
-    init(sm.set_met, 2, 78, kSoftWarps / 2);
-    init(sm.pair_met, 4, 80, 2);
+    init(sm.v_full, kVStages, 28, 33);
+    init(sm.v_empty, kVStages, 32, kCvWarps);
+    init(sm.s_full, kBars, 36, 1);
+    init(sm.p_full, kBars, 42, kTurns ? kSoftWarps / 2 : kSoftWarps);
+    init(sm.pv_done, kBars, 48, 1);
+    init(sm.v16_full, kVBufs, 54, kCvWarps / 2);
+    init(sm.v16_free, kBars, 57, 1);
+    init(sm.drain, 2, 63, 1);
+    init(&sm.q_full, 1, 65, kCvWarps);
+    init(&sm.q_free, 1, 66, 1);
+    init(&sm.sets_met, 1, 67, kSoftWarps);
+    init(sm.set_met, 2, 68, kSoftWarps / 2);
+    init(sm.row_told, 4, 70, kTurns ? 1 : 2);
     if (tid < 96) mbar_fence_init();
     if (tid == 0) sm.lo = sm.hi = 0;
   }
@@ -410,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool good = true;
     Header hd = {};
     // Waits until tile t's stage is free, writes its description and starts its K copy.
-    auto emit = [&](int pos0, int nvalid, int last, int end, int page, float ks, float vs) {
+    auto emit = [&](int pos0, int nvalid, int marks, int page, float ks, float lv, float iv, bool vzero) {
       const int st = t % kStages;
       if (t >= kStages) {
         good = warp_wait(smem_u32(&sm.k_empty[st]), ((t / kStages) - 1) & 1, p.flags);
@@ -418,16 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane == 0) {
         Tile& x = sm.tile[t % kRing];
-        x.pos0 = pos0;
-        x.nvalid = nvalid;
-        x.page = page;
-        x.seg = nseg;
-        x.last = last;
-        x.end = end;
-        x.vzero = vs == 0.f;
-        x.kscale = ks;
-        x.lv = vs == 0.f ? 0.f : log2f(vs);
-        x.iv = vs == 0.f ? 1.f : 1.f / vs;
+        *reinterpret_cast<int4*>(&x.page) = make_int4(page, vzero ? 0 : nvalid, marks, pos0);
+        *reinterpret_cast<float4*>(&x.kscale) = make_float4(ks, lv, iv, 0.f);
         mbar_arrive(smem_u32(&sm.told[t % kTold]));
         const uint32_t kb = smem_u32(&sm.k_full[st]);
         if (nvalid > 0) {
@@ -484,16 +488,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           use = __ballot_sync(0xFFFFFFFFu, in && !twice && lane >= j0 && lane < j1);
         }
         const int count = p.n_ids ? (use ? __popc(use) : 1) : j1 - j0;
-        const int last = t + count - 1;
+        const int first = t, last = t + count - 1, pos = q.N - q.R + row0;
+        auto marks = [&]() { return (t == first ? kFirst : 0) | (t == last ? kLast : 0); };
         const int slot = begin && end ? -1 : (begin ? 1 : 0);
         if (lane == 0) {
           Seg& s = sm.seg[nseg % kRing];
-          s.first = t;
           s.last = last;
           s.row0 = q.r0 + row0;
           s.rows = rows;
           s.head = h;
-          s.pos = q.N - q.R + row0;
+          s.pos = pos;
           s.slot = slot;
         }
         if (slot == 1) {
@@ -510,7 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int c = p.n_ids ? id : base + lane;
           const bool on = p.n_ids ? (use >> lane) & 1u : c < j1;
           int phys = -1;
-          float ks = 1.f, vs = 1.f;
+          float ks = 1.f, lv = 0.f, iv = 1.f;
+          bool vzero = false;
           if (on) {
             phys = table[c];
             if (phys < 0 || phys >= p.num_pages) {
@@ -519,19 +524,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               const long long ph = static_cast<long long>(phys) * p.num_kv_heads + h;
               ks = p.k_scale[ph];
-              vs = p.v_scale[ph];
+              const float vs = p.v_scale[ph];
+              vzero = vs == 0.f;
+              lv = vzero ? 0.f : log2f(vs);
+              iv = vzero ? 1.f : 1.f / vs;
             }
           }
           for (unsigned m = __ballot_sync(0xFFFFFFFFu, on); m != 0u && good; m &= m - 1u) {
             const int src = __ffs(m) - 1;
             const int cc = __shfl_sync(0xFFFFFFFFu, c, src), pp = __shfl_sync(0xFFFFFFFFu, phys, src);
-            const float kk = __shfl_sync(0xFFFFFFFFu, ks, src), vv = __shfl_sync(0xFFFFFFFFu, vs, src);
+            const float kk = __shfl_sync(0xFFFFFFFFu, ks, src), ll = __shfl_sync(0xFFFFFFFFu, lv, src);
+            const float ii = __shfl_sync(0xFFFFFFFFu, iv, src);
+            const bool zz = __shfl_sync(0xFFFFFFFFu, static_cast<int>(vzero), src) != 0;
             const int pos0 = cc * kBlock, nv = q.N - pos0 < kBlock ? q.N - pos0 : kBlock;
-            if (pp < 0) emit(kNoPos, 0, last, 0, 0, 1.f, 1.f);
-            else emit(pos0, nv, last, 0, pp * p.num_kv_heads + h, kk, vv);
+            if (pp < 0) emit(kNoPos, 0, marks(), 0, 1.f, 0.f, 1.f, true);
+            else emit(pos0, nv, marks() | (pos0 + nv - 1 > pos ? kPart : 0), pp * p.num_kv_heads + h, kk, ll, ii, zz);
           }
         }
-        if (p.n_ids && use == 0u && good) emit(kNoPos, 0, last, 0, 0, 1.f, 1.f);
+        if (p.n_ids && use == 0u && good) emit(kNoPos, 0, marks(), 0, 1.f, 0.f, 1.f, true);
         ++nseg;
         left -= kItemCost + nt - at;
         // the next item
@@ -547,11 +557,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (good) emit(kNoPos, 0, INT_MAX, 1, 0, 1.f, 1.f);
+    if (good) emit(kNoPos, 0, kEnd, 0, 1.f, 0.f, 1.f, true);
     // no copy may still be landing when the CTA leaves
     for (int j = t - kStages < 0 ? 0 : t - kStages; j < t; ++j)
       if (!wait_bar(smem_u32(&sm.k_full[j % kStages]), (j / kStages) & 1, p.flags)) break;
     if (lane == 0) reinterpret_cast<Header*>(p.parts)[blockIdx.x] = hd;
+    __syncwarp();
+  } else if (warp == kVWarp) {
+    // ================= V warp: the tiles' V codes by 16-byte asynchronous copies, a lane = one piece of
+    // every 4th row; zeros for rows past the context
+    const uint32_t dst0 = smem_u32(sm.v[0]) + 16u * lane;
+    Ring<kTold> rt;
+    Ring<kVStages> rs;
+    for (int t = 0;; ++t, rt.step(), rs.step()) {
+      if (t >= kVStages && !warp_wait(smem_u32(&sm.v_empty[rs.at]), rs.phase ^ 1u, p.flags)) break;
+      if (!warp_wait(smem_u32(&sm.told[rt.at]), rt.phase, p.flags)) break;
+      const int4 x = *reinterpret_cast<const int4*>(&sm.tile[t % kRing].page);
+      const bool end = x.z & kEnd;
+      if (!end) {
+        const uint8_t* src = p.v_data + static_cast<long long>(x.x) * kTileBytes + 16 * lane;
+        const uint32_t dst = dst0 + rs.at * kTileBytes;
+        const int rows = x.y - (lane >> 3);
+        if (x.y == kBlock) {
+#pragma unroll 8
+          for (int i = 0; i < 32; ++i) cp_async16(dst + 512u * i, src + 512 * i, 16u);
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 32; ++i) cp_async16(dst + 512u * i, src + 512 * i, rows > 4 * i ? 16u : 0u);
+        }
+      }
+      // 32 arrivals when the copies have landed, and one now that hands the description on
+      const uint32_t full = smem_u32(&sm.v_full[rs.at]);
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+      if (lane == 0) mbar_arrive(full);
+      if (end) break;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // none may still be landing when the CTA leaves
     __syncwarp();
   } else if (warp >= kCvWarp0) {
     // ================= converting warps: group h has tokens 64 h .. 64 h + 63 of every tile; thread =
@@ -563,37 +604,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int flip = vc >> 2, ch = 2 * (vc & 3);
     const uint32_t o0 = static_cast<uint32_t>((ch + flip) ^ (vr & 7)) << 4, o1 = o0 ^ 16u;
     const uint32_t slot0 = smem_u32(sm.v[0]) + static_cast<uint32_t>(64 * kDim * h + 16 * r);
-    // Starts the copies of this thread's pieces of tile t (zeros for rows past the context).
-    bool more = true;  // no end mark fetched yet
-    Ring<kTold> rt;
-    Ring<kVStages> rf, rs;  // slots fetched into, slots converted
-    auto fetch = [&](int t) -> bool {
-      if (more) {
-        if (!warp_wait(smem_u32(&sm.told[rt.at]), rt.phase, p.flags)) return false;
-        rt.step();
-        const Tile& x = sm.tile[t % kRing];
-        more = !x.end;
-        const int rows = (x.vzero ? 0 : x.nvalid) - 64 * h - vr;  // > 16 i: row 16 i + vr of this half counts
-        const uint8_t* src = p.v_data + static_cast<long long>(x.page) * kTileBytes + 64 * kDim * h + 16 * r;
-        const uint32_t to = slot0 + rf.at * kTileBytes;
-        rf.step();
-        if (more)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) cp_async16(to + 2048u * i, src + 2048 * i, rows > 16 * i ? 16u : 0u);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      return true;
-    };
-    bool ok = true;
-    for (int t = 0; t < kVStages - 1 && ok; ++t) ok = fetch(t);
+    int k = -1;                        // the segment
+    Ring<kVStages> rs;
     uint32_t uv = h, ub = h, uph = 0;  // half u = 2 t + h: u % 3, u % 6, (u / 6) % 2
-    for (int t = 0; ok; ++t, rs.step()) {
-      const Tile& x = sm.tile[t % kRing];
-      const bool end = x.end;
-      const Seg& sg = sm.seg[x.seg % kRing];
-      if (!end && sg.first == t) {
+    for (int t = 0;; ++t, rs.step()) {
+      if (!warp_wait(smem_u32(&sm.v_full[rs.at]), rs.phase, p.flags)) break;
+      const int4 x = *reinterpret_cast<const int4*>(&sm.tile[t % kRing].page);
+      const bool end = x.z & kEnd;
+      if (x.z & kFirst) {
+        const Seg& sg = sm.seg[++k % kRing];
         // the segment's queries, once the last segment's scores are computed: two threads per row
-        const int k = x.seg;
         if (k > 0 && !warp_wait(smem_u32(&sm.q_free), (k - 1) & 1, p.flags)) break;
         const int rr = 64 * h + (r >> 1), half = r & 1, m = rr % kMpad;
         const bool real = m < G * sg.rows;
@@ -663,20 +683,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
       }
-      asm volatile("cp.async.wait_group %0;" ::"n"(kVStages - 2) : "memory");  // this thread's pieces of tile t
       const uint32_t raw = slot0 + rs.at * kTileBytes;
       // a token that some rows of the segment do not see: its weight is 0 there, but 0 x NaN is
       // NaN, so its NaN codes become 0 here and are put back for the rows that see it
-      if (x.nvalid > 0 && x.pos0 + x.nvalid - 1 > sg.pos) {
+      if (x.z & kPart) {
+        const int pos = sm.seg[k % kRing].pos;
 #pragma unroll 1
         for (int i = 0; i < 16; ++i) {  // word i % 4 of the piece of row 16 (i / 4) + vr
           const int token = 64 * h + 16 * (i >> 2) + vr;
           const uint32_t at = raw + 2048u * (i >> 2) + 4u * (i & 3);
           const uint32_t w = lds_u1(at), nan = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-          if (nan == 0u || token >= x.nvalid || x.pos0 + token <= sg.pos) continue;
+          if (nan == 0u || token >= x.y || x.w + token <= pos) continue;
           for (int z = 0; z < 4; ++z)
-            if ((nan >> (8 * z)) & 1u) atomicMin(&sm.nanpos[x.seg % kRows][16 * vc + 4 * (i & 3) + z], x.pos0 + token);
-          sm.nanany[x.seg % kRows] = 1;
+            if ((nan >> (8 * z)) & 1u) atomicMin(&sm.nanpos[k % kRows][16 * vc + 4 * (i & 3) + z], x.w + token);
+          sm.nanany[k % kRows] = 1;
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(w & ~nan) : "memory");
         }
       }
@@ -685,10 +705,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 4; ++i) {
         const uint4 w = lds_u4(raw + 2048u * i);
         const uint32_t a0 = flip ? w.z : w.x, a1 = flip ? w.w : w.y, b0 = flip ? w.x : w.z, b1 = flip ? w.y : w.w;
-        f[i][0] = e4m3x2_f16x2(a0), f[i][1] = e4m3x2_f16x2(a0 >> 16);
-        f[i][2] = e4m3x2_f16x2(a1), f[i][3] = e4m3x2_f16x2(a1 >> 16);
-        f[i][4] = e4m3x2_f16x2(b0), f[i][5] = e4m3x2_f16x2(b0 >> 16);
-        f[i][6] = e4m3x2_f16x2(b1), f[i][7] = e4m3x2_f16x2(b1 >> 16);
+        e4m3x4_f16x4(a0, f[i][0], f[i][1]);
+        e4m3x4_f16x4(a1, f[i][2], f[i][3]);
+        e4m3x4_f16x4(b0, f[i][4], f[i][5]);
+        e4m3x4_f16x4(b1, f[i][6], f[i][7]);
       }
       // the half that was in this buffer (three halves ago) has been multiplied
       if (2 * t + h >= kVBufs && !(ub < 3u ? warp_wait(smem_u32(&sm.v16_free[ub + 3u]), uph ^ 1u, p.flags)
@@ -706,13 +726,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.v16_full[uv]));
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&sm.v16_full[uv]));
+        mbar_arrive(smem_u32(&sm.v_empty[rs.at]));  // (the stores above have used every value)
+      }
       uv = uv == 0u ? 2u : uv - 1u;  // + 2 mod 3
       ub += 2u;
       if (ub >= 6u) ub -= 6u, uph ^= 1u;
-      if (!fetch(t + kVStages - 1)) break;  // into the slots that tile t - 1 had
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");  // none may still be landing when the CTA leaves
   } else if (warp == kMmaWarp) {
     // ================= S warp: S_t = Q K_t^T into buffer t % 3
     const uint32_t el = elect_one();
@@ -720,26 +741,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc = idesc_e4m3_f32(128, kBlock, false, false);
     int seg = -1;
     bool good = true;
-    Ring<kBars> rb;
     Ring<kStages> rk;
+    Ring<kBars> rb;
+    static_assert(kBars == 2 * kSBufs, "");
     for (int t = 0;; ++t, rb.step(), rk.step()) {
       const uint32_t sb = rb.at < 3u ? rb.at : rb.at - 3u;
       // the buffer's previous weights (of tile t - 3) have been used
-      static_assert(kBars == 2 * kSBufs, "");
       if (t >= kSBufs)
         good = rb.at < 3u ? warp_wait(smem_u32(&sm.pv_done[rb.at + 3u]), rb.phase ^ 1u, p.flags)
                           : warp_wait(smem_u32(&sm.pv_done[rb.at - 3u]), rb.phase, p.flags);
       if (!good || !warp_wait(smem_u32(&sm.k_full[rk.at]), rk.phase, p.flags)) break;
-      const Tile& x = sm.tile[t % kRing];
-      if (x.end) {
+      const int marks = sm.tile[t % kRing].marks;
+      if (marks & kEnd) {
         if (lane == 0) mbar_arrive(smem_u32(&sm.s_full[rb.at]));
         break;
       }
-      const int last = x.last;
-      if (x.seg != seg) {
-        seg = x.seg;
-        if (!warp_wait(smem_u32(&sm.q_full), seg & 1, p.flags)) break;
-      }
+      if (marks & kFirst && !warp_wait(smem_u32(&sm.q_full), ++seg & 1, p.flags)) break;
       tc_fence_after();
       const uint64_t kdesc = kdesc0 + rk.at * (kTileBytes >> 4);
 #pragma unroll
@@ -750,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           part > 0 || kk > 0);
       commit_elect(el, smem_u32(&sm.s_full[rb.at]));
       commit_elect(el, smem_u32(&sm.k_empty[rk.at]));
-      if (t == last) commit_elect(el, smem_u32(&sm.q_free));
+      if (marks & kLast) commit_elect(el, smem_u32(&sm.q_free));
     }
     if (seg >= 0) {  // every MMA of this thread has finished before the tensor memory is released
       commit_elect(el, smem_u32(&sm.drain[0]));
@@ -763,15 +780,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc = idesc_f16_f32(128, kDim, true);
     // 128 dims = two 64-dim halves (the leading offset), 8-token groups 1 KB apart, 16 tokens = 2 KB
     const uint64_t vdesc0 = sdesc_mn_sw128(smem_u32(sm.v16[0][0]), kHalfBytes);
-    int seg = -1;
-    bool good = true;
+    bool good = true, any = false;
     Ring<kBars> rb, ru;    // tiles, halves
     Ring<kVBufs> rv;       // the halves' buffers
     for (int t = 0; good; ++t, rb.step()) {
       if (!warp_wait(smem_u32(&sm.v16_full[rv.at]), rv.phase, p.flags)) break;
-      const Tile& x = sm.tile[t % kRing];
-      if (x.end) break;
-      const int seg_t = x.seg;
+      const int marks = sm.tile[t % kRing].marks;
+      if (marks & kEnd) break;
       if (!warp_wait(smem_u32(&sm.p_full[rb.at]), rb.phase, p.flags)) break;
       const uint32_t pcol = tbase + kColS + kBlock * (rb.at < 3u ? rb.at : rb.at - 3u);
 #pragma unroll
@@ -785,28 +800,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           mma_f16_tmemA_elect(el, tbase + kColO, pcol + 64 * h + 8 * kk, vdesc + 128 * kk, idesc,
-                              seg_t == seg || h > 0 || kk > 0 ? 1u : 0u);
+                              !(marks & kFirst) || h > 0 || kk > 0 ? 1u : 0u);
         commit_elect(el, smem_u32(&sm.v16_free[ru.at]));
       }
+      any = true;  // (a half may be on its way)
       if (!good) break;
-      seg = seg_t;
       commit_elect(el, smem_u32(&sm.pv_done[rb.at]));
     }
-    if (seg >= 0) {
+    if (any) {
       commit_elect(el, smem_u32(&sm.drain[1]));
       warp_wait(smem_u32(&sm.drain[1]), 0, p.flags);
     }
     __syncwarp();
   } else if (warp < kSoftWarps) {
     // ================= softmax warps of set s: TMEM lane l = query row m of copy c, which takes
-    // tokens 128 c / C .. of every tile; this set's kN of them start at token k0
-    constexpr int kN = kMpad / 2;
+    // tokens 128 c / C .. of every tile. With one copy set s takes tiles s, s + 2, ..; with more both sets
+    // take every tile, half of a copy's tokens each. A thread has kN tokens from k0 on.
+    constexpr int kN = kTurns ? kMpad : kMpad / 2;
     const int s = warp / 4, quad = warp % 4;
-    const int l = 32 * quad + lane, m = l % kMpad, c = l / kMpad, k0 = c * kMpad + s * kN;
+    const int l = 32 * quad + lane, m = l % kMpad, c = l / kMpad, k0 = c * kMpad + (kTurns ? 0 : s * kN);
     const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
     const uint32_t p_off = 64u * (k0 / 64) + (k0 % 64) / 2;  // the weights' first column
     const int row = m / G;
-    float mref = -INFINITY, lrun = 0.f;  // the row's reference (both sets'), this set's sum
+    float mref = -INFINITY, lrun = 0.f;  // the row's reference at this set's last tile, this set's sum
     int seg = 0;
     uint32_t met_all = 0, met_set = 0;               // phases of the meeting points
     // A meeting of warps, bounded like every other wait: after a timeout anywhere each warp leaves
@@ -820,9 +836,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The segment's output or partial. Both sets take part: set s writes dims 64 s .. 64 s + 63.
     auto finish = [&](int k) -> bool {
       const Seg sg = sm.seg[k % kRing];
-      if (!warp_wait(smem_u32(&sm.pv_done[sg.last % kBars]), (sg.last / kBars) & 1, p.flags))
-        return false;
-      if (s == 0) sm.xm[l] = mref;
+      if (!warp_wait(smem_u32(&sm.pv_done[sg.last % kBars]), (sg.last / kBars) & 1, p.flags)) return false;
+      sm.xm[s][l] = mref;
       sm.xl[s][l] = lrun;
       if (!meet(&sm.sets_met, met_all)) return false;
       tc_fence_after();
@@ -830,12 +845,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto stats = [&](int mm, float& ref, float& sum) {
         ref = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < C; ++i) ref = fmaxf(ref, sm.xm[i * kMpad + mm]);
+        for (int i = 0; i < C; ++i) ref = fmaxf(ref, fmaxf(sm.xm[0][i * kMpad + mm], sm.xm[1][i * kMpad + mm]));
         const float r0 = ref == -INFINITY ? 0.f : ref;
         sum = 0.f;
 #pragma unroll
         for (int i = 0; i < C; ++i)
-          sum += (sm.xl[0][i * kMpad + mm] + sm.xl[1][i * kMpad + mm]) * ex2(sm.xm[i * kMpad + mm] - r0);
+          sum += sm.xl[0][i * kMpad + mm] * ex2(sm.xm[0][i * kMpad + mm] - r0) +
+                 sm.xl[1][i * kMpad + mm] * ex2(sm.xm[1][i * kMpad + mm] - r0);
       };
       const bool whole = sg.slot < 0;
       const bool nans = sm.nanany[k % kRows] != 0;
@@ -860,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       float my_ref, my_sum;
       stats(m, my_ref, my_sum);
-      const float w0 = ex2(mref - (my_ref == -INFINITY ? 0.f : my_ref));
+      const float w0 = ex2(fmaxf(sm.xm[0][l], sm.xm[1][l]) - (my_ref == -INFINITY ? 0.f : my_ref));
       if constexpr (C == 1) {  // a thread has its row's 64 dims of this set
 #pragma unroll 1
         for (int d = 64 * s; d < 64 * s + 64; d += 16) {
@@ -931,18 +947,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
 
+    int pos_max = 0;      // position of the thread's row, and its scores' factor but for the page's
+    float coef_q = 0.f;
     Ring<kBars> rb;
     for (int t = 0;; ++t, rb.step()) {
       if (!warp_wait(smem_u32(&sm.s_full[rb.at]), rb.phase, p.flags)) break;
-      const Tile& x = sm.tile[t % kRing];
-      if (x.end) break;
+      const int4 x = *reinterpret_cast<const int4*>(&sm.tile[t % kRing].page);
+      const float4 y = *reinterpret_cast<const float4*>(&sm.tile[t % kRing].kscale);
+      if (x.z & kEnd) break;
+      if (x.z & kFirst) {
+        pos_max = sm.seg[seg % kRing].pos + row;
+        coef_q = p.sm_scale_log2 * (NP == 1 ? 1.f : sm.qscale[seg % kRows][l]);
+      }
+      if (kTurns && (t & 1) != s) {  // the other set's tile
+        if (x.z & kLast && !finish(seg++)) break;
+        continue;
+      }
       tc_fence_after();
-      const int pos_max = sm.seg[seg % kRing].pos + row, last = x.last;
-      const float coef_q = p.sm_scale_log2 * (NP == 1 ? 1.f : sm.qscale[seg % kRows][l]), lv = x.lv, iv = x.iv;
-      const bool full_vis = x.pos0 + kBlock - 1 <= pos_max - row;  // every token visible to every row
-      const int lim = pos_max - x.pos0 - k0;                        // token k0 + n visible iff n <= lim
+      const float lv = y.y, iv = y.z;
+      const bool full_vis = !(x.z & kPart) && x.y == kBlock;  // every token visible to every row
+      const int lim = pos_max - x.w - k0;                      // token k0 + n visible iff n <= lim
       // the floor keeps a masked score at -inf when a scale is 0
-      const float coef = fmaxf(coef_q * x.kscale, 1e-30f);
+      const float coef = fmaxf(coef_q * y.x, 1e-30f);
       const uint32_t s_cols = tbase + lane_base + kColS + kBlock * (rb.at < 3u ? rb.at : rb.at - 3u);
       // The loop bodies are short and run several times on purpose: the roles' code together is what
       // an SM's instruction cache has to hold, and fetching it was the bound when they were unrolled.
@@ -955,10 +981,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       float mx = -INFINITY;
       if (kCh > 1 && full_vis) {
-        float m0 = tmem_ld32_max(s_cols + k0), m1 = tmem_ld32_max(s_cols + k0 + 32);  // the TMEM load reduces
-        tc_wait_ld();
-        asm volatile("" : "+f"(m0), "+f"(m1));  // no use moves above the wait
-        mx = fmaxf(m0, m1);
+#pragma unroll 1
+        for (int ch = 0; ch < kCh; ch += 2) {  // the TMEM load reduces
+          float m0 = tmem_ld32_max(s_cols + k0 + 32 * ch), m1 = tmem_ld32_max(s_cols + k0 + 32 * ch + 32);
+          tc_wait_ld();
+          asm volatile("" : "+f"(m0), "+f"(m1));  // no use moves above the wait
+          mx = fmax3(mx, m0, m1);
+        }
       } else {
 #pragma unroll 1
         for (int ch = 0; ch < kCh; ++ch) {
@@ -973,19 +1002,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (kCh > 1) tc_wait_st();
       }
-      // the row's maximum over both sets; after the meeting nobody needs the scores that the weights of
-      // the other set go over
       float* hm = &sm.half_max[t & 1][0][0];
-      hm[128 * s + l] = mx;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.pair_met[quad]));
-      if (!warp_wait(smem_u32(&sm.pair_met[quad]), t & 1, p.flags)) break;
-      mx = fmaxf(mx, hm[128 * (s ^ 1) + l]);
+      float r_old = mref;
+      if constexpr (kTurns) {  // the reference goes from tile to tile and so from set to set
+        if (t > 0 && !warp_wait(smem_u32(&sm.row_told[quad]), (t - 1) & 1, p.flags)) break;
+        r_old = x.z & kFirst ? -INFINITY : sm.half_max[(t - 1) & 1][0][l];
+      } else {
+        // the row's maximum over both sets; after the meeting nobody needs the scores that the weights of
+        // the other set go over
+        hm[128 * s + l] = mx;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.row_told[quad]));
+        if (!warp_wait(smem_u32(&sm.row_told[quad]), t & 1, p.flags)) break;
+        mx = fmaxf(mx, hm[128 * (s ^ 1) + l]);
+      }
       // P is taken relative to a reference that moves only when the maximum passes it by more
       // than kRescaleLog2 (P stays within FP16); O / l does not depend on it
-      const float bmax = fmaf(mx, coef, lv), r_old = mref;
+      const float bmax = fmaf(mx, coef, lv);
       const bool move = bmax > r_old + kRescaleLog2 || (r_old == -INFINITY && bmax != -INFINITY);
       const float m_new = move ? bmax : r_old;
+      if constexpr (kTurns) {
+        hm[l] = m_new;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.row_told[quad]));
+      }
       const float ref = m_new == -INFINITY ? 0.f : m_new;
       const bool rescale = move && r_old != -INFINITY;
       const float off = lv - ref;
@@ -1003,7 +1043,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v[u]) : "f"(e.y), "f"(e.x));
         }
         lsum += acc.x + acc.y;
-        if constexpr (kStep == 32) tmem_st16(s_cols + p_off + 16 * ch, v);
+        if constexpr (kTurns) tmem_st16(s_cols + 64 * (ch >> 1) + 16 * (ch & 1), v);
+        else if constexpr (kStep == 32) tmem_st16(s_cols + p_off, v);
         else tmem_st8(s_cols + p_off, v);
       }
       // the weights of the tokens of other copies are 0: 16-column blocks (32 tokens each, block z at
@@ -1020,17 +1061,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float a = rescale ? ex2(r_old - ref) : 1.f;
 #pragma unroll 1
-        for (int qc = 2 * s; qc < 2 * s + 2; ++qc) {  // this set's half of the dims
-          tmem_scale32(tbase + lane_base + kColO + 32 * qc, a);
-        }
+        for (int d = kTurns ? 0 : 64 * s; d < (kTurns ? kDim : 64 * s + 64); d += 32)
+          tmem_scale32(tbase + lane_base + kColO + d, a);
       }
-      lrun = lrun * ex2(r_old - ref) + lsum * iv;  // r_old -inf: nothing summed yet
+      lrun = lrun * ex2(mref - ref) + lsum * iv;  // mref -inf: nothing summed yet
       mref = m_new;
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[rb.at]));
-      if (t == last && !finish(seg++)) break;
+      if (x.z & kLast && !finish(seg++)) break;
     }
   }
   tc_fence_before();
