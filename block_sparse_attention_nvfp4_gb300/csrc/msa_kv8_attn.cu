@@ -84,7 +84,7 @@ static_assert(kColO + kDim <= kTmemCols, "TMEM");
 constexpr float kRescaleLog2 = 8.f;                  // O is rescaled when the maximum grows by more than 2^8
 constexpr int kNoPos = 1 << 30;                      // position of a tile that nobody sees
 constexpr int kRedStride = 17;                       // floats of a lane's 16 dims in the copies' exchange
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 256, kMergeY = 8;      // CTAs that share an item's rows
 
 enum : int { kEnd = 1, kFirst = 2, kLast = 4, kPart = 8 };
 struct alignas(16) Tile {
@@ -136,10 +136,7 @@ struct Smem {
   uint64_t q_full, q_free, s_full[kBars], p_full[kBars], pv_done[kBars], v16_full[kVBufs], v16_free[kBars], drain[2];
   uint64_t row_told[4];                              // by quadrant: a tile's maxima or reference are there
   uint64_t sets_met, set_met[2];                     // the softmax warps of both sets, or of one, have come here
-  long long part[kThreads / 32];
-  long long lo, hi;
-  int start_b;
-  long long start_off;
+  long long part[kThreads / 32];                     // places on the line by warp's requests
   uint32_t taddr;
 };
 static_assert(sizeof(Smem<2>) + 1024 <= 227 * 1024, "shared memory a CTA may opt into");
@@ -315,11 +312,19 @@ __device__ __forceinline__ long long head_cost(const Kv8AttnParams& p, const Req
   return cost_before(p, q, n - 1) + kItemCost + tiles_of(p, q, n - 1);
 }
 
+// Whether a partial keeps its rows' two copies apart, for the merge to join. Four copies are joined by
+// the CTA: with few rows the partials are many, and the merge would read four times as many terms (one
+// token over 4,096 keys, 4 heads, 8 queries each: 16.7 us joined, 18.5 apart); two are not: 64 ragged
+// requests of up to 8 rows take 202 us joined and 195 apart.
+template <int C>
+constexpr bool kCopiesApart = C == 2;
+
 // C copies of the query rows down the MMA tile (128 / C rows each); NP = E4M3 parts of a query.
 template <int C, int NP>
 __global__ void __launch_bounds__(kThreads, 1)
     kv8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const Kv8AttnParams p) {
   constexpr int kMpad = 128 / C;
+  constexpr bool kApart = kCopiesApart<C>;
   constexpr bool kTurns = C == 1;  // the softmax sets take tiles in turn; otherwise they share every tile
   constexpr int kStages = Smem<NP>::kKStages, kVStages = Smem<NP>::kVStages;
   extern __shared__ uint8_t smem_raw[];
@@ -349,7 +354,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     init(sm.set_met, 2, 68, kSoftWarps / 2);
     init(sm.row_told, 4, 70, kTurns ? 1 : 2);
     if (tid < 96) mbar_fence_init();
-    if (tid == 0) sm.lo = sm.hi = 0;
   }
   for (int i = tid; i < kRows * kDim; i += kThreads) (&sm.nanpos[0][0])[i] = INT_MAX;
   if (tid < kRows) sm.nanany[tid] = 0;
@@ -357,58 +361,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kKWarp && lane == 0)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
 
-  // ---- this CTA's range of the line: every thread sums a run of requests
+  // ---- the line: every thread sums a run of requests; the K warp finds the CTA's range in the sums
+  const int per = (p.num_reqs + kThreads - 1) / kThreads;
+  long long* sums = reinterpret_cast<long long*>(sm.red[0]);  // inclusive within a warp (red has no use yet)
+  static_assert(sizeof(sm.red) >= kThreads * sizeof(long long), "");
   {
-    const int per = (p.num_reqs + kThreads - 1) / kThreads;
     const int b0 = tid * per < p.num_reqs ? tid * per : p.num_reqs;
     const int b1 = b0 + per < p.num_reqs ? b0 + per : p.num_reqs;
-    long long mine = 0;
+    long long incl = 0;
     for (int b = b0; b < b1; ++b) {
       Req q;
-      if (load_req(p, b, &q)) mine += p.num_kv_heads * head_cost(p, q);
+      if (load_req(p, b, &q)) incl += p.num_kv_heads * head_cost(p, q);
       else if (blockIdx.x == 0) set_flag(p.flags, kFlagBadLength);
     }
-    long long incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
       const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
       if (lane >= d) incl += o;
     }
+    sums[tid] = incl;
     if (lane == 31) sm.part[warp] = incl;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += sm.part[w];
-      total += sm.part[w];
-    }
-    // fewer tiles than CTAs: the last CTAs have none (a partial's continuation is in the next CTA)
-    long long lo = 0, hi = 0;
-    if (total < (1LL << 31)) {  // 32-bit division: this is on the way of the first copy
-      const uint32_t tot = static_cast<uint32_t>(total), use = tot < gridDim.x ? tot : gridDim.x;
-      if (blockIdx.x < use) {
-        const uint32_t per = tot / use, more = tot - per * use;  // the first `more` CTAs take one more
-        lo = per * blockIdx.x + (blockIdx.x < more ? blockIdx.x : more);
-        hi = lo + per + (blockIdx.x < more ? 1 : 0);
-      }
-    } else {
-      lo = total * blockIdx.x / gridDim.x;
-      hi = total * (blockIdx.x + 1) / gridDim.x;
-    }
-    long long at = before + incl - mine;
-    if (lo < hi && at <= lo && lo < at + mine) {  // the range starts among this thread's requests
-      for (int b = b0; b < b1; ++b) {
-        Req q;
-        const long long n = load_req(p, b, &q) ? p.num_kv_heads * head_cost(p, q) : 0;
-        if (lo < at + n) {
-          sm.start_b = b;
-          sm.start_off = lo - at;
-          break;
-        }
-        at += n;
-      }
-      sm.lo = lo;
-      sm.hi = hi;
-    }
   }
   fence_proxy_async_smem();
   tc_fence_before();
@@ -445,14 +417,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++t;
     };
 
-    long long left = sm.hi - sm.lo;
+    long long left = 0, start = 0;  // places in the range; the first one's offset in request b
+    int b = 0;
+    {
+      constexpr int kWarps = kThreads / 32;
+      long long incl = lane < kWarps ? sm.part[lane] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      const long long total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+      // fewer tiles than CTAs: the last CTAs have none (a partial's continuation is in the next CTA)
+      long long lo = 0, hi = 0;
+      if (total < (1LL << 31)) {  // 32-bit division: this is on the way of the first copy
+        const uint32_t tot = static_cast<uint32_t>(total), use = tot < gridDim.x ? tot : gridDim.x;
+        if (blockIdx.x < use) {
+          const uint32_t each = tot / use, more = tot - each * use;  // the first `more` CTAs take one more
+          lo = each * blockIdx.x + (blockIdx.x < more ? blockIdx.x : more);
+          hi = lo + each + (blockIdx.x < more ? 1 : 0);
+        }
+      } else {
+        lo = total * blockIdx.x / gridDim.x;
+        hi = total * (blockIdx.x + 1) / gridDim.x;
+      }
+      left = hi - lo;
+      if (left > 0) {
+        // the warp whose requests hold place lo, then the thread, then the request
+        const int w = __ffs(__ballot_sync(0xFFFFFFFFu, lo < incl)) - 1;
+        const long long before = w > 0 ? __shfl_sync(0xFFFFFFFFu, incl, w - 1) : 0;
+        const long long mine = before + sums[32 * w + lane];
+        const int th = __ffs(__ballot_sync(0xFFFFFFFFu, lo < mine)) - 1;
+        long long at = th > 0 ? __shfl_sync(0xFFFFFFFFu, mine, th - 1) : before;
+        b = (32 * w + th) * per;
+        for (int i = 1; i < per && b + 1 < p.num_reqs; ++i) {
+          Req q;
+          const long long n = load_req(p, b, &q) ? p.num_kv_heads * head_cost(p, q) : 0;
+          if (lo < at + n) break;
+          at += n;
+          ++b;
+        }
+        start = lo - at;
+      }
+    }
     if (left > 0) {
-      int b = sm.start_b;
       Req q;
       load_req(p, b, &q);
       int h, ch, at, n_ch = chunks_of(p, q.R);  // at: the CTA's place in the item
       {
-        const long long hc = head_cost(p, q), start = sm.start_off;
+        const long long hc = head_cost(p, q);
         h = start < (1LL << 31) && hc < (1LL << 31)
                 ? static_cast<int>(static_cast<uint32_t>(start) / static_cast<uint32_t>(hc))
                 : static_cast<int>(start / hc);
@@ -858,8 +871,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int M = G * sg.rows;
       float* part = reinterpret_cast<float*>(p.parts + headers_bytes(gridDim.x)) +
                     (2LL * blockIdx.x + (whole ? 0 : sg.slot)) * kPartFloats;
-      // Four dims from d on of row mm, not yet divided by the sum.
-      auto put = [&](int mm, int d, float4 y, float sum) {
+      // Four dims from d on of row mm, not yet divided by the sum: to the output, or to row `at` of the partial.
+      auto put = [&](int mm, int at, int d, float4 y, float sum) {
         const float inv = !whole ? 1.f : (sum == 0.f ? 0.f : 1.f / sum);
         float* f = reinterpret_cast<float*>(&y);
 #pragma unroll
@@ -871,13 +884,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           const long long orow = static_cast<long long>(sg.row0 + mm / G) * (p.num_kv_heads * G) + sg.head * G + mm % G;
           *reinterpret_cast<uint2*>(p.out + orow * kDim + d) = make_uint2(bf16x2_bits(y.x, y.y), bf16x2_bits(y.z, y.w));
         } else {
-          *reinterpret_cast<float4*>(part + mm * kDim + d) = y;
+          *reinterpret_cast<float4*>(part + at * kDim + d) = y;
         }
       };
-      float my_ref, my_sum;
-      stats(m, my_ref, my_sum);
-      const float w0 = ex2(fmaxf(sm.xm[0][l], sm.xm[1][l]) - (my_ref == -INFINITY ? 0.f : my_ref));
-      if constexpr (C == 1) {  // a thread has its row's 64 dims of this set
+      auto put_lse = [&](float ref, float sum) {
+        if (p.lse != nullptr)
+          p.lse[static_cast<long long>(sg.row0 + row) * (p.num_kv_heads * G) + sg.head * G + m % G] =
+              sum == 0.f ? -INFINITY : ((ref == -INFINITY ? 0.f : ref) + log2f(sum)) * 0.69314718055994531f;
+      };
+      const float copy_ref = fmaxf(sm.xm[0][l], sm.xm[1][l]);  // of this copy's tokens
+      if (C == 1 || (kApart && !whole)) {  // a thread has 64 dims of its row's copy
+        const float r0 = copy_ref == -INFINITY ? 0.f : copy_ref;
+        const float sum = sm.xl[0][l] * ex2(sm.xm[0][l] - r0) + sm.xl[1][l] * ex2(sm.xm[1][l] - r0);
 #pragma unroll 1
         for (int d = 64 * s; d < 64 * s + 64; d += 16) {
           uint32_t a[16];
@@ -886,10 +904,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (m < M)
 #pragma unroll
             for (int u = 0; u < 16; u += 4)
-              put(m, d + u, make_float4(w0 * __uint_as_float(a[u]), w0 * __uint_as_float(a[u + 1]),
-                                        w0 * __uint_as_float(a[u + 2]), w0 * __uint_as_float(a[u + 3])), my_sum);
+              put(m, l, d + u, make_float4(__uint_as_float(a[u]), __uint_as_float(a[u + 1]), __uint_as_float(a[u + 2]),
+                                           __uint_as_float(a[u + 3])), sum);
         }
-      } else {
+        if (m < M && s == 0) {
+          if (whole) {
+            put_lse(copy_ref, sum);
+          } else {
+            part[128 * kDim + l] = copy_ref;
+            part[128 * kDim + 128 + l] = sum;
+          }
+        }
+      } else if constexpr (C > 1) {
+        float my_ref, my_sum;
+        stats(m, my_ref, my_sum);
+        const float w0 = ex2(copy_ref - (my_ref == -INFINITY ? 0.f : my_ref));
         // Copy c finishes dims kD c .. of this set's 64: in round r every lane hands 16 dims to copy
         // c + r and takes 16 from copy c - r, in a fixed order.
         constexpr int kD = 64 / C;
@@ -924,15 +953,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (m < M)
 #pragma unroll
           for (int u = 0; u < kD; u += 4)
-            put(m, 64 * s + kD * c + u, make_float4(y[u], y[u + 1], y[u + 2], y[u + 3]), my_sum);
-      }
-      if (m < M && s == 0 && c == 0) {
-        if (!whole) {
-          part[128 * kDim + m] = my_ref;
-          part[128 * kDim + 128 + m] = my_sum;
-        } else if (p.lse != nullptr) {
-          p.lse[static_cast<long long>(sg.row0 + row) * (p.num_kv_heads * G) + sg.head * G + m % G] =
-              my_sum == 0.f ? -INFINITY : ((my_ref == -INFINITY ? 0.f : my_ref) + log2f(my_sum)) * 0.69314718055994531f;
+            put(m, m, 64 * s + kD * c + u, make_float4(y[u], y[u + 1], y[u + 2], y[u + 3]), my_sum);
+        if (m < M && s == 0 && c == 0) {
+          if (whole) {
+            put_lse(my_ref, my_sum);
+          } else {
+            part[128 * kDim + m] = my_ref;
+            part[128 * kDim + 128 + m] = my_sum;
+          }
         }
       }
       // O, the exchange and the NaN marks are free again
@@ -1082,9 +1110,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partials of an item that starts in CTA blockIdx.x's range and ends in a later one's
-// (log-sum-exp, partials in tile order). A warp takes a query row, 4 dims per lane; with more than
-// 8 partials four warps share a row, every fourth partial each, and the first adds their sums.
-__global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnParams p, int grid) {
+// (log-sum-exp), partials in tile order and each one's copies of a row in turn. A warp takes a query
+// row, 4 dims per lane; with more than 8 terms the CTA's 8 warps share a row, every eighth term each,
+// and the first adds their sums.
+__global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnParams p, int grid, int copies_log2) {
   constexpr int kWarps = kMergeThreads / 32;
   __shared__ float4 part_o[kWarps][32];
   __shared__ float part_l[kWarps];
@@ -1103,32 +1132,48 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnP
   }
   if (cta + n > grid) n = grid - cta;
   const float* parts = reinterpret_cast<const float*>(p.parts + headers_bytes(grid));
-  auto part = [&](int i) { return parts + (i == 0 ? 2LL * cta + 1 : 2LL * (cta + i)) * kPartFloats; };
-  const int rows = me.rows * p.q_per_kv;
-  const int share = n > 8 ? 4 : 1, per = kWarps / share;  // warps of a row, rows at a time
+  auto part = [&](int e) {
+    const int i = e >> copies_log2;
+    return parts + (i == 0 ? 2LL * cta + 1 : 2LL * (cta + i)) * kPartFloats;
+  };
+  auto row = [&](int e, int m) { return (e & ((1 << copies_log2) - 1)) * (128 >> copies_log2) + m; };
+  const int rows = me.rows * p.q_per_kv, terms = n << copies_log2;
+  const int share = terms > 8 ? kWarps : 1, per = kWarps / share;  // warps of a row, rows at a time
   for (int m0 = per * blockIdx.y; m0 < rows; m0 += per * gridDim.y) {
     const int m = m0 + warp / share, first = warp % share;
     float lt = 0.f, ref = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (m < rows) {
       float mt = -INFINITY;
-      for (int i = lane; i < n; i += 32) mt = fmaxf(mt, part(i)[128 * kDim + m]);
+      for (int e = lane; e < terms; e += 32) mt = fmaxf(mt, part(e)[128 * kDim + row(e, m)]);
 #pragma unroll
       for (int d = 16; d; d /= 2) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, d));
       ref = mt == -INFINITY ? 0.f : mt;
+      // a lane has one term's weight and sum; the warp then adds the terms' rows one after the other
+      for (int base = first; base < terms; base += 32 * share) {
+        const int e = base + lane * share;
+        float w = 0.f;
+        if (e < terms) {
+          const float* q = part(e) + 128 * kDim + row(e, m);
+          w = ex2(q[0] - ref);
+          lt += w * q[128];
+        }
+        const int left = (terms - base + share - 1) / share, count = left < 32 ? left : 32;
 #pragma unroll 8
-      for (int i = first; i < n; i += share) {
-        const float* q = part(i);
-        const float w = ex2(q[128 * kDim + m] - ref);
-        const float4 x = *reinterpret_cast<const float4*>(q + m * kDim + 4 * lane);
-        lt += w * q[128 * kDim + 128 + m];
-        if (w != 0.f) {
-          o.x += w * x.x;
-          o.y += w * x.y;
-          o.z += w * x.z;
-          o.w += w * x.w;
+        for (int j = 0; j < count; ++j) {
+          const int ej = base + j * share;
+          const float4 x = *reinterpret_cast<const float4*>(part(ej) + row(ej, m) * kDim + 4 * lane);
+          const float wj = __shfl_sync(0xFFFFFFFFu, w, j);
+          if (wj != 0.f) {
+            o.x += wj * x.x;
+            o.y += wj * x.y;
+            o.z += wj * x.z;
+            o.w += wj * x.w;
+          }
         }
       }
+#pragma unroll
+      for (int d = 16; d; d /= 2) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, d);
     }
     if (share > 1) {
       part_o[warp][lane] = o;
@@ -1136,7 +1181,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnP
       __syncthreads();
       if (first == 0)
 #pragma unroll
-        for (int i = 1; i < 4; ++i) {
+        for (int i = 1; i < kWarps; ++i) {
           const float4 x = part_o[warp + i][lane];
           o.x += x.x;
           o.y += x.y;
@@ -1165,7 +1210,7 @@ cudaError_t launch(const CUtensorMap& kmap, const Kv8AttnParams& prm, int grid, 
   kv8_attn_kernel<C, NP><<<grid, kThreads, smem, st>>>(kmap, prm);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 16 / C);
+  cfg.gridDim = dim3(grid, kMergeY);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -1173,7 +1218,7 @@ cudaError_t launch(const CUtensorMap& kmap, const Kv8AttnParams& prm, int grid, 
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel, prm, grid);
+  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel, prm, grid, kCopiesApart<C> ? 1 : 0);
 }
 
 // Copies of the query rows that a request of max_rows rows (taken as a power of two) leaves room
