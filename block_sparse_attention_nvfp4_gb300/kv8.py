@@ -58,7 +58,8 @@ def _call(dev, stream, fn, what, *args):
 
 
 class _Handle:
-    """Tensors that are checked and marshalled once: setting an attribute marshals again."""
+    """Tensors that are checked and marshalled once: setting an attribute, or a tensor whose storage
+    has moved, marshals again."""
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
@@ -84,7 +85,8 @@ class KV8Batch(_Handle):
 def _geometry(batch, dev):
     """(B, rows, most rows per request, row length of the table, the three tensors' addresses)."""
     got = batch.__dict__.get("_marshalled")
-    if got is None or got[0] != dev:
+    if got is None or got[0] != dev or got[1][4] != batch.context_lens.data_ptr() or \
+            got[1][5] != batch.q_indptr.data_ptr() or got[1][6] != batch.block_table.data_ptr():
         B, M = batch.num_reqs, int(batch.block_table.shape[1])
         got = (dev, (B, int(batch.total_rows), int(batch.max_rows_per_req), M,
                      _plain(batch.context_lens, torch.int32, (B,), dev, "context_lens"),
@@ -121,7 +123,8 @@ class KV8Cache(_Handle):
     def _pointers(self):
         """(device, pages, KV heads, addresses of k_data, k_scale, v_data, v_scale)."""
         got = self.__dict__.get("_marshalled")
-        if got is None:
+        if got is None or got[3] != self.k_data.data_ptr() or got[4] != self.k_scale.data_ptr() or \
+                got[5] != self.v_data.data_ptr() or got[6] != self.v_scale.data_ptr():
             P, H, dev = self.num_pages, self.num_kv_heads, self.k_data.device
             codes = (torch.uint8, torch.float8_e4m3fn)
             got = (dev, P, H, _plain(self.k_data, codes, (P, H, BLOCK, DIM), dev, "k_data"),
@@ -171,7 +174,8 @@ class KV8Cache(_Handle):
 class KV8Attention:
     """Attention over a KV8Cache for a batch; owns its workspace and outputs (`out` BF16
     [rows, heads, 128], `lse` FP32 [rows, heads]). Single tokens, speculative rows and prompts
-    (causal) take the same call; a batch of the same sizes can be bound with `rebind`."""
+    (causal) take the same call; a batch of the same sizes can be bound with `rebind`, and tensors
+    that were replaced in the cache or in a KV8Batch are seen by the next call."""
 
     def __init__(self, cache: KV8Cache, batch: KV8Batch, sm_scale: Optional[float] = None, with_lse: bool = True):
         self.cache = cache
@@ -193,8 +197,10 @@ class KV8Attention:
 
     def rebind(self, batch: KV8Batch):
         """Point at another batch of the same sizes."""
-        dev, P, H, kd, ks, vd, vs = self.cache._pointers()
-        B, total, most, M, lens, indptr, table = _geometry(batch, dev)
+        self._cache_at = self.cache._pointers()
+        dev, P, H, kd, ks, vd, vs = self._cache_at
+        self._batch_at = _geometry(batch, dev)
+        B, total, most, M, lens, indptr, table = self._batch_at
         rows, heads = self.out.shape[:2]
         q = batch.q
         _need(q is not None and q.device == dev and q.shape == (rows, heads, DIM) and rows == total,
@@ -205,6 +211,8 @@ class KV8Attention:
         _need(old is None or (old.num_reqs, old.max_rows_per_req, old.max_pages_per_req) == (B, most, M),
               "rebind: expected a batch of the same sizes")
         self.batch = batch
+        self._held = (batch.q, batch.context_lens, batch.q_indptr, batch.block_table)   # as long as they are bound
+        self._follows = isinstance(batch, KV8Batch)
         self.args = _lib.Kv8AttnArgs(B, total, most, P, M, H, heads // H, 0, _Q_TYPES[q.dtype], float(self.sm_scale),
                                      _rows(q, heads, "q"), lens, indptr, table, None, q.data_ptr(), kd, ks, vd, vs,
                                      self.out.data_ptr(), self.lse.data_ptr() if self.lse is not None else None)
@@ -214,11 +222,17 @@ class KV8Attention:
         """softmax(sm_scale q k) v of every row over the keys it may see: of all blocks, or of
         those in block_ids (int32 [B, H, n <= 32], -1 = unused), e.g. the ones that
         MSADecoder.select_blocks chose. Returns `out`; `lse` has ln(sum(exp))."""
+        batch = self.batch
+        if self.cache._pointers() is not self._cache_at or (self._follows and (
+                _geometry(batch, self.device) is not self._batch_at or batch.q is not self._held[0] or
+                batch.q.data_ptr() != self.args.q)):
+            self.rebind(batch)
         a = self.args
         if block_ids is None:
             a.block_ids, a.n_block_ids = None, 0
         else:
             n = int(block_ids.shape[-1])
+            _need(n >= 1, "block_ids: expected at least one id (None: all blocks)")
             a.block_ids = _plain(block_ids, torch.int32, (a.num_reqs, a.num_kv_heads, n), self.device, "block_ids")
             a.n_block_ids = n
         _call(self.device, stream, _lib.load().msa_kv8_attn, "msa_kv8_attn", self._ref, self._ws[0], self._ws[1])

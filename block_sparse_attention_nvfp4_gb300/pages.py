@@ -13,7 +13,7 @@ from .kv8 import BLOCK, KV8Cache, _call, _need, _plain
 
 
 def _planes(cache, num_pages: int, dev):
-    """(data, strips, slot_bytes, page_bytes) of every plane of a cache."""
+    """(name, data, strips, slot_bytes, page_bytes) of every plane of a cache."""
     names = ("k_data", "k_scale", "v_data", "v_scale") + (("ki_data", "ki_scale") if isinstance(cache, KVCache) else ())
     for name in names:
         t = getattr(cache, name)
@@ -21,10 +21,10 @@ def _planes(cache, num_pages: int, dev):
         _need(t.shape[0] == num_pages, f"{name}: expected {num_pages} pages, got {t.shape[0]}")
         size = t.element_size()
         if t.dim() == 2:     # scales kept once for a page
-            yield t.data_ptr(), 0, 0, t.shape[1] * size
+            yield name, t.data_ptr(), 0, 0, t.shape[1] * size
         else:
             _need(t.shape[-2] == BLOCK, f"{name}: expected {BLOCK} slots in a page, got shape {tuple(t.shape)}")
-            yield t.data_ptr(), (t.shape[1] if t.dim() == 4 else 1), t.shape[-1] * size, 0
+            yield name, t.data_ptr(), (t.shape[1] if t.dim() == 4 else 1), t.shape[-1] * size, 0
 
 
 class PagePool:
@@ -33,7 +33,8 @@ class PagePool:
     seq_lens int32 [S], block_table int32 [S, M] and ref_counts int32 [P] are the caller's
     tensors (slices of them are the context_lens and block_table of a decode batch); the
     operators change them in place, in stream order. ref_counts[p] is the number of rows that
-    hold page p, 0 = free. Sequence and page lists are int32 CUDA tensors."""
+    hold page p, 0 = free. Sequence and page lists are int32 CUDA tensors. The tensors are bound when
+    the pool is made: after one is replaced every operator raises."""
 
     def __init__(self, caches: Sequence[Union[KVCache, KV8Cache]], seq_lens: torch.Tensor, block_table: torch.Tensor,
                  ref_counts: torch.Tensor):
@@ -46,11 +47,13 @@ class PagePool:
         a.seq_lens = _plain(seq_lens, torch.int32, (S,), dev, "seq_lens")
         a.block_table = _plain(block_table, torch.int32, (S, M), dev, "block_table")
         a.ref_counts = _plain(ref_counts, torch.int32, (P,), dev, "ref_counts")
-        planes = [x for c in self.caches for x in _planes(c, P, dev)]
+        planes = [(c, *x) for c in self.caches for x in _planes(c, P, dev)]
         _need(len(planes) <= _lib.MAX_PLANES, f"at most {_lib.MAX_PLANES} planes, got {len(planes)}")
         a.num_planes = len(planes)
-        for i, (data, strips, slot, page) in enumerate(planes):
+        for i, (_, _, data, strips, slot, page) in enumerate(planes):
             a.planes[i].data, a.planes[i].strips, a.planes[i].slot_bytes, a.planes[i].page_bytes = data, strips, slot, page
+        own = [(self, name, getattr(self, name).data_ptr()) for name in ("seq_lens", "block_table", "ref_counts")]
+        self._bound = [(o, name, getattr(o, name), at) for o, name, at in own + [x[:3] for x in planes]]
         n = ctypes.c_size_t(0)
         _lib._check(_lib.load().msa_pages_workspace_size(ctypes.byref(a), ctypes.byref(n)), "msa_pages_workspace_size")
         with torch.cuda.device(dev):
@@ -73,6 +76,9 @@ class PagePool:
         return t.data_ptr()
 
     def _run(self, name: str, stream, *args):
+        for owner, field, tensor, at in self._bound:
+            if getattr(owner, field) is not tensor or tensor.data_ptr() != at:
+                raise ValueError(f"{field}: was replaced after the pool was made")
         _call(self.device, stream, getattr(_lib.load(), name), name, self._ref, *args, *self._ws)
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor, tokens: Optional[torch.Tensor] = None, stream=None):

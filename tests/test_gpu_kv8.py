@@ -484,3 +484,73 @@ def test_chosen_blocks_then_attention():
     qv = batch.q.view(torch.float8_e4m3fn).double().view(-1, 4, 8, 128)
     ref = _kv8.attend(qv, cache, wl.context_lens, wl.q_indptr, wl.block_table, ids.cpu().numpy())
     _assert_attends(out, att.lse, ref)
+
+
+def test_attend_more_requests_than_threads():
+    """A thread of the planning code sums several requests; some have no row, some one token."""
+    rng = np.random.default_rng(5)
+    lens = [int(n) for n in rng.integers(0, 300, 1500)]
+    rows = [min(n, int(r)) for n, r in zip(lens, rng.integers(0, 3, 1500))]
+    _check_attend(lens, rows, 1, 4, "e4m3", seed=17)
+
+
+@pytest.mark.parametrize("lens,rows,H,G", [
+    ([4096, 4096, 900], [1, 1, 1], 4, 8),                # few rows: four copies of them in a tile
+    ([9000, 260, 3000], [8, 1, 5], 2, 8),                # two
+    ([5000, 300], [300, 300], 2, 8),                     # one: rows by chunks
+])
+@pytest.mark.parametrize("q_type", ["e4m3", "bf16"])
+def test_many_runs_give_the_same_bits(lens, rows, H, G, q_type):
+    cache, batch, *_ = _attn_case(lens, rows, H, G, q_type, 23)
+    att = KV8Attention(cache, batch)
+    first, lse = att.attend().clone(), att.lse.clone()
+    for _ in range(40):
+        att.out.fill_(7.0)
+        assert torch.equal(att.attend(), first) and torch.equal(att.lse, lse)
+    assert att.errors() == 0
+
+
+def test_two_calls_at_once():
+    """Two attentions, and an append to a third cache, in flight together on their own streams."""
+    a = _attn_case([6000, 900], [2, 8], 4, 8, "bf16", 31)
+    b = _attn_case([300, 2000], [300, 40], 4, 8, "e4m3", 32)
+    atts = [KV8Attention(x[0], x[1]) for x in (a, b)]
+    want = [(att.attend().clone(), att.lse.clone()) for att in atts]
+    lens, indptr, table, pages, x, planes = _append_case([700, 130, 2000], [3, 8, 1], 4, torch.bfloat16, 33)
+    caches = [KV8Cache(**{n: _cuda(p) for n, p in planes.items()}) for _ in range(2)]
+    kb = KV8Batch(_cuda(lens), _cuda(indptr), _cuda(table), total_rows=int(indptr[-1]), max_rows_per_req=8)
+    k, v, ws = x["k"].cuda(), x["v"].cuda(), _ws()
+    caches[0].append(kb, k, v, ws)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for att in atts:
+        att.out.zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for att, s in zip(atts, streams):
+            att.attend(stream=s)
+    caches[1].append(kb, k, v, ws, stream=streams[2])
+    torch.cuda.synchronize()
+    for att, (out, lse) in zip(atts, want):
+        assert torch.equal(att.out, out) and torch.equal(att.lse, lse) and att.errors() == 0
+    for n in planes:
+        assert torch.equal(getattr(caches[0], n), getattr(caches[1], n))
+    assert _lib.msa_get_error(ws) == 0
+
+
+def test_replaced_tensors_are_seen():
+    cache, batch, lens, indptr, table, qv, _ = _attn_case([900, 300], [2, 1], 2, 8, "bf16", 41)
+    att = KV8Attention(cache, batch)
+    att.attend()
+    batch.q = (batch.q.float() * -1.5).to(torch.bfloat16)
+    _assert_attends(att.attend(), att.lse, _kv8.attend(batch.q.double().view(qv.shape), cache, lens, indptr, table))
+    cache.k_data, cache.k_scale = cache.v_data.clone(), cache.v_scale.clone()
+    qv = batch.q.double().view(qv.shape)
+    _assert_attends(att.attend(), att.lse, _kv8.attend(qv, cache, lens, indptr, table))
+    batch.context_lens.data = _cuda(np.array([500, 300], np.int32))       # the same object, another storage
+    _assert_attends(att.attend(), att.lse, _kv8.attend(qv, cache, np.array([500, 300], np.int32), indptr, table))
+    with pytest.raises(ValueError):
+        att.attend(torch.zeros((2, 2, 0), dtype=torch.int32, device="cuda"))
+    batch.q = batch.q[:2]
+    with pytest.raises(ValueError):
+        att.attend()

@@ -318,3 +318,48 @@ def test_a_serving_run_over_the_8_bit_cache():
     step({0: 1, 2: 2, 4: 1, 5: 130})
     pool.free(_i32(0, 2, 4, 5))
     assert pool.errors() == 0 and torch.all(pool.ref_counts == 0)
+
+
+@pytest.mark.parametrize("S,pages", [(9000, 30000), (50, 5003)])
+def test_plans_over_large_pools(S, pages):
+    """More sequences and pages than one pass of the planning code takes; no cache bytes."""
+    rng = np.random.default_rng(S)
+    lens = [int(x) for x in rng.integers(0, 700 if S > 1000 else 9000, S)]
+    empty = [int(x) for x in rng.permutation(S)[:S // 3]]
+    for s in empty:
+        lens[s] = 0
+    pool, ref, dev = _state(None, pages, lens, 80, 5, shared=False)
+    others = np.array([s for s in range(S) if lens[s] > 0])
+    parents = [int(x) for x in rng.choice(others, len(empty))]
+    pool.fork(_i32(*parents), _i32(*empty))
+    ref.fork(parents, empty)
+    assert pool.errors() == 0
+    _same(pool, ref, dev)
+    rows = [int(x) for x in rng.permutation(S)[:S // 2]]
+    to = [min(int(ref.lens[s]) + int(rng.choice([0, 1, 130, 700])), 80 * 128) for s in rows]
+    pool.reserve(_i32(*rows), _i32(*to))
+    ref.reserve(rows, to)
+    assert pool.errors() == 0
+    _same(pool, ref, dev)
+    gone = [int(x) for x in rng.permutation(S)[:S // 2]]
+    pool.free(_i32(*gone))
+    ref.free(gone)
+    assert pool.errors() == 0
+    _same(pool, ref, dev)
+    live = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pool.compact(num_live=live)
+    assert int(live) == ref.compact()
+    assert pool.errors() == 0
+    _same(pool, ref, dev)
+
+
+def test_replaced_tensors_are_refused():
+    pool, ref, dev = _state("kv8", 20, [300, 0], 4, 3)
+    pool.fork(_i32(0), _i32(1))
+    pool.caches[0].k_data = pool.caches[0].k_data.clone()
+    with pytest.raises(ValueError):
+        pool.free(_i32(1))
+    pool, ref, dev = _state("kv8", 20, [300, 0], 4, 3)
+    pool.block_table = pool.block_table.clone()
+    with pytest.raises(ValueError):
+        pool.fork(_i32(0), _i32(1))
