@@ -83,7 +83,10 @@ constexpr uint32_t kColS = 0, kColO = kSBufs * kBlock, kTmemCols = 512;
 static_assert(kColO + kDim <= kTmemCols, "TMEM");
 constexpr float kRescaleLog2 = 8.f;                  // O is rescaled when the maximum grows by more than 2^8
 constexpr int kNoPos = 1 << 30;                      // position of a tile that nobody sees
-constexpr int kRedStride = 17;                       // floats of a lane's 16 dims in the copies' exchange
+// Exchange between the copies of a row: two copies hand over 16 dims of every lane at a time, four put
+// down whole rows, some at a time (floats of a lane or row, padded).
+constexpr int kHandStride = 17, kRedRows = 32, kRedStride = 68;
+static_assert(128 * kHandStride == kRedRows * kRedStride, "");
 constexpr int kMergeThreads = 256, kMergeY = 8;      // CTAs that share an item's rows
 
 enum : int { kEnd = 1, kFirst = 2, kLast = 4, kPart = 8 };
@@ -123,7 +126,7 @@ struct Smem {
   uint8_t k[kKStages][kTileBytes];                   // B of S (K-major), 128-byte swizzle
   uint8_t v[kVStages][kTileBytes];                   // V codes as they are in the page
   uint8_t v16[kVBufs][2][kHalfBytes];                // B of O (MN-major): [dim half][token][64 dims]
-  float red[2][128 * kRedStride];                    // by set: what the lanes hand to another copy
+  float red[2][kRedRows * kRedStride];               // by set: what the copies exchange
   float qscale[kRows][128];                          // 2^e of each tile row (BF16 queries)
   int nanpos[kRows][kDim];                           // first position with a NaN value in a dim, of partly seen tokens
   int nanany[kRows];
@@ -919,41 +922,85 @@ __global__ void __launch_bounds__(kThreads, 1)
         float my_ref, my_sum;
         stats(m, my_ref, my_sum);
         const float w0 = ex2(copy_ref - (my_ref == -INFINITY ? 0.f : my_ref));
-        // Copy c finishes dims kD c .. of this set's 64: in round r every lane hands 16 dims to copy
-        // c + r and takes 16 from copy c - r, in a fixed order.
-        constexpr int kD = 64 / C;
-        float* red = sm.red[s];
-        float y[kD];
+        if constexpr (C == 4) {
+          // Some rows at a time (one round for a decode step's few): every copy's lane puts its row's 64
+          // dims of this set down, then the set's threads add the copies up in a fixed order, 4 dims of
+          // a row each.
+          constexpr int kG = kRedRows / C;
+          float* red = sm.red[s];
+#pragma unroll 1
+          for (int g = 0; g < M; g += kG) {
+            if (g > 0 && !meet(&sm.set_met[s], met_set)) return false;  // the rows before have been read
+            const bool mine = m >= g && m < g + kG;
+            const uint32_t to = smem_u32(red + (c * kG + m - g) * kRedStride);
+#pragma unroll 1
+            for (int d = 0; d < 64; d += 16) {
+              uint32_t a[16];
+              tmem_ld16(tbase + lane_base + kColO + 64 * s + d, a);
+              tc_wait_ld();
+              if (mine)
 #pragma unroll
-        for (int ch = 0; ch < kD / 16; ++ch) {
-          uint32_t a[16];
-          tmem_ld16(tbase + lane_base + kColO + 64 * s + kD * c + 16 * ch, a);
-          tc_wait_ld();
+                for (int u = 0; u < 16; u += 4)
+                  st_shared_v4(to + 4u * (d + u), __float_as_uint(w0 * __uint_as_float(a[u])),
+                               __float_as_uint(w0 * __uint_as_float(a[u + 1])), __float_as_uint(w0 * __uint_as_float(a[u + 2])),
+                               __float_as_uint(w0 * __uint_as_float(a[u + 3])));
+            }
+            if (!meet(&sm.set_met[s], met_set)) return false;
+#pragma unroll 1
+            for (int i = l >> 4; i < kG && g + i < M; i += 8) {
+              const int d = 4 * (l & 15);
+              float4 y = *reinterpret_cast<const float4*>(red + i * kRedStride + d);
 #pragma unroll
-          for (int u = 0; u < 16; ++u) y[16 * ch + u] = w0 * __uint_as_float(a[u]);
-        }
-#pragma unroll
-        for (int step = 0; step < (C - 1) * (kD / 16); ++step) {
-          const int r = 1 + step / (kD / 16), ch = step % (kD / 16), to = (c + r) % C, from = (c + C - r) % C;
-          uint32_t a[16];
-          tmem_ld16(tbase + lane_base + kColO + 64 * s + kD * to + 16 * ch, a);
-          tc_wait_ld();
-          if (step > 0 && !meet(&sm.set_met[s], met_set)) return false;  // the last round's values are in y
-#pragma unroll
-          for (int u = 0; u < 16; ++u) red[l * kRedStride + u] = w0 * __uint_as_float(a[u]);
-          if (!meet(&sm.set_met[s], met_set)) return false;
-          float z = 0.f;
-#pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            y[16 * ch + u] += red[(from * kMpad + m) * kRedStride + u];
-            z = fmaxf(z, y[16 * ch + u]);
+              for (int z = 1; z < C; ++z) {
+                const float4 o = *reinterpret_cast<const float4*>(red + (z * kG + i) * kRedStride + d);
+                y.x += o.x;
+                y.y += o.y;
+                y.z += o.z;
+                y.w += o.w;
+              }
+              float ref, sum = 1.f;
+              if (whole) stats(g + i, ref, sum);
+              put(g + i, g + i, 64 * s + d, y, sum);
+            }
           }
-          sm.xm2[s][l] = z;  // (a store of what was read: the loads are over when the next meeting is reached)
-        }
-        if (m < M)
+        } else {
+          // Copy c finishes dims kD c .. of this set's 64: in round r every lane hands 16 dims to copy
+          // c + r and takes 16 from copy c - r, in a fixed order.
+          // (Rows at a time lose here: with up to 64 rows 64 ragged requests took 202 us against 196.)
+          constexpr int kD = 64 / C;
+          float* red = sm.red[s];
+          float y[kD];
 #pragma unroll
-          for (int u = 0; u < kD; u += 4)
-            put(m, m, 64 * s + kD * c + u, make_float4(y[u], y[u + 1], y[u + 2], y[u + 3]), my_sum);
+          for (int ch = 0; ch < kD / 16; ++ch) {
+            uint32_t a[16];
+            tmem_ld16(tbase + lane_base + kColO + 64 * s + kD * c + 16 * ch, a);
+            tc_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 16; ++u) y[16 * ch + u] = w0 * __uint_as_float(a[u]);
+          }
+#pragma unroll
+          for (int step = 0; step < (C - 1) * (kD / 16); ++step) {
+            const int r = 1 + step / (kD / 16), ch = step % (kD / 16), to = (c + r) % C, from = (c + C - r) % C;
+            uint32_t a[16];
+            tmem_ld16(tbase + lane_base + kColO + 64 * s + kD * to + 16 * ch, a);
+            tc_wait_ld();
+            if (step > 0 && !meet(&sm.set_met[s], met_set)) return false;  // the last round's values are in y
+#pragma unroll
+            for (int u = 0; u < 16; ++u) red[l * kHandStride + u] = w0 * __uint_as_float(a[u]);
+            if (!meet(&sm.set_met[s], met_set)) return false;
+            float z = 0.f;
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+              y[16 * ch + u] += red[(from * kMpad + m) * kHandStride + u];
+              z = fmaxf(z, y[16 * ch + u]);
+            }
+            sm.xm2[s][l] = z;  // (a store of what was read: the loads are over when the next meeting is reached)
+          }
+          if (m < M)
+#pragma unroll
+            for (int u = 0; u < kD; u += 4)
+              put(m, m, 64 * s + kD * c + u, make_float4(y[u], y[u + 1], y[u + 2], y[u + 3]), my_sum);
+        }
         if (m < M && s == 0 && c == 0) {
           if (whole) {
             put_lse(my_ref, my_sum);
@@ -1144,6 +1191,14 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnP
     float lt = 0.f, ref = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (m < rows) {
+      // rows on their way while the weights are found (one token over 4,096 keys 16.5 -> 15.5 us; 8 of them
+      // cost a prompt's many short joins 3 us)
+      constexpr int kAhead = 4;
+      float4 ahead[kAhead];
+      auto o_of = [&](int e) { return reinterpret_cast<const float4*>(part(e) + row(e, m) * kDim)[lane]; };
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (first + j * share < terms) ahead[j] = o_of(first + j * share);
       float mt = -INFINITY;
       for (int e = lane; e < terms; e += 32) mt = fmaxf(mt, part(e)[128 * kDim + row(e, m)]);
 #pragma unroll
@@ -1158,11 +1213,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnP
           w = ex2(q[0] - ref);
           lt += w * q[128];
         }
-        const int left = (terms - base + share - 1) / share, count = left < 32 ? left : 32;
-#pragma unroll 8
-        for (int j = 0; j < count; ++j) {
-          const int ej = base + j * share;
-          const float4 x = *reinterpret_cast<const float4*>(part(ej) + row(ej, m) * kDim + 4 * lane);
+        auto add = [&](const float4& x, int j) {
           const float wj = __shfl_sync(0xFFFFFFFFu, w, j);
           if (wj != 0.f) {
             o.x += wj * x.x;
@@ -1170,7 +1221,15 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnP
             o.z += wj * x.z;
             o.w += wj * x.w;
           }
+        };
+        const int left = (terms - base + share - 1) / share, count = left < 32 ? left : 32;
+        int j = 0;
+        if (base == first) {
+#pragma unroll
+          for (; j < kAhead; ++j) add(ahead[j], j);  // (weights past the last term are 0)
         }
+#pragma unroll 4
+        for (; j < count; ++j) add(o_of(base + j * share), j);
       }
 #pragma unroll
       for (int d = 16; d; d /= 2) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, d);
