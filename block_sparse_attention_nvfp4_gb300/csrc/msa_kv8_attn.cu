@@ -87,7 +87,7 @@ constexpr int kNoPos = 1 << 30;                      // position of a tile that 
 // down whole rows, some at a time (floats of a lane or row, padded).
 constexpr int kHandStride = 17, kRedRows = 32, kRedStride = 68;
 static_assert(128 * kHandStride == kRedRows * kRedStride, "");
-constexpr int kMergeThreads = 256, kMergeY = 8;      // CTAs that share an item's rows
+constexpr int kMergeThreads = 512, kMergeY = 4;      // CTAs that share an item, 32 dims each
 
 enum : int { kEnd = 1, kFirst = 2, kLast = 4, kPart = 8 };
 struct alignas(16) Tile {
@@ -155,6 +155,10 @@ struct Header {
   int pad[2];
 };
 constexpr long long kPartFloats = 128LL * kDim + 256;  // O, m, l
+// Where dims d .. d + 3 of row l of a partial's O are: 8 rows' 16-byte pieces side by side, so that
+// lanes with a row each and lanes with some rows and dims each both move whole lines. (Rows one after
+// the other cost the writer 32 lines a store: 3 us for 128 rows instead of 1.)
+__device__ __forceinline__ int part_at(int l, int d) { return (((l >> 3) * (kDim / 4) + (d >> 2)) * 8 + (l & 7)) * 4; }
 __host__ __device__ inline size_t headers_bytes(int grid) { return (grid * sizeof(Header) + 255) / 256 * 256; }
 
 // A bounded wait (kWaitLimitNs). A try suspends the warp for up to 20 us, so that waiting roles
@@ -874,20 +878,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int M = G * sg.rows;
       float* part = reinterpret_cast<float*>(p.parts + headers_bytes(gridDim.x)) +
                     (2LL * blockIdx.x + (whole ? 0 : sg.slot)) * kPartFloats;
-      // Four dims from d on of row mm, not yet divided by the sum: to the output, or to row `at` of the partial.
-      auto put = [&](int mm, int at, int d, float4 y, float sum) {
+      // 4 N dims from d on of row mm, not yet divided by the sum: to the output, or to row `at` of the partial.
+      auto put = [&](int mm, int at, int d, auto& f, float sum) {
+        constexpr int kF = sizeof(f) / sizeof(float);
         const float inv = !whole ? 1.f : (sum == 0.f ? 0.f : 1.f / sum);
-        float* f = reinterpret_cast<float*>(&y);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kF; ++u) {
           f[u] *= inv;
           if (nans && sm.nanpos[k % kRows][d + u] <= sg.pos + mm / G) f[u] = __int_as_float(0x7FFFFFFF);
         }
         if (whole) {
           const long long orow = static_cast<long long>(sg.row0 + mm / G) * (p.num_kv_heads * G) + sg.head * G + mm % G;
-          *reinterpret_cast<uint2*>(p.out + orow * kDim + d) = make_uint2(bf16x2_bits(y.x, y.y), bf16x2_bits(y.z, y.w));
+          uint16_t* to = p.out + orow * kDim + d;
+          if constexpr (kF % 8 == 0) {
+#pragma unroll
+            for (int u = 0; u < kF; u += 8)
+              *reinterpret_cast<uint4*>(to + u) = make_uint4(bf16x2_bits(f[u], f[u + 1]), bf16x2_bits(f[u + 2], f[u + 3]),
+                                                             bf16x2_bits(f[u + 4], f[u + 5]), bf16x2_bits(f[u + 6], f[u + 7]));
+          } else {
+            *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]));
+          }
         } else {
-          *reinterpret_cast<float4*>(part + at * kDim + d) = y;
+#pragma unroll
+          for (int u = 0; u < kF; u += 4)
+            *reinterpret_cast<float4*>(part + part_at(at, d + u)) = make_float4(f[u], f[u + 1], f[u + 2], f[u + 3]);
         }
       };
       auto put_lse = [&](float ref, float sum) {
@@ -904,11 +918,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t a[16];
           tmem_ld16(tbase + lane_base + kColO + d, a);
           tc_wait_ld();
-          if (m < M)
+          float f[16];
 #pragma unroll
-            for (int u = 0; u < 16; u += 4)
-              put(m, l, d + u, make_float4(__uint_as_float(a[u]), __uint_as_float(a[u + 1]), __uint_as_float(a[u + 2]),
-                                           __uint_as_float(a[u + 3])), sum);
+          for (int u = 0; u < 16; ++u) f[u] = __uint_as_float(a[u]);
+          if (m < M) put(m, l, d, f, sum);
         }
         if (m < M && s == 0) {
           if (whole) {
@@ -946,21 +959,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                                __float_as_uint(w0 * __uint_as_float(a[u + 3])));
             }
             if (!meet(&sm.set_met[s], met_set)) return false;
-#pragma unroll 1
-            for (int i = l >> 4; i < kG && g + i < M; i += 8) {
-              const int d = 4 * (l & 15);
-              float4 y = *reinterpret_cast<const float4*>(red + i * kRedStride + d);
+            static_assert(kG == 8, "");  // a thread has 4 dims of a row
+            const int i = l & 7, d = 4 * (l >> 3);
+            if (g + i < M) {
+              float f[4] = {};
 #pragma unroll
-              for (int z = 1; z < C; ++z) {
+              for (int z = 0; z < C; ++z) {
                 const float4 o = *reinterpret_cast<const float4*>(red + (z * kG + i) * kRedStride + d);
-                y.x += o.x;
-                y.y += o.y;
-                y.z += o.z;
-                y.w += o.w;
+                f[0] += o.x;
+                f[1] += o.y;
+                f[2] += o.z;
+                f[3] += o.w;
               }
               float ref, sum = 1.f;
               if (whole) stats(g + i, ref, sum);
-              put(g + i, g + i, 64 * s + d, y, sum);
+              put(g + i, g + i, 64 * s + d, f, sum);
             }
           }
         } else {
@@ -996,10 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             sm.xm2[s][l] = z;  // (a store of what was read: the loads are over when the next meeting is reached)
           }
-          if (m < M)
-#pragma unroll
-            for (int u = 0; u < kD; u += 4)
-              put(m, m, 64 * s + kD * c + u, make_float4(y[u], y[u + 1], y[u + 2], y[u + 3]), my_sum);
+          if (m < M) put(m, m, 64 * s + kD * c, y, my_sum);
         }
         if (m < M && s == 0 && c == 0) {
           if (whole) {
@@ -1157,13 +1167,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partials of an item that starts in CTA blockIdx.x's range and ends in a later one's
-// (log-sum-exp), partials in tile order and each one's copies of a row in turn. A warp takes a query
-// row, 4 dims per lane; with more than 8 terms the CTA's 8 warps share a row, every eighth term each,
-// and the first adds their sums.
-__global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnParams p, int grid, int copies_log2) {
-  constexpr int kWarps = kMergeThreads / 32;
-  __shared__ float4 part_o[kWarps][32];
-  __shared__ float part_l[kWarps];
+// (log-sum-exp), partials in tile order and each one's copies of a row in turn. CTA blockIdx.y has
+// dims 32 y .. 32 y + 31; a warp 8 rows and 16 dims, 4 dims of a row per lane. With at most 8 terms
+// the 8 pairs of warps take 8 rows each; with more they share 8 rows, every eighth term each, and
+// the first joins their sums. The terms come in runs of kRun whose loads are all in flight at once.
+__global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8AttnParams p, int grid, int copies_log2) {
+  constexpr int kPairs = kMergeThreads / 64;
+  __shared__ float4 part_o[kPairs][64];
+  __shared__ float part_l[kPairs][64], part_m[kPairs][64];
   pdl_wait_primary();
   const Header* hd = reinterpret_cast<const Header*>(p.parts);
   const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1185,79 +1196,82 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const Kv8AttnP
   };
   auto row = [&](int e, int m) { return (e & ((1 << copies_log2) - 1)) * (128 >> copies_log2) + m; };
   const int rows = me.rows * p.q_per_kv, terms = n << copies_log2;
-  const int share = terms > 8 ? kWarps : 1, per = kWarps / share;  // warps of a row, rows at a time
-  for (int m0 = per * blockIdx.y; m0 < rows; m0 += per * gridDim.y) {
-    const int m = m0 + warp / share, first = warp % share;
-    float lt = 0.f, ref = 0.f;
+  const bool shared = terms > kPairs;
+  const int pair = warp >> 1, d = 32 * blockIdx.y + 16 * (warp & 1) + 4 * (lane >> 3);
+  const int first = shared ? pair : 0, step = shared ? kPairs : 1;
+  for (int m0 = shared ? 0 : 8 * pair; m0 < rows; m0 += shared ? 8 : 8 * kPairs) {
+    const int m = m0 + (lane & 7);
+    const bool on = m < rows;
+    constexpr int kRun = 4;
+    float ref = -INFINITY, lt = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m < rows) {
-      // rows on their way while the weights are found (one token over 4,096 keys 16.5 -> 15.5 us; 8 of them
-      // cost a prompt's many short joins 3 us)
-      constexpr int kAhead = 4;
-      float4 ahead[kAhead];
-      auto o_of = [&](int e) { return reinterpret_cast<const float4*>(part(e) + row(e, m) * kDim)[lane]; };
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-        if (first + j * share < terms) ahead[j] = o_of(first + j * share);
-      float mt = -INFINITY;
-      for (int e = lane; e < terms; e += 32) mt = fmaxf(mt, part(e)[128 * kDim + row(e, m)]);
-#pragma unroll
-      for (int d = 16; d; d /= 2) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, d));
-      ref = mt == -INFINITY ? 0.f : mt;
-      // a lane has one term's weight and sum; the warp then adds the terms' rows one after the other
-      for (int base = first; base < terms; base += 32 * share) {
-        const int e = base + lane * share;
-        float w = 0.f;
-        if (e < terms) {
-          const float* q = part(e) + 128 * kDim + row(e, m);
-          w = ex2(q[0] - ref);
-          lt += w * q[128];
-        }
-        auto add = [&](const float4& x, int j) {
-          const float wj = __shfl_sync(0xFFFFFFFFu, w, j);
-          if (wj != 0.f) {
-            o.x += wj * x.x;
-            o.y += wj * x.y;
-            o.z += wj * x.z;
-            o.w += wj * x.w;
-          }
-        };
-        const int left = (terms - base + share - 1) / share, count = left < 32 ? left : 32;
-        int j = 0;
-        if (base == first) {
-#pragma unroll
-          for (; j < kAhead; ++j) add(ahead[j], j);  // (weights past the last term are 0)
-        }
-#pragma unroll 4
-        for (; j < count; ++j) add(o_of(base + j * share), j);
+    auto add = [&](float w, const float4& x, float l) {
+      lt += w * l;
+      if (w != 0.f) {
+        o.x += w * x.x;
+        o.y += w * x.y;
+        o.z += w * x.z;
+        o.w += w * x.w;
       }
+    };
+    auto lower = [&](float to) {  // everything so far relative to a larger reference
+      const float w = ref == to ? 1.f : ex2(ref - to), l = lt;
+      const float4 x = o;
+      lt = 0.f;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
+      add(w, x, l);
+      ref = to;
+    };
+    if (on)
+#pragma unroll 1
+      for (int e0 = first; e0 < terms; e0 += kRun * step) {
+        float4 x[kRun];
+        float mm[kRun], ll[kRun], top = ref;
 #pragma unroll
-      for (int d = 16; d; d /= 2) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, d);
-    }
-    if (share > 1) {
-      part_o[warp][lane] = o;
-      if (lane == 0) part_l[warp] = lt;
-      __syncthreads();
-      if (first == 0)
-#pragma unroll
-        for (int i = 1; i < kWarps; ++i) {
-          const float4 x = part_o[warp + i][lane];
-          o.x += x.x;
-          o.y += x.y;
-          o.z += x.z;
-          o.w += x.w;
-          lt += part_l[warp + i];
+        for (int j = 0; j < kRun; ++j) {
+          const int e = e0 + j * step;
+          mm[j] = -INFINITY;
+          if (e < terms) {
+            const float* q = part(e);
+            const int at = row(e, m);
+            x[j] = *reinterpret_cast<const float4*>(q + part_at(at, d));
+            mm[j] = q[128 * kDim + at];
+            ll[j] = q[128 * kDim + 128 + at];
+          }
         }
+#pragma unroll
+        for (int j = 0; j < kRun; ++j) top = fmaxf(top, mm[j]);
+        lower(top);
+        const float base = top == -INFINITY ? 0.f : top;  // nothing seen (a NaN sum still counts)
+#pragma unroll
+        for (int j = 0; j < kRun; ++j)
+          if (e0 + j * step < terms) add(ex2(mm[j] - base), x[j], ll[j]);
+      }
+    if (shared) {
+      const int at = 32 * (warp & 1) + lane;
+      part_o[pair][at] = o;
+      part_l[pair][at] = lt;
+      part_m[pair][at] = ref;
+      __syncthreads();
+      if (pair == 0) {
+        float top = ref;
+#pragma unroll
+        for (int i = 1; i < kPairs; ++i) top = fmaxf(top, part_m[i][at]);
+        lower(top);
+        const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int i = 1; i < kPairs; ++i) add(ex2(part_m[i][at] - base), part_o[i][at], part_l[i][at]);
+      }
     }
-    if (first == 0 && m < rows) {
+    if (first == 0 && on) {
       const float inv = lt == 0.f ? 0.f : 1.f / lt;
       const long long orow = static_cast<long long>(me.row0 + m / p.q_per_kv) * (p.num_kv_heads * p.q_per_kv) +
                              me.head * p.q_per_kv + m % p.q_per_kv;
-      *reinterpret_cast<uint2*>(p.out + orow * kDim + 4 * lane) =
+      *reinterpret_cast<uint2*>(p.out + orow * kDim + d) =
           make_uint2(bf16x2_bits(o.x * inv, o.y * inv), bf16x2_bits(o.z * inv, o.w * inv));
-      if (lane == 0 && p.lse != nullptr) p.lse[orow] = lt == 0.f ? -INFINITY : (ref + log2f(lt)) * 0.69314718055994531f;
+      if (d == 0 && p.lse != nullptr) p.lse[orow] = lt == 0.f ? -INFINITY : (ref + log2f(lt)) * 0.69314718055994531f;
     }
-    if (share > 1) __syncthreads();
+    if (shared) __syncthreads();
   }
 }
 
