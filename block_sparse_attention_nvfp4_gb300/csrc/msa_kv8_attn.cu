@@ -42,8 +42,9 @@
 //     rows' reference goes from set to set through shared memory. With more copies, where a row
 //     has few tokens, both sets share every tile: of the tokens that a copy takes, set 0 has the
 //     first half and set 1 the second, and the two threads of a row exchange their maxima.
-//     (One scheme for both: 2,053 rows on 16,421 tokens, 4 x 8 heads, BF16, take 488 us with shared
-//     tiles and 444 in turn; 64 ragged requests of up to 8 rows 202 us shared and 215 in turn.)
+//     (One scheme for both, measured when the rest was slower: 2,053 rows on 16,421 tokens, 4 x 8 heads,
+//     BF16, took 488 us with shared tiles and 444 in turn; 64 ragged requests of up to 8 rows 202 us
+//     shared and 215 in turn.)
 //
 // What bounds it now: the roles' instruction streams. A tile costs a CTA 1,750 to 2,000 cycles
 // whether its bytes come from HBM or L2, most of them the dependent instructions of a single warp
@@ -278,7 +279,9 @@ __device__ __forceinline__ uint32_t f32x2_e4m3x2(float a, float b) {  // a in th
 }
 
 // ---- the line of tiles
-constexpr int kItemCost = 4;
+// Places of an item before its tiles. 64 ragged requests / 16 requests with 16 listed blocks each take
+// 191 / 25.1 us with 4 places, 185 / 24.9 with 5, 180 / 26.1 with 6.
+constexpr int kItemCost = 5;
 struct Req {
   int N, R, r0;
 };
@@ -319,19 +322,11 @@ __device__ __forceinline__ long long head_cost(const Kv8AttnParams& p, const Req
   return cost_before(p, q, n - 1) + kItemCost + tiles_of(p, q, n - 1);
 }
 
-// Whether a partial keeps its rows' two copies apart, for the merge to join. Four copies are joined by
-// the CTA: with few rows the partials are many, and the merge would read four times as many terms (one
-// token over 4,096 keys, 4 heads, 8 queries each: 16.7 us joined, 18.5 apart); two are not: 64 ragged
-// requests of up to 8 rows take 202 us joined and 195 apart.
-template <int C>
-constexpr bool kCopiesApart = C == 2;
-
 // C copies of the query rows down the MMA tile (128 / C rows each); NP = E4M3 parts of a query.
 template <int C, int NP>
 __global__ void __launch_bounds__(kThreads, 1)
     kv8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const Kv8AttnParams p) {
   constexpr int kMpad = 128 / C;
-  constexpr bool kApart = kCopiesApart<C>;
   constexpr bool kTurns = C == 1;  // the softmax sets take tiles in turn; otherwise they share every tile
   constexpr int kStages = Smem<NP>::kKStages, kVStages = Smem<NP>::kVStages;
   extern __shared__ uint8_t smem_raw[];
@@ -878,8 +873,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int M = G * sg.rows;
       float* part = reinterpret_cast<float*>(p.parts + headers_bytes(gridDim.x)) +
                     (2LL * blockIdx.x + (whole ? 0 : sg.slot)) * kPartFloats;
-      // 4 N dims from d on of row mm, not yet divided by the sum: to the output, or to row `at` of the partial.
-      auto put = [&](int mm, int at, int d, auto& f, float sum) {
+      // 4 N dims from d on of row mm, not yet divided by the sum: to the output, or to the partial.
+      auto put = [&](int mm, int d, auto& f, float sum) {
         constexpr int kF = sizeof(f) / sizeof(float);
         const float inv = !whole ? 1.f : (sum == 0.f ? 0.f : 1.f / sum);
 #pragma unroll
@@ -901,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int u = 0; u < kF; u += 4)
-            *reinterpret_cast<float4*>(part + part_at(at, d + u)) = make_float4(f[u], f[u + 1], f[u + 2], f[u + 3]);
+            *reinterpret_cast<float4*>(part + part_at(mm, d + u)) = make_float4(f[u], f[u + 1], f[u + 2], f[u + 3]);
         }
       };
       auto put_lse = [&](float ref, float sum) {
@@ -910,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum == 0.f ? -INFINITY : ((ref == -INFINITY ? 0.f : ref) + log2f(sum)) * 0.69314718055994531f;
       };
       const float copy_ref = fmaxf(sm.xm[0][l], sm.xm[1][l]);  // of this copy's tokens
-      if (C == 1 || (kApart && !whole)) {  // a thread has 64 dims of its row's copy
+      if constexpr (C == 1) {  // a thread has 64 dims of its row
         const float r0 = copy_ref == -INFINITY ? 0.f : copy_ref;
         const float sum = sm.xl[0][l] * ex2(sm.xm[0][l] - r0) + sm.xl[1][l] * ex2(sm.xm[1][l] - r0);
 #pragma unroll 1
@@ -921,17 +916,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           float f[16];
 #pragma unroll
           for (int u = 0; u < 16; ++u) f[u] = __uint_as_float(a[u]);
-          if (m < M) put(m, l, d, f, sum);
+          if (m < M) put(m, d, f, sum);
         }
         if (m < M && s == 0) {
           if (whole) {
             put_lse(copy_ref, sum);
           } else {
-            part[128 * kDim + l] = copy_ref;
-            part[128 * kDim + 128 + l] = sum;
+            part[128 * kDim + m] = copy_ref;
+            part[128 * kDim + 128 + m] = sum;
           }
         }
-      } else if constexpr (C > 1) {
+      } else {
         float my_ref, my_sum;
         stats(m, my_ref, my_sum);
         const float w0 = ex2(copy_ref - (my_ref == -INFINITY ? 0.f : my_ref));
@@ -973,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               float ref, sum = 1.f;
               if (whole) stats(g + i, ref, sum);
-              put(g + i, g + i, 64 * s + d, f, sum);
+              put(g + i, 64 * s + d, f, sum);
             }
           }
         } else {
@@ -1009,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             sm.xm2[s][l] = z;  // (a store of what was read: the loads are over when the next meeting is reached)
           }
-          if (m < M) put(m, m, 64 * s + kD * c, y, my_sum);
+          if (m < M) put(m, 64 * s + kD * c, y, my_sum);
         }
         if (m < M && s == 0 && c == 0) {
           if (whole) {
@@ -1167,11 +1162,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partials of an item that starts in CTA blockIdx.x's range and ends in a later one's
-// (log-sum-exp), partials in tile order and each one's copies of a row in turn. CTA blockIdx.y has
-// dims 32 y .. 32 y + 31; a warp 8 rows and 16 dims, 4 dims of a row per lane. With at most 8 terms
-// the 8 pairs of warps take 8 rows each; with more they share 8 rows, every eighth term each, and
-// the first joins their sums. The terms come in runs of kRun whose loads are all in flight at once.
-__global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8AttnParams p, int grid, int copies_log2) {
+// (log-sum-exp), partials in tile order. CTA blockIdx.y has dims 32 y .. 32 y + 31; a warp 8 rows and
+// 16 dims, 4 dims of a row per lane. With at most 8 partials the 8 pairs of warps take 8 rows each; with
+// more they share 8 rows, every eighth partial each, and the first joins their sums.
+// Bound: latency (headers, then all of a run's loads at once) and the time to start 4 CTAs per SM:
+// runs of 4 in 64 registers measured best (one token over 4,096 keys: 14.7 us, runs of 8 in 128
+// registers 16.5).
+__global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8AttnParams p, int grid) {
   constexpr int kPairs = kMergeThreads / 64;
   __shared__ float4 part_o[kPairs][64];
   __shared__ float part_l[kPairs][64], part_m[kPairs][64];
@@ -1190,19 +1187,15 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8At
   }
   if (cta + n > grid) n = grid - cta;
   const float* parts = reinterpret_cast<const float*>(p.parts + headers_bytes(grid));
-  auto part = [&](int e) {
-    const int i = e >> copies_log2;
-    return parts + (i == 0 ? 2LL * cta + 1 : 2LL * (cta + i)) * kPartFloats;
-  };
-  auto row = [&](int e, int m) { return (e & ((1 << copies_log2) - 1)) * (128 >> copies_log2) + m; };
-  const int rows = me.rows * p.q_per_kv, terms = n << copies_log2;
-  const bool shared = terms > kPairs;
+  auto part = [&](int i) { return parts + (i == 0 ? 2LL * cta + 1 : 2LL * (cta + i)) * kPartFloats; };
+  const int rows = me.rows * p.q_per_kv;
+  const bool shared = n > kPairs;
   const int pair = warp >> 1, d = 32 * blockIdx.y + 16 * (warp & 1) + 4 * (lane >> 3);
   const int first = shared ? pair : 0, step = shared ? kPairs : 1;
   for (int m0 = shared ? 0 : 8 * pair; m0 < rows; m0 += shared ? 8 : 8 * kPairs) {
     const int m = m0 + (lane & 7);
     const bool on = m < rows;
-    constexpr int kRun = 4;
+    constexpr int kRun = 4;  // partials whose loads are in flight at once
     float ref = -INFINITY, lt = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float w, const float4& x, float l) {
@@ -1224,19 +1217,18 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8At
     };
     if (on)
 #pragma unroll 1
-      for (int e0 = first; e0 < terms; e0 += kRun * step) {
+      for (int e0 = first; e0 < n; e0 += kRun * step) {
         float4 x[kRun];
         float mm[kRun], ll[kRun], top = ref;
 #pragma unroll
         for (int j = 0; j < kRun; ++j) {
           const int e = e0 + j * step;
           mm[j] = -INFINITY;
-          if (e < terms) {
+          if (e < n) {
             const float* q = part(e);
-            const int at = row(e, m);
-            x[j] = *reinterpret_cast<const float4*>(q + part_at(at, d));
-            mm[j] = q[128 * kDim + at];
-            ll[j] = q[128 * kDim + 128 + at];
+            x[j] = *reinterpret_cast<const float4*>(q + part_at(m, d));
+            mm[j] = q[128 * kDim + m];
+            ll[j] = q[128 * kDim + 128 + m];
           }
         }
 #pragma unroll
@@ -1245,7 +1237,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8At
         const float base = top == -INFINITY ? 0.f : top;  // nothing seen (a NaN sum still counts)
 #pragma unroll
         for (int j = 0; j < kRun; ++j)
-          if (e0 + j * step < terms) add(ex2(mm[j] - base), x[j], ll[j]);
+          if (e0 + j * step < n) add(ex2(mm[j] - base), x[j], ll[j]);
       }
     if (shared) {
       const int at = 32 * (warp & 1) + lane;
@@ -1291,7 +1283,7 @@ cudaError_t launch(const CUtensorMap& kmap, const Kv8AttnParams& prm, int grid, 
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel, prm, grid, kCopiesApart<C> ? 1 : 0);
+  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel, prm, grid);
 }
 
 // Copies of the query rows that a request of max_rows rows (taken as a power of two) leaves room
