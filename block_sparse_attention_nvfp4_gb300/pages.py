@@ -3,6 +3,7 @@ without a synchronisation (msa_pages_* in include/msa.h)."""
 from __future__ import annotations
 
 import ctypes
+import operator
 from typing import Optional, Sequence, Union
 
 import torch
@@ -10,6 +11,9 @@ import torch
 from . import _lib
 from .api import KVCache
 from .kv8 import BLOCK, KV8Cache, _call, _need, _plain
+
+
+_data_ptr = torch.Tensor.data_ptr
 
 
 def _planes(cache, num_pages: int, dev):
@@ -52,8 +56,11 @@ class PagePool:
         a.num_planes = len(planes)
         for i, (_, _, data, strips, slot, page) in enumerate(planes):
             a.planes[i].data, a.planes[i].strips, a.planes[i].slot_bytes, a.planes[i].page_bytes = data, strips, slot, page
-        own = [(self, name, getattr(self, name).data_ptr()) for name in ("seq_lens", "block_table", "ref_counts")]
-        self._bound = [(o, name, getattr(o, name), at) for o, name, at in own + [x[:3] for x in planes]]
+        # (owner, its tensors' names, how to get them, where they were)
+        names = [(self, ("seq_lens", "block_table", "ref_counts"))]
+        names += [(c, tuple(dict.fromkeys(x[1] for x in planes if x[0] is c))) for c in self.caches]
+        self._bound = [(o, n, get, list(map(_data_ptr, get(o)))) for o, n, get in
+                       ((o, n, operator.attrgetter(*n)) for o, n in names)]
         n = ctypes.c_size_t(0)
         _lib._check(_lib.load().msa_pages_workspace_size(ctypes.byref(a), ctypes.byref(n)), "msa_pages_workspace_size")
         with torch.cuda.device(dev):
@@ -76,9 +83,10 @@ class PagePool:
         return t.data_ptr()
 
     def _run(self, name: str, stream, *args):
-        for owner, field, tensor, at in self._bound:
-            if getattr(owner, field) is not tensor or tensor.data_ptr() != at:
-                raise ValueError(f"{field}: was replaced after the pool was made")
+        for owner, names, get, at in self._bound:
+            now = list(map(_data_ptr, get(owner)))
+            if now != at:
+                raise ValueError(f"{names[[x == y for x, y in zip(now, at)].index(False)]}: was replaced after the pool was made")
         _call(self.device, stream, getattr(_lib.load(), name), name, self._ref, *args, *self._ws)
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor, tokens: Optional[torch.Tensor] = None, stream=None):
