@@ -472,8 +472,8 @@ msa_status msa_pages_workspace_size(const msa_page_pool* pool, size_t* bytes);
 /* Copy page src[i] to page dst[i] in every plane, i < n: the first tokens[i] slots of each
  * strip exactly (tokens NULL: all 128), and what the page keeps once. Reads and writes no
  * counts or tables (seq_lens, block_table and ref_counts may be NULL). A negative src or
- * dst skips the pair; so does src = dst; tokens outside 0 .. 128 set MSA_FLAG_BAD_LENGTH. Targets are distinct and no target is a source of
- * the same call (they would race). */
+ * dst skips the pair; so does src = dst; tokens outside 0 .. 128 set MSA_FLAG_BAD_LENGTH.
+ * Targets are distinct and no target is a source of the same call (they would race). */
 msa_status msa_pages_copy(const msa_page_pool* pool, int32_t n, const int32_t* src, const int32_t* dst,
                           const int32_t* tokens, void* ws, size_t ws_bytes, void* stream);
 
