@@ -554,3 +554,35 @@ def test_replaced_tensors_are_seen():
     batch.q = batch.q[:2]
     with pytest.raises(ValueError):
         att.attend()
+
+
+def test_offsets_past_32_bits():
+    """A cache of 4.6 GB a plane: the same tokens on its last pages give the same bits as on a small one."""
+    from block_sparse_attention_nvfp4_gb300 import PagePool
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB")
+    lens, rows = [900, 300], [900, 300]
+    lens, indptr, table, pages, x, planes = _append_case(lens, rows, 4, torch.bfloat16, 51)
+    k, v = x["k"].cuda(), x["v"].cuda()
+    q = torch.randn((3, 32, 128), device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(torch.bfloat16)
+    total = 70000
+    got = []
+    for size, first in ((pages, 0), (total, total - pages)):
+        cache = KV8Cache.empty(size, 4)
+        t = _cuda(np.where(table >= 0, table + first, table).astype(np.int32))
+        ws = _ws()
+        cache.append(KV8Batch(_cuda(lens), _cuda(indptr), t, total_rows=1200, max_rows_per_req=900), k, v, ws)
+        att = KV8Attention(cache, KV8Batch(_cuda(lens), _cuda(np.array([0, 2, 3], np.int32)), t, q, total_rows=3,
+                                           max_rows_per_req=2))
+        att.attend()
+        assert _lib.msa_get_error(ws) == 0 and att.errors() == 0
+        got.append([att.out, att.lse] + [getattr(cache, n)[first:].clone() for n in planes])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    pool = PagePool([cache], torch.zeros(1, dtype=torch.int32, device="cuda"),
+                    torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.zeros(total, dtype=torch.int32, device="cuda"))
+    pool.copy(_cuda(np.array([total - 1, total - pages], np.int32)), _cuda(np.array([total // 2, total - pages - 1], np.int32)))
+    for n in planes:
+        p = getattr(cache, n)
+        assert torch.equal(p[total // 2], p[total - 1]) and torch.equal(p[total - pages - 1], p[total - pages])
+    assert pool.errors() == 0
