@@ -166,39 +166,41 @@ constexpr long long kPartFloats = 128LL * kDim + 256;  // O, m, l
 __device__ __forceinline__ int part_at(int l, int d) { return (((l >> 3) * (kDim / 4) + (d >> 2)) * 8 + (l & 7)) * 4; }
 __host__ __device__ inline size_t headers_bytes(int grid) { return (grid * sizeof(Header) + 255) / 256 * 256; }
 
-// A bounded wait (kWaitLimitNs). A try suspends the warp for up to 20 us, so that waiting roles
-// leave the issue slots to the others; the timer is read once in 64 tries, because its latency
-// would otherwise be part of every hand-over.
+// A bounded wait: 2^31 cycles, about a second. A try suspends the warp for a while by itself.
 __device__ __forceinline__ bool try_bar(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(20000u)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
-static __device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, uint32_t* flags) {
-  long long t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    if (try_bar(bar, parity)) return true;
-    if ((i & 63u) == 0u) {
-      const long long now = global_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitLimitNs) {
-        set_flag(flags, kFlagTimeout);
-        return false;
-      }
-    }
-  }
-}
+constexpr uint32_t kWaitCycles = 0x7FFFFFFFu;
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t* flags) {
-  return try_bar(bar, parity) || wait_bar_slow(bar, parity, flags);
+  const uint32_t t0 = clock();
+  while (!try_bar(bar, parity))
+    if (static_cast<uint32_t>(clock()) - t0 > kWaitCycles) {
+      set_flag(flags, kFlagTimeout);
+      return false;
+    }
+  return true;
 }
-// The whole warp waits, converged (one lane asking for all leaves the others to a divergent
-// barrier, which wakes ~1,500 cycles late).
+// The whole warp waits, converged: its lanes vote on every try (one lane asking for all leaves the
+// others to a divergent barrier, which wakes ~1,500 cycles late). The loop stands in line: as a
+// function of its own, the call's registers cost the roles more than the code (64 ragged requests
+// 184 -> 171 us), and a loop without the clock's delay between tries takes the issue slots of the
+// working warps (275 us).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t* flags) {
-  return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, flags));
+  if (__all_sync(0xFFFFFFFFu, try_bar(bar, parity))) return true;
+  const uint32_t t0 = clock();
+  do {
+    if (__any_sync(0xFFFFFFFFu, static_cast<uint32_t>(clock()) - t0 > kWaitCycles)) {
+      set_flag(flags, kFlagTimeout);
+      return false;
+    }
+  } while (!__all_sync(0xFFFFFFFFu, try_bar(bar, parity)));
+  return true;
 }
 // The MMAs and commits with the election inside: the issuing warp stays converged, so that its
 // descriptors live in uniform registers (8 products issue in 260 cycles against 450 from a
