@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t dst = dst0 + rs.at * kTileBytes;
         const int rows = x.y - (lane >> 3);
         if (x.y == kBlock) {
-#pragma unroll 8
+#pragma unroll
           for (int i = 0; i < 32; ++i) cp_async16(dst + 512u * i, src + 512 * i, 16u);
         } else {
 #pragma unroll 1
@@ -721,6 +721,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(w & ~nan) : "memory");
         }
       }
+      // the half that was in this buffer (three halves ago) has been multiplied (waiting here and not
+      // with the converted values in registers: prompt 430 -> 398 us)
+      if (2 * t + h >= kVBufs && !(ub < 3u ? warp_wait(smem_u32(&sm.v16_free[ub + 3u]), uph ^ 1u, p.flags)
+                                           : warp_wait(smem_u32(&sm.v16_free[ub - 3u]), uph, p.flags)))
+        break;
       uint32_t f[4][8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -731,10 +736,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         e4m3x4_f16x4(b0, f[i][4], f[i][5]);
         e4m3x4_f16x4(b1, f[i][6], f[i][7]);
       }
-      // the half that was in this buffer (three halves ago) has been multiplied
-      if (2 * t + h >= kVBufs && !(ub < 3u ? warp_wait(smem_u32(&sm.v16_free[ub + 3u]), uph ^ 1u, p.flags)
-                                           : warp_wait(smem_u32(&sm.v16_free[ub - 3u]), uph, p.flags)))
-        break;
       if (end) {
         if (h == 0 && lane == 0) mbar_arrive(smem_u32(&sm.v16_full[uv]));
         break;
@@ -745,12 +746,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         st_shared_v4(dst + 2048u * i + o0, f[i][0], f[i][1], f[i][2], f[i][3]);
         st_shared_v4(dst + 2048u * i + o1, f[i][4], f[i][5], f[i][6], f[i][7]);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.v_empty[rs.at]));  // (the stores above have used every value)
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&sm.v16_full[uv]));
-        mbar_arrive(smem_u32(&sm.v_empty[rs.at]));  // (the stores above have used every value)
-      }
+      if (lane == 0) mbar_arrive(smem_u32(&sm.v16_full[uv]));
       uv = uv == 0u ? 2u : uv - 1u;  // + 2 mod 3
       ub += 2u;
       if (ub >= 6u) ub -= 6u, uph ^= 1u;
@@ -1068,11 +1068,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float mx = -INFINITY;
       if (kCh > 1 && full_vis) {
 #pragma unroll 1
-        for (int ch = 0; ch < kCh; ch += 2) {  // the TMEM load reduces
-          float m0 = tmem_ld32_max(s_cols + k0 + 32 * ch), m1 = tmem_ld32_max(s_cols + k0 + 32 * ch + 32);
+        for (int ch = 0; ch < kCh; ++ch) {  // the TMEM load reduces (two at a time spill: prompt 398 us, not 380)
+          float m0 = tmem_ld32_max(s_cols + k0 + 32 * ch);
           tc_wait_ld();
-          asm volatile("" : "+f"(m0), "+f"(m1));  // no use moves above the wait
-          mx = fmax3(mx, m0, m1);
+          asm volatile("" : "+f"(m0));  // no use moves above the wait
+          mx = fmaxf(mx, m0);
         }
       } else {
 #pragma unroll 1
