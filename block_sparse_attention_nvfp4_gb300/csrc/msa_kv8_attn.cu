@@ -16,10 +16,11 @@
 //
 // Floors: memory for few rows (a token and head is 256 bytes; the MMAs of a 128-token tile take
 // less than its copy), tensor and exponential rate for prompts. Measured on a GB300 (graph replays):
-//   one token over 4,096 keys, 4 x 8 heads, E4M3 queries                  14.7 us  (fixed costs)
-//   64 ragged requests, 512 .. 65,536 keys, up to 8 rows, BF16 queries   185 us   4.6 TB/s
-//   16 requests with 16 listed blocks each, 8 rows, E4M3 queries          24.8 us  1.4 TB/s
-//   2,053 rows on 16,421 keys, BF16 / E4M3 queries                      430 / 419 us  1.2 PFLOP/s
+//   one token over 4,096 keys, 4 x 8 heads, E4M3 queries                 14.6 us  (fixed costs)
+//   64 ragged requests, 512 .. 65,536 keys, up to 8 rows, BF16 queries   165 us   5.2 TB/s
+//   16 requests of one row over 16,384 keys, BF16 / E4M3 queries         59.5 / 57 us  4.5 TB/s
+//   16 requests with 16 listed blocks each, 8 rows, E4M3 queries         24.0 us  1.4 TB/s
+//   2,053 rows on 16,421 keys, BF16 / E4M3 queries                       372 / 364 us  1.4 PFLOP/s
 //
 // Work. An item is a (request, KV head, chunk of query rows); its tiles are the pages its
 // last row sees, or its block ids. All items' tiles form one line that the CTAs (one per SM)
@@ -39,7 +40,7 @@
 //   * V warp: copies the tiles' V codes (16-byte asynchronous copies, zeros past the context). K and
 //     V come by different paths: tensor and bulk copies alone measured 20-23 bytes a cycle and SM
 //     whatever is in flight, a tile's 32 KB then 1,400 cycles even from L2; both paths together 50;
-//   * 8 converting warps, four for each 64-token half of a tile: V to FP16 in three buffers that
+//   * 8 converting warps, four for each 64-token half of a tile: V to FP16 in four buffers that
 //     the halves take in turn; at a segment's first tile they also lay out its queries;
 //   * S warp (three score buffers in tensor memory) and P V warp (one O);
 //   * 8 softmax warps in two sets. With one copy (prompts) a set takes every other tile, and the
@@ -50,9 +51,11 @@
 //     BF16, took 488 us with shared tiles and 444 in turn; 64 ragged requests of up to 8 rows 202 us
 //     shared and 215 in turn.)
 //
-// What bounds it now: the roles' instruction streams. A tile costs a CTA 1,750 to 2,000 cycles
+// What bounds it now: the roles' instruction streams. A tile costs a CTA 1,600 to 1,800 cycles
 // whether its bytes come from HBM or L2, most of them the dependent instructions of a single warp
-// between two hand-overs (about 6 cycles each with five warps a scheduler).
+// between two hand-overs (about 6 cycles each with five warps a scheduler). What the loops hold in
+// registers and how long their code is count for more than the work in them: unrolling the reading
+// of a row's maximum four times costs a prompt 40 %.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -72,10 +75,10 @@ constexpr int kSoftWarps = 8;                        // warps 0..7: two sets of 
 constexpr int kMmaWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11;
 constexpr int kCvWarp0 = 12, kCvWarps = 8;           // two groups of 4
 constexpr int kThreads = (kCvWarp0 + kCvWarps) * 32;
-constexpr int kVBufs = 3;                            // FP16 halves of V
+constexpr int kVBufs = 4;                            // FP16 halves of V
 // A wait on a barrier's parity has to be for its current phase or the one before. Waiters that
-// fall behind therefore have barriers that go round 6 tiles or halves (no wait is 6 behind), or 12
-// tiles for a tile's description (up to 9 ahead).
+// fall behind therefore have barriers that go round 6 tiles or 8 halves (no wait is as far behind), or
+// 12 tiles for a tile's description (up to 9 ahead).
 constexpr int kBars = 6, kTold = 12;
 constexpr int kRing = 16;                            // tiles and segments whose description is kept
 constexpr int kRows = 8;                             // segments whose query scales and NaN marks are kept
@@ -126,7 +129,7 @@ struct Ring {
 
 template <int NP>
 struct Smem {
-  static constexpr int kKStages = 4, kVStages = NP == 1 ? 4 : 3;
+  static constexpr int kKStages = 3, kVStages = NP == 1 ? 4 : 3;
   uint8_t q[NP][kTileBytes];                         // A of S: copies of the query rows, by part
   uint8_t k[kKStages][kTileBytes];                   // B of S (K-major), 128-byte swizzle
   uint8_t v[kVStages][kTileBytes];                   // V codes as they are in the page
@@ -141,7 +144,7 @@ struct Smem {
   Seg seg[kRing];
   uint64_t k_full[kKStages], k_empty[kKStages], told[kTold];
   uint64_t v_full[kVStages], v_empty[kVStages];
-  uint64_t q_full, q_free, s_full[kBars], p_full[kBars], pv_done[kBars], v16_full[kVBufs], v16_free[kBars], drain[2];
+  uint64_t q_full, q_free, s_full[kBars], p_full[kBars], pv_done[kBars], v16_full[kVBufs], v16_free[2 * kVBufs], drain[2];
   uint64_t row_told[4];                              // by quadrant: a tile's maxima or reference are there
   uint64_t sets_met, set_met[2];                     // the softmax warps of both sets, or of one, have come here
   long long part[kThreads / 32];                     // places on the line by warp's requests
@@ -354,13 +357,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     init(sm.p_full, kBars, 42, kTurns ? kSoftWarps / 2 : kSoftWarps);
     init(sm.pv_done, kBars, 48, 1);
     init(sm.v16_full, kVBufs, 54, kCvWarps / 2);
-    init(sm.v16_free, kBars, 57, 1);
-    init(sm.drain, 2, 63, 1);
-    init(&sm.q_full, 1, 65, kCvWarps);
-    init(&sm.q_free, 1, 66, 1);
-    init(&sm.sets_met, 1, 67, kSoftWarps);
-    init(sm.set_met, 2, 68, kSoftWarps / 2);
-    init(sm.row_told, 4, 70, kTurns ? 1 : 2);
+    init(sm.v16_free, 2 * kVBufs, 58, 1);
+    init(sm.drain, 2, 66, 1);
+    init(&sm.q_full, 1, 68, kCvWarps);
+    init(&sm.q_free, 1, 69, 1);
+    init(&sm.sets_met, 1, 70, kSoftWarps);
+    init(sm.set_met, 2, 72, kSoftWarps / 2);
+    init(sm.row_told, 4, 74, kTurns ? 1 : 2);
     if (tid < 96) mbar_fence_init();
   }
   for (int i = tid; i < kRows * kDim; i += kThreads) (&sm.nanpos[0][0])[i] = INT_MAX;
@@ -619,15 +622,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================= converting warps: group h has tokens 64 h .. 64 h + 63 of every tile; thread =
     // one 16-byte piece of every 16th row
     const int h = (warp - kCvWarp0) / 4, r = (tid - kCvWarp0 * 32) & 127;
-    const int vr = r >> 3, vc = r & 7;  // V row (mod 16) and 16-byte piece
-    // 16 codes -> two 16-byte pieces of dim half vc / 4; the second half's threads store theirs the
-    // other way round, so that a row's 8 threads meet 8 different banks
-    const int flip = vc >> 2, ch = 2 * (vc & 3);
-    const uint32_t o0 = static_cast<uint32_t>((ch + flip) ^ (vr & 7)) << 4, o1 = o0 ^ 16u;
-    const uint32_t slot0 = smem_u32(sm.v[0]) + static_cast<uint32_t>(64 * kDim * h + 16 * r);
+    // V row (mod 16) and 16-byte piece: 16 codes become two 16-byte pieces of dim half vc / 4. The second
+    // half's threads take the row beside, so that 8 neighbours meet 8 different bank groups
+    const int vc = r & 7, vr = (r >> 3) ^ (vc >> 2);
+    const uint32_t o0 = static_cast<uint32_t>((2 * (vc & 3)) ^ (vr & 7)) << 4, o1 = o0 ^ 16u;
+    const uint32_t slot0 = smem_u32(sm.v[0]) + static_cast<uint32_t>(64 * kDim * h + kDim * vr + 16 * vc);
     int k = -1;                        // the segment
     Ring<kVStages> rs;
-    uint32_t uv = h, ub = h, uph = 0;  // half u = 2 t + h: u % 3, u % 6, (u / 6) % 2
     for (int t = 0;; ++t, rs.step()) {
       if (!warp_wait(smem_u32(&sm.v_full[rs.at]), rs.phase, p.flags)) break;
       const int4 x = *reinterpret_cast<const int4*>(&sm.tile[t % kRing].page);
@@ -721,26 +722,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(w & ~nan) : "memory");
         }
       }
-      // the half that was in this buffer (three halves ago) has been multiplied (waiting here and not
+      // the half that was in this buffer (four halves ago) has been multiplied (waiting here and not
       // with the converted values in registers: prompt 430 -> 398 us)
-      if (2 * t + h >= kVBufs && !(ub < 3u ? warp_wait(smem_u32(&sm.v16_free[ub + 3u]), uph ^ 1u, p.flags)
-                                           : warp_wait(smem_u32(&sm.v16_free[ub - 3u]), uph, p.flags)))
+      const uint32_t u = 2 * t + h, uv = u % kVBufs;
+      if (t >= 2 && !warp_wait(smem_u32(&sm.v16_free[(u - kVBufs) % (2 * kVBufs)]), ((u - kVBufs) / (2 * kVBufs)) & 1, p.flags))
         break;
       uint32_t f[4][8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint4 w = lds_u4(raw + 2048u * i);
-        const uint32_t a0 = flip ? w.z : w.x, a1 = flip ? w.w : w.y, b0 = flip ? w.x : w.z, b1 = flip ? w.y : w.w;
-        e4m3x4_f16x4(a0, f[i][0], f[i][1]);
-        e4m3x4_f16x4(a1, f[i][2], f[i][3]);
-        e4m3x4_f16x4(b0, f[i][4], f[i][5]);
-        e4m3x4_f16x4(b1, f[i][6], f[i][7]);
+        e4m3x4_f16x4(w.x, f[i][0], f[i][1]);
+        e4m3x4_f16x4(w.y, f[i][2], f[i][3]);
+        e4m3x4_f16x4(w.z, f[i][4], f[i][5]);
+        e4m3x4_f16x4(w.w, f[i][6], f[i][7]);
       }
       if (end) {
         if (h == 0 && lane == 0) mbar_arrive(smem_u32(&sm.v16_full[uv]));
         break;
       }
-      const uint32_t dst = smem_u32(sm.v16[uv][flip]) + static_cast<uint32_t>(vr) * 128u;
+      const uint32_t dst = smem_u32(sm.v16[uv][vc >> 2]) + static_cast<uint32_t>(vr) * 128u;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         st_shared_v4(dst + 2048u * i + o0, f[i][0], f[i][1], f[i][2], f[i][3]);
@@ -751,9 +751,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.v16_full[uv]));
-      uv = uv == 0u ? 2u : uv - 1u;  // + 2 mod 3
-      ub += 2u;
-      if (ub >= 6u) ub -= 6u, uph ^= 1u;
     }
   } else if (warp == kMmaWarp) {
     // ================= S warp: S_t = Q K_t^T into buffer t % 3
@@ -802,7 +799,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 128 dims = two 64-dim halves (the leading offset), 8-token groups 1 KB apart, 16 tokens = 2 KB
     const uint64_t vdesc0 = sdesc_mn_sw128(smem_u32(sm.v16[0][0]), kHalfBytes);
     bool good = true, any = false;
-    Ring<kBars> rb, ru;    // tiles, halves
+    Ring<kBars> rb;        // tiles
+    Ring<2 * kVBufs> ru;   // halves
     Ring<kVBufs> rv;       // the halves' buffers
     for (int t = 0; good; ++t, rb.step()) {
       if (!warp_wait(smem_u32(&sm.v16_full[rv.at]), rv.phase, p.flags)) break;
@@ -1295,8 +1293,8 @@ cudaError_t launch(const CUtensorMap& kmap, const Kv8AttnParams& prm, int grid, 
 
 // Copies of the query rows that a request of max_rows rows (taken as a power of two) leaves room
 // for, and the rows of a chunk. At 8 query rows (one token, 8 queries a head) 16 requests over 16,384
-// keys take 63.7 us with four copies, 67.8 with two, 71.9 with one; at up to 64 rows 64 ragged
-// requests take 185 us with two and 192 with one.
+// keys took 63.7 us with four copies, 67.8 with two, 71.9 with one; at up to 64 rows 64 ragged
+// requests 185 us with two and 192 with one.
 int copies_for(int max_rows, int q_per_kv) {
   long long r = 1;
   while (r < max_rows && r < 128) r *= 2;
