@@ -16,11 +16,12 @@
 //
 // Floors: memory for few rows (a token and head is 256 bytes; the MMAs of a 128-token tile take
 // less than its copy), tensor and exponential rate for prompts. Measured on a GB300 (graph replays):
-//   one token over 4,096 keys, 4 x 8 heads, E4M3 queries                 14.6 us  (fixed costs)
-//   64 ragged requests, 512 .. 65,536 keys, up to 8 rows, BF16 queries   165 us   5.2 TB/s
-//   16 requests of one row over 16,384 keys, BF16 / E4M3 queries         59.5 / 57 us  4.5 TB/s
-//   16 requests with 16 listed blocks each, 8 rows, E4M3 queries         24.0 us  1.4 TB/s
-//   2,053 rows on 16,421 keys, BF16 / E4M3 queries                       372 / 364 us  1.4 PFLOP/s
+//   64 requests of one row over 65,536 keys, 4 x 8 heads, E4M3 queries   658 us   6.5 TB/s
+//   64 of one row over 16,384 keys, BF16 / E4M3 queries             188 / 177 us  5.7 / 6.1 TB/s
+//   64 ragged requests, 512 .. 65,536 keys, up to 8 rows, BF16 queries   164 us   5.2 TB/s
+//   one token over 4,096 keys, E4M3 queries                             14.6 us  (fixed costs)
+//   16 requests with 16 listed blocks each, 8 rows, E4M3 queries        24.1 us  1.4 TB/s
+//   2,053 rows on 16,421 keys, BF16 / E4M3 queries                  373 / 366 us  1.4 PFLOP/s
 //
 // Work. An item is a (request, KV head, chunk of query rows); its tiles are the pages its
 // last row sees, or its block ids. All items' tiles form one line that the CTAs (one per SM)
@@ -51,11 +52,12 @@
 //     BF16, took 488 us with shared tiles and 444 in turn; 64 ragged requests of up to 8 rows 202 us
 //     shared and 215 in turn.)
 //
-// What bounds it now: the roles' instruction streams. A tile costs a CTA 1,600 to 1,800 cycles
-// whether its bytes come from HBM or L2, most of them the dependent instructions of a single warp
-// between two hand-overs (about 6 cycles each with five warps a scheduler). What the loops hold in
-// registers and how long their code is count for more than the work in them: unrolling the reading
-// of a row's maximum four times costs a prompt 40 %.
+// What bounds it now: long decode, memory (0.97 of the copy rate in the first line above; from L2 the
+// same work takes 565 us). Prompts, the roles' instruction streams: a tile costs a CTA about 1,780
+// cycles against 1,024 of tensor work with BF16 queries (768 with E4M3), most of them the dependent
+// instructions of single warps between two hand-overs. What the loops hold in registers and how long
+// their code is count for more there than the work in them: reading a row's maximum in a loop
+// unrolled four times costs a prompt 40 %.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -288,8 +290,8 @@ __device__ __forceinline__ uint32_t f32x2_e4m3x2(float a, float b) {  // a in th
 }
 
 // ---- the line of tiles
-// Places of an item before its tiles. 64 ragged requests / 16 requests with 16 listed blocks each take
-// 191 / 25.1 us with 4 places, 185 / 24.9 with 5, 180 / 26.1 with 6.
+// Places of an item before its tiles. When this was chosen 64 ragged requests / 16 requests with 16
+// listed blocks each took 191 / 25.1 us with 4 places, 185 / 24.9 with 5, 180 / 26.1 with 6.
 constexpr int kItemCost = 5;
 struct Req {
   int N, R, r0;
