@@ -18,10 +18,10 @@
 // less than its copy), tensor and exponential rate for prompts. Measured on a GB300 (graph replays):
 //   64 requests of one row over 65,536 keys, 4 x 8 heads, E4M3 queries   658 us   6.5 TB/s
 //   64 of one row over 16,384 keys, BF16 / E4M3 queries             188 / 177 us  5.7 / 6.1 TB/s
-//   64 ragged requests, 512 .. 65,536 keys, up to 8 rows, BF16 queries   164 us   5.2 TB/s
-//   one token over 4,096 keys, E4M3 queries                             14.6 us  (fixed costs)
-//   16 requests with 16 listed blocks each, 8 rows, E4M3 queries        24.1 us  1.4 TB/s
-//   2,053 rows on 16,421 keys, BF16 / E4M3 queries                  373 / 366 us  1.4 PFLOP/s
+//   64 ragged requests, 512 .. 65,536 keys, up to 8 rows, BF16 queries   162 us   5.3 TB/s
+//   one token over 4,096 keys, E4M3 queries                             14.5 us  (fixed costs)
+//   16 requests with 16 listed blocks each, 8 rows, E4M3 queries        23.1 us  1.5 TB/s
+//   2,053 rows on 16,421 keys, BF16 / E4M3 queries                  358 / 357 us  1.5 PFLOP/s
 //
 // Work. An item is a (request, KV head, chunk of query rows); its tiles are the pages its
 // last row sees, or its block ids. All items' tiles form one line that the CTAs (one per SM)
@@ -53,7 +53,7 @@
 //     shared and 215 in turn.)
 //
 // What bounds it now: long decode, memory (0.97 of the copy rate in the first line above; from L2 the
-// same work takes 565 us). Prompts, the roles' instruction streams: a tile costs a CTA about 1,780
+// same work takes 565 us). Prompts, the roles' instruction streams: a tile costs a CTA about 1,700
 // cycles against 1,024 of tensor work with BF16 queries (768 with E4M3), most of them the dependent
 // instructions of single warps between two hand-overs. What the loops hold in registers and how long
 // their code is count for more there than the work in them: reading a row's maximum in a loop
@@ -729,6 +729,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t u = 2 * t + h, uv = u % kVBufs;
       if (t >= 2 && !warp_wait(smem_u32(&sm.v16_free[(u - kVBufs) % (2 * kVBufs)]), ((u - kVBufs) / (2 * kVBufs)) & 1, p.flags))
         break;
+      if (end) {
+        if (h == 0 && lane == 0) mbar_arrive(smem_u32(&sm.v16_full[uv]));
+        break;
+      }
       uint32_t f[4][8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -738,21 +742,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         e4m3x4_f16x4(w.z, f[i][4], f[i][5]);
         e4m3x4_f16x4(w.w, f[i][6], f[i][7]);
       }
-      if (end) {
-        if (h == 0 && lane == 0) mbar_arrive(smem_u32(&sm.v16_full[uv]));
-        break;
-      }
       const uint32_t dst = smem_u32(sm.v16[uv][vc >> 2]) + static_cast<uint32_t>(vr) * 128u;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         st_shared_v4(dst + 2048u * i + o0, f[i][0], f[i][1], f[i][2], f[i][3]);
         st_shared_v4(dst + 2048u * i + o1, f[i][4], f[i][5], f[i][6], f[i][7]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.v_empty[rs.at]));  // (the stores above have used every value)
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.v16_full[uv]));
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&sm.v16_full[uv]));
+        mbar_arrive(smem_u32(&sm.v_empty[rs.at]));  // (the stores above have used every value)
+      }
     }
   } else if (warp == kMmaWarp) {
     // ================= S warp: S_t = Q K_t^T into buffer t % 3
@@ -766,11 +767,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(kBars == 2 * kSBufs, "");
     for (int t = 0;; ++t, rb.step(), rk.step()) {
       const uint32_t sb = rb.at < 3u ? rb.at : rb.at - 3u;
+      if (!warp_wait(smem_u32(&sm.k_full[rk.at]), rk.phase, p.flags)) break;
       // the buffer's previous weights (of tile t - 3) have been used
       if (t >= kSBufs)
         good = rb.at < 3u ? warp_wait(smem_u32(&sm.pv_done[rb.at + 3u]), rb.phase ^ 1u, p.flags)
                           : warp_wait(smem_u32(&sm.pv_done[rb.at - 3u]), rb.phase, p.flags);
-      if (!good || !warp_wait(smem_u32(&sm.k_full[rk.at]), rk.phase, p.flags)) break;
+      if (!good) break;
       const int marks = sm.tile[t % kRing].marks;
       if (marks & kEnd) {
         if (lane == 0) mbar_arrive(smem_u32(&sm.s_full[rb.at]));
@@ -1116,11 +1118,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool rescale = move && r_old != -INFINITY;
       const float off = lv - ref;
       const float2 coef2 = make_float2(coef, coef), off2 = make_float2(off, off);
-      float lsum = 0.f;
+      float2 acc = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int ch = 0; ch < kCh; ++ch) {
         if (kCh > 1) load(ch);
-        float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < kStep / 2; ++u) {  // scores -> columns of FP16 pairs
           const float2 d = __ffma2_rn(make_float2(__uint_as_float(v[2 * u]), __uint_as_float(v[2 * u + 1])), coef2, off2);
@@ -1128,7 +1129,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc = __fadd2_rn(acc, e);
           asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v[u]) : "f"(e.y), "f"(e.x));
         }
-        lsum += acc.x + acc.y;
         if constexpr (kTurns) tmem_st16(s_cols + 64 * (ch >> 1) + 16 * (ch & 1), v);
         else if constexpr (kStep == 32) tmem_st16(s_cols + p_off, v);
         else tmem_st8(s_cols + p_off, v);
@@ -1150,7 +1150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int d = kTurns ? 0 : 64 * s; d < (kTurns ? kDim : 64 * s + 64); d += 32)
           tmem_scale32(tbase + lane_base + kColO + d, a);
       }
-      lrun = lrun * ex2(mref - ref) + lsum * iv;  // mref -inf: nothing summed yet
+      lrun = lrun * ex2(mref - ref) + (acc.x + acc.y) * iv;  // mref -inf: nothing summed yet
       mref = m_new;
       tc_wait_st();
       tc_fence_before();
