@@ -660,6 +660,7 @@ msa_status msa_pages_compact(const msa_page_pool* a, int32_t* new_block_table, i
   const int row_units = (p.max_pages + kTableChunk - 1) / kTableChunk;
   const long long most = static_cast<long long>(p.num_seqs) * row_units +
                          static_cast<long long>(p.num_pages / 2 + 1) * p.chunks;
+  if (most == 0) return MSA_OK;  // neither sequences nor planes: only the counts move
   return launch_chained(compact_move_kernel, copy_grid(most, sms), st, p, l, new_block_table, row_units);
 }
 

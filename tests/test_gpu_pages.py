@@ -363,3 +363,17 @@ def test_replaced_tensors_are_refused():
     pool.block_table = pool.block_table.clone()
     with pytest.raises(ValueError):
         pool.fork(_i32(0), _i32(1))
+
+
+def test_a_pool_of_counts_alone():
+    """No sequences and no caches: compact moves the counts, the other operators have nothing to do."""
+    z = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    pool = PagePool([], none, torch.zeros((0, 3), dtype=torch.int32, device="cuda"), z(0, 2, 0, 1, 5))
+    live = z(-1)
+    pool.compact(num_live=live)
+    pool.fork(none, none)
+    pool.reserve(none, none)
+    pool.free(none)
+    pool.copy(none, none)
+    assert int(live) == 3 and pool.ref_counts.tolist() == [1, 2, 5, 0, 0] and pool.errors() == 0
