@@ -13,9 +13,6 @@ from .api import KVCache
 from .kv8 import BLOCK, KV8Cache, _call, _need, _plain
 
 
-_data_ptr = torch.Tensor.data_ptr
-
-
 def _planes(cache, num_pages: int, dev):
     """(name, data, strips, slot_bytes, page_bytes) of every plane of a cache."""
     names = ("k_data", "k_scale", "v_data", "v_scale") + (("ki_data", "ki_scale") if isinstance(cache, KVCache) else ())
@@ -56,11 +53,11 @@ class PagePool:
         a.num_planes = len(planes)
         for i, (_, _, data, strips, slot, page) in enumerate(planes):
             a.planes[i].data, a.planes[i].strips, a.planes[i].slot_bytes, a.planes[i].page_bytes = data, strips, slot, page
-        # (owner, its tensors' names, how to get them, where they were)
+        # (owner, its tensors' names, how to get them, the ones that are bound)
         names = [(self, ("seq_lens", "block_table", "ref_counts"))]
         names += [(c, tuple(dict.fromkeys(x[1] for x in planes if x[0] is c))) for c in self.caches]
-        self._bound = [(o, n, get, list(map(_data_ptr, get(o)))) for o, n, get in
-                       ((o, n, operator.attrgetter(*n)) for o, n in names)]
+        self._bound = [(o, n, operator.attrgetter(*n)) for o, n in names]
+        self._bound = [(o, n, get, get(o)) for o, n, get in self._bound]
         n = ctypes.c_size_t(0)
         _lib._check(_lib.load().msa_pages_workspace_size(ctypes.byref(a), ctypes.byref(n)), "msa_pages_workspace_size")
         with torch.cuda.device(dev):
@@ -76,17 +73,16 @@ class PagePool:
         return PagePool(caches, z(num_seqs), z(num_seqs, max_pages).fill_(-1), z(ref.shape[0]))
 
     def _list(self, t: torch.Tensor, n: int, name: str) -> int:
-        if t.dtype is not torch.int32 or t.get_device() != self._index or t.dim() != 1 or t.numel() != n or \
-                not t.is_contiguous():
+        if t.dtype is not torch.int32 or t.get_device() != self._index or t.shape != (n,) or not t.is_contiguous():
             raise ValueError(f"{name}: expected a contiguous int32 list of {n} on {self.device}, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
         return t.data_ptr()
 
     def _run(self, name: str, stream, *args):
-        for owner, names, get, at in self._bound:
-            now = list(map(_data_ptr, get(owner)))
-            if now != at:
-                raise ValueError(f"{names[[x == y for x, y in zip(now, at)].index(False)]}: was replaced after the pool was made")
+        for owner, names, get, bound in self._bound:
+            if not all(map(operator.is_, get(owner), bound)):
+                changed = [n for n, x, y in zip(names, get(owner), bound) if x is not y]
+                raise ValueError(f"{', '.join(changed)}: replaced after the pool was made")
         _call(self.device, stream, getattr(_lib.load(), name), name, self._ref, *args, *self._ws)
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor, tokens: Optional[torch.Tensor] = None, stream=None):
