@@ -196,11 +196,13 @@ class KV8Attention:
         self._ws = (self.ws.data_ptr(), self.ws.numel())
 
     def rebind(self, batch: KV8Batch):
-        """Point at another batch of the same sizes."""
-        self._cache_at = self.cache._pointers()
-        dev, P, H, kd, ks, vd, vs = self._cache_at
-        self._batch_at = _geometry(batch, dev)
-        B, total, most, M, lens, indptr, table = self._batch_at
+        """Point at another batch of the same sizes. One that does not fit raises, and what was bound
+        stays bound."""
+        cache_at = self.cache._pointers()
+        dev, P, H, kd, ks, vd, vs = cache_at
+        _need(dev == self.device, f"cache: expected it on {self.device}, got {dev}")
+        batch_at = _geometry(batch, dev)
+        B, total, most, M, lens, indptr, table = batch_at
         rows, heads = self.out.shape[:2]
         q = batch.q
         _need(q is not None and q.device == dev and q.shape == (rows, heads, DIM) and rows == total,
@@ -210,13 +212,17 @@ class KV8Attention:
         old = getattr(self, "args", None)
         _need(old is None or (old.num_reqs, old.max_rows_per_req, old.max_pages_per_req) == (B, most, M),
               "rebind: expected a batch of the same sizes")
-        self.batch = batch
-        self._held = (batch.q, batch.context_lens, batch.q_indptr, batch.block_table)   # as long as they are bound
-        self._follows = isinstance(batch, KV8Batch)
-        self.args = _lib.Kv8AttnArgs(B, total, most, P, M, H, heads // H, 0, _Q_TYPES[q.dtype], float(self.sm_scale),
-                                     _rows(q, heads, "q"), lens, indptr, table, None, q.data_ptr(), kd, ks, vd, vs,
-                                     self.out.data_ptr(), self.lse.data_ptr() if self.lse is not None else None)
-        self._ref = ctypes.byref(self.args)
+        args = _lib.Kv8AttnArgs(B, total, most, P, M, H, heads // H, 0, _Q_TYPES[q.dtype], float(self.sm_scale),
+                                _rows(q, heads, "q"), lens, indptr, table, None, q.data_ptr(), kd, ks, vd, vs,
+                                self.out.data_ptr(), self.lse.data_ptr() if self.lse is not None else None)
+        # Every check has passed. attend() compares these marks with the tensors: set earlier, they
+        # would hide from the call after a refused one that its arguments are still the old ones.
+        self._cache_at, self._batch_at = cache_at, batch_at
+        self.batch, self._follows = batch, isinstance(batch, KV8Batch)
+        c = self.cache
+        self._held = (batch.q, batch.context_lens, batch.q_indptr, batch.block_table,   # as long as they are bound
+                      c.k_data, c.k_scale, c.v_data, c.v_scale)
+        self.args, self._ref = args, ctypes.byref(args)
 
     def attend(self, block_ids: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """softmax(sm_scale q k) v of every row over the keys it may see: of all blocks, or of
