@@ -12,6 +12,8 @@ from . import _lib
 from .api import KVCache
 from .kv8 import BLOCK, KV8Cache, _call, _need, _plain
 
+_address = torch.Tensor.data_ptr
+
 
 def _planes(cache, num_pages: int, dev):
     """(name, data, strips, slot_bytes, page_bytes) of every plane of a cache."""
@@ -35,7 +37,7 @@ class PagePool:
     tensors (slices of them are the context_lens and block_table of a decode batch); the
     operators change them in place, in stream order. ref_counts[p] is the number of rows that
     hold page p, 0 = free. Sequence and page lists are int32 CUDA tensors. The tensors are bound when
-    the pool is made: after one is replaced every operator raises."""
+    the pool is made: after one is replaced, or its storage has moved, every operator raises."""
 
     def __init__(self, caches: Sequence[Union[KVCache, KV8Cache]], seq_lens: torch.Tensor, block_table: torch.Tensor,
                  ref_counts: torch.Tensor):
@@ -53,11 +55,11 @@ class PagePool:
         a.num_planes = len(planes)
         for i, (_, _, data, strips, slot, page) in enumerate(planes):
             a.planes[i].data, a.planes[i].strips, a.planes[i].slot_bytes, a.planes[i].page_bytes = data, strips, slot, page
-        # (owner, its tensors' names, how to get them, the ones that are bound)
+        # (owner, its tensors' names, how to get them, the ones that are bound, their addresses)
         names = [(self, ("seq_lens", "block_table", "ref_counts"))]
         names += [(c, tuple(dict.fromkeys(x[1] for x in planes if x[0] is c))) for c in self.caches]
         self._bound = [(o, n, operator.attrgetter(*n)) for o, n in names]
-        self._bound = [(o, n, get, get(o)) for o, n, get in self._bound]
+        self._bound = [(o, n, get, get(o), tuple(map(_address, get(o)))) for o, n, get in self._bound]
         n = ctypes.c_size_t(0)
         _lib._check(_lib.load().msa_pages_workspace_size(ctypes.byref(a), ctypes.byref(n)), "msa_pages_workspace_size")
         with torch.cuda.device(dev):
@@ -79,10 +81,12 @@ class PagePool:
         return t.data_ptr()
 
     def _run(self, name: str, stream, *args):
-        for owner, names, get, bound in self._bound:
-            if not all(map(operator.is_, get(owner), bound)):
-                changed = [n for n, x, y in zip(names, get(owner), bound) if x is not y]
-                raise ValueError(f"{', '.join(changed)}: replaced after the pool was made")
+        for owner, names, get, bound, at in self._bound:
+            now = get(owner)
+            # the same objects may have got other storages (set_, resize_, .data)
+            if not all(map(operator.is_, now, bound)) or tuple(map(_address, now)) != at:
+                changed = [n for n, x, y, a in zip(names, now, bound, at) if x is not y or _address(x) != a]
+                raise ValueError(f"{', '.join(changed)}: replaced or moved after the pool was made")
         _call(self.device, stream, getattr(_lib.load(), name), name, self._ref, *args, *self._ws)
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor, tokens: Optional[torch.Tensor] = None, stream=None):

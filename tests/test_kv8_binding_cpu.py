@@ -131,3 +131,26 @@ def test_a_refused_rebind_leaves_the_old_batch_bound(launches):
         att.rebind(KV8Batch(_i32(2), _i32(3), _i32(2, 9), batch.q, total_rows=3, max_rows_per_req=2))
     att.attend()
     assert att.batch is batch and _bound(launches[-1]) == _bound(launches[0])
+
+
+@pytest.mark.parametrize("name", ["seq_lens", "block_table", "ref_counts", "k_data", "v_scale"])
+def test_a_pool_refuses_tensors_whose_storage_moved(launches, monkeypatch, name):
+    cache = KV8Cache.empty(6, 2, device="cpu")
+    monkeypatch.setattr(pages, "_planes", lambda c, n, dev: [
+        (x, getattr(c, x).data_ptr(), 0, 0, 8) for x in ("k_data", "k_scale", "v_data", "v_scale")])
+    monkeypatch.setattr(PagePool, "_list", lambda self, t, n, name: t.data_ptr())
+    pool = PagePool([cache], _i32(3), _i32(3, 4), _i32(6))
+    seqs = _i32(2)
+    pool.free(seqs)
+    assert len(launches) == 1
+    t = getattr(pool, name) if hasattr(pool, name) else getattr(cache, name)
+    keep = t.data                                         # (the old storage stays allocated)
+    t.data = keep.clone()
+    for call in (lambda: pool.free(seqs), lambda: pool.copy(seqs, seqs), lambda: pool.fork(seqs, seqs),
+                 lambda: pool.reserve(seqs, seqs), pool.compact):
+        with pytest.raises(ValueError, match=name):
+            call()
+    assert len(launches) == 1
+    t.data = keep
+    pool.free(seqs)
+    assert len(launches) == 2
