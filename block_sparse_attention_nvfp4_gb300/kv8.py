@@ -175,7 +175,8 @@ class KV8Attention:
     """Attention over a KV8Cache for a batch; owns its workspace and outputs (`out` BF16
     [rows, heads, 128], `lse` FP32 [rows, heads]). Single tokens, speculative rows and prompts
     (causal) take the same call; a batch of the same sizes can be bound with `rebind`, and tensors
-    that were replaced in the cache or in a KV8Batch are seen by the next call."""
+    that were replaced in the cache or in the batch (a KV8Batch or a DecodeBatch) are seen by the
+    next call, which raises when they do not fit."""
 
     def __init__(self, cache: KV8Cache, batch: KV8Batch, sm_scale: Optional[float] = None, with_lse: bool = True):
         self.cache = cache
@@ -224,14 +225,25 @@ class KV8Attention:
                       c.k_data, c.k_scale, c.v_data, c.v_scale)
         self.args, self._ref = args, ctypes.byref(args)
 
+    def _batch_changed(self, batch) -> bool:
+        """Whether a tensor or a size of the bound batch is another than the bound one."""
+        a, held = self.args, self._held
+        if batch.q is not held[0] or batch.q.data_ptr() != a.q:
+            return True
+        if self._follows:
+            return _geometry(batch, self.device) is not self._batch_at
+        # a DecodeBatch keeps no marks of its own
+        t = (batch.context_lens, batch.q_indptr, batch.block_table)
+        return not (t[0] is held[1] and t[1] is held[2] and t[2] is held[3] and
+                    batch.total_rows == a.total_rows and batch.max_rows_per_req == a.max_rows_per_req and
+                    (t[0].data_ptr(), t[1].data_ptr(), t[2].data_ptr()) == self._batch_at[4:])
+
     def attend(self, block_ids: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """softmax(sm_scale q k) v of every row over the keys it may see: of all blocks, or of
         those in block_ids (int32 [B, H, n <= 32], -1 = unused), e.g. the ones that
         MSADecoder.select_blocks chose. Returns `out`; `lse` has ln(sum(exp))."""
         batch = self.batch
-        if self.cache._pointers() is not self._cache_at or (self._follows and (
-                _geometry(batch, self.device) is not self._batch_at or batch.q is not self._held[0] or
-                batch.q.data_ptr() != self.args.q)):
+        if self.cache._pointers() is not self._cache_at or self._batch_changed(batch):
             self.rebind(batch)
         a = self.args
         if block_ids is None:

@@ -154,3 +154,22 @@ def test_a_pool_refuses_tensors_whose_storage_moved(launches, monkeypatch, name)
     t.data = keep
     pool.free(seqs)
     assert len(launches) == 2
+
+
+def test_replaced_tensors_of_a_decode_batch_are_seen(launches):
+    cache = KV8Cache.empty(6, 2, device="cpu")
+    q = torch.zeros((3, 8, 128), dtype=torch.uint8)
+    batch = DecodeBatch(_i32(2), _i32(3), _i32(2, 4), q, torch.zeros((3, 4, 128), dtype=torch.uint8), 3, 2)
+    att = KV8Attention(cache, batch)
+    att.attend()
+    batch.q = torch.ones_like(q)
+    att.attend()
+    assert launches[-1].q == batch.q.data_ptr() != launches[0].q
+    batch.context_lens = _i32(2)
+    att.attend()
+    assert launches[-1].context_lens == batch.context_lens.data_ptr()
+    batch.context_lens.data = _i32(2)                     # the same object, another storage
+    att.attend()
+    assert launches[-1].context_lens == batch.context_lens.data_ptr()
+    batch.total_rows = 2
+    _raises_until_put_back(att, launches, lambda: setattr(batch, "total_rows", 3))
