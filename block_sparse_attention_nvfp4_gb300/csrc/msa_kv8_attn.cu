@@ -91,7 +91,10 @@ constexpr uint32_t kHalfBytes = 64 * 128;            // FP16 V: 64 tokens x 64 d
 constexpr int kSBufs = 3;
 constexpr uint32_t kColS = 0, kColO = kSBufs * kBlock, kTmemCols = 512;
 static_assert(kColO + kDim <= kTmemCols, "TMEM");
-constexpr float kRescaleLog2 = 8.f;                  // O is rescaled when the maximum grows by more than 2^8
+// The largest weight of a row is 2^7 when its reference is set and may grow to 2^15 before O is rescaled: the
+// upper part of FP16's range, so that weights vanish below 2^-32 of the largest and not below 2^-25 (a
+// million keys at the border are then 2^-12 of a row; at 2^-25 they were a few hundredths of it).
+constexpr float kStartLog2 = 7.f, kTopLog2 = 15.f;
 constexpr int kNoPos = 1 << 30;                      // position of a tile that nobody sees
 // Exchange between the copies of a row: two copies hand over 16 dims of every lane at a time, four put
 // down whole rows, some at a time (floats of a lane or row, padded).
@@ -1105,10 +1108,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mx = fmaxf(mx, hm[128 * (s ^ 1) + l]);
       }
       // P is taken relative to a reference that moves only when the maximum passes it by more
-      // than kRescaleLog2 (P stays within FP16); O / l does not depend on it
+      // than kTopLog2 (P stays within FP16); O / l does not depend on it
       const float bmax = fmaf(mx, coef, lv);
-      const bool move = bmax > r_old + kRescaleLog2 || (r_old == -INFINITY && bmax != -INFINITY);
-      const float m_new = move ? bmax : r_old;
+      const bool move = bmax > r_old + kTopLog2 || (r_old == -INFINITY && bmax != -INFINITY);
+      const float m_new = move ? bmax - kStartLog2 : r_old;
       if constexpr (kTurns) {
         hm[l] = m_new;
         __syncwarp();
