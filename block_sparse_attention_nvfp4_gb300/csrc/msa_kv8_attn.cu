@@ -5,7 +5,10 @@
 // x_t = sm_scale log2(e) k_scale (q . k_t) + log2(v_scale):
 //   out = sum_t 2^(x_t - m) v_t / sum_t 2^(x_t - m) / v_scale_t,  m the running maximum of x,
 // an online softmax in FP32. The value scale sits in the exponent, so the weights that meet the
-// V codes have one range whatever the pages' scales are, and the sum divides it out again.
+// V codes have one range whatever the pages' scales are, and the sum divides it out again. Two pages' scales
+// may lie 2^120 apart while their keys count alike in the sum, and FP32 ends at 2^-126: sums are carried
+// from reference to reference in two steps, and a tile whose weights lie far below the row's others is
+// summed relative to its own maximum.
 //
 // Products. S = Q K^T is an FP8 product straight from the cache's bytes: K is copied into
 // shared memory and never converted. BF16 queries become two E4M3 rows, q = (hi + lo) 2^e (8
@@ -95,6 +98,7 @@ static_assert(kColO + kDim <= kTmemCols, "TMEM");
 // upper part of FP16's range, so that weights vanish below 2^-32 of the largest and not below 2^-25 (a
 // million keys at the border are then 2^-12 of a row; at 2^-25 they were a few hundredths of it).
 constexpr float kStartLog2 = 7.f, kTopLog2 = 15.f;
+constexpr float kFaintLog2 = 60.f;                   // a tile's weights below 2^-60 are 0 in FP16 by far
 constexpr int kNoPos = 1 << 30;                      // position of a tile that nobody sees
 // Exchange between the copies of a row: two copies hand over 16 dims of every lane at a time, four put
 // down whole rows, some at a time (floats of a lane or row, padded).
@@ -254,6 +258,9 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr) : "memory");
+}
 // 16 bytes to shared memory, asynchronously; the first `bytes` (0 or 16) are copied, the others zero.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -262,6 +269,12 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+// A sum brought from reference m to m_to >= m: in two steps, because a sum is relative to a reference with a
+// value scale in it, may be as large as 2^67 for that, and counts although 2^(m - m_to) is below FP32's range.
+__device__ __forceinline__ float carry(float sum, float m, float m_to) {
+  const float h = ex2(0.5f * (m - m_to));
+  return sum * h * h;
 }
 // 32 columns of the warp's lanes times a factor per lane.
 __device__ __forceinline__ void tmem_scale32(uint32_t taddr, float a) {
@@ -876,8 +889,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         sum = 0.f;
 #pragma unroll
         for (int i = 0; i < C; ++i)
-          sum += sm.xl[0][i * kMpad + mm] * ex2(sm.xm[0][i * kMpad + mm] - r0) +
-                 sm.xl[1][i * kMpad + mm] * ex2(sm.xm[1][i * kMpad + mm] - r0);
+          sum += carry(sm.xl[0][i * kMpad + mm], sm.xm[0][i * kMpad + mm], r0) +
+                 carry(sm.xl[1][i * kMpad + mm], sm.xm[1][i * kMpad + mm], r0);
       };
       const bool whole = sg.slot < 0;
       const bool nans = sm.nanany[k % kRows] != 0;
@@ -918,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float copy_ref = fmaxf(sm.xm[0][l], sm.xm[1][l]);  // of this copy's tokens
       if constexpr (C == 1) {  // a thread has 64 dims of its row
         const float r0 = copy_ref == -INFINITY ? 0.f : copy_ref;
-        const float sum = sm.xl[0][l] * ex2(sm.xm[0][l] - r0) + sm.xl[1][l] * ex2(sm.xm[1][l] - r0);
+        const float sum = carry(sm.xl[0][l], sm.xm[0][l], r0) + carry(sm.xl[1][l], sm.xm[1][l], r0);
 #pragma unroll 1
         for (int d = 64 * s; d < 64 * s + 64; d += 16) {
           uint32_t a[16];
@@ -1119,7 +1132,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float ref = m_new == -INFINITY ? 0.f : m_new;
       const bool rescale = move && r_old != -INFINITY;
-      const float off = lv - ref;
+      // A tile whose weights are all 0 in FP16 may still count in the sum, where its values' scale is far
+      // below the row's others: its keys are then summed relative to its own maximum, mxs. With one copy a
+      // loop of its own does it, a score at a time: what matters there is how little code it is (E4M3
+      // prompts took 2.5 % more with 32 at a time, 5 % with selects among the weights as below, 0.5 % so).
+      const bool faint = bmax < m_new - kFaintLog2 && mx != -INFINITY;
+      const bool some_faint = __any_sync(0xFFFFFFFFu, faint);
+      const float mxs = mx * coef;
+      float own = 0.f;
+      if constexpr (kTurns) {
+        if (some_faint) {
+#pragma unroll 1
+          for (int n = 0; n < kN; ++n) {
+            uint32_t x;
+            tmem_ld1(s_cols + n, x);
+            tc_wait_ld();
+            own += ex2(fmaf(__uint_as_float(x), coef, -mxs));
+          }
+        }
+      }
+      const float off = !kTurns && faint ? -mxs : lv - ref;
       const float2 coef2 = make_float2(coef, coef), off2 = make_float2(off, off);
       float2 acc = make_float2(0.f, 0.f);
 #pragma unroll 1
@@ -1132,6 +1164,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc = __fadd2_rn(acc, e);
           asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v[u]) : "f"(e.y), "f"(e.x));
         }
+        if (!kTurns && some_faint)
+#pragma unroll
+          for (int u = 0; u < kStep / 2; ++u) v[u] = faint ? 0u : v[u];
         if constexpr (kTurns) tmem_st16(s_cols + 64 * (ch >> 1) + 16 * (ch & 1), v);
         else if constexpr (kStep == 32) tmem_st16(s_cols + p_off, v);
         else tmem_st8(s_cols + p_off, v);
@@ -1153,7 +1188,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int d = kTurns ? 0 : 64 * s; d < (kTurns ? kDim : 64 * s + 64); d += 32)
           tmem_scale32(tbase + lane_base + kColO + d, a);
       }
-      lrun = lrun * ex2(mref - ref) + (acc.x + acc.y) * iv;  // mref -inf: nothing summed yet
+      const float sum = kTurns && faint ? own : acc.x + acc.y;
+      lrun = carry(lrun, mref, ref) + sum * (faint ? ex2(mxs - ref) : iv);  // mref -inf: nothing summed yet
       mref = m_new;
       tc_wait_st();
       tc_fence_before();
@@ -1208,8 +1244,9 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8At
     constexpr int kRun = 4;  // partials whose loads are in flight at once
     float ref = -INFINITY, lt = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float w, const float4& x, float l) {
-      lt += w * l;
+    auto add = [&](float m, float m_to, const float4& x, float l) {
+      const float h = ex2(0.5f * (m - m_to)), w = h * h;  // the sum in two steps: see carry()
+      lt += l * h * h;
       if (w != 0.f) {
         o.x += w * x.x;
         o.y += w * x.y;
@@ -1218,11 +1255,11 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8At
       }
     };
     auto lower = [&](float to) {  // everything so far relative to a larger reference
-      const float w = ref == to ? 1.f : ex2(ref - to), l = lt;
+      const float l = lt;
       const float4 x = o;
       lt = 0.f;
       o = make_float4(0.f, 0.f, 0.f, 0.f);
-      add(w, x, l);
+      add(ref == to ? 0.f : ref, ref == to ? 0.f : to, x, l);
       ref = to;
     };
     if (on)
@@ -1247,7 +1284,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8At
         const float base = top == -INFINITY ? 0.f : top;  // nothing seen (a NaN sum still counts)
 #pragma unroll
         for (int j = 0; j < kRun; ++j)
-          if (e0 + j * step < n) add(ex2(mm[j] - base), x[j], ll[j]);
+          if (e0 + j * step < n) add(mm[j], base, x[j], ll[j]);
       }
     if (shared) {
       const int at = 32 * (warp & 1) + lane;
@@ -1262,7 +1299,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8At
         lower(top);
         const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
-        for (int i = 1; i < kPairs; ++i) add(ex2(part_m[i][at] - base), part_o[i][at], part_l[i][at]);
+        for (int i = 1; i < kPairs; ++i) add(part_m[i][at], base, part_o[i][at], part_l[i][at]);
       }
     }
     if (first == 0 && on) {

@@ -8,6 +8,7 @@ import torch
 
 from block_sparse_attention_nvfp4_gb300 import KV8Attention, KV8Batch, KV8Cache
 from tests import _kv8
+from tests.test_gpu_kv8 import _assert_attends
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
@@ -75,3 +76,29 @@ def test_a_faint_tail_beside_one_large_key(rows, where):
             assert bool((over <= 0).all()), (r, h, float(over.max()), float(out[0, r, h, 0]), float(want[0]))
             lse = att.lse.double().view(reqs, rows, G)[:, r, h]
             assert bool(((lse - math.log(norm)).abs() <= d + 2.0 ** -18 + 2.0 ** -22 * math.log(norm)).all())
+
+
+@pytest.mark.parametrize("rows", [1, 8, 16])
+@pytest.mark.parametrize("reqs", [1, 160])
+@pytest.mark.parametrize("x", [3.0, 7.0, 24.0, 40.0])
+@pytest.mark.parametrize("span", [60, 40, 33])
+@pytest.mark.parametrize("order", [(0, 1), (1, 0), (0, 0, 1, 0), (1, 0, 0, 0, 0, 1, 0)])
+def test_value_scales_do_not_weigh_the_sum(rows, reqs, x, span, order):
+    """Page 0 has value scale 2^-span, page 1 2^span; every key scores 0 but one of page 1, x (base 2). The
+    tokens of both count alike in the sum, whatever their values' scales are."""
+    n, G = 128 * len(order) + rows, 8
+    cache = KV8Cache.empty(3, 1)
+    g = torch.Generator("cuda").manual_seed(3)
+    cache.k_scale.fill_(1.0)
+    cache.v_data.copy_(torch.randint(0x20, 0x48, cache.v_data.shape, dtype=torch.uint8, device="cuda", generator=g))
+    cache.v_scale[0], cache.v_scale[1], cache.v_scale[2] = 2.0 ** -span, 2.0 ** span, 1.0
+    cache.k_data[1, 0, 17, 0] = ONE
+    q = torch.zeros((reqs * rows, G, 128), device="cuda")
+    q[:, :, 0] = x
+    batch, lens, indptr, table = _batch(reqs, n, rows, G, q.to(torch.float8_e4m3fn).view(torch.uint8), list(order) + [2])
+    att = KV8Attention(cache, batch, sm_scale=math.log(2.0))
+    out = att.attend()
+    assert att.errors() == 0
+    qv = batch.q.view(torch.float8_e4m3fn).double().view(-1, 1, G, 128)
+    one = _kv8.attend(qv[:rows], cache, lens[:1], indptr[:2], table[:1], sm_scale=math.log(2.0))
+    _assert_attends(out, att.lse, [t.repeat(reqs, *[1] * (t.dim() - 1)) for t in one])
