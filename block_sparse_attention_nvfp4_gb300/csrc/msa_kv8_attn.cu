@@ -98,6 +98,7 @@ static_assert(kColO + kDim <= kTmemCols, "TMEM");
 // upper part of FP16's range, so that weights vanish below 2^-32 of the largest and not below 2^-25 (a
 // million keys at the border are then 2^-12 of a row; at 2^-25 they were a few hundredths of it).
 constexpr float kStartLog2 = 7.f, kTopLog2 = 15.f;
+constexpr float kZeroLog2 = -64.f;                   // stands for the logarithm of a value scale of 0
 constexpr float kFaintLog2 = 60.f;                   // a tile's weights below 2^-60 are 0 in FP16 by far
 constexpr int kNoPos = 1 << 30;                      // position of a tile that nobody sees
 // Exchange between the copies of a row: two copies hand over 16 dims of every lane at a time, four put
@@ -568,8 +569,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               ks = p.k_scale[ph];
               const float vs = p.v_scale[ph];
               vzero = vs == 0.f;
-              lv = vzero ? 0.f : log2f(vs);
-              iv = vzero ? 1.f : 1.f / vs;
+              // a page of scale 0 has keys but no values: below every scale, so that its scores do not
+              // raise the reference and take the other pages' weights out of FP16's range
+              lv = vzero ? kZeroLog2 : log2f(vs);
+              iv = vzero ? exp2f(-kZeroLog2) : 1.f / vs;
             }
           }
           for (unsigned m = __ballot_sync(0xFFFFFFFFu, on); m != 0u && good; m &= m - 1u) {

@@ -1,5 +1,6 @@
 """GPU tests of the softmax weights of the 8-bit attention where the exponents of FP16 and FP32
-end: long faint tails beside one large key, value scales over their whole range."""
+end: long faint tails beside one large key, value scales over their whole range, pages whose
+value scale is 0."""
 import math
 
 import numpy as np
@@ -102,3 +103,25 @@ def test_value_scales_do_not_weigh_the_sum(rows, reqs, x, span, order):
     qv = batch.q.view(torch.float8_e4m3fn).double().view(-1, 1, G, 128)
     one = _kv8.attend(qv[:rows], cache, lens[:1], indptr[:2], table[:1], sm_scale=math.log(2.0))
     _assert_attends(out, att.lse, [t.repeat(reqs, *[1] * (t.dim() - 1)) for t in one])
+
+
+@pytest.mark.parametrize("rows", [1, 8, 16])
+@pytest.mark.parametrize("zero", [[0], [5], [0, 1, 2, 9], list(range(10))])
+@pytest.mark.parametrize("reqs", [1, 40])
+@pytest.mark.parametrize("level", [-18, 20])
+def test_pages_of_scale_zero(rows, zero, reqs, level):
+    """A page whose value scale is 0 counts in the sum alone; the weights of the others keep their bits
+    however small or large their values' scale is."""
+    n, G = 1280 + rows, 8
+    kd, ks = _kv8.fill(11, 1, 5)
+    vd, vs = _kv8.fill(11, 1, 6)
+    vs *= 2.0 ** level
+    vs[zero] = 0.0
+    cache = KV8Cache(kd, ks, vd, vs)
+    g = torch.Generator("cuda").manual_seed(rows)
+    q = torch.randn((reqs * rows, G, 128), device="cuda", generator=g).to(torch.bfloat16)
+    batch, lens, indptr, table = _batch(reqs, n, rows, G, q)
+    att = KV8Attention(cache, batch)
+    out = att.attend()
+    assert att.errors() == 0
+    _assert_attends(out, att.lse, _kv8.attend(q.double().view(-1, 1, G, 128), cache, lens, indptr, table))
