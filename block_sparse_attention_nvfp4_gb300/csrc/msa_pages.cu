@@ -59,7 +59,7 @@ struct Lists {
   int32_t* tokens;  //     slots to copy
   int32_t* len;     //     fork: the parent's length before the call (-1: the entry does nothing)
   int32_t* free_ids;  // [num_pages] free pages in id order; compact: targets
-  int32_t* map;       // [num_pages] compact: new id of a live page
+  int32_t* map;       // [num_pages] compact: new id of a page, -1 when its count is 0
   int32_t* count;     // compact: number of moves, then where the sources start in free_ids
 };
 
@@ -351,6 +351,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Pool p
       if (id >= live) break;
       if (get(r, k) <= 0) {
         l.free_ids[at++] = id;
+        l.map[id] = -1;
       } else {
         l.map[id] = id;
         if (new_refs != p.refs) new_refs[id] = get(r, k);
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Pool p
         new_refs[to] = ref;
         ++at;
       } else {
-        l.map[id] = id;
+        l.map[id] = -1;
       }
     }
     moved += total;
@@ -494,7 +495,8 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const Pool p
       for (int c = c0 + threadIdx.x; c < c1; c += kCopyThreads) {
         int id = p.table[row + c];
         if (c < np) {
-          if (in(id, p.num_pages)) id = l.map[id];
+          const int to = in(id, p.num_pages) ? l.map[id] : -1;  // -1: no page of the pool, or one that nobody counts
+          if (to >= 0) id = to;
           else set_flag(p.flags, kFlagBadPage);
         }
         new_table[row + c] = id;

@@ -503,7 +503,8 @@ msa_status msa_pages_free(const msa_page_pool* pool, int32_t n, const int32_t* s
 /* Compact: with L pages live (count > 0), those with ids >= L move to the free ids below L,
  * the k-th of them to the k-th, in every plane; new_block_table and new_ref_counts get the
  * tables after the move (they may be the pool's own: in place; entries that no sequence holds
- * are copied as they are). num_live (device, one int32, or NULL) gets L. */
+ * are copied as they are). A held entry whose page nobody counts, or is outside the pool, is copied
+ * as it is too and sets MSA_FLAG_BAD_PAGE. num_live (device, one int32, or NULL) gets L. */
 msa_status msa_pages_compact(const msa_page_pool* pool, int32_t* new_block_table, int32_t* new_ref_counts,
                              int32_t* num_live, void* ws, size_t ws_bytes, void* stream);
 
