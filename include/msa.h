@@ -445,8 +445,8 @@ msa_status msa_kv8_attn(const msa_kv8_attn_args* args, void* ws, size_t ws_bytes
  * multiple of 4) that belong to the page as a whole, such as the scales of the 8-bit cache.
  * Data pointers are 16-byte aligned. At most 2^20 pages and 2^20 sequences.
  *
- * Lists (src, dst, parents, ...) are device arrays of n int32. Sequence and page ids outside
- * the pool set MSA_FLAG_BAD_SEQ or MSA_FLAG_BAD_PAGE, and their entry does nothing. */
+ * Lists (src, dst, parents, ...) are device arrays of n int32. Sequence and page ids in them that
+ * are outside the pool set MSA_FLAG_BAD_SEQ or MSA_FLAG_BAD_PAGE, and their entry does nothing. */
 #define MSA_MAX_PLANES 16
 typedef struct {
   void* data;
@@ -483,7 +483,9 @@ msa_status msa_pages_copy(const msa_page_pool* pool, int32_t n, const int32_t* s
  * read as they were before the call. A child must be an empty sequence (length 0) and
  * appear once (MSA_FLAG_BAD_SEQ otherwise; of a repeated child the first entry stands).
  * When the free pages run out, this and all later entries that need one do nothing
- * (MSA_FLAG_NO_PAGE). n <= num_seqs. */
+ * (MSA_FLAG_NO_PAGE). A parent whose partly filled last page is outside the pool is not forked; an
+ * entry outside the pool among its full pages is copied into the child's row as it is and counted
+ * nowhere (MSA_FLAG_BAD_PAGE in both cases). n <= num_seqs. */
 msa_status msa_pages_fork(const msa_page_pool* pool, int32_t n, const int32_t* parents, const int32_t* children,
                           void* ws, size_t ws_bytes, void* stream);
 

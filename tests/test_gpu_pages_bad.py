@@ -1,10 +1,11 @@
-"""GPU tests of page operators on rows that list pages they should not: pages that nobody counts."""
+"""GPU tests of page operators on rows that list pages they should not: pages that nobody counts, and
+page ids outside the pool."""
 import numpy as np
 import pytest
 import torch
 
 from block_sparse_attention_nvfp4_gb300 import _lib
-from tests.test_gpu_pages import _same, _state
+from tests.test_gpu_pages import _i32, _same, _state
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
@@ -61,3 +62,35 @@ def test_compact_leaves_entries_of_uncounted_pages():
         for p in np.flatnonzero(counted):
             refs[to.get(p, p)] = ref.refs[p]
         assert np.array_equal(r.cpu().numpy(), refs)
+
+
+def test_fork_of_a_row_with_a_bad_full_page():
+    """The child is made with the entry as it stands; the page is counted nowhere and flagged."""
+    for bad in (30, -3):
+        pool, ref, dev = _state("kv8", 30, [400, 0, 0], 5, 3)
+        before = ref.refs.copy()
+        pool.block_table[0, 1] = bad
+        pool.fork(_i32(0), _i32(1))
+        assert pool.errors() == _lib.FLAG_BAD_PAGE
+        t = pool.block_table.cpu().numpy()
+        assert pool.seq_lens.tolist() == [400, 400, 0] and np.array_equal(t[1, :3], t[0, :3])
+        free = int(np.flatnonzero(before == 0)[0])
+        before[[t[0, 0], t[0, 2]]] += 1
+        before[free] = 1
+        assert t[1, 3] == free and np.array_equal(pool.ref_counts.cpu().numpy(), before)
+        pool.free(_i32(1))                                   # and freed but for that entry
+        assert pool.errors() == _lib.FLAG_BAD_PAGE
+        before[[t[0, 0], t[0, 2]]] -= 1
+        before[free] = 0
+        assert np.array_equal(pool.ref_counts.cpu().numpy(), before) and pool.seq_lens.tolist() == [400, 0, 0]
+
+
+def test_fork_of_a_row_with_a_bad_last_page():
+    """Its partly filled last page cannot be copied: the entry does nothing, the others are served."""
+    pool, ref, dev = _state("kv8", 30, [400, 300, 0, 0], 5, 3)
+    pool.block_table[0, 3] = 30
+    pool.fork(_i32(0, 1), _i32(2, 3))
+    assert pool.errors() == _lib.FLAG_BAD_PAGE
+    ref.fork([1], [3])
+    ref.table[0, 3] = 30
+    _same(pool, ref, dev)
