@@ -114,7 +114,9 @@ class PagePool:
     def compact(self, block_table: Optional[torch.Tensor] = None, ref_counts: Optional[torch.Tensor] = None,
                 num_live: Optional[torch.Tensor] = None, stream=None):
         """Move the live pages to the ids 0 .. L - 1, in place or with the new tables written to the
-        given tensors (both or neither); num_live (int32 [1]) gets L."""
+        given tensors (both or neither); num_live (int32 [1]) gets L. The pages move either way: with
+        tensors of their own, copy them over the pool's before its next operator, whose free pages
+        would otherwise be ones in use."""
         if (block_table is None) != (ref_counts is None):
             raise ValueError("compact: give both tables or neither")
         a = self.args

@@ -506,7 +506,10 @@ msa_status msa_pages_free(const msa_page_pool* pool, int32_t n, const int32_t* s
  * the k-th of them to the k-th, in every plane; new_block_table and new_ref_counts get the
  * tables after the move (they may be the pool's own: in place; entries that no sequence holds
  * are copied as they are). A held entry whose page nobody counts, or is outside the pool, is copied
- * as it is too and sets MSA_FLAG_BAD_PAGE. num_live (device, one int32, or NULL) gets L. */
+ * as it is too and sets MSA_FLAG_BAD_PAGE. num_live (device, one int32, or NULL) gets L.
+ * With tables of their own the pool's block_table and ref_counts still describe where the pages were:
+ * copy the new ones over them before the next operator on this pool, which would otherwise give out
+ * pages that are in use. */
 msa_status msa_pages_compact(const msa_page_pool* pool, int32_t* new_block_table, int32_t* new_ref_counts,
                              int32_t* num_live, void* ws, size_t ws_bytes, void* stream);
 

@@ -94,3 +94,19 @@ def test_fork_of_a_row_with_a_bad_last_page():
     ref.fork([1], [3])
     ref.table[0, 3] = 30
     _same(pool, ref, dev)
+
+
+def test_compact_beside_then_the_next_operator():
+    """Tables of their own are copied over the pool's before it goes on."""
+    pool, ref, dev = _state("kv8", 30, [0, 900, 0, 300], 9, 3, shared=False)
+    t, r = torch.empty_like(pool.block_table), torch.empty_like(pool.ref_counts)
+    pool.compact(t, r)
+    assert ref.compact() == 11
+    pool.block_table.copy_(t)
+    pool.ref_counts.copy_(r)
+    pool.reserve(_i32(0, 3), _i32(1000, 700))
+    ref.reserve([0, 3], [1000, 700])
+    pool.fork(_i32(1), _i32(2))
+    ref.fork([1], [2])
+    assert pool.errors() == 0
+    _same(pool, ref, dev)
