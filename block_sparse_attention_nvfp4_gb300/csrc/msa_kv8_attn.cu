@@ -12,7 +12,9 @@
 //
 // Products. S = Q K^T is an FP8 product straight from the cache's bytes: K is copied into
 // shared memory and never converted. BF16 queries become two E4M3 rows, q = (hi + lo) 2^e (8
-// significant bits = two 4-bit significands), so S costs two FP8 products instead of a
+// significant bits = two 4-bit significands; exact while lo is a multiple of E4M3's smallest step,
+// 2^-9 with the row's largest element in (224, 448], so down to 2^-9.8 of the largest, and within
+// half that step, 2^-17.8 of the largest, below), so S costs two FP8 products instead of a
 // conversion of K. P V runs in FP16: V codes are widened (exact), P is FP16 (an E4M3 P loses
 // 2^-4 of a weight, and two E4M3 parts lose weights below 2^-18 of the largest, which a long
 // context's tail adds up to).

@@ -390,9 +390,11 @@ msa_status msa_kv8_append(const msa_kv8_append_args* args, void* ws, size_t ws_b
  * gets 0 and lse -inf. NaN and infinities in slots that a row does not see never reach it.
  *
  * Queries are E4M3 codes or BF16. Sums are FP32; softmax weights are rounded to FP16 for
- * the product with V, the output to BF16. A BF16 query row is taken as the sum of two E4M3
- * rows times a power of two (8 + 8 bits of significand for elements down to 2^-14 of
- * the row's largest, an absolute error below 2^-18 of it for smaller ones).
+ * the product with V (half a step, and those below 2^-32 of the row's largest vanish there, a weight
+ * taken times its page's value scale), the output to BF16. A BF16 query row is taken as the sum of two
+ * E4M3 rows times a power of two: exactly for elements down to 2^-9.8 of the row's largest, with an
+ * absolute error of at most 2^-17.8 of the largest for smaller ones. A row with an infinity or a NaN
+ * gives NaN.
  *
  * block_ids [B][H][n_block_ids]: logical blocks of each (request, KV head), in any order,
  * -1 = unused; an id outside the context, or one listed twice, sets MSA_FLAG_BAD_IDS and

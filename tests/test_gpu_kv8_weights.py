@@ -125,3 +125,31 @@ def test_pages_of_scale_zero(rows, zero, reqs, level):
     out = att.attend()
     assert att.errors() == 0
     _assert_attends(out, att.lse, _kv8.attend(q.double().view(-1, 1, G, 128), cache, lens, indptr, table))
+
+
+@pytest.mark.parametrize("rows", [1, 8, 16])
+def test_small_elements_of_a_bf16_query(rows):
+    """A row with one large element and 127 small ones, each at the worst place of the split into two E4M3
+    rows: half their smallest step, 2^-10 with the largest element at 225, at most 2^-17.8 of the
+    largest. Keys see the small ones alone, so that a score is off by up to 127 times that; the
+    rest of its error is that of _kv8.attend."""
+    n, G = 128 + rows, 8
+    cache = KV8Cache.empty(2, 1)
+    g = torch.Generator("cuda").manual_seed(rows)
+    cache.k_scale.fill_(1.0)
+    cache.v_scale.fill_(1.0)
+    cache.v_data.copy_(torch.randint(0x30, 0x39, cache.v_data.shape, dtype=torch.uint8, device="cuda", generator=g))
+    cache.k_data[:, :, ::2, 1:] = ONE                         # every other key sums the small elements up
+    small = 0.125 * (1 + 2.0 ** -7) * torch.exp2(-torch.arange(G, device="cuda").float())
+    q = small[None, :, None].repeat(rows, 1, 128)
+    q[:, :, 0] = 225.0
+    q = q.to(torch.bfloat16)
+    batch, lens, indptr, table = _batch(1, n, rows, G, q)
+    att = KV8Attention(cache, batch, sm_scale=1.0)
+    out = att.attend()
+    assert att.errors() == 0
+    want, lse, _, _ = _kv8.attend(q.double().view(rows, 1, G, 128), cache, lens, indptr, table, sm_scale=1.0)
+    d = 127 * 225 * 2.0 ** -17.8 + 2.0 ** -16 * 127 * 0.126
+    assert bool(((att.lse.double() - lse).abs() <= d + 2.0 ** -18 + 2.0 ** -22 * lse.abs()).all())
+    rel = 2.0 ** -11 + 2.0 ** -18 + math.expm1(2 * d)         # the values are positive: sum p |v| is the output
+    assert bool(((out.double() - want).abs() <= (2.0 ** -8 + rel * (1 + 2.0 ** -8)) * want + 2.0 ** -20).all())
