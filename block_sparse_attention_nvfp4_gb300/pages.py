@@ -55,16 +55,21 @@ class PagePool:
         a.num_planes = len(planes)
         for i, (_, _, data, strips, slot, page) in enumerate(planes):
             a.planes[i].data, a.planes[i].strips, a.planes[i].slot_bytes, a.planes[i].page_bytes = data, strips, slot, page
-        # (owner, its tensors' names, how to get them, the ones that are bound, their addresses)
+        # (owner, its tensors' names, how to get them, the ones that are bound), and the addresses of all
         names = [(self, ("seq_lens", "block_table", "ref_counts"))]
         names += [(c, tuple(dict.fromkeys(x[1] for x in planes if x[0] is c))) for c in self.caches]
         self._bound = [(o, n, operator.attrgetter(*n)) for o, n in names]
-        self._bound = [(o, n, get, get(o), tuple(map(_address, get(o)))) for o, n, get in self._bound]
+        self._bound = [(o, n, get, get(o)) for o, n, get in self._bound]
+        self._tensors = [t for x in self._bound for t in x[3]]
+        self._at = list(map(_address, self._tensors))
         n = ctypes.c_size_t(0)
         _lib._check(_lib.load().msa_pages_workspace_size(ctypes.byref(a), ctypes.byref(n)), "msa_pages_workspace_size")
         with torch.cuda.device(dev):
             self.ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
             _lib.msa_workspace_init(self.ws)
+        lib = _lib.load()
+        self._fns = {n: getattr(lib, n) for n in ("msa_pages_copy", "msa_pages_fork", "msa_pages_reserve",
+                                                  "msa_pages_free", "msa_pages_compact")}
         self._ref, self._ws, self._index = ctypes.byref(a), (self.ws.data_ptr(), self.ws.numel()), dev.index
 
     @staticmethod
@@ -81,13 +86,15 @@ class PagePool:
         return t.data_ptr()
 
     def _run(self, name: str, stream, *args):
-        for owner, names, get, bound, at in self._bound:
-            now = get(owner)
-            # the same objects may have got other storages (set_, resize_, .data)
-            if not all(map(operator.is_, now, bound)) or tuple(map(_address, now)) != at:
-                changed = [n for n, x, y, a in zip(names, now, bound, at) if x is not y or _address(x) != a]
-                raise ValueError(f"{', '.join(changed)}: replaced or moved after the pool was made")
-        _call(self.device, stream, getattr(_lib.load(), name), name, self._ref, *args, *self._ws)
+        for owner, names, get, bound in self._bound:
+            if not all(map(operator.is_, get(owner), bound)):
+                changed = [n for n, x, y in zip(names, get(owner), bound) if x is not y]
+                raise ValueError(f"{', '.join(changed)}: replaced after the pool was made")
+        if list(map(_address, self._tensors)) != self._at:   # the same objects with other storages (set_, resize_, .data)
+            names = [n for x in self._bound for n in x[1]]
+            changed = [n for n, t, a in zip(names, self._tensors, self._at) if _address(t) != a]
+            raise ValueError(f"{', '.join(changed)}: moved after the pool was made")
+        _call(self.device, stream, self._fns[name], name, self._ref, *args, *self._ws)
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor, tokens: Optional[torch.Tensor] = None, stream=None):
         """Copy page src[i] to dst[i] in every plane: the first tokens[i] slots, or all."""
