@@ -17,11 +17,12 @@
 //   * append_rows_kernel (at most 8 rows per request, so at most two pages): CTA = (request, first or
 //     second page), each warp whole (head, K or V) pairs; the pairs whose scale moved are rescaled by the
 //     whole CTA after. The source rows are asked for before the page is known. One token for each of 256
-//     requests, 4 heads, BF16: 6.3 us,
-//     20.7 with the other kernel.
+//     requests, 4 heads, BF16: 6.2 us, 20.6 with the other kernel.
 //   * append_tile_kernel: CTA = one (request, page, head, K or V), up to 128 x 128 values in
 //     registers; the next unit is located while this one's rows are on their way. 8 ragged prompts of
-//     44,000 tokens together, 4 heads, BF16 (134 MB read and written): 29 us, 0.69 of the copy rate.
+//     44,000 tokens together, 4 heads, BF16 (134 MB read and written): 29 us, 0.69 of the copy rate. What is
+//     missing: a CTA's loads wait for its stores (load, maximum, barrier, convert, store, one unit after the
+//     other; four CTAs on an SM cover it in part), and 4.6 rounds of units leave a tail of about a tenth.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

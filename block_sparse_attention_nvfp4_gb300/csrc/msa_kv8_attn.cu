@@ -21,12 +21,14 @@
 //
 // Floors: memory for few rows (a token and head is 256 bytes; the MMAs of a 128-token tile take
 // less than its copy), tensor and exponential rate for prompts. Measured on a GB300 (graph replays):
-//   64 requests of one row over 65,536 keys, 4 x 8 heads, E4M3 queries   658 us   6.5 TB/s
-//   64 of one row over 16,384 keys, BF16 / E4M3 queries             188 / 177 us  5.7 / 6.1 TB/s
-//   64 ragged requests, 512 .. 65,536 keys, up to 8 rows, BF16 queries   162 us   5.3 TB/s
+//   64 requests of one row over 65,536 keys, 4 x 8 heads, E4M3 queries   669 us   6.4 TB/s
+//   64 of one row over 16,384 keys, BF16 / E4M3 queries             190 / 178 us  5.7 / 6.0 TB/s
+//   64 ragged requests, 512 .. 65,536 keys, up to 8 rows, BF16 queries   163 us   5.3 TB/s
 //   one token over 4,096 keys, E4M3 queries                             14.5 us  (fixed costs)
-//   16 requests with 16 listed blocks each, 8 rows, E4M3 queries        23.1 us  1.5 TB/s
-//   2,053 rows on 16,421 keys, BF16 / E4M3 queries                  358 / 357 us  1.5 PFLOP/s
+//   16 requests with 16 listed blocks each, 8 rows, E4M3 queries        24.5 us  1.4 TB/s
+//   2,053 rows on 16,421 keys, BF16 / E4M3 queries                  370 / 361 us  1.4 PFLOP/s
+// (The figures beside the choices below are replays of this kernel with the one thing changed, in turn
+// with it as it is.)
 //
 // Work. An item is a (request, KV head, chunk of query rows); its tiles are the pages its
 // last row sees, or its block ids. All items' tiles form one line that the CTAs (one per SM)
@@ -53,16 +55,15 @@
 //     rows' reference goes from set to set through shared memory. With more copies, where a row
 //     has few tokens, both sets share every tile: of the tokens that a copy takes, set 0 has the
 //     first half and set 1 the second, and the two threads of a row exchange their maxima.
-//     (One scheme for both, measured when the rest was slower: 2,053 rows on 16,421 tokens, 4 x 8 heads,
-//     BF16, took 488 us with shared tiles and 444 in turn; 64 ragged requests of up to 8 rows 202 us
-//     shared and 215 in turn.)
+//     (When both were built in both forms, prompts were 9 % faster in turn and 64 ragged requests of up
+//     to 8 rows 6 % slower.)
 //
-// What bounds it now: long decode, memory (0.97 of the copy rate in the first line above; from L2 the
-// same work takes 565 us). Prompts, the roles' instruction streams: a tile costs a CTA about 1,700
-// cycles against 1,024 of tensor work with BF16 queries (768 with E4M3), most of them the dependent
-// instructions of single warps between two hand-overs. What the loops hold in registers and how long
-// their code is count for more there than the work in them: reading a row's maximum in a loop
-// unrolled four times costs a prompt 40 %.
+// What bounds it now: long decode, memory (0.96 of the copy rate in the first line above; the same work on
+// pages that L2 holds takes 575 us). Prompts, the roles' instruction streams: a tile costs a CTA about 900
+// ns against 1,024 cycles of tensor work with BF16 queries and 768 with E4M3, so that these gain only
+// 2 %; most of it are the dependent instructions of single warps between two hand-overs. What the loops
+// hold in registers and how long their code is count for more there than the work in them: reading a
+// row's maximum in a loop unrolled twice costs a prompt 4 % (BF16) or 6 % (E4M3), four times 29 or 45 %.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -177,7 +178,8 @@ struct Header {
 constexpr long long kPartFloats = 128LL * kDim + 256;  // O, m, l
 // Where dims d .. d + 3 of row l of a partial's O are: 8 rows' 16-byte pieces side by side, so that
 // lanes with a row each and lanes with some rows and dims each both move whole lines. (Rows one after
-// the other cost the writer 32 lines a store: 3 us for 128 rows instead of 1.)
+// the other cost the writer 32 lines a store: one token over 4,096 keys 16.4 us instead of 14.4, 16
+// requests with 16 listed blocks 26.5 instead of 25.)
 __device__ __forceinline__ int part_at(int l, int d) { return (((l >> 3) * (kDim / 4) + (d >> 2)) * 8 + (l & 7)) * 4; }
 __host__ __device__ inline size_t headers_bytes(int grid) { return (grid * sizeof(Header) + 255) / 256 * 256; }
 
@@ -204,8 +206,8 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t
 // The whole warp waits, converged: its lanes vote on every try (one lane asking for all leaves the
 // others to a divergent barrier, which wakes ~1,500 cycles late). The loop stands in line: as a
 // function of its own, the call's registers cost the roles more than the code (64 ragged requests
-// 184 -> 171 us), and a loop without the clock's delay between tries takes the issue slots of the
-// working warps (275 us).
+// 193 us instead of 164, a BF16 prompt 409 instead of 370), and a loop that counts its tries and does not
+// read the clock between them takes the issue slots of the working warps (64 ragged requests 173 us).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t* flags) {
   if (__all_sync(0xFFFFFFFFu, try_bar(bar, parity))) return true;
   const uint32_t t0 = clock();
@@ -309,8 +311,8 @@ __device__ __forceinline__ uint32_t f32x2_e4m3x2(float a, float b) {  // a in th
 }
 
 // ---- the line of tiles
-// Places of an item before its tiles. When this was chosen 64 ragged requests / 16 requests with 16
-// listed blocks each took 191 / 25.1 us with 4 places, 185 / 24.9 with 5, 180 / 26.1 with 6.
+// Places of an item before its tiles. 64 ragged requests / 16 requests with 16 listed blocks each take
+// 168 / 24.7 us with 4 places, 164 / 25.0 with 5, 163 / 25.3 with 6.
 constexpr int kItemCost = 5;
 struct Req {
   int N, R, r0;
@@ -746,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // the half that was in this buffer (four halves ago) has been multiplied (waiting here and not
-      // with the converted values in registers: prompt 430 -> 398 us)
+      // with the converted values in registers: BF16 prompt 392 -> 370 us, 64 ragged requests 168 -> 164)
       const uint32_t u = 2 * t + h, uv = u % kVBufs;
       if (t >= 2 && !warp_wait(smem_u32(&sm.v16_free[(u - kVBufs) % (2 * kVBufs)]), ((u - kVBufs) / (2 * kVBufs)) & 1, p.flags))
         break;
@@ -1003,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           // Copy c finishes dims kD c .. of this set's 64: in round r every lane hands 16 dims to copy
           // c + r and takes 16 from copy c - r, in a fixed order.
-          // (Rows at a time lose here: with up to 64 rows 64 ragged requests took 202 us against 196.)
+          // (Rows at a time, as above, were 3 % slower here for 64 ragged requests when both were built.)
           constexpr int kD = 64 / C;
           float* red = sm.red[s];
           float y[kD];
@@ -1091,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float mx = -INFINITY;
       if (kCh > 1 && full_vis) {
 #pragma unroll 1
-        for (int ch = 0; ch < kCh; ++ch) {  // the TMEM load reduces (two at a time spill: prompt 398 us, not 380)
+        for (int ch = 0; ch < kCh; ++ch) {  // the TMEM load reduces (two at a time spill: BF16 prompt 385 us, not 370)
           float m0 = tmem_ld32_max(s_cols + k0 + 32 * ch);
           tc_wait_ld();
           asm volatile("" : "+f"(m0));  // no use moves above the wait
@@ -1216,8 +1218,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // 16 dims, 4 dims of a row per lane. With at most 8 partials the 8 pairs of warps take 8 rows each; with
 // more they share 8 rows, every eighth partial each, and the first joins their sums.
 // Bound: latency (headers, then all of a run's loads at once) and the time to start 4 CTAs per SM:
-// runs of 4 in 64 registers measured best (one token over 4,096 keys: 14.7 us, runs of 8 in 128
-// registers 16.5).
+// runs of 4 in 64 registers measured best (one token over 4,096 keys: 14.4 us, runs of 8 in 128
+// registers 16.5; 64 ragged requests 164 and 167).
 __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8AttnParams p, int grid) {
   constexpr int kPairs = kMergeThreads / 64;
   __shared__ float4 part_o[kPairs][64];
@@ -1239,7 +1241,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8At
   const float* parts = reinterpret_cast<const float*>(p.parts + headers_bytes(grid));
   auto part = [&](int i) { return parts + (i == 0 ? 2LL * cta + 1 : 2LL * (cta + i)) * kPartFloats; };
   const int rows = me.rows * p.q_per_kv;
-  // (one token over 4,096 keys: 14.7 us shared, 18.3 not; 16 requests with 16 listed blocks: 32.2 and 24.8)
+  // (one token over 4,096 keys: 14.4 us shared, 18.5 not; 16 requests with 16 listed blocks: 32 and 25)
   const bool shared = n > kPairs;
   const int pair = warp >> 1, d = 32 * blockIdx.y + 16 * (warp & 1) + 4 * (lane >> 3);
   const int first = shared ? pair : 0, step = shared ? kPairs : 1;
@@ -1340,8 +1342,8 @@ cudaError_t launch(const CUtensorMap& kmap, const Kv8AttnParams& prm, int grid, 
 
 // Copies of the query rows that a request of max_rows rows (taken as a power of two) leaves room
 // for, and the rows of a chunk. At 8 query rows (one token, 8 queries a head) 16 requests over 16,384
-// keys took 63.7 us with four copies, 67.8 with two, 71.9 with one; at up to 64 rows 64 ragged
-// requests 185 us with two and 192 with one.
+// keys take 60.3 us with four copies, 61.6 with two, 63.4 with one, and one token over 4,096 keys 14.4,
+// 14.4 and 16.3; at up to 64 rows 64 ragged requests 164 us with two and 168 with one.
 int copies_for(int max_rows, int q_per_kv) {
   long long r = 1;
   while (r < max_rows && r < 128) r *= 2;

@@ -14,7 +14,7 @@
 // Measured (graph replays): 1,024 pages of 131 KB copied in 45 us (268 MB, 0.89 of the copy rate);
 // 2,048 live pages of 4,096 compacted in 51 us, of which the plan is 6; 256 forks of 16 long parents
 // with 256 reservations 23 us (plan 7, tails and rows 10, reservations 5); a fork to 4 children, their
-// growth and their end 14.5 us, four launches of 3 to 4 us each.
+// growth and their end 12.5 us, four launches of about 3 us each.
 // Sources are live pages and targets are free ones, so no order among the copies matters.
 #include <climits>
 #include <cstdint>

@@ -338,7 +338,8 @@ msa_status msa_kv_insert_nvfp4(const msa_kv_insert_args* args, void* ws, size_t 
  *   k_data, v_data   [P][H][128][128]  (H = num_kv_heads)   k_scale, v_scale   [P][H]
  * and the stored value is E4M3(code) * scale. Pages, block tables, lengths and row
  * pointers are those of msa_decode_args. Data pointers must be 16-byte aligned. Scales are
- * 0 or in [2^-60, 2^60]. */
+ * 0 or in [2^-60, 2^60] (the append keeps to that for values up to 448 * 2^60); those of one cache may
+ * differ by any of it from page to page. */
 typedef enum { MSA_TYPE_E4M3 = 0, MSA_TYPE_BF16 = 1, MSA_TYPE_F16 = 2, MSA_TYPE_F32 = 3 } msa_type;
 
 /* Append: request b's R = q_indptr[b+1] - q_indptr[b] new tokens, rows q_indptr[b] .. of
@@ -352,8 +353,8 @@ typedef enum { MSA_TYPE_E4M3 = 0, MSA_TYPE_BF16 = 1, MSA_TYPE_F16 = 2, MSA_TYPE_
  * E4M3 is a floating format, so a power-of-two scale costs no precision against any other
  * and a later growth of the scale re-rounds only what falls among the subnormals. An
  * infinity saturates to 448 scales and takes no part in `need`; a NaN stays a NaN. An old
- * scale that is not positive and finite counts as 0 (the old slots become 0). Slots past
- * the new tokens are left as they are. A NULL source (k or v) leaves its planes untouched
+ * scale that is not positive and finite counts as 0 (the old slots become 0, NaN codes stay NaN).
+ * Slots past the new tokens are left as they are. A NULL source (k or v) leaves its planes untouched
  * (its plane pointers may then be NULL).
  * Two requests that write into the same page race; the caller keeps written pages
  * unshared (msa_pages_fork does). A page id outside [0, num_pages) skips that page and sets
