@@ -193,7 +193,7 @@ class KV8Attention:
             _lib._check(_lib.load().msa_kv8_attn_workspace_size(ctypes.byref(self.args), ctypes.byref(n)),
                         "msa_kv8_attn_workspace_size")
             self.ws = torch.empty(n.value, dtype=torch.uint8, device=self.device)
-            _lib.msa_workspace_init(self.ws)
+            _lib.msa_workspace_init(self.ws[:256])   # the flags: a call on another stream may follow at once
         self._ws = (self.ws.data_ptr(), self.ws.numel())
 
     def rebind(self, batch: KV8Batch):

@@ -66,7 +66,7 @@ class PagePool:
         _lib._check(_lib.load().msa_pages_workspace_size(ctypes.byref(a), ctypes.byref(n)), "msa_pages_workspace_size")
         with torch.cuda.device(dev):
             self.ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
-            _lib.msa_workspace_init(self.ws)
+            _lib.msa_workspace_init(self.ws[:256])   # the flags: a call on another stream may follow at once
         lib = _lib.load()
         self._fns = {n: getattr(lib, n) for n in ("msa_pages_copy", "msa_pages_fork", "msa_pages_reserve",
                                                   "msa_pages_free", "msa_pages_compact")}

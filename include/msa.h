@@ -431,7 +431,8 @@ typedef struct {
  * args and the SM count; not by the lengths). Host-only. */
 msa_status msa_kv8_attn_workspace_size(const msa_kv8_attn_args* args, size_t* bytes);
 
-/* ws: 256-byte aligned, zero-filled once (msa_workspace_init); rules as above. */
+/* ws: 256-byte aligned, its first 256 bytes (the error flags) zero-filled once; what the others hold
+ * does not matter. Rules as above. */
 msa_status msa_kv8_attn(const msa_kv8_attn_args* args, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- pages
@@ -469,7 +470,8 @@ typedef struct {
   msa_page_plane planes[MSA_MAX_PLANES];
 } msa_page_pool;
 
-/* Bytes of workspace the page operators need (by num_seqs and num_pages). Host-only. */
+/* Bytes of workspace the page operators need (by num_seqs and num_pages): 256-byte aligned, the first 256
+ * bytes zero-filled once; one workspace serves the calls on one stream. Host-only. */
 msa_status msa_pages_workspace_size(const msa_page_pool* pool, size_t* bytes);
 
 /* Copy page src[i] to page dst[i] in every plane, i < n: the first tokens[i] slots of each
