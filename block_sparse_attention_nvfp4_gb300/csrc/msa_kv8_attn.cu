@@ -59,11 +59,12 @@
 //     to 8 rows 6 % slower.)
 //
 // What bounds it now: long decode, memory (0.96 of the copy rate in the first line above; the same work on
-// pages that L2 holds takes 575 us). Prompts, the roles' instruction streams: a tile costs a CTA about 900
-// ns against 1,024 cycles of tensor work with BF16 queries and 768 with E4M3, so that these gain only
-// 2 %; most of it are the dependent instructions of single warps between two hand-overs. What the loops
-// hold in registers and how long their code is count for more there than the work in them: reading a
-// row's maximum in a loop unrolled twice costs a prompt 4 % (BF16) or 6 % (E4M3), four times 29 or 45 %.
+// pages that L2 holds takes 575 us). Prompts, the roles' instruction streams: a tile costs a CTA 1,720
+// cycles against 1,024 of tensor work with BF16 queries (62 % by the counter) and 1,700 against 768 with
+// E4M3 (47 %), which therefore gain only 2 %; most of it are the dependent instructions of single warps
+// between two hand-overs. What the loops hold in registers and how long their code is count for more
+// there than the work in them: reading a row's maximum in a loop unrolled twice costs a prompt 4 % (BF16)
+// or 6 % (E4M3), four times 29 or 45 %.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
