@@ -122,8 +122,14 @@ struct Kv8AttnParams {
   uint8_t* parts;            // workspace: the CTAs' headers and partials
   uint16_t* out;
   float* lse;
+  // msa_kv8_attn_window
+  int window, sinks, sink_pages;
+  // msa_kv8_attn_shared
+  int num_groups;
+  const int4* groups;        // [num_groups] {shared pages (0: none), first row, rows, first member}
+  const int32_t* skip;       // [num_reqs] pages that a request's group has for it
+  float* halves;             // [2][total_rows][heads][128], then [2][total_rows][heads] log2 of the sums
 };
-cudaError_t launch_kv8_attn(const CUtensorMap& kmap, const Kv8AttnParams& prm, bool q_bf16, int grid, cudaStream_t st);
 
 // Merge of the rank-local candidate lists of indexer decode context parallelism
 // (msa_dcp_merge_topk).

@@ -1,0 +1,34 @@
+// msa_kv8_attn_window: attention over the 8-bit cache to a window of the last tokens and to the first ones (sinks).
+// A row at position p sees t <= p with t > p - window or t < sinks. The kernel is msa_kv8_attn.cuh's: a chunk's tiles
+// are the sinks' pages and those from its first row's window to its last row, so the pages between are neither looked
+// up nor read, and the line of tiles that the CTAs share counts what is left. A chunk has at most `window` rows, so
+// that a token which its last row has left is never one that its first row does not see yet: what a NaN value
+// reaches is then a prefix or a suffix of the rows.
+// Floor and bounds: those of msa_kv8_attn over the tokens seen.
+#include "msa_kv8_attn.cuh"
+
+using namespace msa;
+
+extern "C" {
+
+msa_status msa_kv8_attn_window(const msa_kv8_attn_args* a, int32_t window, int32_t sinks, void* ws, size_t ws_bytes,
+                               void* stream) {
+  msa_status s = check_args(a);
+  if (s != MSA_OK) return s;
+  if (window < 1 || sinks < 0 || a->n_block_ids != 0) return MSA_ERR_INVALID_ARG;
+  Kv8AttnParams p;
+  CUtensorMap kmap;
+  int sms = 0, copies = 0;
+  if ((s = set_params(a, ws, ws_bytes, 0, a->max_rows_per_req, &p, &kmap, &sms, &copies)) != MSA_OK) return s;
+  if (a->num_reqs == 0 || a->total_rows == 0) return MSA_OK;
+  const int most = a->max_pages_per_req * kBlock;  // (no request is longer)
+  p.window = window < most ? window : most;
+  p.sinks = sinks < most ? sinks : most;
+  p.sink_pages = (p.sinks + kBlock - 1) / kBlock;
+  while (p.chunk > p.window) p.chunk /= 2, --p.chunk_log2;
+  const cudaError_t e =
+      launch_form<kWindow>(kmap, p, copies, a->q_type == MSA_TYPE_BF16, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+}
+
+}  // extern "C"

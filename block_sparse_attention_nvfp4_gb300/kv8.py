@@ -14,6 +14,7 @@ import torch
 from . import _lib
 
 DIM, BLOCK = 128, 128
+_INT_MAX = 2 ** 31 - 1
 _SRC_TYPES = {torch.bfloat16: _lib.TYPE_BF16, torch.float16: _lib.TYPE_F16, torch.float32: _lib.TYPE_F32}
 _Q_TYPES = {torch.uint8: _lib.TYPE_E4M3, torch.float8_e4m3fn: _lib.TYPE_E4M3, torch.bfloat16: _lib.TYPE_BF16}
 
@@ -174,11 +175,14 @@ class KV8Cache(_Handle):
 class KV8Attention:
     """Attention over a KV8Cache for a batch; owns its workspace and outputs (`out` BF16
     [rows, heads, 128], `lse` FP32 [rows, heads]). Single tokens, speculative rows and prompts
-    (causal) take the same call; a batch of the same sizes can be bound with `rebind`, and tensors
+    (causal) take the same call, to all tokens, to listed blocks, to a window and sinks, or with the pages
+    that requests have in common read once (`attend_shared`, for up to `max_groups` groups: their
+    workspace is laid out here); a batch of the same sizes can be bound with `rebind`, and tensors
     that were replaced in the cache or in the batch (a KV8Batch or a DecodeBatch) are seen by the
     next call, which raises when they do not fit."""
 
-    def __init__(self, cache: KV8Cache, batch: KV8Batch, sm_scale: Optional[float] = None, with_lse: bool = True):
+    def __init__(self, cache: KV8Cache, batch: KV8Batch, sm_scale: Optional[float] = None, with_lse: bool = True,
+                 max_groups: int = 0):
         self.cache = cache
         self.sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(DIM)
         self.device = cache.k_data.device
@@ -188,11 +192,15 @@ class KV8Attention:
         self.out = torch.empty((rows, heads, DIM), dtype=torch.bfloat16, device=self.device)
         self.lse = torch.empty((rows, heads), dtype=torch.float32, device=self.device) if with_lse else None
         self.rebind(batch)
-        n = ctypes.c_size_t(0)
+        self.max_groups = int(max_groups)
+        n, more = ctypes.c_size_t(0), ctypes.c_size_t(0)
         with torch.cuda.device(self.device):
-            _lib._check(_lib.load().msa_kv8_attn_workspace_size(ctypes.byref(self.args), ctypes.byref(n)),
-                        "msa_kv8_attn_workspace_size")
-            self.ws = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+            lib = _lib.load()
+            _lib._check(lib.msa_kv8_attn_workspace_size(self._ref, ctypes.byref(n)), "msa_kv8_attn_workspace_size")
+            if self.max_groups:
+                _lib._check(lib.msa_kv8_attn_shared_workspace_size(self._ref, self.max_groups, ctypes.byref(more)),
+                            "msa_kv8_attn_shared_workspace_size")
+            self.ws = torch.empty(max(n.value, more.value), dtype=torch.uint8, device=self.device)
             _lib.msa_workspace_init(self.ws[:256])   # the flags: a call on another stream may follow at once
         self._ws = (self.ws.data_ptr(), self.ws.numel())
 
@@ -238,14 +246,27 @@ class KV8Attention:
                     batch.total_rows == a.total_rows and batch.max_rows_per_req == a.max_rows_per_req and
                     (t[0].data_ptr(), t[1].data_ptr(), t[2].data_ptr()) == self._batch_at[4:])
 
-    def attend(self, block_ids: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    def _current(self):
+        """The arguments, marshalled again if a tensor was replaced."""
+        if self.cache._pointers() is not self._cache_at or self._batch_changed(self.batch):
+            self.rebind(self.batch)
+        return self.args
+
+    def attend(self, block_ids: Optional[torch.Tensor] = None, stream=None, *, window: Optional[int] = None,
+               sinks: int = 0) -> torch.Tensor:
         """softmax(sm_scale q k) v of every row over the keys it may see: of all blocks, or of
         those in block_ids (int32 [B, H, n <= 32], -1 = unused), e.g. the ones that
-        MSADecoder.select_blocks chose. Returns `out`; `lse` has ln(sum(exp))."""
-        batch = self.batch
-        if self.cache._pointers() is not self._cache_at or self._batch_changed(batch):
-            self.rebind(batch)
-        a = self.args
+        MSADecoder.select_blocks chose; with a window, its last `window` keys (its own among them) and
+        the first `sinks` ones. Returns `out`; `lse` has ln(sum(exp))."""
+        a = self._current()
+        if window is not None:
+            _need(block_ids is None, "block_ids: not with a window")
+            _need(0 < window <= _INT_MAX and 0 <= sinks <= _INT_MAX, f"window, sinks: expected at least 1 and 0, got {window}, {sinks}")
+            a.block_ids, a.n_block_ids = None, 0
+            _call(self.device, stream, _lib.load().msa_kv8_attn_window, "msa_kv8_attn_window", self._ref, window, sinks,
+                  self._ws[0], self._ws[1])
+            return self.out
+        _need(sinks == 0, "sinks: only with a window")
         if block_ids is None:
             a.block_ids, a.n_block_ids = None, 0
         else:
@@ -254,6 +275,19 @@ class KV8Attention:
             a.block_ids = _plain(block_ids, torch.int32, (a.num_reqs, a.num_kv_heads, n), self.device, "block_ids")
             a.n_block_ids = n
         _call(self.device, stream, _lib.load().msa_kv8_attn, "msa_kv8_attn", self._ref, self._ws[0], self._ws[1])
+        return self.out
+
+    def attend_shared(self, group_indptr: torch.Tensor, stream=None) -> torch.Tensor:
+        """attend() to all keys, for requests whose block tables begin with the same pages: the leading pages
+        that the requests group_indptr[g] .. group_indptr[g+1] - 1 (int32 on the GPU, at most
+        max_groups groups) have in common are found and read once for all of the group's rows."""
+        n = group_indptr.numel() - 1
+        _need(0 <= n <= self.max_groups, f"group_indptr: expected 1 to {self.max_groups + 1} entries (max_groups), got {n + 1}")
+        a = self._current()
+        at = _plain(group_indptr, torch.int32, (n + 1,), self.device, "group_indptr")
+        a.block_ids, a.n_block_ids = None, 0
+        _call(self.device, stream, _lib.load().msa_kv8_attn_shared, "msa_kv8_attn_shared", self._ref, n, at, self._ws[0],
+              self._ws[1])
         return self.out
 
     def errors(self, stream=None) -> int:

@@ -435,6 +435,27 @@ msa_status msa_kv8_attn_workspace_size(const msa_kv8_attn_args* args, size_t* by
  * does not matter. Rules as above. */
 msa_status msa_kv8_attn(const msa_kv8_attn_args* args, void* ws, size_t ws_bytes, void* stream);
 
+/* Attention to a window and to the first tokens: a row at position p sees the keys t <= p with
+ * t > p - window or t < sinks (window >= 1, sinks >= 0; a row always sees its own token). Pages that no row
+ * of a request sees are neither looked up in its block table nor read, so their entries may be stale.
+ * block_ids NULL and n_block_ids 0; workspace (msa_kv8_attn_workspace_size) and everything else as for
+ * msa_kv8_attn, which a window of the whole context equals. */
+msa_status msa_kv8_attn_window(const msa_kv8_attn_args* args, int32_t window, int32_t sinks, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/* Attention for requests whose block tables begin with the same pages (as msa_pages_fork leaves them): what
+ * msa_kv8_attn computes, within the same bounds, with each group's common pages read once for all of its rows.
+ * Group g is the requests group_indptr[g] .. group_indptr[g+1] - 1 (device int32 [num_groups + 1], not decreasing,
+ * within 0 .. num_reqs); requests outside every group are taken alone. How many leading pages the rows of a
+ * group's members list in common is found on the device, in each call; only pages that all query rows of
+ * the group see whole are shared. A decreasing or out-of-range group_indptr sets MSA_FLAG_BAD_LENGTH and every
+ * request is taken alone; so are the members of a group one of whose lengths is inconsistent.
+ * block_ids NULL and n_block_ids 0. num_groups 0 .. 4096. The workspace holds both halves of every row in
+ * FP32: msa_kv8_attn_shared_workspace_size (host-only), its first 256 bytes zero-filled once. */
+msa_status msa_kv8_attn_shared_workspace_size(const msa_kv8_attn_args* args, int32_t num_groups, size_t* bytes);
+msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* args, int32_t num_groups, const int32_t* group_indptr, void* ws,
+                               size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- pages
  *
  * A pool of pages shared by sequences, and the operators that move them. All state is on
