@@ -33,7 +33,8 @@ EXPORTS = ("msa_status_string", "msa_workspace_size", "msa_workspace_init", "msa
            "msa_selftest_wait_timeout", "msa_sparse_attn_decode_small_rows", "msa_kv8_append",
            "msa_kv8_attn_workspace_size", "msa_kv8_attn", "msa_pages_workspace_size", "msa_pages_copy",
            "msa_pages_fork", "msa_pages_reserve", "msa_pages_free", "msa_pages_compact", "msa_kv8_attn_window",
-           "msa_kv8_attn_shared", "msa_kv8_attn_shared_workspace_size")
+           "msa_kv8_attn_shared", "msa_kv8_attn_shared_workspace_size", "msa_kv8_attn_weights",
+           "msa_kv8_attn_weights_workspace_size")
 
 
 class MSAError(RuntimeError):
@@ -143,6 +144,8 @@ def load(path: str = LIB_PATH):
             lib.msa_kv8_attn_window.argtypes = [ctypes.POINTER(Kv8AttnArgs), i32, i32, vp, sz, vp]
             lib.msa_kv8_attn_shared_workspace_size.argtypes = [ctypes.POINTER(Kv8AttnArgs), i32, ctypes.POINTER(sz)]
             lib.msa_kv8_attn_shared.argtypes = [ctypes.POINTER(Kv8AttnArgs), i32, vp, vp, sz, vp]
+            lib.msa_kv8_attn_weights_workspace_size.argtypes = [ctypes.POINTER(Kv8AttnArgs), ctypes.POINTER(sz)]
+            lib.msa_kv8_attn_weights.argtypes = [ctypes.POINTER(Kv8AttnArgs), vp, ctypes.c_float, vp, vp, i64, vp, sz, vp]
             pp = ctypes.POINTER(PagePoolArgs)
             lib.msa_pages_workspace_size.argtypes = [pp, ctypes.POINTER(sz)]
             lib.msa_pages_copy.argtypes = [pp, i32, vp, vp, vp, vp, sz, vp]

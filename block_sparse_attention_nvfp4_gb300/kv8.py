@@ -176,13 +176,14 @@ class KV8Attention:
     """Attention over a KV8Cache for a batch; owns its workspace and outputs (`out` BF16
     [rows, heads, 128], `lse` FP32 [rows, heads]). Single tokens, speculative rows and prompts
     (causal) take the same call, to all tokens, to listed blocks, to a window and sinks, or with the pages
-    that requests have in common read once (`attend_shared`, for up to `max_groups` groups: their
-    workspace is laid out here); a batch of the same sizes can be bound with `rebind`, and tensors
+    that requests have in common read once (`attend_shared`, for up to `max_groups` groups);
+    `add_weights` (with_weights) says how much attention each cached token got. The workspace is laid out
+    for what is asked for here; a batch of the same sizes can be bound with `rebind`, and tensors
     that were replaced in the cache or in the batch (a KV8Batch or a DecodeBatch) are seen by the
     next call, which raises when they do not fit."""
 
     def __init__(self, cache: KV8Cache, batch: KV8Batch, sm_scale: Optional[float] = None, with_lse: bool = True,
-                 max_groups: int = 0):
+                 max_groups: int = 0, with_weights: bool = False):
         self.cache = cache
         self.sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(DIM)
         self.device = cache.k_data.device
@@ -193,14 +194,18 @@ class KV8Attention:
         self.lse = torch.empty((rows, heads), dtype=torch.float32, device=self.device) if with_lse else None
         self.rebind(batch)
         self.max_groups = int(max_groups)
-        n, more = ctypes.c_size_t(0), ctypes.c_size_t(0)
+        self.with_weights = bool(with_weights)
+        n, more, most = ctypes.c_size_t(0), ctypes.c_size_t(0), ctypes.c_size_t(0)
         with torch.cuda.device(self.device):
             lib = _lib.load()
             _lib._check(lib.msa_kv8_attn_workspace_size(self._ref, ctypes.byref(n)), "msa_kv8_attn_workspace_size")
             if self.max_groups:
                 _lib._check(lib.msa_kv8_attn_shared_workspace_size(self._ref, self.max_groups, ctypes.byref(more)),
                             "msa_kv8_attn_shared_workspace_size")
-            self.ws = torch.empty(max(n.value, more.value), dtype=torch.uint8, device=self.device)
+            if self.with_weights:
+                _lib._check(lib.msa_kv8_attn_weights_workspace_size(self._ref, ctypes.byref(most)),
+                            "msa_kv8_attn_weights_workspace_size")
+            self.ws = torch.empty(max(n.value, more.value, most.value), dtype=torch.uint8, device=self.device)
             _lib.msa_workspace_init(self.ws[:256])   # the flags: a call on another stream may follow at once
         self._ws = (self.ws.data_ptr(), self.ws.numel())
 
@@ -289,6 +294,26 @@ class KV8Attention:
         _call(self.device, stream, _lib.load().msa_kv8_attn_shared, "msa_kv8_attn_shared", self._ref, n, at, self._ws[0],
               self._ws[1])
         return self.out
+
+    def add_weights(self, old: Optional[torch.Tensor], new: torch.Tensor, keep: float = 1.0,
+                    lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """new[b, h, t] = keep old[b, h, t] + the softmax weights that token t of request b got from this batch's rows, over the
+        queries of KV head h; the batch's own tokens, whose slots are new, start from 0, and so does every token
+        with old None. FP32 [B, H, L], L at least the block table's tokens; `new` may be `old`. lse (FP32
+        [rows, heads]) is what attend() to all keys left in `lse`, unless given. Needs with_weights."""
+        _need(self.with_weights, "add_weights: make the object with with_weights=True")
+        a = self._current()
+        lse = self.lse if lse is None else lse
+        _need(lse is not None, "lse: expected one, as the object keeps none")
+        shape = (a.num_reqs, a.num_kv_heads, int(new.shape[-1]) if new.dim() else 0)
+        _need(shape[2] >= a.max_pages_per_req * BLOCK, f"new: expected at least {a.max_pages_per_req * BLOCK} tokens a head, got {shape[2]}")
+        at = _plain(new, torch.float32, shape, self.device, "new")
+        from_ = None if old is None else _plain(old, torch.float32, shape, self.device, "old")
+        lse_at = _plain(lse, torch.float32, tuple(self.out.shape[:2]), self.device, "lse")
+        a.block_ids, a.n_block_ids = None, 0
+        _call(self.device, stream, _lib.load().msa_kv8_attn_weights, "msa_kv8_attn_weights", self._ref, lse_at, keep, from_, at,
+              shape[2], self._ws[0], self._ws[1])
+        return new
 
     def errors(self, stream=None) -> int:
         """Device error flags since the last read (synchronises the stream)."""

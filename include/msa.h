@@ -456,6 +456,23 @@ msa_status msa_kv8_attn_shared_workspace_size(const msa_kv8_attn_args* args, int
 msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* args, int32_t num_groups, const int32_t* group_indptr, void* ws,
                                size_t ws_bytes, void* stream);
 
+/* Attention weights by token: what the softmax of this step's rows gave to each cached token,
+ *   new[b][h][t] = (t < N - R ? keep old[b][h][t] : 0) + sum exp(sm_scale q . k_t - lse),   t < N,
+ * the sum over the rows of request b that see t and the queries of KV head h. lse (device, FP32
+ * [total_rows][H q_per_kv]) is what msa_kv8_attn wrote for the same rows; rows whose lse is not finite, or
+ * whose query holds an infinity or a NaN, are left out. The request's own tokens (t >= N - R) are new and start from
+ * 0; old NULL or keep 0: so does every token. A request without rows gets keep old. Entries t >= N are left as they
+ * are. old and new: FP32 [num_reqs][H][head_stride], head_stride >= 128 max_pages_per_req; new may be old, and
+ * does not overlap it otherwise. keep: finite, >= 0 (below 1 for weights that fade).
+ * Scores are those of msa_kv8_attn, sums FP32 in an order that does not depend on timing. Tokens on pages
+ * outside [0, num_pages) get nothing from the rows and set MSA_FLAG_BAD_PAGE; requests with inconsistent lengths
+ * are left unwritten and set MSA_FLAG_BAD_LENGTH. Of args block_ids is NULL, n_block_ids 0, and v_data, v_scale,
+ * out and lse are not used. Workspace: msa_kv8_attn_weights_workspace_size (host-only), its first 256 bytes
+ * zero-filled once. */
+msa_status msa_kv8_attn_weights_workspace_size(const msa_kv8_attn_args* args, size_t* bytes);
+msa_status msa_kv8_attn_weights(const msa_kv8_attn_args* args, const float* lse, float keep, const float* old_weights,
+                                float* new_weights, int64_t head_stride, void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- pages
  *
  * A pool of pages shared by sequences, and the operators that move them. All state is on

@@ -79,3 +79,40 @@ def close(got, want, tol, what=""):
         i = tuple(int(x) for x in bad.nonzero()[0])
         raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {i}: got {got[i].item()}, "
                              f"want {want[i].item()} +- {tol[i].item()}")
+
+
+def weights(q, lse, cache, lens, indptr, table, old, keep, exact_q=True, sm_scale=1.0 / math.sqrt(DIM)):
+    """{(b, h): (new weights of tokens 0 .. N - 1, their bounds)} in 64 bits. lse: what the kernel was given.
+
+    The bounds: with a score's error d (as in attend) and its argument s log2 e - lse log2 e rounded three times in
+    FP32 (2^-23 of the larger of |s|, |lse|, times ln 2 / ln 2), a weight w moves by w (e^d' - 1); the exponential adds 2^-21;
+    n FP32 sums of non-negative numbers add n 2^-24 of the sum, of which the kernel's two chains see half each."""
+    rows, H, G = q.shape[:3]
+    lse = lse.double().view(rows, H, G)
+    got = {}
+    for b, n in enumerate(lens):
+        n, r0, r = int(n), int(indptr[b]), int(indptr[b + 1] - indptr[b])
+        t = torch.arange(n, device="cuda")
+        for h in range(H):
+            good, k, _, _ = tokens(cache, table[b], h, t)
+            dead = torch.isnan(k).any(1)
+            k = torch.nan_to_num(k)
+            w = torch.zeros(n, dtype=torch.float64, device="cuda")
+            tol = torch.zeros_like(w)
+            for r1 in range(0, r, 256):
+                p = torch.arange(n - r + r1, min(n, n - r + r1 + 256), device="cuda")
+                sl = slice(r0 + r1, r0 + r1 + len(p))
+                qq, y = q[sl, h], lse[sl, h]
+                use = torch.isfinite(y) & torch.isfinite(qq).all(-1)
+                qq = torch.nan_to_num(qq, posinf=0.0, neginf=0.0)
+                s = torch.einsum("rgd,td->rgt", qq, k) * sm_scale
+                seen = (t[None] <= p[:, None])[:, None] & use[..., None] & (good & ~dead)[None, None]
+                x = torch.where(seen, torch.exp(s - torch.where(use, y, 0.0)[..., None]), 0.0)
+                mag = torch.einsum("rgd,td->rgt", qq.abs(), k.abs()) * sm_scale
+                low = 0.0 if exact_q else (k.abs().sum(1) * sm_scale)[None, None] * qq.abs().amax(-1)[..., None] * 2.0 ** -17.8
+                d = 2.0 ** -16 * mag + low + 2.0 ** -22 * (s.abs() + torch.where(use, y, 0.0).abs()[..., None])
+                w += x.sum((0, 1))
+                tol += torch.where(seen, x * (torch.expm1(d) + 2.0 ** -21), 0.0).sum((0, 1))
+            first = torch.where(t < n - r, keep * old[b, h, :n].double(), 0.0) if old is not None else torch.zeros_like(w)
+            got[b, h] = first + w, tol + (r * G + 4) * 2.0 ** -24 * (w + first.abs()) + 1e-37
+    return got
