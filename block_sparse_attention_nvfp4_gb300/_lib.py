@@ -34,7 +34,7 @@ EXPORTS = ("msa_status_string", "msa_workspace_size", "msa_workspace_init", "msa
            "msa_kv8_attn_workspace_size", "msa_kv8_attn", "msa_pages_workspace_size", "msa_pages_copy",
            "msa_pages_fork", "msa_pages_reserve", "msa_pages_free", "msa_pages_compact", "msa_kv8_attn_window",
            "msa_kv8_attn_shared", "msa_kv8_attn_shared_workspace_size", "msa_kv8_attn_weights",
-           "msa_kv8_attn_weights_workspace_size")
+           "msa_kv8_attn_weights_workspace_size", "msa_pages_evict", "msa_pages_evict_scratch_size")
 
 
 class MSAError(RuntimeError):
@@ -101,6 +101,13 @@ class PagePoolArgs(ctypes.Structure):
                 ("ref_counts", ctypes.c_void_p), ("planes", PagePlane * MAX_PLANES)]
 
 
+class Kv8EvictCache(ctypes.Structure):
+    """Mirror of msa_kv8_evict_cache."""
+    _fields_ = [("k_data", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_data", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("head_stride", ctypes.c_int64),
+                ("num_kv_heads", ctypes.c_int32)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -153,6 +160,9 @@ def load(path: str = LIB_PATH):
             lib.msa_pages_reserve.argtypes = [pp, i32, vp, vp, vp, sz, vp]
             lib.msa_pages_free.argtypes = [pp, i32, vp, vp, sz, vp]
             lib.msa_pages_compact.argtypes = [pp, vp, vp, vp, vp, sz, vp]
+            cp = ctypes.POINTER(Kv8EvictCache)
+            lib.msa_pages_evict_scratch_size.argtypes = [pp, i32, cp, i32, i32, ctypes.POINTER(sz)]
+            lib.msa_pages_evict.argtypes = [pp, i32, vp, vp, i32, cp, i32, i32, i32, vp, sz, vp, sz, vp]
             for f in EXPORTS[1:]:
                 getattr(lib, f).restype = ctypes.c_int
             _lib = lib

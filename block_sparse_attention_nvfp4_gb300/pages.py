@@ -1,5 +1,5 @@
 """A pool of cache pages shared by sequences, on the device: copy, fork, reserve, free and compact
-without a synchronisation (msa_pages_* in include/msa.h)."""
+without a synchronisation, and sequences cut to their heaviest tokens (msa_pages_* in include/msa.h)."""
 from __future__ import annotations
 
 import ctypes
@@ -10,7 +10,7 @@ import torch
 
 from . import _lib
 from .api import KVCache
-from .kv8 import BLOCK, KV8Cache, _call, _need, _plain
+from .kv8 import _INT_MAX, BLOCK, KV8Cache, _call, _need, _plain
 
 _address = torch.Tensor.data_ptr
 
@@ -69,7 +69,8 @@ class PagePool:
             _lib.msa_workspace_init(self.ws[:256])   # the flags: a call on another stream may follow at once
         lib = _lib.load()
         self._fns = {n: getattr(lib, n) for n in ("msa_pages_copy", "msa_pages_fork", "msa_pages_reserve",
-                                                  "msa_pages_free", "msa_pages_compact")}
+                                                  "msa_pages_free", "msa_pages_compact", "msa_pages_evict")}
+        self._scratch, self._scratches = None, []   # evict's; outgrown ones live on, as captured graphs may hold them
         self._ref, self._ws, self._index = ctypes.byref(a), (self.ws.data_ptr(), self.ws.numel()), dev.index
 
     @staticmethod
@@ -133,6 +134,41 @@ class PagePool:
             t = _plain(block_table, torch.int32, (a.num_seqs, a.max_pages_per_seq), self.device, "block_table")
             r = self._list(ref_counts, a.num_pages, "ref_counts")
         self._run("msa_pages_compact", stream, t, r, None if num_live is None else self._list(num_live, 1, "num_live"))
+
+    def evict(self, parents: torch.Tensor, children: torch.Tensor, weights: Union[torch.Tensor, Sequence[torch.Tensor]],
+              keep: int, sinks: int = 0, recent: int = 0, stream=None):
+        """Make children[i] the parents[i] cut to `keep` tokens, on pages of its own: of a longer sequence every KV head
+        keeps the first `sinks`, the last `recent` and the heaviest others (equal weights: the lowest
+        positions), in the order of their positions. weights (one for each cache) are FP32 [S, H, L], L at least the
+        block table's tokens, a row for each sequence as KV8Attention.add_weights fills them; the children's
+        rows get the kept tokens' weights. A child is an empty sequence, or its own parent: the
+        sequence is cut where it stands, and its old pages are given back. All caches have to be KV8Caches."""
+        a, dev = self.args, self.device
+        weights = [weights] if isinstance(weights, torch.Tensor) else list(weights)
+        _need(all(isinstance(c, KV8Cache) for c in self.caches), "evict: every cache of the pool has to be a KV8Cache")
+        _need(len(weights) == len(self.caches) >= 1, f"weights: expected {len(self.caches)} (one for each cache), got {len(weights)}")
+        n = children.numel()
+        at = self._list(parents, n, "parents"), self._list(children, n, "children")
+        caches = (_lib.Kv8EvictCache * len(weights))()
+        for x, c, w in zip(caches, self.caches, weights):
+            _, _, x.num_kv_heads, x.k_data, x.k_scale, x.v_data, x.v_scale = c._pointers()
+            shape = (a.num_seqs, x.num_kv_heads, int(w.shape[-1]) if w.dim() else 0)
+            _need(shape[2] >= a.max_pages_per_seq * BLOCK,
+                  f"weights: expected at least {a.max_pages_per_seq * BLOCK} tokens a head, got {shape[2]}")
+            x.weights, x.head_stride = _plain(w, torch.float32, shape, dev, "weights"), shape[2]
+        _need(0 < keep <= _INT_MAX and 0 <= sinks and 0 <= recent and sinks + recent <= keep,
+              f"evict: expected keep >= 1 and sinks + recent <= keep, got {keep}, {sinks}, {recent}")
+        need = ctypes.c_size_t(0)
+        _lib._check(_lib.load().msa_pages_evict_scratch_size(self._ref, len(weights), caches, n, keep, ctypes.byref(need)),
+                    "msa_pages_evict_scratch_size")
+        if self._scratch is None or self._scratch.numel() < need.value:
+            if self._scratch is not None:
+                self._scratches.append(self._scratch)
+            size = max(need.value, 2 * (self._scratch.numel() if self._scratch is not None else 0), 256)
+            with torch.cuda.device(dev), torch.cuda.stream(stream):
+                self._scratch = torch.empty(size, dtype=torch.uint8, device=dev)
+        self._run("msa_pages_evict", stream, n, *at, len(weights), caches, keep, sinks, recent, self._scratch.data_ptr(),
+                  self._scratch.numel())
 
     def errors(self, stream=None) -> int:
         """Device error flags since the last read (synchronises the stream)."""

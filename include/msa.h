@@ -556,6 +556,41 @@ msa_status msa_pages_free(const msa_page_pool* pool, int32_t n, const int32_t* s
 msa_status msa_pages_compact(const msa_page_pool* pool, int32_t* new_block_table, int32_t* new_ref_counts,
                              int32_t* num_live, void* ws, size_t ws_bytes, void* stream);
 
+/* Evict: child[i] becomes parents[i] cut to `keep` tokens, on pages of its own. Of a sequence of N > keep tokens
+ * every KV head of every cache keeps the first `sinks`, the last `recent` and the keep - sinks - recent others of the
+ * largest weight (equal weights: the lowest positions; negative ones and NaN count as 0). The kept tokens stand in the
+ * order of their positions, at positions 0 .. keep - 1: a head's tokens need not be another's. A sequence of at
+ * most `keep` tokens keeps all. The new pages are the lowest ids with count 0, given out in list order.
+ * weights [num_seqs][num_kv_heads][head_stride] are what msa_kv8_attn_weights adds up (row s: sequence s); the
+ * child's row gets the kept tokens' weights, its other entries stay.
+ * A new page's scale is the largest of its tokens' old scales (one that is not positive and finite counts
+ * as 0); a token's code is E4M3(E4M3(code) * old / new), the code as it was where old = new. Slots behind the
+ * last kept token stay. Tokens on pages outside the pool become zeros and set MSA_FLAG_BAD_PAGE.
+ * child = parent cuts a sequence where it stands: its old pages' counts fall by one (pages that others
+ * share stay theirs); one that has at most `keep` tokens is left as it is. Otherwise the child must be empty, and
+ * the parent stays. All parents are read as they were before the call; one that is cut where it stands may
+ * not be another entry's parent. A child appears once. MSA_FLAG_BAD_SEQ, MSA_FLAG_BAD_LENGTH and
+ * MSA_FLAG_NO_PAGE (there have to be ceil(keep / 128) free pages for each, before any is given back) as
+ * for msa_pages_fork: the entry does nothing.
+ * The pool's planes are not looked at: `caches` (host array, 1 .. 4) are all the caches on its pages. keep >= 1,
+ * sinks + recent <= keep, n <= num_seqs. scratch: device memory of msa_pages_evict_scratch_size bytes (host-only),
+ * 16-byte aligned, whatever it holds; ws as for the other page operators. */
+typedef struct {
+  uint8_t* k_data;             /* planes of an 8-bit cache, as in msa_kv8_append_args */
+  float* k_scale;
+  uint8_t* v_data;
+  float* v_scale;
+  float* weights;              /* [num_seqs][num_kv_heads][head_stride] */
+  int64_t head_stride;         /* >= 128 max_pages_per_seq */
+  int32_t num_kv_heads;        /* 1 .. 64 */
+} msa_kv8_evict_cache;
+
+msa_status msa_pages_evict_scratch_size(const msa_page_pool* pool, int32_t num_caches, const msa_kv8_evict_cache* caches,
+                                        int32_t n, int32_t keep, size_t* bytes);
+msa_status msa_pages_evict(const msa_page_pool* pool, int32_t n, const int32_t* parents, const int32_t* children,
+                           int32_t num_caches, const msa_kv8_evict_cache* caches, int32_t keep, int32_t sinks,
+                           int32_t recent, void* scratch, size_t scratch_bytes, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

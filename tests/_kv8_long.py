@@ -116,3 +116,69 @@ def weights(q, lse, cache, lens, indptr, table, old, keep, exact_q=True, sm_scal
             first = torch.where(t < n - r, keep * old[b, h, :n].double(), 0.0) if old is not None else torch.zeros_like(w)
             got[b, h] = first + w, tol + (r * G + 4) * 2.0 ** -24 * (w + first.abs()) + 1e-37
     return got
+
+
+def kept(w, n, keep, sinks, recent):
+    """Positions that a head keeps of n tokens with weights w (float32 numpy), in order."""
+    if n <= keep:
+        return np.arange(n)
+    t = np.arange(n)
+    must = (t < sinks) | (t >= n - recent)
+    key = np.where(w[:n] > 0, w[:n], np.float32(0.0))          # negative and NaN: 0
+    rest = t[~must]
+    order = rest[np.lexsort((rest, -key[rest].astype(np.float64)))]
+    return np.sort(np.concatenate([t[must], order[:keep - sinks - recent]]))
+
+
+def evict(state, caches, weights, parents, children, keep, sinks, recent):
+    """msa_pages_evict on numpy state, in place: state = (lens, table, refs); caches: dicts of k_data, k_scale, v_data,
+    v_scale; weights: one [S, H, L] for each. Entries that do nothing are left out."""
+    val = e4m3_values()
+    lens, table, refs = state
+    old_lens, old_table = lens.copy(), table.copy()
+    old = [{n: a.copy() for n, a in c.items()} for c in caches]
+    old_w = [w.copy() for w in weights]
+    free = [p for p in range(len(refs)) if refs[p] == 0]
+    inplace = {p for p, c in zip(parents, children) if p == c}
+    seen, out = set(), False
+    for par, ch in zip(parents, children):
+        if not (0 <= par < len(lens) and 0 <= ch < len(lens)):
+            continue
+        first, _ = ch not in seen, seen.add(ch)
+        if not first or (par != ch and (old_lens[ch] != 0 or par in inplace)):
+            continue
+        n = int(old_lens[par])
+        m = min(n, keep)
+        if n == 0 or (par == ch and n <= keep):
+            continue
+        need = (m + BLOCK - 1) // BLOCK
+        if out or need > len(free):      # (this entry and all later ones that need pages)
+            out = True
+            continue
+        ids, free = free[:need], free[need:]
+        for c, o, w, ow in zip(caches, old, weights, old_w):
+            for h in range(w.shape[1]):
+                t = kept(ow[par, h], n, keep, sinks, recent)
+                w[ch, h, :m] = ow[par, h, t]
+                page = old_table[par, t // BLOCK]
+                good = (page >= 0) & (page < len(refs))
+                pg = np.where(good, page, 0)
+                for k in ("k", "v"):
+                    s = o[k + "_scale"][pg, h].astype(np.float32)
+                    s = np.where(good & (s > 0) & np.isfinite(s), s, np.float32(0))
+                    codes = np.where(good[:, None], o[k + "_data"][pg, h, t % BLOCK], 0).astype(np.uint8)
+                    for i, p in enumerate(ids):
+                        a, b = i * BLOCK, min(m, (i + 1) * BLOCK)
+                        top = s[a:b].max()
+                        ratio = (s[a:b] / top if top > 0 else np.zeros(b - a, np.float32)).astype(np.float32)
+                        x = (val[codes[a:b]].astype(np.float32) * ratio[:, None]).astype(np.float64)
+                        c[k + "_data"][p, h, :b - a] = np.where((ratio == 1)[:, None], codes[a:b], e4m3_codes(x))
+                        c[k + "_scale"][p, h] = top
+        for p in ids:
+            refs[p] = 1
+        if par == ch:
+            for x in old_table[par, :(n + BLOCK - 1) // BLOCK]:
+                if 0 <= x < len(refs):
+                    refs[x] = max(0, refs[x] - 1)
+        table[ch, :need] = ids
+        lens[ch] = m
