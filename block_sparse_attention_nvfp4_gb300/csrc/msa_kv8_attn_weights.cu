@@ -9,15 +9,15 @@
 // kv8_weights_queries_kernel lays out once, with each row's factor and -lse log2 e: a prompt's queries
 // meet every page of keys, and would be converted 128 times otherwise. Sums are FP32.
 //
-// Work. A unit is two pages of keys against a chunk of 128 query rows ("columns"); each set of four epilogue warps
-// has one of the two pages, so the chunk is loaded once for both. A request's pairs of pages have as many units as
+// Work. A unit is four pages of keys (a "quad") against a chunk of 128 query rows ("columns"); each of four sets of
+// four warps has one of the pages, so the chunk is loaded once for all. A request's quads have as many units as
 // chunks see them (one for decode steps). All units form a line that the CTAs (one per SM) take in equal
-// contiguous ranges; a pair that is cut leaves its sums in the workspace, and kv8_weights_merge_kernel adds them
+// contiguous ranges; a quad that is cut leaves its sums in the workspace, and kv8_weights_merge_kernel adds them
 // up in order: no atomics, the same bits every time.
 //
-// Roles: a warp that finds the units and starts the copies (K pairs and query chunks by tensor copies, three
-// stages each), one that issues the products, and two sets of four that exponentiate and sum, each with two
-// score buffers in tensor memory.
+// Roles: a warp that finds the units and starts the copies (pages and query chunks by tensor copies, two stages
+// each), one that issues the products, and the four sets, which exponentiate and sum. A set has one score buffer: its
+// next scores are computed while the other sets are at work.
 //
 // Floors: few rows, memory (128 bytes of a key, 4 read and 4 written per token and head); prompts, exponentials and
 // products alike (two E4M3 products of 128 x 128 x 128 cost what 128 x 128 exponentials do).
@@ -28,14 +28,13 @@
 namespace msa {
 namespace {
 
-constexpr int kSets = 2, kMmaWarp = 8, kLoadWarp = 9, kThreads = 320;
-constexpr int kStages = 3;                    // of key pairs, and of query chunks
-constexpr int kBufs = 2;                      // score buffers of a set
+constexpr int kSets = 4, kMmaWarp = 4 * kSets, kLoadWarp = kMmaWarp + 1, kThreads = 32 * (kLoadWarp + 1);
+constexpr int kKStages = 2, kQStages = 2, kCStages = 4;  // of quads of keys, of query chunks, of their factors
 constexpr int kCols = 128;                    // columns of a chunk
-constexpr int kRing = 16;                     // units whose description is kept (at most 8 are under way)
+constexpr int kRing = 16;                     // units whose description is kept (fewer are under way)
 constexpr uint32_t kTileBytes = kBlock * kDim;
 constexpr uint32_t kTmemCols = 512;
-static_assert(kSets * kBufs * kCols <= static_cast<int>(kTmemCols), "TMEM");
+static_assert(kSets * kCols <= static_cast<int>(kTmemCols), "TMEM");
 
 struct WeightsParams {
   int num_reqs, total_rows, max_rows, num_pages, max_pages, num_kv_heads, q_per_kv;
@@ -51,40 +50,40 @@ struct WeightsParams {
   float* new_weights;
   long long stride;          // elements between heads
   uint32_t* flags;
-  uint8_t* parts;            // headers, then 2 partials of 256 sums for each CTA
+  uint8_t* parts;            // headers, then 2 partials of 512 sums for each CTA
   uint8_t* codes;            // [parts of a query][heads][rows x queries a head][128]
-  float* coef;               // [heads][rows x queries a head] factors of the scores (BF16 queries)
-  float* nlse;               // [heads][rows x queries a head] -lse log2 e; -inf: the row counts for nothing
+  float* coef;               // [heads][rows x queries a head] factors of the scores (BF16 queries); then a 0
+  float* nlse;               // [heads][rows x queries a head] -lse log2 e; then a -inf (-inf counts for nothing)
 };
 
-enum : int { kEnd = 1, kNewK = 2, kLastK = 4, kNewQ = 8, kLastQ = 16, kTile0 = 32, kTile1 = 64, kNoQ = 128 };
+enum : int { kEnd = 1, kNewK = 2, kLastK = 4, kNewQ = 8, kLastQ = 16, kNoQ = 32, kTile0 = 64 };  // kTile0 << e: page e is there
 struct alignas(16) Unit {
   int flags, pos0, first, N;  // position of the first token, of the first row; tokens
-  int c0, cols;               // first column, columns of the chunk that are there
-  float ks0, ks1;             // the pages' key scales
-  long long off;              // of the head's weights
-  int slot, pad;              // -1: the whole pair is this CTA's, else its partial
+  int c0, cols, slot, pad;    // first column, columns of the chunk that are there; -1: the whole quad is this CTA's, else
+                              // its partial
+  float ks[kSets];            // the pages' key scales
+  long long off, pad2;        // of the head's weights
 };
 
 template <int NP>
 struct Smem {
-  uint8_t k[kStages][kSets][kTileBytes];
-  uint8_t q[kStages][NP][kTileBytes];
-  float coef[kStages][kCols], nlse[kStages][kCols];
+  uint8_t k[kKStages][kSets][kTileBytes];
+  uint8_t q[kQStages][NP][kTileBytes];
+  float coef[kCStages][kCols], nlse[kCStages][kCols];
   Unit unit[kRing];
-  uint64_t told[kRing], k_full[kStages], k_empty[kStages], q_full[kStages], q_empty[kStages];
-  uint64_t s_full[kSets][kBufs], s_empty[kSets][kBufs], drain;
+  uint64_t told[kRing], k_full[kKStages][kSets], k_empty[kKStages], q_full[kQStages], q_empty[kQStages];
+  uint64_t c_full[kCStages], c_empty[kCStages], s_full[kSets], s_empty[kSets], drain;
   long long sums[kThreads], part[kThreads / 32];
   uint32_t taddr;
 };
 
 struct Header {
-  int tail;            // 1: partial 1 starts a pair that goes on in the next CTA's partial 0
-  int cont, cont_end;  // partial 0 goes on with an earlier CTA's pair; and ends it
-  int pos0, first, N;  // of the pair in partial 1
+  int tail;            // 1: partial 1 starts a quad that goes on in the next CTA's partial 0
+  int cont, cont_end;  // partial 0 goes on with an earlier CTA's quad; and ends it
+  int pos0, first, N;  // of the quad in partial 1
   long long off;
 };
-constexpr int kPairTokens = kSets * kBlock;
+constexpr int kQuadTokens = kSets * kBlock;
 __host__ __device__ inline size_t header_bytes(int grid) { return (grid * sizeof(Header) + 255) / 256 * 256; }
 
 __device__ __forceinline__ bool load_req(const WeightsParams& p, int b, int* N, int* R, int* r0) {
@@ -94,30 +93,31 @@ __device__ __forceinline__ bool load_req(const WeightsParams& p, int b, int* N, 
   return *N >= 0 && *N <= p.max_pages * static_cast<long long>(kBlock) && *R >= 0 && *R <= p.max_rows && *R <= *N &&
          *r0 >= 0 && *r0 <= p.total_rows - *R;
 }
-// The pairs of a request's head: pair i is seen by the chunks from max(0, 2 G i - a) on, a = ceil((N - R) G / 128)
-// (the first column that sees token 256 i is (256 i - (N - R)) G).
-struct Pairs {
-  int count, chunks, G;
+// The quads of a request's head: quad i is seen by the chunks from max(0, 4 G i - a) on, a = ceil((N - R) G / 128)
+// (the first column that sees token 512 i is (512 i - (N - R)) G).
+struct Quads {
+  int count, chunks, step;
   long long a;
-  __device__ __forceinline__ Pairs(int N, int R, int G_)
-      : count((N + kPairTokens - 1) / kPairTokens), chunks((R * G_ + kCols - 1) / kCols), G(G_),
-        a((static_cast<long long>(N - R) * G_ + kCols - 1) / kCols) {
-    if (chunks == 0) {  // no rows: a unit without columns for each pair, which copies what is kept
+  __device__ __forceinline__ Quads(int N, int R, int G)
+      : count((N + kQuadTokens - 1) / kQuadTokens), chunks((R * G + kCols - 1) / kCols), step(kSets * G),
+        a((static_cast<long long>(N - R) * G + kCols - 1) / kCols) {
+    if (chunks == 0) {  // no rows: a unit without columns for each quad, which copies what is kept
       chunks = 1;
       a = LLONG_MAX / 4;
     }
   }
   __device__ __forceinline__ int first_chunk(int i) const {
-    const long long j = 2LL * G * i - a;
+    const long long j = static_cast<long long>(step) * i - a;
     return j > 0 ? static_cast<int>(j) : 0;
   }
-  __device__ __forceinline__ long long before(int i) const {  // units before pair i
-    const long long k0 = a / (2 * G) + 1;                      // the first pair that not all chunks see
+  __device__ __forceinline__ long long before(int i) const {  // units before quad i
+    const long long k0 = a / step + 1;                         // the first quad that not all chunks see
     long long n = static_cast<long long>(i) * chunks;
-    if (i > k0) n -= G * (i * (i - 1LL) - k0 * (k0 - 1)) - a * (i - k0);
+    if (i > k0) n -= step * ((i * (i - 1LL) - k0 * (k0 - 1)) / 2) - a * (i - k0);
     return n;
   }
 };
+static_assert(kQuadTokens == kSets * kCols, "");
 
 // Query rows as the products take them: E4M3 codes head by head (two parts of a BF16 row, with 2^e), and -lse log2 e.
 // A warp per row and query head. Bound: memory, latency for few rows.
@@ -126,6 +126,10 @@ __global__ void __launch_bounds__(256) kv8_weights_queries_kernel(const WeightsP
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, G = p.q_per_kv, heads = p.num_kv_heads * G;
   const long long per = static_cast<long long>(p.total_rows) * G, n = per * p.num_kv_heads;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {  // columns that are not there
+    if constexpr (NP == 2) p.coef[n] = 0.f;
+    p.nlse[n] = -INFINITY;
+  }
   for (long long i = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < n; i += gridDim.x * 8LL) {
     const int row = static_cast<int>(i / heads), hd = static_cast<int>(i % heads);
     const long long to = (hd / G) * per + static_cast<long long>(row) * G + hd % G;
@@ -172,8 +176,8 @@ __global__ void __launch_bounds__(256) kv8_weights_queries_kernel(const WeightsP
   }
 }
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 template <int NP>
@@ -189,13 +193,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tid >= first && tid < first + n) mbar_init(smem_u32(bar + (tid - first)), count);
     };
     init(sm.told, kRing, 0, 1);
-    init(sm.k_full, kStages, 16, 1);
-    init(sm.k_empty, kStages, 20, 1);
-    init(sm.q_full, kStages, 24, 33);
-    init(sm.q_empty, kStages, 28, 1 + 4 * kSets);
-    init(&sm.s_full[0][0], kSets * kBufs, 32, 1);
-    init(&sm.s_empty[0][0], kSets * kBufs, 36, 4);
-    init(&sm.drain, 1, 40, 1);
+    init(&sm.k_full[0][0], kKStages * kSets, 16, 1);
+    init(sm.k_empty, kKStages, 24, 1);
+    init(sm.q_full, kQStages, 26, 1);
+    init(sm.q_empty, kQStages, 28, 1);
+    init(sm.c_full, kCStages, 30, 32);
+    init(sm.c_empty, kCStages, 34, 4 * kSets);
+    init(sm.s_full, kSets, 38, 1);
+    init(sm.s_empty, kSets, 42, 4);
+    init(&sm.drain, 1, 46, 1);
     if (tid < 64) mbar_fence_init();
   }
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&sm.taddr), kTmemCols);
@@ -209,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = b0; b < b1; ++b) {
       int N, R, r0;
       if (load_req(p, b, &N, &R, &r0)) {
-        const Pairs x(N, R, G);
+        const Quads x(N, R, G);
         incl += p.num_kv_heads * x.before(x.count);
       } else if (blockIdx.x == 0) {
         set_flag(p.flags, kFlagBadLength);
@@ -234,7 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     Header hd = {};
     int u = 0;
     bool good = true, waited = false;
-    Ring<kStages> rk, rq;
+    Ring<kKStages> rk;
+    Ring<kQStages> rq;
+    Ring<kCStages> rc;
     int nk = 0, nq = 0;
     long long left = 0, start = 0;  // units in the range; the first one's offset in request b
     int b = 0;
@@ -268,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           int N, R, r0;
           long long n = 0;
           if (load_req(p, b, &N, &R, &r0)) {
-            const Pairs x(N, R, G);
+            const Quads x(N, R, G);
             n = p.num_kv_heads * x.before(x.count);
           }
           if (lo < at + n) break;
@@ -285,13 +293,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++b >= p.num_reqs) break;
         continue;
       }
-      const Pairs x(N, R, G);
+      const Quads x(N, R, G);
       const long long per_head = x.before(x.count);
       if (per_head == 0) {
         if (++b >= p.num_reqs) break;
         continue;
       }
-      int i = 0, at = 0;  // the pair, and the CTA's place in it
+      int i = 0, at = 0;  // the quad, and the CTA's place in it
       if (h < 0) {
         h = static_cast<int>(start / per_head);
         const long long off = start - h * per_head;
@@ -310,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int base = -32, phys = -1, have_q = -1;  // lanes hold tiles base .. base + 31
       float ks = 0.f;
       for (; i < x.count && left > 0 && good; ++i) {
-        if (2 * i >= base + 32) {
-          base = 2 * i;
+        if (kSets * i >= base + 32) {
+          base = kSets * i;
           phys = -1;
           ks = 0.f;
           if (base + lane < tiles) {
@@ -324,8 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const int p0 = __shfl_sync(0xFFFFFFFFu, phys, 2 * i - base), p1 = __shfl_sync(0xFFFFFFFFu, phys, 2 * i + 1 - base);
-        const float ks0 = __shfl_sync(0xFFFFFFFFu, ks, 2 * i - base), ks1 = __shfl_sync(0xFFFFFFFFu, ks, 2 * i + 1 - base);
+        // lane e < 4: page e of the quad
+        const int page = __shfl_sync(0xFFFFFFFFu, phys, kSets * i - base + (lane & (kSets - 1)));
+        const float scale = __shfl_sync(0xFFFFFFFFu, ks, kSets * i - base + (lane & (kSets - 1)));
+        const int there = __ballot_sync(0xFFFFFFFFu, page >= 0) & ((1 << kSets) - 1);
         const int j0 = x.first_chunk(i), n = x.chunks - j0;
         const int take = n - at < left ? n - at : static_cast<int>(left);
         const bool begin = at == 0, end = at + take == n;
@@ -333,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long off = (static_cast<long long>(b) * p.num_kv_heads + h) * p.stride;
         if (slot == 1) {
           hd.tail = 1;
-          hd.pos0 = i * kPairTokens;
+          hd.pos0 = i * kQuadTokens;
           hd.first = N - R;
           hd.N = N;
           hd.off = off;
@@ -343,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         left -= take;
         for (int j = j0 + at; j < j0 + at + take && good; ++j, ++u) {
-          int flags = (p0 >= 0 ? kTile0 : 0) | (p1 >= 0 ? kTile1 : 0);
+          int flags = there * kTile0;
           const bool new_k = j == j0 + at, last_k = j + 1 == j0 + at + take;
           const bool new_q = cols > 0 && have_q != j;
           const bool same_next = last_k && i + 1 < x.count && left > 0 && x.first_chunk(i + 1) == j;
@@ -353,32 +363,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (new_q) flags |= kNewQ;
           if (cols == 0) flags |= kNoQ;
           else if (!same_next) flags |= kLastQ;
-          if (new_k && nk >= kStages) good = warp_wait(smem_u32(&sm.k_empty[rk.at]), rk.phase ^ 1u, p.flags);
-          if (good && new_q && nq >= kStages) good = warp_wait(smem_u32(&sm.q_empty[rq.at]), rq.phase ^ 1u, p.flags);
+          if (new_k && nk >= kKStages) good = warp_wait(smem_u32(&sm.k_empty[rk.at]), rk.phase ^ 1u, p.flags);
+          if (good && new_q && nq >= kQStages) good = warp_wait(smem_u32(&sm.q_empty[rq.at]), rq.phase ^ 1u, p.flags);
+          if (good && new_q && nq >= kCStages) good = warp_wait(smem_u32(&sm.c_empty[rc.at]), rc.phase ^ 1u, p.flags);
           if (!good) break;
           if (lane == 0) {
             Unit& x1 = sm.unit[u % kRing];
             x1.flags = flags;
-            x1.pos0 = i * kPairTokens;
+            x1.pos0 = i * kQuadTokens;
             x1.first = N - R;
             x1.N = N;
             x1.c0 = kCols * j;
             x1.cols = here;
-            x1.ks0 = ks0;
-            x1.ks1 = ks1;
-            x1.off = off;
             x1.slot = slot;
-            mbar_arrive(smem_u32(&sm.told[u % kRing]));
-            if (new_k) {
-              const uint32_t kb = smem_u32(&sm.k_full[rk.at]);
-              const uint32_t bytes = cols == 0 ? 0u : ((p0 >= 0 ? kTileBytes : 0u) + (p1 >= 0 ? kTileBytes : 0u));
-              if (bytes > 0) {
-                mbar_arrive_expect_tx(kb, bytes);
-                if (p0 >= 0) tma_load_2d(smem_u32(sm.k[rk.at][0]), &kmap, 0, (p0 * p.num_kv_heads + h) * kBlock, kb);
-                if (p1 >= 0) tma_load_2d(smem_u32(sm.k[rk.at][1]), &kmap, 0, (p1 * p.num_kv_heads + h) * kBlock, kb);
-              } else {
-                mbar_arrive(kb);
-              }
+            x1.off = off;
+          }
+          if (lane < kSets) sm.unit[u % kRing].ks[lane] = scale;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.told[u % kRing]));
+          if (new_k && lane < kSets) {
+            const uint32_t kb = smem_u32(&sm.k_full[rk.at][lane]);
+            if (cols > 0 && page >= 0) {
+              mbar_arrive_expect_tx(kb, kTileBytes);
+              tma_load_2d(smem_u32(sm.k[rk.at][lane]), &kmap, 0, (page * p.num_kv_heads + h) * kBlock, kb);
+            } else {
+              mbar_arrive(kb);
             }
           }
           __syncwarp();
@@ -386,18 +395,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!waited) pdl_wait_primary();  // (keys, lengths and tables are older than the kernel before)
             waited = true;
             const uint32_t qb = smem_u32(&sm.q_full[rq.at]);
+            const long long row = qrow0 + kCols * static_cast<long long>(j);
+            const long long all = static_cast<long long>(p.num_kv_heads) * p.total_rows * G;
 #pragma unroll
             for (int k = 0; k < kCols / 32; ++k) {
               const int c = 32 * k + lane;
-              const long long src = qrow0 + kCols * static_cast<long long>(j) + (c < here ? c : 0);
-              cp_async4(smem_u32(&sm.nlse[rq.at][c]), p.nlse + src, c < here ? 4u : 0u);
-              if constexpr (NP == 2) cp_async4(smem_u32(&sm.coef[rq.at][c]), p.coef + src, c < here ? 4u : 0u);
+              const long long src = c < here ? row + c : all;
+              cp_async4(smem_u32(&sm.nlse[rc.at][c]), p.nlse + src);
+              if constexpr (NP == 2) cp_async4(smem_u32(&sm.coef[rc.at][c]), p.coef + src);
             }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(qb) : "memory");
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sm.c_full[rc.at])) : "memory");
             if (lane == 0) {
               mbar_arrive_expect_tx(qb, NP * kTileBytes);
-              const long long row = qrow0 + kCols * static_cast<long long>(j);
-              const long long all = static_cast<long long>(p.num_kv_heads) * p.total_rows * G;
 #pragma unroll
               for (int part = 0; part < NP; ++part)
                 tma_load_2d(smem_u32(sm.q[rq.at][part]), &qmap, 0, static_cast<int>(row + part * all), qb);
@@ -406,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             have_q = j;
             ++nq;
             rq.step();
+            rc.step();
           }
           if (new_k) {
             ++nk;
@@ -426,46 +436,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!waited) pdl_wait_primary();
     // no copy may still be landing when the CTA leaves
-    for (int j = nk - kStages < 0 ? 0 : nk - kStages; j < nk; ++j)
-      if (!wait_bar(smem_u32(&sm.k_full[j % kStages]), (j / kStages) & 1, p.flags)) break;
-    for (int j = nq - kStages < 0 ? 0 : nq - kStages; j < nq; ++j)
-      if (!wait_bar(smem_u32(&sm.q_full[j % kStages]), (j / kStages) & 1, p.flags)) break;
+    for (int j = nk - kKStages < 0 ? 0 : nk - kKStages; j < nk; ++j)
+      for (int e = 0; e < kSets; ++e)
+        if (!wait_bar(smem_u32(&sm.k_full[j % kKStages][e]), (j / kKStages) & 1, p.flags)) break;
+    for (int j = nq - kQStages < 0 ? 0 : nq - kQStages; j < nq; ++j)
+      if (!wait_bar(smem_u32(&sm.q_full[j % kQStages]), (j / kQStages) & 1, p.flags)) break;
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (lane == 0) reinterpret_cast<Header*>(p.parts)[blockIdx.x] = hd;
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    // ================= products: set e's scores of unit u into its buffer u % 2
+    // ================= products: set e's scores of unit u into its buffer
     const uint32_t el = elect_one();
     const uint64_t kdesc0 = sdesc_kmajor_sw128(smem_u32(sm.k[0][0])), qdesc0 = sdesc_kmajor_sw128(smem_u32(sm.q[0][0]));
-    Ring<kStages> rk, rq;
+    Ring<kKStages> rk;
+    Ring<kQStages> rq;
     Ring<kRing> rt;
-    bool any = false;
-    for (int u = 0;; ++u, rt.step()) {
+    bool any = false, good = true;
+    for (int u = 0; good; ++u, rt.step()) {
       if (!warp_wait(smem_u32(&sm.told[rt.at]), rt.phase, p.flags)) break;
       const int flags = sm.unit[rt.at].flags;
       if (flags & kEnd) break;
       const int cols = sm.unit[rt.at].cols;
-      if (flags & kNewK && !warp_wait(smem_u32(&sm.k_full[rk.at]), rk.phase, p.flags)) break;
       if (flags & kNewQ && !warp_wait(smem_u32(&sm.q_full[rq.at]), rq.phase, p.flags)) break;
-      const uint32_t buf = u & 1u;
-      const uint32_t idesc = idesc_e4m3_f32(kBlock, cols > 0 ? (cols + 15) / 16 * 16 : 16, false, false);
-      bool good = true;
-#pragma unroll
-      for (int e = 0; e < kSets; ++e) {
-        if (u >= kBufs) good = warp_wait(smem_u32(&sm.s_empty[e][buf]), ((u >> 1) - 1) & 1, p.flags);
+      // (whole 32 columns: that is what the sets read; rows that are not the request's are finite)
+      const uint32_t idesc = idesc_e4m3_f32(kBlock, cols > 0 ? (cols + 31) / 32 * 32 : 32, false, false);
+      const uint64_t qdesc = qdesc0 + rq.at * NP * (kTileBytes >> 4);
+#pragma unroll 1
+      for (int e = 0; e < kSets && good; ++e) {
+        if (flags & kNewK) good = warp_wait(smem_u32(&sm.k_full[rk.at][e]), rk.phase, p.flags);
+        if (good && u > 0) good = warp_wait(smem_u32(&sm.s_empty[e]), (u - 1) & 1, p.flags);
         if (!good) break;
         tc_fence_after();
-        if (!(flags & kNoQ) && flags & (e == 0 ? kTile0 : kTile1)) {
-          const uint64_t kdesc = kdesc0 + (rk.at * kSets + e) * (kTileBytes >> 4), qdesc = qdesc0 + rq.at * NP * (kTileBytes >> 4);
+        if (!(flags & kNoQ) && flags & (kTile0 << e)) {
+          const uint64_t kdesc = kdesc0 + (rk.at * kSets + e) * (kTileBytes >> 4);
 #pragma unroll
           for (int part = 0; part < NP; ++part)
 #pragma unroll
             for (int kk = 0; kk < kDim / 32; ++kk)
-              mma_f8_ss_elect(el, tbase + (e * kBufs + buf) * kCols, kdesc + 2 * kk, qdesc + part * (kTileBytes >> 4) + 2 * kk,
-                              idesc, part > 0 || kk > 0);
+              mma_f8_ss_elect(el, tbase + e * kCols, kdesc + 2 * kk, qdesc + part * (kTileBytes >> 4) + 2 * kk, idesc,
+                              part > 0 || kk > 0);
           any = true;
         }
-        commit_elect(el, smem_u32(&sm.s_full[e][buf]));
+        commit_elect(el, smem_u32(&sm.s_full[e]));
       }
       if (!good) break;
       if (flags & kLastK) {
@@ -483,10 +495,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // ================= set e: exponentials and sums of page 2 i + e, a token per thread
+    // ================= set e: exponentials and sums of page 4 i + e, a token per thread
     const int e = warp / 4, quad = warp % 4, l = 32 * quad + lane;
-    const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
-    Ring<kStages> rq;
+    const uint32_t s_cols = tbase + (static_cast<uint32_t>(32 * quad) << 16) + e * kCols;
+    Ring<kCStages> rc;
     Ring<kRing> rt;
     float2 acc = make_float2(0.f, 0.f);
     float old = 0.f;
@@ -495,24 +507,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int4 x = *reinterpret_cast<const int4*>(&sm.unit[rt.at].flags);
       if (x.x & kEnd) break;
       const int4 y = *reinterpret_cast<const int4*>(&sm.unit[rt.at].c0);
-      const int4 z = *reinterpret_cast<const int4*>(&sm.unit[rt.at].off);
-      const long long off = static_cast<long long>(static_cast<uint32_t>(z.x)) | static_cast<long long>(z.y) << 32;
+      const float ks = sm.unit[rt.at].ks[e] * (NP == 1 ? p.sm_scale_log2 : 1.f);
+      const long long off = sm.unit[rt.at].off;
       const int t = x.y + kBlock * e + l;
       if (x.x & kNewK) {
         acc = make_float2(0.f, 0.f);
         old = 0.f;
-        if (z.z < 0 && p.old_weights != nullptr && t < x.z) old = p.keep * p.old_weights[off + t];  // (on its way meanwhile)
+        if (y.z < 0 && p.old_weights != nullptr && t < x.z) old = p.keep * p.old_weights[off + t];  // (on its way meanwhile)
       }
-      if (x.x & kNewQ && !warp_wait(smem_u32(&sm.q_full[rq.at]), rq.phase, p.flags)) break;
-      const uint32_t buf = u & 1u;
-      if (!warp_wait(smem_u32(&sm.s_full[e][buf]), (u >> 1) & 1, p.flags)) break;
-      if (!(x.x & kNoQ) && x.x & (e == 0 ? kTile0 : kTile1)) {
+      if (x.x & kNewQ && !warp_wait(smem_u32(&sm.c_full[rc.at]), rc.phase, p.flags)) break;
+      if (!warp_wait(smem_u32(&sm.s_full[e]), u & 1, p.flags)) break;
+      // the scores have been read (in registers): the buffer is free
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty[e]));
+      };
+      if (!(x.x & kNoQ) && x.x & (kTile0 << e)) {
         tc_fence_after();
-        const uint32_t s_cols = tbase + lane_base + (e * kBufs + buf) * kCols;
-        const float ks = __int_as_float(e == 0 ? y.z : y.w) * (NP == 1 ? p.sm_scale_log2 : 1.f);
         const float2 ks2 = make_float2(ks, ks);
-        const float* coef = sm.coef[rq.at];
-        const float* nlse = sm.nlse[rq.at];
+        const float* coef = sm.coef[rc.at];
+        const float* nlse = sm.nlse[rc.at];
         // the exponents' arguments of 4 columns
         auto args = [&](const uint32_t* v, int c, float2& a, float2& b) {
           const float4 n = *reinterpret_cast<const float4*>(nlse + c);
@@ -527,57 +542,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             b = __ffma2_rn(__fmul2_rn(b, ks2), make_float2(f.z, f.w), make_float2(n.z, n.w));
           }
         };
-        // the first column that sees the thread's token; the page's last token decides for all
+        // the columns before lo do not see the thread's token; the page's last token decides for all threads
         const long long last = static_cast<long long>(x.y + kBlock * e + kBlock - 1 - x.z) * G - y.x;
-        if (y.y == kCols && last <= 0) {
+        if (last <= 0) {  // (columns that are not there have factors that leave 0)
+          const int n = (y.y + 31) / 32;
 #pragma unroll 1
-          for (int ch = 0; ch < kCols / 32; ++ch) {
+          for (int ch = 0; ch < n; ++ch) {
             uint32_t v[32];
             tmem_ld32(s_cols + 32 * ch, v);
             tc_wait_ld();
+            if (ch + 1 == n) release();
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < 32; c += 4) {
               float2 a, b;
               args(v + c, 32 * ch + c, a, b);
               acc = __fadd2_rn(acc, make_float2(ex2(a.x), ex2(a.y)));
-              acc = __fadd2_rn(acc, make_float2(ex2(b.x), ex2(b.y)));
+              sum = __fadd2_rn(sum, make_float2(ex2(b.x), ex2(b.y)));
             }
+            acc = __fadd2_rn(acc, sum);
           }
         } else {
           const int ahead = t - x.z;  // of the first row
-          const int lo = ahead > 0 ? ahead * G - y.x : 0;
+          const int lo = ahead > 0 ? ahead * G - y.x : 0, n = (y.y + 15) / 16;
 #pragma unroll 1
-          for (int ch = 0; ch < (y.y + 15) / 16; ++ch) {
+          for (int ch = 0; ch < n; ++ch) {
             uint32_t v[16];
             tmem_ld16(s_cols + 16 * ch, v);
             tc_wait_ld();
+            if (ch + 1 == n) release();
 #pragma unroll
             for (int c = 0; c < 16; c += 4) {
               float2 a, b;
               const int at = 16 * ch + c;
               args(v + c, at, a, b);
-              acc.x += at >= lo && at < y.y ? ex2(a.x) : 0.f;
-              acc.y += at + 1 >= lo && at + 1 < y.y ? ex2(a.y) : 0.f;
-              acc.x += at + 2 >= lo && at + 2 < y.y ? ex2(b.x) : 0.f;
-              acc.y += at + 3 >= lo && at + 3 < y.y ? ex2(b.y) : 0.f;
+              acc.x += at >= lo ? ex2(a.x) : 0.f;
+              acc.y += at + 1 >= lo ? ex2(a.y) : 0.f;
+              acc.x += at + 2 >= lo ? ex2(b.x) : 0.f;
+              acc.y += at + 3 >= lo ? ex2(b.y) : 0.f;
             }
           }
         }
+      } else {
+        release();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&sm.s_empty[e][buf]));
-        if (x.x & kLastQ) mbar_arrive(smem_u32(&sm.q_empty[rq.at]));
+      if (x.x & kLastQ) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.c_empty[rc.at]));
+        rc.step();
       }
-      if (x.x & kLastQ) rq.step();
       if (x.x & kLastK) {
         float w = acc.x + acc.y;
         if (isnan(w)) w = 0.f;  // a NaN in the key: every row that sees it is NaN and counts for nothing
-        if (z.z < 0) {
+        if (y.z < 0) {
           if (t < x.w) p.new_weights[off + t] = old + w;
         } else {
-          reinterpret_cast<float*>(p.parts + header_bytes(gridDim.x))[(2LL * blockIdx.x + z.z) * kPairTokens + kBlock * e + l] = w;
+          reinterpret_cast<float*>(p.parts + header_bytes(gridDim.x))[(2LL * blockIdx.x + y.z) * kQuadTokens + kBlock * e + l] = w;
         }
       }
     }
@@ -590,16 +610,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Adds up the sums of a pair that starts in CTA blockIdx.x's range and ends in a later one's, in order.
-__global__ void __launch_bounds__(kPairTokens) kv8_weights_merge_kernel(const WeightsParams p, int grid) {
+// Adds up the sums of a quad that starts in CTA blockIdx.x's range and ends in a later one's, in order.
+__global__ void __launch_bounds__(kQuadTokens) kv8_weights_merge_kernel(const WeightsParams p, int grid) {
   pdl_wait_primary();
   const Header* hd = reinterpret_cast<const Header*>(p.parts);
   const Header me = hd[blockIdx.x];
   if (!me.tail) return;
   const float* part = reinterpret_cast<const float*>(p.parts + header_bytes(grid));
-  float w = part[(2LL * blockIdx.x + 1) * kPairTokens + threadIdx.x];
+  float w = part[(2LL * blockIdx.x + 1) * kQuadTokens + threadIdx.x];
   for (int i = blockIdx.x + 1; i < grid && hd[i].cont; ++i) {
-    w += part[2LL * i * kPairTokens + threadIdx.x];
+    w += part[2LL * i * kQuadTokens + threadIdx.x];
     if (hd[i].cont_end) break;
   }
   const int t = me.pos0 + threadIdx.x;
@@ -618,9 +638,9 @@ msa_status launch(const CUtensorMap& kmap, const CUtensorMap& qmap, const Weight
   kv8_weights_queries_kernel<NP><<<grid, 256, 0, st>>>(p);
   if (cudaGetLastError() != cudaSuccess) return MSA_ERR_CUDA;
   if (launch_after(kv8_weights_kernel<NP>, dim3(sms), kThreads, smem, st, kmap, qmap, p) != cudaSuccess) return MSA_ERR_CUDA;
-  // (pairs of one unit are never cut)
+  // (quads of one unit are never cut)
   if (static_cast<long long>(p.max_rows) * p.q_per_kv <= kCols) return MSA_OK;
-  return launch_after(kv8_weights_merge_kernel, dim3(sms), kPairTokens, 0, st, p, sms) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+  return launch_after(kv8_weights_merge_kernel, dim3(sms), kQuadTokens, 0, st, p, sms) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
@@ -632,9 +652,9 @@ Layout layout(const msa_kv8_attn_args* a, int sms) {
   const size_t np = a->q_type == MSA_TYPE_BF16 ? 2 : 1;
   Layout l;
   l.parts = 256;
-  l.coef = up256(l.parts + header_bytes(sms) + 2 * static_cast<size_t>(sms) * kPairTokens * sizeof(float));
-  l.nlse = up256(l.coef + (np == 2 ? rows * sizeof(float) : 0));
-  l.codes = up256(l.nlse + rows * sizeof(float));
+  l.coef = up256(l.parts + header_bytes(sms) + 2 * static_cast<size_t>(sms) * kQuadTokens * sizeof(float));
+  l.nlse = up256(l.coef + (np == 2 ? (rows + 1) * sizeof(float) : 0));
+  l.codes = up256(l.nlse + (rows + 1) * sizeof(float));
   l.total = up256(l.codes + np * rows * kDim);
   return l;
 }
