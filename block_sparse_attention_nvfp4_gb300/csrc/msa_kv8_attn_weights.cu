@@ -28,7 +28,7 @@
 namespace msa {
 namespace {
 
-constexpr int kSets = 4, kMmaWarp = 4 * kSets, kLoadWarp = kMmaWarp + 1, kThreads = 32 * (kLoadWarp + 1);
+constexpr int kSets = 4, kMmaWarp = 4 * kSets, kMmaWarps = 2, kLoadWarp = kMmaWarp + kMmaWarps, kThreads = 32 * (kLoadWarp + 1);
 constexpr int kKStages = 2, kQStages = 2, kCStages = 4;  // of quads of keys, of query chunks, of their factors
 constexpr int kCols = 128;                    // columns of a chunk
 constexpr int kRing = 16;                     // units whose description is kept (fewer are under way)
@@ -72,7 +72,7 @@ struct Smem {
   float coef[kCStages][kCols], nlse[kCStages][kCols];
   Unit unit[kRing];
   uint64_t told[kRing], k_full[kKStages][kSets], k_empty[kKStages], q_full[kQStages], q_empty[kQStages];
-  uint64_t c_full[kCStages], c_empty[kCStages], s_full[kSets], s_empty[kSets], drain;
+  uint64_t c_full[kCStages], c_empty[kCStages], s_full[kSets], s_empty[kSets], drain[kMmaWarps];
   long long sums[kThreads], part[kThreads / 32];
   uint32_t taddr;
 };
@@ -120,58 +120,83 @@ struct Quads {
 static_assert(kQuadTokens == kSets * kCols, "");
 
 // Query rows as the products take them: E4M3 codes head by head (two parts of a BF16 row, with 2^e), and -lse log2 e.
-// A warp per row and query head. Bound: memory, latency for few rows.
+// Half a warp per row and query head, 8 elements a lane; kRows of them are on their way at once, without which the
+// latency of a prompt's 65,696 rows was 15 us of 253. Bound: memory, latency for few rows.
 template <int NP>
 __global__ void __launch_bounds__(256) kv8_weights_queries_kernel(const WeightsParams p) {
+  constexpr int kRows = 4;
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, G = p.q_per_kv, heads = p.num_kv_heads * G;
-  const long long per = static_cast<long long>(p.total_rows) * G, n = per * p.num_kv_heads;
+  const int lane = threadIdx.x & 15;
+  const uint32_t G = p.q_per_kv, heads = p.num_kv_heads * G, per = p.total_rows * G, n = per * p.num_kv_heads;  // below 2^30
   if (blockIdx.x == 0 && threadIdx.x == 0) {  // columns that are not there
     if constexpr (NP == 2) p.coef[n] = 0.f;
     p.nlse[n] = -INFINITY;
   }
-  for (long long i = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < n; i += gridDim.x * 8LL) {
-    const int row = static_cast<int>(i / heads), hd = static_cast<int>(i % heads);
-    const long long to = (hd / G) * per + static_cast<long long>(row) * G + hd % G;
-    const float lse = p.lse[i];
-    const long long at = row * p.q_stride + hd * kDim + 4 * lane;
-    bool odd = !(fabsf(lse) <= 3.402823466e38f);  // -inf, inf, NaN
-    uint32_t hi, lo = 0u;
-    float coef = p.sm_scale_log2;
-    if constexpr (NP == 1) {
-      hi = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.q) + at);
-      odd |= __vcmpeq4(hi & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u;
-      odd = __any_sync(0xFFFFFFFFu, odd);
-    } else {
-      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + at);
-      uint32_t big = __vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu);
+  const uint32_t step = gridDim.x * 16u, half = threadIdx.x >> 4 & 1u;
+  for (uint32_t w0 = blockIdx.x * 16u + (threadIdx.x >> 5) * 2u; w0 < n; w0 += kRows * step) {  // (whole warps: they exchange)
+    const uint32_t i0 = w0 + half;
+    uint4 w[kRows];
+    float lse[kRows];
 #pragma unroll
-      for (int d = 1; d < 32; d *= 2) big = __vmaxu2(big, __shfl_xor_sync(0xFFFFFFFFu, big, d));
-      const uint32_t amax = max(big & 0xFFFFu, big >> 16);
-      odd |= amax >= 0x7F80u;
-      // the smallest 2^e with amax <= 448 2^e, not below 2^-120: the attention's split
-      int e = static_cast<int>(amax >> 7) - 127 - 8 + ((amax & 0x7Fu) > 0x60u ? 1 : 0);
-      e = e < -120 ? -120 : e;
-      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      coef *= odd ? 1.f : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      const uint32_t x[2] = {w.x, w.y};
-      hi = 0u;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float a = __uint_as_float(x[k] << 16) * inv, b = __uint_as_float(x[k] & 0xFFFF0000u) * inv;
-        const uint32_t hc = f32x2_e4m3x2(a, b);
-        const uint32_t hh = e4m3x2_f16x2(hc);
-        const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&hh));
-        hi |= hc << (16 * k);
-        lo |= f32x2_e4m3x2(a - hv.x, b - hv.y) << (16 * k);
+    for (int k = 0; k < kRows; ++k) {
+      const uint32_t i = i0 + k * step < n ? i0 + k * step : n - 1u, row = i / heads;
+      const long long at = row * p.q_stride + (i - row * heads) * kDim + 8 * lane;
+      lse[k] = p.lse[i];
+      if constexpr (NP == 1) {
+        const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.q) + at);
+        w[k] = make_uint4(x.x, x.y, 0u, 0u);
+      } else {
+        w[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at);
       }
     }
-    if (odd) hi = lo = 0u;
-    *reinterpret_cast<uint32_t*>(p.codes + to * kDim + 4 * lane) = hi;
-    if constexpr (NP == 2) *reinterpret_cast<uint32_t*>(p.codes + (n + to) * kDim + 4 * lane) = lo;
-    if (lane == 0) {
-      if constexpr (NP == 2) p.coef[to] = coef;
-      p.nlse[to] = odd ? -INFINITY : lse * -1.4426950408889634f;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const uint32_t i = i0 + k * step;
+      bool odd = !(fabsf(lse[k]) <= 3.402823466e38f);  // -inf, inf, NaN
+      uint2 hi, lo = make_uint2(0u, 0u);
+      float coef = p.sm_scale_log2;
+      if constexpr (NP == 1) {
+        hi = make_uint2(w[k].x, w[k].y);
+        uint32_t nan = __vcmpeq4(hi.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(hi.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+#pragma unroll
+        for (int d = 1; d < 16; d *= 2) nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, d);
+        odd |= nan != 0u;
+      } else {
+        const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+        uint32_t big = 0u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) big = __vmaxu2(big, x[c] & 0x7FFF7FFFu);
+#pragma unroll
+        for (int d = 1; d < 16; d *= 2) big = __vmaxu2(big, __shfl_xor_sync(0xFFFFFFFFu, big, d));
+        const uint32_t amax = max(big & 0xFFFFu, big >> 16);
+        odd |= amax >= 0x7F80u;
+        // the smallest 2^e with amax <= 448 2^e, not below 2^-120: the attention's split
+        int e = static_cast<int>(amax >> 7) - 127 - 8 + ((amax & 0x7Fu) > 0x60u ? 1 : 0);
+        e = e < -120 ? -120 : e;
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        coef *= odd ? 1.f : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        uint32_t hc[4], lc[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float a = __uint_as_float(x[c] << 16) * inv, b = __uint_as_float(x[c] & 0xFFFF0000u) * inv;
+          hc[c] = f32x2_e4m3x2(a, b);
+          const uint32_t hh = e4m3x2_f16x2(hc[c]);
+          const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&hh));
+          lc[c] = f32x2_e4m3x2(a - hv.x, b - hv.y);
+        }
+        hi = make_uint2(hc[0] | hc[1] << 16, hc[2] | hc[3] << 16);
+        lo = make_uint2(lc[0] | lc[1] << 16, lc[2] | lc[3] << 16);
+      }
+      if (i >= n) continue;
+      if (odd) hi = lo = make_uint2(0u, 0u);
+      const uint32_t row = i / heads, hd = i - row * heads, kv = hd / G;
+      const long long to = kv * per + row * G + (hd - kv * G);
+      *reinterpret_cast<uint2*>(p.codes + to * kDim + 8 * lane) = hi;
+      if constexpr (NP == 2) *reinterpret_cast<uint2*>(p.codes + (n + to) * kDim + 8 * lane) = lo;
+      if (lane == 0) {
+        if constexpr (NP == 2) p.coef[to] = coef;
+        p.nlse[to] = odd ? -INFINITY : lse[k] * -1.4426950408889634f;
+      }
     }
   }
 }
@@ -194,14 +219,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     init(sm.told, kRing, 0, 1);
     init(&sm.k_full[0][0], kKStages * kSets, 16, 1);
-    init(sm.k_empty, kKStages, 24, 1);
+    init(sm.k_empty, kKStages, 24, kMmaWarps);
     init(sm.q_full, kQStages, 26, 1);
-    init(sm.q_empty, kQStages, 28, 1);
+    init(sm.q_empty, kQStages, 28, kMmaWarps);
     init(sm.c_full, kCStages, 30, 32);
     init(sm.c_empty, kCStages, 34, 4 * kSets);
     init(sm.s_full, kSets, 38, 1);
     init(sm.s_empty, kSets, 42, 4);
-    init(&sm.drain, 1, 46, 1);
+    init(sm.drain, kMmaWarps, 46, 1);
     if (tid < 64) mbar_fence_init();
   }
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&sm.taddr), kTmemCols);
@@ -444,8 +469,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (lane == 0) reinterpret_cast<Header*>(p.parts)[blockIdx.x] = hd;
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ================= products: set e's scores of unit u into its buffer
+  } else if (warp >= kMmaWarp) {
+    // ================= products: set e's scores of unit u into its buffer, each warp for half of the sets (one warp for
+    // all took longer to issue them than the tensor cores to compute them)
+    const int part0 = (warp - kMmaWarp) * (kSets / kMmaWarps);
     const uint32_t el = elect_one();
     const uint64_t kdesc0 = sdesc_kmajor_sw128(smem_u32(sm.k[0][0])), qdesc0 = sdesc_kmajor_sw128(smem_u32(sm.q[0][0]));
     Ring<kKStages> rk;
@@ -462,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc = idesc_e4m3_f32(kBlock, cols > 0 ? (cols + 31) / 32 * 32 : 32, false, false);
       const uint64_t qdesc = qdesc0 + rq.at * NP * (kTileBytes >> 4);
 #pragma unroll 1
-      for (int e = 0; e < kSets && good; ++e) {
+      for (int e = part0; e < part0 + kSets / kMmaWarps && good; ++e) {
         if (flags & kNewK) good = warp_wait(smem_u32(&sm.k_full[rk.at][e]), rk.phase, p.flags);
         if (good && u > 0) good = warp_wait(smem_u32(&sm.s_empty[e]), (u - 1) & 1, p.flags);
         if (!good) break;
@@ -490,8 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (any) {  // every MMA of this thread has finished before the tensor memory is released
-      commit_elect(el, smem_u32(&sm.drain));
-      warp_wait(smem_u32(&sm.drain), 0, p.flags);
+      commit_elect(el, smem_u32(&sm.drain[warp - kMmaWarp]));
+      warp_wait(smem_u32(&sm.drain[warp - kMmaWarp]), 0, p.flags);
     }
     __syncwarp();
   } else {
@@ -633,7 +660,7 @@ msa_status launch(const CUtensorMap& kmap, const CUtensorMap& qmap, const Weight
   const int smem = static_cast<int>(sizeof(Smem<NP>)) + 1024;
   if (cudaFuncSetAttribute(kv8_weights_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return MSA_ERR_CUDA;
-  const long long rows = static_cast<long long>(p.total_rows) * p.num_kv_heads * p.q_per_kv, ctas = (rows + 7) / 8, cap = 8LL * sms;
+  const long long rows = static_cast<long long>(p.total_rows) * p.num_kv_heads * p.q_per_kv, ctas = (rows + 15) / 16, cap = 4LL * sms;
   const int grid = static_cast<int>(ctas < 1 ? 1 : ctas < cap ? ctas : cap);
   kv8_weights_queries_kernel<NP><<<grid, 256, 0, st>>>(p);
   if (cudaGetLastError() != cudaSuccess) return MSA_ERR_CUDA;
