@@ -71,6 +71,12 @@ class PagePool:
         self._fns = {n: getattr(lib, n) for n in ("msa_pages_copy", "msa_pages_fork", "msa_pages_reserve",
                                                   "msa_pages_free", "msa_pages_compact", "msa_pages_evict")}
         self._scratch, self._scratches = None, []   # evict's; outgrown ones live on, as captured graphs may hold them
+        self._evict_caches, self._evict_heads = None, 0
+        if self.caches and all(isinstance(c, KV8Cache) for c in self.caches):
+            self._evict_caches = (_lib.Kv8EvictCache * len(self.caches))()
+            for x, c in zip(self._evict_caches, self.caches):
+                _, _, x.num_kv_heads, x.k_data, x.k_scale, x.v_data, x.v_scale = c._pointers()
+                self._evict_heads += x.num_kv_heads
         self._ref, self._ws, self._index = ctypes.byref(a), (self.ws.data_ptr(), self.ws.numel()), dev.index
 
     @staticmethod
@@ -143,32 +149,31 @@ class PagePool:
         block table's tokens, a row for each sequence as KV8Attention.add_weights fills them; the children's
         rows get the kept tokens' weights. A child is an empty sequence, or its own parent: the
         sequence is cut where it stands, and its old pages are given back. All caches have to be KV8Caches."""
-        a, dev = self.args, self.device
-        weights = [weights] if isinstance(weights, torch.Tensor) else list(weights)
-        _need(all(isinstance(c, KV8Cache) for c in self.caches), "evict: every cache of the pool has to be a KV8Cache")
-        _need(len(weights) == len(self.caches) >= 1, f"weights: expected {len(self.caches)} (one for each cache), got {len(weights)}")
+        a, caches = self.args, self._evict_caches
+        if caches is None:
+            raise ValueError("evict: every cache of the pool has to be a KV8Cache, and at least one")
+        weights = (weights,) if isinstance(weights, torch.Tensor) else tuple(weights)
+        if len(weights) != len(caches):
+            raise ValueError(f"weights: expected {len(caches)} (one for each cache), got {len(weights)}")
         n = children.numel()
         at = self._list(parents, n, "parents"), self._list(children, n, "children")
-        caches = (_lib.Kv8EvictCache * len(weights))()
-        for x, c, w in zip(caches, self.caches, weights):
-            _, _, x.num_kv_heads, x.k_data, x.k_scale, x.v_data, x.v_scale = c._pointers()
-            shape = (a.num_seqs, x.num_kv_heads, int(w.shape[-1]) if w.dim() else 0)
-            _need(shape[2] >= a.max_pages_per_seq * BLOCK,
-                  f"weights: expected at least {a.max_pages_per_seq * BLOCK} tokens a head, got {shape[2]}")
-            x.weights, x.head_stride = _plain(w, torch.float32, shape, dev, "weights"), shape[2]
-        _need(0 < keep <= _INT_MAX and 0 <= sinks and 0 <= recent and sinks + recent <= keep,
-              f"evict: expected keep >= 1 and sinks + recent <= keep, got {keep}, {sinks}, {recent}")
-        need = ctypes.c_size_t(0)
-        _lib._check(_lib.load().msa_pages_evict_scratch_size(self._ref, len(weights), caches, n, keep, ctypes.byref(need)),
-                    "msa_pages_evict_scratch_size")
-        if self._scratch is None or self._scratch.numel() < need.value:
+        for x, w in zip(caches, weights):
+            tokens = w.shape[-1] if w.dim() else 0
+            if tokens < a.max_pages_per_seq * BLOCK:
+                raise ValueError(f"weights: expected at least {a.max_pages_per_seq * BLOCK} tokens a head, got {tokens}")
+            x.weights, x.head_stride = _plain(w, torch.float32, (a.num_seqs, x.num_kv_heads, tokens), self.device, "weights"), tokens
+        if not (0 < keep <= _INT_MAX and 0 <= sinks and 0 <= recent and sinks + recent <= keep):
+            raise ValueError(f"evict: expected keep >= 1 and sinks + recent <= keep, got {keep}, {sinks}, {recent}")
+        # (what msa_pages_evict_scratch_size says)
+        need = 8 * n * self._evict_heads * min(keep, a.max_pages_per_seq * BLOCK)
+        if self._scratch is None or self._scratch[1] < need:
             if self._scratch is not None:
                 self._scratches.append(self._scratch)
-            size = max(need.value, 2 * (self._scratch.numel() if self._scratch is not None else 0), 256)
-            with torch.cuda.device(dev), torch.cuda.stream(stream):
-                self._scratch = torch.empty(size, dtype=torch.uint8, device=dev)
-        self._run("msa_pages_evict", stream, n, *at, len(weights), caches, keep, sinks, recent, self._scratch.data_ptr(),
-                  self._scratch.numel())
+            size = max(need, 2 * (self._scratch[1] if self._scratch is not None else 0), 256)
+            with torch.cuda.device(self.device), torch.cuda.stream(stream):
+                t = torch.empty(size, dtype=torch.uint8, device=self.device)
+            self._scratch = (t.data_ptr(), size, t)
+        self._run("msa_pages_evict", stream, n, *at, len(caches), caches, keep, sinks, recent, *self._scratch[:2])
 
     def errors(self, stream=None) -> int:
         """Device error flags since the last read (synchronises the stream)."""
