@@ -1,16 +1,17 @@
 // Eviction (msa_pages_evict): a sequence cut to its first tokens, its last ones and, head by head, the heaviest
 // between, moved to pages of its own in the order of their positions. Two launches:
-//   * kv8_evict_select_kernel: its first CTA is the plan (checks, new pages: the lowest free ids in list order); the
-//     others take a (sequence, cache, head) each. The weight of the last token kept is found by radix
-//     selection: three histograms over 11, 10 and 10 bits of the weights as numbers (non-negative FP32 numbers
-//     order like their bits), then one pass that writes the kept positions and weights in order; of equal
-//     weights the lowest positions stay. Bound: latency and L2 (the weights are read four times, the first time
-//     from memory).
+//   * the first CTA of kv8_evict_select_kernel is the plan: checks, new pages (the lowest free ids in list order);
+//   * its others, one for each (sequence, cache, head): the weight of the last token kept is found by
+//     radix selection, three histograms over 11, 10 and 10 bits of the weights as numbers (non-negative FP32 numbers
+//     order like their bits), then the kept positions and weights are written in order; of equal weights the lowest
+//     positions stay. The weights are read once where they fit the registers (8,192 tokens), else four times.
+//     Bound: instructions and latency. (Clusters of two or four CTAs a head, whose histograms were added up through
+//     distributed shared memory, were no faster and slower: their reading took what the split saved.)
 //   * kv8_evict_move_kernel: a CTA per (sequence, cache, head, new page) gathers the codes of 128 kept tokens. The new
 //     page's scale is the largest of its tokens' pages'; codes of pages with that scale move as they are, the
 //     others are multiplied by the scales' ratio and rounded once (exact between powers of two but for what falls
 //     among the subnormals). Bound: memory, 128 bytes read here and there for each K and V row. The last CTA of a
-//     sequence rewrites its row of the block table, its length and its old pages' counts.
+//     sequence to have read its old row of the block table rewrites it, the length and the old pages' counts.
 // Ranks come from sums, so nothing depends on timing.
 #include "msa_kv8_pipe.cuh"
 #include "msa_pages.cuh"
@@ -18,7 +19,7 @@
 namespace msa {
 namespace {
 
-constexpr int kMoveThreads = 256;
+constexpr int kSelectThreads = 1024, kMoveThreads = 256;
 constexpr int kMaxCaches = MSA_MAX_PLANES / 4;
 
 struct EvictCache {
@@ -116,26 +117,59 @@ __device__ void plan(const Pool& p, const Lists& l, const EvictParams& e, int32_
       for (int k = tid & 31; k < l.src[i]; k += 32) p.refs[l.free_ids[l.dst[i] + k]] = 1;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) kv8_evict_select_kernel(const Pool p, const Lists l, const EvictParams e) {
-  __shared__ int32_t shared[kSmemSeqs];
-  __shared__ int s_digit, s_above;
-  __shared__ int w_sure[kPlanWarps], w_tie[kPlanWarps];
+// CTA 0: the plan. The others: one per (sequence, cache, head), x among all caches' heads.
+__global__ void __launch_bounds__(kSelectThreads) kv8_evict_select_kernel(const Pool p, const Lists l, const EvictParams e) {
+  static_assert(kSelectThreads == kPlanThreads, "");
+  constexpr int kWarps = kSelectThreads / 32;
+  // A round takes kRun x 4 tokens a thread: lanes have 4 in a row, warps 128, and the CTA's 4,096 follow each other.
+  constexpr int kRun = 2, kStep = 4 * kSelectThreads, kRound = kRun * kStep;
+  __shared__ int hist[kSmemSeqs];                    // by pass: 2,048, 1,024 and 1,024 digits; the plan's claims
+  static_assert(kSmemSeqs >= 4096, "");
+  __shared__ int w_part[kWarps], s_found[2];
+  __shared__ alignas(8) int2 w_kept[kRun * kWarps];  // by run and warp: tokens kept for sure, and ties
   pdl_launch_dependents();
   if (blockIdx.x == 0) {
-    plan(p, l, e, shared);
+    plan(p, l, e, hist);
     return;
   }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int i = (blockIdx.x - 1) / e.heads, x = (blockIdx.x - 1) % e.heads;
+  const int item = blockIdx.x - 1, i = item / e.heads, x = item % e.heads;
   const int par = e.parents[i];
-  if (!in(par, p.num_seqs)) return;
-  const int N = p.seq_lens[par];
+  const int N = in(par, p.num_seqs) ? p.seq_lens[par] : -1;
   if (!good_len(p, N) || N <= e.keep) return;
   int head;
   const EvictCache& c = e.caches[cache_of(e, x, &head)];
   const float* w = c.weights + (static_cast<long long>(par) * c.heads + head) * c.stride;
   const int lo = e.sinks, hi = N - e.recent;
   auto key = [](float v) { return v > 0.f ? __float_as_uint(v) : 0u; };  // (negative and NaN: 0)
+  const bool wide = (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
+  const int own = 128 * warp + 4 * lane;
+  // the next round's tokens are on their way while these are looked at (7 us a pass of 65,536 tokens without)
+  float4 v[kRun], next[kRun];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      const int t = base + kStep * k + own;
+      next[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (wide && t + 3 < N) {
+        next[k] = *reinterpret_cast<const float4*>(w + t);
+      } else {
+        if (t < N) next[k].x = w[t];
+        if (t + 1 < N) next[k].y = w[t + 1];
+        if (t + 2 < N) next[k].z = w[t + 2];
+        if (t + 3 < N) next[k].w = w[t + 3];
+      }
+    }
+  };
+  const bool once = N <= kRound;
+  auto step = [&](int base) {
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) v[k] = next[k];
+    if (!once) load(base + kRound < N ? base + kRound : 0);  // (the first again, for the pass that follows)
+  };
+  load(0);
+  for (int k = tid; k < 4096; k += kSelectThreads) hist[k] = 0;
+  __syncthreads();
 
   // the key of the last of the `m` heaviest in [lo, hi), and how many of the tokens that have it stay
   const int m = e.keep - e.sinks - e.recent;
@@ -145,99 +179,111 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_evict_select_kernel(const Po
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int bits = pass == 0 ? 11 : 10, shift = 20 - 10 * pass, bins = 1 << bits, above = shift + bits;
-      for (int k = tid; k < bins; k += kPlanThreads) shared[k] = 0;
-      __syncthreads();
-      constexpr int kRun = 8;
-      for (int base = lo; base < hi; base += kRun * kPlanThreads) {
-        float v[kRun];
+      int* h = hist + (pass == 0 ? 0 : 1024 + 1024 * pass);
+      for (int base = 0; base < N; base += kRound) {
+        step(base);
 #pragma unroll
         for (int k = 0; k < kRun; ++k) {
-          const int t = base + k * kPlanThreads + tid;
-          v[k] = t < hi ? w[t] : 0.f;
-        }
+          const int t0 = base + kStep * k + 128 * warp, t = t0 + 4 * lane;
+          if (t0 >= hi) break;
+          const float f[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+          const bool all = t0 >= lo && t0 + 127 < hi;
 #pragma unroll
-        for (int k = 0; k < kRun; ++k) {
-          const int t = base + k * kPlanThreads + tid;
-          const uint32_t u = key(v[k]);
-          if (t < hi && (pass == 0 || u >> above == found >> above)) atomicAdd(&shared[u >> shift & (bins - 1)], 1);
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t u = key(f[c]);
+            if ((pass == 0 || u >> above == found >> above) && (all || (t + c >= lo && t + c < hi)))
+              atomicAdd(&h[u >> shift & (bins - 1)], 1);
+          }
         }
       }
       __syncthreads();
       // from the highest digit down: the one where the count reaches `rest`
-      const int per = bins / kPlanThreads;  // 2 or 1
-      int mine = 0;
-      for (int k = 0; k < per; ++k) mine += shared[bins - 1 - (tid * per + k)];
-      int total;
-      int at = cta_exclusive_sum(mine, &total);
-      for (int k = 0; k < per; ++k) {
-        const int d = bins - 1 - (tid * per + k), n = shared[d];
-        if (at < rest && at + n >= rest) {
-          s_digit = d;
-          s_above = at;
-        }
-        at += n;
+      const int per = bins / kSelectThreads;  // 2 or 1
+      const int d0 = bins - 1 - tid * per, n0 = h[d0], n1 = per > 1 ? h[d0 - 1] : 0;
+      int incl = n0 + n1;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      if (lane == 31) w_part[warp] = incl;
+      __syncthreads();
+      const int at = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w_part[lane] : 0) + incl - n0 - n1;
+      if (at < rest && at + n0 + n1 >= rest) {
+        const bool second = at + n0 < rest;
+        s_found[0] = second ? d0 - 1 : d0;
+        s_found[1] = second ? at + n0 : at;
       }
       __syncthreads();
-      found |= static_cast<uint32_t>(s_digit) << shift;
-      rest -= s_above;
-      __syncthreads();
+      found |= static_cast<uint32_t>(s_found[0]) << shift;
+      rest -= s_found[1];
     }
   }
   const int ties = rest;
-  // the kept tokens in order: a warp has 256 in a row, 32 at a time
-  int32_t* pos = e.pos + (static_cast<long long>(i) * e.heads + x) * e.cap;
-  float* weight = e.weight + (static_cast<long long>(i) * e.heads + x) * e.cap;
+  // the kept tokens in order: sums over a lane's four, over lanes, over (run, warp); sure ones in the low half of a
+  // word, ties in the high one
+  int32_t* pos = e.pos + static_cast<long long>(item) * e.cap;
+  float* weight = e.weight + static_cast<long long>(item) * e.cap;
   int sure_all = 0, tie_all = 0;
-  constexpr int kRows = 8;
-  for (int base = 0; base < N; base += kRows * kPlanThreads) {
-    float v[kRows];
-    unsigned sure[kRows], tie[kRows];
-    const int t0 = base + warp * 32 * kRows + lane;
+  for (int base = 0; base < N; base += kRound) {
+    step(base);
+    uint32_t kind[kRun], incl[kRun];  // kind: 4 bits of sure tokens, then 4 of ties
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) v[k] = t0 + 32 * k < N ? w[t0 + 32 * k] : 0.f;
-    int n_sure = 0, n_tie = 0;
+    for (int k = 0; k < kRun; ++k) {
+      const int t0 = base + kStep * k + 128 * warp, t = t0 + 4 * lane;
+      const float f[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      kind[k] = 0u;
+      if (t0 >= lo && t0 + 127 < hi) {
+        if (m > 0)
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      const int t = t0 + 32 * k;
-      const bool fixed = t < lo || t >= hi;
-      const uint32_t u = key(v[k]);
-      sure[k] = __ballot_sync(0xFFFFFFFFu, t < N && (fixed || (m > 0 && u > found)));
-      tie[k] = __ballot_sync(0xFFFFFFFFu, t < N && !fixed && m > 0 && u == found);
-      n_sure += __popc(sure[k]);
-      n_tie += __popc(tie[k]);
-    }
-    if (lane == 0) {
-      w_sure[warp] = n_sure;
-      w_tie[warp] = n_tie;
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t u = key(f[c]);
+            kind[k] |= u > found ? 1u << c : u == found ? 16u << c : 0u;
+          }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t u = key(f[c]);
+          const bool fixed = t + c < lo || t + c >= hi;
+          if (t + c < N && (fixed || m > 0)) kind[k] |= fixed || u > found ? 1u << c : u == found ? 16u << c : 0u;
+        }
+      }
+      incl[k] = __popc(kind[k] & 15u) | __popc(kind[k] >> 4) << 16;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, incl[k], d);
+        if (lane >= d) incl[k] += o;
+      }
+      if (lane == 31) w_kept[k * kWarps + warp] = make_int2(incl[k] & 0xFFFFu, incl[k] >> 16);
     }
     __syncthreads();
-    const int a = w_sure[lane], b = w_tie[lane];
-    int sa = a, sb = b;
+    static_assert(kRun == 2 && kWarps == 32, "");  // a lane has the same warp of both runs
+    const int2 a = w_kept[lane], b = w_kept[kWarps + lane];
+    const int first_sure = __reduce_add_sync(0xFFFFFFFFu, a.x), first_tie = __reduce_add_sync(0xFFFFFFFFu, a.y);
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int oa = __shfl_up_sync(0xFFFFFFFFu, sa, d), ob = __shfl_up_sync(0xFFFFFFFFu, sb, d);
-      if (lane >= d) {
-        sa += oa;
-        sb += ob;
+    for (int k = 0; k < kRun; ++k) {
+      const int2 n = k == 0 ? a : b;
+      int s_at = sure_all + (k == 0 ? 0 : first_sure) + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? n.x : 0);
+      int t_at = tie_all + (k == 0 ? 0 : first_tie) + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? n.y : 0);
+      s_at += (incl[k] & 0xFFFFu) - __popc(kind[k] & 15u);
+      t_at += (incl[k] >> 16) - __popc(kind[k] >> 4);
+      const int t = base + kStep * k + own;
+      const float f[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool sure = kind[k] >> c & 1u, tie = kind[k] >> c & 16u;
+        if (sure || (tie && t_at < ties)) {
+          const int to = s_at + min(t_at, ties);
+          pos[to] = t + c;
+          weight[to] = f[c];
+        }
+        s_at += sure;
+        t_at += tie;
       }
     }
-    int sure_at = sure_all + __shfl_sync(0xFFFFFFFFu, sa - a, warp), tie_at = tie_all + __shfl_sync(0xFFFFFFFFu, sb - b, warp);
-    sure_all += __shfl_sync(0xFFFFFFFFu, sa, 31);
-    tie_all += __shfl_sync(0xFFFFFFFFu, sb, 31);
-    const unsigned below = (1u << lane) - 1u;
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      const int rank = tie_at + __popc(tie[k] & below);
-      const bool kept = (sure[k] >> lane & 1u) || ((tie[k] >> lane & 1u) && rank < ties);
-      if (kept) {
-        const int to = sure_at + __popc(sure[k] & below) + (rank < ties ? rank : ties);
-        pos[to] = t0 + 32 * k;
-        weight[to] = v[k];
-      }
-      sure_at += __popc(sure[k]);
-      tie_at += __popc(tie[k]);
-    }
-    __syncthreads();  // the warps' counts are free again
+    sure_all += first_sure + __reduce_add_sync(0xFFFFFFFFu, b.x);
+    tie_all += first_tie + __reduce_add_sync(0xFFFFFFFFu, b.y);
+    __syncthreads();  // the counts are free again
   }
 }
 
@@ -309,6 +355,8 @@ __global__ void __launch_bounds__(kMoveThreads) kv8_evict_move_kernel(const Pool
   if (tid == 0) {
     c.k_scale[to] = scale[0];
     c.v_scale[to] = scale[1];
+    // The last CTA of the sequence to come here: nobody reads its old row any more (the reads' values were used above).
+    s_last = atomicAdd(&l.tokens[i], 1) == need * e.heads - 1;
   }
   __syncthreads();
   // thread: one 16-byte piece of every 32nd row, all loads on their way at once
@@ -333,13 +381,6 @@ __global__ void __launch_bounds__(kMoveThreads) kv8_evict_move_kernel(const Pool
       if (row < count)
         reinterpret_cast<uint4*>((z == 0 ? c.k_data : c.v_data) + (to * kBlock + row) * kDim)[piece] = v[z][k];
     }
-  // the sequence's last CTA: nobody reads its old row any more
-  __syncthreads();
-  if (tid == 0) {
-    __threadfence();
-    s_last = atomicAdd(&l.tokens[i], 1) == need * e.heads - 1;
-  }
-  __syncthreads();
   if (!s_last) return;
   int32_t* row = p.table + static_cast<long long>(ch) * p.max_pages;
   if (par == ch)
@@ -431,7 +472,7 @@ msa_status msa_pages_evict(const msa_page_pool* a, int32_t n, const int32_t* par
   if (n == 0) return MSA_OK;
   const Lists l = carve(ws, p.num_seqs, p.num_pages);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  kv8_evict_select_kernel<<<static_cast<unsigned>(items + 1), kPlanThreads, 0, st>>>(p, l, e);
+  kv8_evict_select_kernel<<<static_cast<unsigned>(items + 1), kSelectThreads, 0, st>>>(p, l, e);
   if ((s = launched()) != MSA_OK) return s;
   return launch_chained(kv8_evict_move_kernel, static_cast<int>(moves), kMoveThreads, st, p, l, e, pages);
 }
