@@ -150,7 +150,7 @@ def load(path: str = LIB_PATH):
             lib.msa_kv8_attn.argtypes = [ctypes.POINTER(Kv8AttnArgs), vp, sz, vp]
             lib.msa_kv8_attn_window.argtypes = [ctypes.POINTER(Kv8AttnArgs), i32, i32, vp, sz, vp]
             lib.msa_kv8_attn_shared_workspace_size.argtypes = [ctypes.POINTER(Kv8AttnArgs), i32, ctypes.POINTER(sz)]
-            lib.msa_kv8_attn_shared.argtypes = [ctypes.POINTER(Kv8AttnArgs), i32, vp, vp, sz, vp]
+            lib.msa_kv8_attn_shared.argtypes = [ctypes.POINTER(Kv8AttnArgs), i32, vp, i32, vp, sz, vp]
             lib.msa_kv8_attn_weights_workspace_size.argtypes = [ctypes.POINTER(Kv8AttnArgs), ctypes.POINTER(sz)]
             lib.msa_kv8_attn_weights.argtypes = [ctypes.POINTER(Kv8AttnArgs), vp, ctypes.c_float, vp, vp, i64, vp, sz, vp]
             pp = ctypes.POINTER(PagePoolArgs)

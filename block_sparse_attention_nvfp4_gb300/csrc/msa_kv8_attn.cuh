@@ -203,7 +203,10 @@ __host__ __device__ inline size_t headers_bytes(int grid) { return (grid * sizeo
 // ---- the line of tiles
 // Places of an item before its tiles. 64 ragged requests / 16 requests with 16 listed blocks each take
 // 168 / 24.7 us with 4 places, 164 / 25.0 with 5, 163 / 25.3 with 6.
-constexpr int kItemCost = 5;
+// With shared pages, where tiles are full of rows: 64 rows of one prompt 51.5 / 50.9 / 53.8 us with 5, 6 or 7 places, four
+// prompts of 16 requests 130 / 122 / 122.
+template <Form F>
+constexpr int kItemCost = F == kShared ? 6 : 5;
 struct Req {
   int N, R, r0;
   int row;       // its row of the block table
@@ -288,13 +291,13 @@ __device__ __forceinline__ long long tiles_before(const Kv8AttnParams& p, const 
 // Places on the line before row chunk i (at most the last one), and of one KV head of the request.
 template <Form F>
 __device__ __forceinline__ long long cost_before(const Kv8AttnParams& p, const Req& q, int i) {
-  return i > 0 ? tiles_before<F>(p, q, i) + static_cast<long long>(i) * kItemCost : 0;
+  return i > 0 ? tiles_before<F>(p, q, i) + static_cast<long long>(i) * kItemCost<F> : 0;
 }
 template <Form F>
 __device__ __forceinline__ long long head_cost(const Kv8AttnParams& p, const Req& q) {
   if (q.R == 0) return 0;
   const int n = chunks_of(p, q.R);
-  return cost_before<F>(p, q, n - 1) + kItemCost + tiles_of<F>(p, q, n - 1);
+  return cost_before<F>(p, q, n - 1) + kItemCost<F> + tiles_of<F>(p, q, n - 1);
 }
 // Where a half of a row that is joined later is kept (FP32, divided by its sum), and its log2 of the sum.
 __device__ __forceinline__ float* half_row(const Kv8AttnParams& p, int dest, long long orow) {
@@ -468,8 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       while (left > 0 && good) {
         const int nt = tiles_of<F>(p, q, ch);
-        const int j0 = at > kItemCost ? at - kItemCost : 0;
-        const long long to = at + left - kItemCost;
+        const int j0 = at > kItemCost<F> ? at - kItemCost<F> : 0;
+        const long long to = at + left - kItemCost<F>;
         const int j1 = to < nt ? static_cast<int>(to) : nt;
         if (j1 <= j0) break;  // the range ends before the item's first tile
         const int nb = (q.N + kBlock - 1) / kBlock;
@@ -559,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (n_ids && use == 0u && good) emit(kNoPos, 0, marks(), 0, 1.f, 0.f, 1.f, true);
         ++nseg;
-        left -= kItemCost + nt - at;
+        left -= kItemCost<F> + nt - at;
         // the next item
         at = 0;
         if (left > 0 && ++ch == n_ch) {
@@ -1237,7 +1240,9 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8At
   auto part = [&](int i) { return parts + (i == 0 ? 2LL * cta + 1 : 2LL * (cta + i)) * kPartFloats; };
   const int rows = me.rows * p.q_per_kv;
   // (one token over 4,096 keys: 14.4 us shared, 18.5 not; 16 requests with 16 listed blocks: 32 and 25)
-  const bool shared = n > kPairs;
+  // With shared pages an item has many rows and many partials at once: 8 rows after the other would take longer than every
+  // pair's own rows over all partials (16 requests of one row on 8,192 shared keys 43.7 us, not 29.7).
+  const bool shared = n > kPairs && (F == kAll || (rows + 7) / 8 < (rows + 63) / 64 * ((n + 3) / 4));
   const int pair = warp >> 1, d = 32 * blockIdx.y + 16 * (warp & 1) + 4 * (lane >> 3);
   const int first = shared ? pair : 0, step = shared ? kPairs : 1;
   for (int m0 = shared ? 0 : 8 * pair; m0 < rows; m0 += shared ? 8 : 8 * kPairs) {

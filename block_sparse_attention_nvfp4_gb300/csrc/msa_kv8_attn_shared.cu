@@ -13,16 +13,26 @@ namespace msa {
 namespace {
 
 constexpr int kGroupThreads = 512, kJoinThreads = 256;
-// A group shares its pages when that saves at least this many tiles a head: (members - 1) x pages.
-constexpr int kMinSaved = 8;
+// Pages, over all KV heads and groups, that sharing has to save before it pays. The groups' kernel, the second kind of
+// items and the joining cost some 8 us against the plain call, which is taken where the sizes leave less than kMinSizes to
+// save. Behind the groups' kernel, with tiles laid out for a group's rows, it pays sooner: from kMinSaved on. Measured (4 KV
+// heads, BF16, one row a member; shared / behind the groups' kernel but alone / the plain call, us):
+//   768 saved, 4 members   28.7 / 24.6 / 20.5      1,536, 4 groups of 4   26.7 / 30.8 / 26.7
+//   896, 8 members         24.2 / 26.1 / 20.6      1,792, 8 members       26.4 / 30.7 / 26.7
+//   960, 16 members        24.9 / 26.7 / 22.5      3,840, 16 members      29.2 / 43.0 / 36.9
+constexpr int kMinSizes = 1536, kMinSaved = 768;
 
 // CTA g: group g; the last CTA: the requests outside every group. groups[g] = {shared pages (0: none), first row, rows,
-// first member}, skip[b] = shared pages of request b. Bound: latency, four dependent reads.
+// first member}, skip[b] = shared pages of request b. Bound: latency, a chain of dependent reads (the bounds, the
+// lengths, the tables); the members' entries are compared kRun at a time, all on their way at once (one after the other
+// 64 members of 128 pages took 9.3 us).
 __global__ void __launch_bounds__(kGroupThreads) kv8_groups_kernel(const Kv8AttnParams p, const int32_t* indptr, int4* groups,
-                                                                   int32_t* skip) {
-  __shared__ int s_limit, s_members, s_bad;
+                                                                   int32_t* skip, long long least) {
+  __shared__ int s_limit, s_members, s_pages;
   pdl_launch_dependents();
   const int tid = threadIdx.x, g = blockIdx.x, n = p.num_groups;
+  if (tid == 0) s_limit = s_pages = INT_MAX, s_members = 0;
+  const int b0 = g < n ? indptr[g] : 0, b1 = g < n ? indptr[g + 1] : 0;
   bool bad = false;  // one bad entry: no group shares anything (two groups might claim a request)
   for (int i = tid; i <= n; i += kGroupThreads) {
     const int x = indptr[i];
@@ -31,49 +41,67 @@ __global__ void __launch_bounds__(kGroupThreads) kv8_groups_kernel(const Kv8Attn
   bad = __syncthreads_or(bad);
   if (bad && g == 0 && tid == 0) set_flag(p.flags, kFlagBadLength);
   if (g == n) {
-    const int b0 = bad ? 0 : indptr[0], b1 = bad ? 0 : indptr[n];
+    const int first = bad ? 0 : indptr[0], last = bad ? 0 : indptr[n];
     for (int b = tid; b < p.num_reqs; b += kGroupThreads)
-      if (b < b0 || b >= b1) skip[b] = 0;
+      if (b < first || b >= last) skip[b] = 0;
     return;
   }
   if (bad) {
     if (tid == 0) groups[g] = make_int4(0, 0, 0, 0);
     return;
   }
-  const int b0 = indptr[g], b1 = indptr[g + 1];
-  if (tid == 0) s_limit = INT_MAX, s_members = 0, s_bad = 0;
-  __syncthreads();
+  int limit = INT_MAX, members = 0;
+  bool wrong = false;
   for (int b = b0 + tid; b < b1; b += kGroupThreads) {
     Req q;
     if (!load_req<kAll>(p, b, &q)) {  // (its flag is the attention's to set)
-      s_bad = 1;
+      wrong = true;
     } else if (q.R > 0) {
-      atomicMin(&s_limit, (q.N - q.R) / kBlock);
-      atomicAdd(&s_members, 1);
+      limit = min(limit, (q.N - q.R) / kBlock);
+      ++members;
     }
   }
-  __syncthreads();
-  int pages = s_bad || s_members < 2 ? 0 : s_limit;
-  const int members = s_members;
-  __syncthreads();
-  if (tid == 0) s_limit = pages;
-  __syncthreads();
-  // the first page that some member's row has different from the first member's (requests without rows count too:
-  // they have nothing to read)
-  const long long most = p.max_pages;
-  const int32_t* first = p.block_table + b0 * most;
-  for (int b = b0 + 1 + (tid >> 5); b < b1; b += kGroupThreads / 32) {
-    if (p.q_indptr[b + 1] == p.q_indptr[b]) continue;
-    const int32_t* row = p.block_table + b * most;
-    for (int c = tid & 31; c < pages; c += 32)
-      if (row[c] != first[c]) {
-        atomicMin(&s_limit, c);
-        break;
-      }
+  limit = __reduce_min_sync(0xFFFFFFFFu, limit);
+  members = __reduce_add_sync(0xFFFFFFFFu, members);
+  if ((tid & 31) == 0) {
+    if (limit != INT_MAX) atomicMin(&s_limit, limit);
+    if (members > 0) atomicAdd(&s_members, members);
   }
+  wrong = __syncthreads_or(wrong);
+  members = s_members;
+  const int most = wrong || members < 2 ? 0 : s_limit;
+  // the first page that some member's row has different from the first one's (members without rows have nothing to read:
+  // they count as equal)
+  const int32_t* first = p.block_table + static_cast<long long>(b0) * p.max_pages;
+  constexpr int kRun = 8;
+  int differs = INT_MAX;
+  if (most > 0) {
+    // thread tid's entries among all members' pages in a row: tid, tid + kGroupThreads, ..
+    const int dm = kGroupThreads / most, dc = kGroupThreads - dm * most;
+    int m = tid / most, at = tid - m * most;
+    while (m < b1 - b0) {
+      int c[kRun], mine[kRun], theirs[kRun], rows[kRun];
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) {
+        const bool on = m < b1 - b0;
+        c[k] = on ? at : 0;
+        mine[k] = first[c[k]];
+        theirs[k] = on ? first[m * static_cast<long long>(p.max_pages) + c[k]] : mine[k];
+        rows[k] = on ? p.q_indptr[b0 + m + 1] - p.q_indptr[b0 + m] : 0;
+        m += dm;
+        at += dc;
+        if (at >= most) at -= most, ++m;
+      }
+#pragma unroll
+      for (int k = 0; k < kRun; ++k)
+        if (mine[k] != theirs[k] && rows[k] > 0) differs = min(differs, c[k]);
+    }
+  }
+  differs = __reduce_min_sync(0xFFFFFFFFu, differs);
+  if (differs != INT_MAX && (tid & 31) == 0) atomicMin(&s_pages, differs);
   __syncthreads();
-  pages = s_limit;
-  if (static_cast<long long>(members - 1) * pages < kMinSaved) pages = 0;
+  int pages = min(most, s_pages);
+  if (static_cast<long long>(members - 1) * pages * p.num_kv_heads < least) pages = 0;
   for (int b = b0 + tid; b < b1; b += kGroupThreads) skip[b] = pages;
   if (tid == 0) groups[g] = make_int4(pages, b0 < b1 ? p.q_indptr[b0] : 0, b0 < b1 ? p.q_indptr[b1] - p.q_indptr[b0] : 0, b0);
 }
@@ -144,12 +172,15 @@ msa_status msa_kv8_attn_shared_workspace_size(const msa_kv8_attn_args* a, int32_
   return MSA_OK;
 }
 
-msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* a, int32_t num_groups, const int32_t* group_indptr, void* ws,
-                               size_t ws_bytes, void* stream) {
+msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* a, int32_t num_groups, const int32_t* group_indptr,
+                               int32_t min_saved, void* ws, size_t ws_bytes, void* stream) {
   msa_status s = check_groups(a, num_groups);
   if (s != MSA_OK) return s;
   if (a->n_block_ids != 0 || (num_groups > 0 && group_indptr == nullptr)) return MSA_ERR_INVALID_ARG;
-  if (num_groups == 0) return msa_kv8_attn(a, ws, ws_bytes, stream);
+  const long long saved = min_saved >= 0 ? min_saved : kMinSaved;
+  // what sharing could save at most, by the sizes
+  const long long most_saved = static_cast<long long>(a->num_reqs - num_groups) * a->max_pages_per_req * a->num_kv_heads;
+  if (num_groups == 0 || (min_saved < 0 && most_saved < kMinSizes)) return msa_kv8_attn(a, ws, ws_bytes, stream);
   Kv8AttnParams p;
   CUtensorMap kmap;
   int sms = 0, copies = 0;
@@ -170,7 +201,8 @@ msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* a, int32_t num_groups, c
   p.skip = skip;
   p.halves = reinterpret_cast<float*>(at + groups_bytes(num_groups) + skip_bytes(a));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  kv8_groups_kernel<<<num_groups + 1, kGroupThreads, 0, st>>>(p, group_indptr, groups, skip);
+  // (each group by itself: its part of what has to be saved)
+  kv8_groups_kernel<<<num_groups + 1, kGroupThreads, 0, st>>>(p, group_indptr, groups, skip, (saved + num_groups - 1) / num_groups);
   if (cudaGetLastError() != cudaSuccess) return MSA_ERR_CUDA;
   if (launch_form<kShared>(kmap, p, copies, a->q_type == MSA_TYPE_BF16, sms, st) != cudaSuccess) return MSA_ERR_CUDA;
   const long long heads = static_cast<long long>(a->total_rows) * a->num_kv_heads * a->q_per_kv;

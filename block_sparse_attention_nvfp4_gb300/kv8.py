@@ -282,17 +282,20 @@ class KV8Attention:
         _call(self.device, stream, _lib.load().msa_kv8_attn, "msa_kv8_attn", self._ref, self._ws[0], self._ws[1])
         return self.out
 
-    def attend_shared(self, group_indptr: torch.Tensor, stream=None) -> torch.Tensor:
+    def attend_shared(self, group_indptr: torch.Tensor, stream=None, *, min_saved: Optional[int] = None) -> torch.Tensor:
         """attend() to all keys, for requests whose block tables begin with the same pages: the leading pages
         that the requests group_indptr[g] .. group_indptr[g+1] - 1 (int32 on the GPU, at most
-        max_groups groups) have in common are found and read once for all of the group's rows."""
+        max_groups groups) have in common are found and read once for all of the group's rows. min_saved: pages,
+        over all KV heads and groups, that this has to save, else requests are taken alone (None: the
+        library's choice; where the sizes leave less to save, the call is attend() itself)."""
         n = group_indptr.numel() - 1
+        _need(min_saved is None or 0 <= min_saved <= _INT_MAX, f"min_saved: expected at least 0, got {min_saved}")
         _need(0 <= n <= self.max_groups, f"group_indptr: expected 1 to {self.max_groups + 1} entries (max_groups), got {n + 1}")
         a = self._current()
         at = _plain(group_indptr, torch.int32, (n + 1,), self.device, "group_indptr")
         a.block_ids, a.n_block_ids = None, 0
-        _call(self.device, stream, _lib.load().msa_kv8_attn_shared, "msa_kv8_attn_shared", self._ref, n, at, self._ws[0],
-              self._ws[1])
+        _call(self.device, stream, _lib.load().msa_kv8_attn_shared, "msa_kv8_attn_shared", self._ref, n, at,
+              -1 if min_saved is None else min_saved, self._ws[0], self._ws[1])
         return self.out
 
     def add_weights(self, old: Optional[torch.Tensor], new: torch.Tensor, keep: float = 1.0,

@@ -450,11 +450,14 @@ msa_status msa_kv8_attn_window(const msa_kv8_attn_args* args, int32_t window, in
  * group's members list in common is found on the device, in each call; only pages that all query rows of
  * the group see whole are shared. A decreasing or out-of-range group_indptr sets MSA_FLAG_BAD_LENGTH and every
  * request is taken alone; so are the members of a group one of whose lengths is inconsistent.
+ * min_saved: pages, over all KV heads and groups, that sharing has to save; a group that does not save its part
+ * (min_saved / num_groups) is taken alone. Negative: the library's own choice, which is msa_kv8_attn itself, without a look
+ * at group_indptr, when the sizes in args leave less to save ((num_reqs - num_groups) max_pages_per_req H).
  * block_ids NULL and n_block_ids 0. num_groups 0 .. 4096. The workspace holds both halves of every row in
  * FP32: msa_kv8_attn_shared_workspace_size (host-only), its first 256 bytes zero-filled once. */
 msa_status msa_kv8_attn_shared_workspace_size(const msa_kv8_attn_args* args, int32_t num_groups, size_t* bytes);
-msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* args, int32_t num_groups, const int32_t* group_indptr, void* ws,
-                               size_t ws_bytes, void* stream);
+msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* args, int32_t num_groups, const int32_t* group_indptr,
+                               int32_t min_saved, void* ws, size_t ws_bytes, void* stream);
 
 /* Attention weights by token: what the softmax of this step's rows gave to each cached token,
  *   new[b][h][t] = (t < N - R ? keep old[b][h][t] : 0) + sum exp(sm_scale q . k_t - lse),   t < N,

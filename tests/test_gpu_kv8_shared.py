@@ -48,7 +48,7 @@ def check(cache, batch, lens, indptr, table, indptr_g, flags=0, most=None, what=
     att = KV8Attention(cache, batch, max_groups=most or len(indptr_g) - 1)
     att.out.fill_(7.0)
     att.lse.fill_(7.0)
-    out = att.attend_shared(ints(indptr_g))
+    out = att.attend_shared(ints(indptr_g), min_saved=1)
     assert att.errors() == flags
     n, heads = batch.q.shape[:2]
     q64 = batch.q.double().view(n, cache.num_kv_heads, heads // cache.num_kv_heads, 128)
@@ -114,7 +114,7 @@ def test_a_request_with_a_bad_length_leaves_its_group_alone():
     batch.context_lens = ints(bad)
     att = KV8Attention(cache, batch, max_groups=2)
     att.out.fill_(7.0)
-    out = att.attend_shared(ints(g))
+    out = att.attend_shared(ints(g), min_saved=1)
     assert att.errors() == _lib.FLAG_BAD_LENGTH
     q64 = batch.q.double().view(-1, 2, 8, 128)
     want, _, tol, _ = _kv8_long.attend(q64, cache, lens, indptr, table, ALL)
@@ -160,28 +160,28 @@ def test_rows_behind_stay_and_runs_are_equal():
     batch = KV8Batch(batch.context_lens, batch.q_indptr, batch.block_table, q, total_rows=6, max_rows_per_req=2)
     att = KV8Attention(cache, batch, max_groups=1)
     att.out.fill_(3.0)
-    first = att.attend_shared(ints(g)).clone()
+    first = att.attend_shared(ints(g), min_saved=1).clone()
     assert (first[4:] == 3.0).all()
     for _ in range(30):
-        assert torch.equal(att.attend_shared(ints(g)), first)
+        assert torch.equal(att.attend_shared(ints(g), min_saved=1), first)
     # calls with and without groups take turns on one workspace
     plain = att.attend().clone()
-    assert torch.equal(att.attend_shared(ints(g)), first) and torch.equal(att.attend(), plain)
+    assert torch.equal(att.attend_shared(ints(g), min_saved=1), first) and torch.equal(att.attend(), plain)
 
 
 def test_captured_and_replayed_on_two_streams():
     cache, batch, *_, g = setup([(40, [(5 + i, 1) for i in range(20)])], 4, 8, "bf16", 127)
     gi = ints(g)
     a, b = (KV8Attention(cache, batch, max_groups=1) for _ in range(2))
-    want = a.attend_shared(gi).clone(), a.lse.clone()
+    want = a.attend_shared(gi, min_saved=1).clone(), a.lse.clone()
     graphs = []
     for att in (a, b):
-        att.attend_shared(gi)
+        att.attend_shared(gi, min_saved=1)
         torch.cuda.synchronize()
         att.out.zero_()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            att.attend_shared(gi)
+            att.attend_shared(gi, min_saved=1)
         graphs.append((graph, torch.cuda.Stream()))
     torch.cuda.synchronize()
     for _ in range(20):
@@ -218,11 +218,30 @@ def test_beams_forked_on_the_pool():
         pool.reserve(ints(range(1, 9)), ints([n + step] * 8))
         batch = append(1, 8, 1)
         att = KV8Attention(cache, batch, max_groups=1)
-        out = att.attend_shared(ints([0, 8])).clone()
+        out = att.attend_shared(ints([0, 8]), min_saved=1).clone()
         assert pool.errors() == 0 and att.errors() == 0
         want, _, tol, _ = _kv8_long.attend(batch.q.double().view(8, H, G, 128), cache, [n + step] * 8, np.arange(9),
                                            pool.block_table[1:].cpu().numpy(), ALL, False)
         _kv8_long.close(out, want, tol, f"step {step}")
+
+
+def test_what_sharing_has_to_save():
+    """A group that saves too little is taken alone, by the same kernel or by the plain call; the bits tell them apart from
+    the shared form only within its bounds."""
+    cache, batch, lens, indptr, table, g = setup([(40, [(5 + i, 1) for i in range(20)]), (12, [(9, 2)] * 3)], 4, 8, "bf16", 147)
+    att = KV8Attention(cache, batch, max_groups=2)
+    plain = att.attend().clone(), att.lse.clone()
+    want, lse, tol, tol_lse = _kv8_long.attend(batch.q.double().view(-1, 4, 8, 128), cache, lens, indptr, table, ALL, False)
+    for least in (None, 0, 1, 2 * 12 * 2 * 4, 2 * 12 * 2 * 4 + 1, 2 * 40 * 19 * 4, 2 * 40 * 19 * 4 + 1, 2 ** 31 - 1):
+        out = att.attend_shared(ints(g), min_saved=least)
+        _kv8_long.close(out, want, tol, f"out at {least}")
+        _kv8_long.close(att.lse, lse, tol_lse, f"lse at {least}")
+    assert att.errors() == 0
+    narrow = setup([(3, [(5, 1), (7, 1)])], 2, 8, "bf16", 157)
+    att = KV8Attention(*narrow[:2], max_groups=1)
+    plain = att.attend().clone(), att.lse.clone()
+    out = att.attend_shared(ints([5, -1]))          # too little to save by the sizes: the groups are not looked at
+    assert torch.equal(out, plain[0]) and torch.equal(att.lse, plain[1]) and att.errors() == 0
 
 
 def test_refusals():
@@ -232,6 +251,9 @@ def test_refusals():
               ints([[0, 2]]), ints([0, 9, 2, 9])[::2]):
         with pytest.raises(ValueError):
             att.attend_shared(g)
+    for least in (-1, 2 ** 31):
+        with pytest.raises(ValueError):
+            att.attend_shared(ints([0, 2]), min_saved=least)
     with pytest.raises(ValueError):
         KV8Attention(cache, batch).attend_shared(ints([0, 2]))
     with pytest.raises(_lib.MSAError):
