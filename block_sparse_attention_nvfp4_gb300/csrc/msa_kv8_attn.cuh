@@ -1365,7 +1365,8 @@ inline int copies_for(int max_rows, int q_per_kv) {
 // Bytes of workspace before what a form adds: flags, the CTAs' headers, two partials for each CTA.
 inline size_t base_workspace(int sms) { return 256 + headers_bytes(sms) + 2 * static_cast<size_t>(sms) * kPartFloats * sizeof(float); }
 
-// The checks of the pointers, and the kernel's parameters; `more`: bytes of workspace that the form adds.
+// The checks of the pointers, and the kernel's parameters; `more`: bytes of workspace that the form adds, from the next
+// multiple of 256 on.
 // rows: query rows of a request, or of what its items are made of, that the tile is laid out for.
 inline msa_status set_params(const msa_kv8_attn_args* a, void* ws, size_t ws_bytes, size_t more, int rows, Kv8AttnParams* out,
                       CUtensorMap* kmap, int* sms, int* copies) {
@@ -1385,7 +1386,8 @@ inline msa_status set_params(const msa_kv8_attn_args* a, void* ws, size_t ws_byt
     return MSA_ERR_INVALID_ARG;
   if (ws == nullptr || unaligned(ws, 256)) return MSA_ERR_WORKSPACE;
   if ((s = check_device(sms)) != MSA_OK) return s;
-  if (ws_bytes < base_workspace(*sms) + more) return MSA_ERR_WORKSPACE;
+  const size_t base = base_workspace(*sms);
+  if (ws_bytes < (more > 0 ? (base + 255) / 256 * 256 + more : base)) return MSA_ERR_WORKSPACE;
   Kv8AttnParams p = {};
   p.num_reqs = a->num_reqs;
   p.total_rows = a->total_rows;

@@ -187,13 +187,9 @@ msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* a, int32_t num_groups, c
   // items of the shared pages have the rows of a group, on average
   const int rows = (a->total_rows + num_groups - 1) / num_groups;
   const int most = rows > a->max_rows_per_req ? rows : a->max_rows_per_req;
-  if ((s = check_device(&sms)) != MSA_OK) return s;
-  const size_t base = up256(base_workspace(sms));
-  if ((s = set_params(a, ws, ws_bytes, base - base_workspace(sms) + added_workspace(a, num_groups), most, &p, &kmap, &sms,
-                      &copies)) != MSA_OK)
-    return s;
+  if ((s = set_params(a, ws, ws_bytes, added_workspace(a, num_groups), most, &p, &kmap, &sms, &copies)) != MSA_OK) return s;
   if (a->num_reqs == 0 || a->total_rows == 0) return MSA_OK;
-  uint8_t* at = static_cast<uint8_t*>(ws) + base;
+  uint8_t* at = static_cast<uint8_t*>(ws) + up256(base_workspace(sms));
   int4* groups = reinterpret_cast<int4*>(at);
   int32_t* skip = reinterpret_cast<int32_t*>(at + groups_bytes(num_groups));
   p.num_groups = num_groups;
