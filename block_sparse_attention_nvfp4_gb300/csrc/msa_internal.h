@@ -102,6 +102,13 @@ struct Kv8AppendParams {
   uint32_t* flags;
 };
 
+// A chunk of a group's rows: places on the line up to its end (of one KV head, from the group's first chunk on), and the
+// member that its first row is of.
+struct GroupChunk {
+  long long places;
+  int first, pad;
+};
+
 // Attention over the 8-bit cache (msa_kv8_attn).
 struct Kv8AttnParams {
   int num_reqs, total_rows, max_rows, num_pages, max_pages, num_kv_heads, q_per_kv;
@@ -127,8 +134,9 @@ struct Kv8AttnParams {
   // msa_kv8_attn_shared
   int num_groups;
   const int4* groups;        // [num_groups] {shared pages (0: none), first row, rows, first member}
-  const int32_t* skip;       // [num_reqs] pages that a request's group has for it
-  float* halves;             // [2][total_rows][heads][128], then [2][total_rows][heads] log2 of the sums
+  const int32_t* group_indptr;
+  const int32_t* skip;       // [num_reqs] shared pages of a request's group
+  const GroupChunk* chunks;  // group g's row chunks from (first row) / chunk + g on
 };
 
 // Merge of the rank-local candidate lists of indexer decode context parallelism

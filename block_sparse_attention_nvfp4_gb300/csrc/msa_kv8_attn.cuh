@@ -117,16 +117,16 @@ constexpr int kHandStride = 17, kRedRows = 32, kRedStride = 68;
 static_assert(128 * kHandStride == kRedRows * kRedStride, "");
 constexpr int kMergeThreads = 512, kMergeY = 4;      // CTAs that share an item, 32 dims each
 
-enum : int { kEnd = 1, kFirst = 2, kLast = 4, kPart = 8 };
+enum : int { kEnd = 1, kFirst = 2, kLast = 4, kPart = 8, kOthers = 16 };
 struct alignas(16) Tile {
   int page;      // physical page x KV heads + head
   int rows;      // V rows to read: tokens inside the context; 0 when its values count for nothing
   int marks;     // kEnd: no tile, the work is over; kFirst, kLast of its segment; kPart: some rows do
-                 // not see all of its tokens
-  int pos0;      // position of its first token
+                 // not see all of its tokens; kOthers: rows see all of its tokens or none
+  int pos0;      // position of its first token (kShared: row r sees token k from pos0 + k <= r on)
   float kscale;
   float lv, iv;  // log2 of the value scale, and its inverse
-  int pad;
+  int span;      // kShared: the first row that sees the tile (16 bits), and behind the last
 };
 
 // NaN values under a window: the rows of a chunk that see a NaN in a dim are those from row `up` on (its first token
@@ -152,7 +152,6 @@ struct Seg {
   int head;      // KV head
   int pos;       // position of row0
   int slot;      // -1: a whole item, else the CTA's partial 0 or 1
-  int dest;      // kShared: 0: the output, 1 or 2: the shared or the own half of rows that are joined later
 };
 
 template <int NP>
@@ -165,7 +164,7 @@ struct Smem {
   float red[2][kRedRows * kRedStride];               // by set: what the copies exchange
   float qscale[kRows][128];                          // 2^e of each tile row (BF16 queries)
   int nanpos[kRows][kDim];                           // first position with a NaN value in a dim, of partly seen tokens
-                                                     // (kWindow: see mark_nan)
+                                                     // (kWindow: see mark_nan; kShared: a bit for each row that sees one)
   int nanany[kRows];
   float half_max[2][2][128];                         // by tile parity: each set's maxima, or the reference
   float xm[2][128], xl[2][128], xm2[2][128];
@@ -189,8 +188,7 @@ struct Header {
   int row0, rows, head;
   int cont;          // 1: partial 0 is a part of an item that an earlier CTA started
   int cont_end;      //    and its last one
-  int dest;          // of the item that starts in partial 1, as in Seg
-  int pad;
+  int pad[2];
 };
 constexpr long long kPartFloats = 128LL * kDim + 256;  // O, m, l
 // Where dims d .. d + 3 of row l of a partial's O are: 8 rows' 16-byte pieces side by side, so that
@@ -203,39 +201,45 @@ __host__ __device__ inline size_t headers_bytes(int grid) { return (grid * sizeo
 // ---- the line of tiles
 // Places of an item before its tiles. 64 ragged requests / 16 requests with 16 listed blocks each take
 // 168 / 24.7 us with 4 places, 164 / 25.0 with 5, 163 / 25.3 with 6.
-// With shared pages, where tiles are full of rows: 64 rows of one prompt 51.5 / 50.9 / 53.8 us with 5, 6 or 7 places, four
-// prompts of 16 requests 130 / 122 / 122.
+// (With shared pages 3, 6 and 10 places measure within 1 %.)
+constexpr int kSharedRows = 32;  // query rows of an item at most: a bit each
 template <Form F>
 constexpr int kItemCost = F == kShared ? 6 : 5;
 struct Req {
   int N, R, r0;
-  int row;       // its row of the block table
-  int pages;     // kShared: the pages that the rows of a group share; for a request the ones it leaves to its group
-  bool group;    // kShared
+  int row;       // its row of the block table (a group: its first member)
+  // kShared: pages > 0: a group, whose rows are all members' and whose first pages are those of every member; members
+  // row .. end - 1, and what kv8_groups_kernel found out about its row chunks
+  int pages, end;
+  const GroupChunk* chunks;
 };
-// What items are made of: requests; with shared pages the groups before them, whose items are their shared pages
-// for the rows of all members.
+// What items are made of: requests; with shared pages the groups before them. An item of a group is a chunk of its
+// rows: its tiles are the group's pages, which all rows see, and then each member's own, for the member's rows.
 template <Form F>
 __device__ __forceinline__ int units_of(const Kv8AttnParams& p) {
   return F == kShared ? p.num_groups + p.num_reqs : p.num_reqs;
 }
 template <Form F>
 __device__ __forceinline__ bool load_req(const Kv8AttnParams& p, int b, Req* q) {
-  q->group = false;
   q->pages = 0;
   if constexpr (F == kShared) {
     if (b < p.num_groups) {
       const int4 g = p.groups[b];
-      q->group = true;
-      q->pages = g.x;
-      q->N = g.x * kBlock;
+      q->N = 0;
       q->r0 = g.y;
       q->R = g.x > 0 ? g.z : 0;
       q->row = g.w;
+      q->pages = g.x;
+      q->end = p.group_indptr[b + 1];
+      q->chunks = p.chunks + (g.y >> p.chunk_log2) + b;
       return true;
     }
     b -= p.num_groups;
-    q->pages = p.skip[b];
+    if (p.skip[b] > 0) {  // a group has it
+      q->R = 0;
+      return true;
+    }
+    q->end = b + 1;
   }
   q->row = b;
   q->N = p.context_lens[b];
@@ -251,16 +255,16 @@ __device__ __forceinline__ int gap_of(const Kv8AttnParams& p, const Req& q, int 
   const int g = (from >> 7) - p.sink_pages;
   return g > 0 ? g : 0;
 }
-// Tiles of row chunk i: the pages up to its last row's position, without those that none of its rows sees or
-// that the request's group has.
+// Tiles of row chunk i: the pages up to its last row's position, without those that none of its rows sees.
 template <Form F>
 __device__ __forceinline__ int tiles_of(const Kv8AttnParams& p, const Req& q, int i) {
   if (F == kAll && p.n_ids) return p.n_ids;
-  if (F == kShared && q.group) return q.pages;
+  if (F == kShared && q.pages > 0)
+    return static_cast<int>(q.chunks[i].places - (i > 0 ? q.chunks[i - 1].places : 0)) - kItemCost<F>;
   const int end = (i + 1) << p.chunk_log2;
   const int last = q.N - q.R + (end < q.R ? end : q.R) - 1;
   const int n = (last >> 7) + 1;
-  return F == kWindow ? n - gap_of(p, q, i) : F == kShared ? n - q.pages : n;
+  return F == kWindow ? n - gap_of(p, q, i) : n;
 }
 // Tiles of the chunks before i (i at most the last chunk, so each of them is whole). With
 // base = N - R - 1 = 128 a + r0 and u = 128 / chunk chunks to a page, chunk k has
@@ -269,14 +273,12 @@ __device__ __forceinline__ int tiles_of(const Kv8AttnParams& p, const Req& q, in
 template <Form F>
 __device__ __forceinline__ long long tiles_before(const Kv8AttnParams& p, const Req& q, int i) {
   if (F == kAll && p.n_ids) return static_cast<long long>(i) * p.n_ids;
-  if (F == kShared && q.group) return static_cast<long long>(i) * q.pages;
   const int base = q.N - q.R - 1, a = base >> 7, c0 = (base & 127) >> p.chunk_log2, lu = 7 - p.chunk_log2;
   auto floors = [lu](long long m) {  // sum of j >> lu over j < m
     const long long w = m >> lu, rem = m & ((1LL << lu) - 1);
     return (w * (w - 1) / 2 << lu) + w * rem;
   };
   long long n = static_cast<long long>(i) * (1 + a) + floors(c0 + i + 1LL) - floors(c0 + 1LL);
-  if constexpr (F == kShared) n -= static_cast<long long>(i) * q.pages;
   if constexpr (F == kWindow) {
     const int from = q.N - q.R - p.window + 1;  // position where the window of chunk 0 starts; chunk k's k chunk later
     long long k0 = (128LL * (p.sink_pages + 1) - from + p.chunk - 1) >> p.chunk_log2;  // the first with a gap
@@ -291,6 +293,7 @@ __device__ __forceinline__ long long tiles_before(const Kv8AttnParams& p, const 
 // Places on the line before row chunk i (at most the last one), and of one KV head of the request.
 template <Form F>
 __device__ __forceinline__ long long cost_before(const Kv8AttnParams& p, const Req& q, int i) {
+  if (F == kShared && q.pages > 0) return i > 0 ? q.chunks[i - 1].places : 0;
   return i > 0 ? tiles_before<F>(p, q, i) + static_cast<long long>(i) * kItemCost<F> : 0;
 }
 template <Form F>
@@ -299,15 +302,6 @@ __device__ __forceinline__ long long head_cost(const Kv8AttnParams& p, const Req
   const int n = chunks_of(p, q.R);
   return cost_before<F>(p, q, n - 1) + kItemCost<F> + tiles_of<F>(p, q, n - 1);
 }
-// Where a half of a row that is joined later is kept (FP32, divided by its sum), and its log2 of the sum.
-__device__ __forceinline__ float* half_row(const Kv8AttnParams& p, int dest, long long orow) {
-  return p.halves + ((dest - 1) * static_cast<long long>(p.total_rows) * p.num_kv_heads * p.q_per_kv + orow) * kDim;
-}
-__device__ __forceinline__ float* half_lse(const Kv8AttnParams& p, int dest, long long orow) {
-  const long long rows = static_cast<long long>(p.total_rows) * p.num_kv_heads * p.q_per_kv;
-  return p.halves + 2 * rows * kDim + (dest - 1) * rows + orow;
-}
-
 // C copies of the query rows down the MMA tile (128 / C rows each); NP = E4M3 parts of a query.
 template <int C, int NP, Form F>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -343,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     init(sm.row_told, 4, 74, kTurns ? 1 : 2);
     if (tid < 96) mbar_fence_init();
   }
-  for (int i = tid; i < kRows * kDim; i += kThreads) (&sm.nanpos[0][0])[i] = F == kWindow ? kNoNan : INT_MAX;
+  for (int i = tid; i < kRows * kDim; i += kThreads) (&sm.nanpos[0][0])[i] = F == kWindow ? kNoNan : F == kShared ? 0 : INT_MAX;
   if (tid < kRows) sm.nanany[tid] = 0;
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&sm.taddr), kTmemCols);
   if (warp == kKWarp && lane == 0)
@@ -384,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool good = true;
     Header hd = {};
     // Waits until tile t's stage is free, writes its description and starts its K copy.
-    auto emit = [&](int pos0, int nvalid, int marks, int page, float ks, float lv, float iv, bool vzero) {
+    auto emit = [&](int pos0, int nvalid, int marks, int page, float ks, float lv, float iv, bool vzero, int span = 0) {
       const int st = t % kStages;
       if (t >= kStages) {
         good = warp_wait(smem_u32(&sm.k_empty[st]), ((t / kStages) - 1) & 1, p.flags);
@@ -393,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         Tile& x = sm.tile[t % kRing];
         *reinterpret_cast<int4*>(&x.page) = make_int4(page, vzero ? 0 : nvalid, marks, pos0);
-        *reinterpret_cast<float4*>(&x.kscale) = make_float4(ks, lv, iv, 0.f);
+        *reinterpret_cast<float4*>(&x.kscale) = make_float4(ks, lv, iv, __int_as_float(span));
         mbar_arrive(smem_u32(&sm.told[t % kTold]));
         const uint32_t kb = smem_u32(&sm.k_full[st]);
         if (nvalid > 0) {
@@ -492,10 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           use = __ballot_sync(0xFFFFFFFFu, in && !twice && lane >= j0 && lane < j1);
         }
         const int count = n_ids ? (use ? __popc(use) : 1) : j1 - j0;
-        // (all rows of a group see all of its tiles, whose tokens count from 0)
-        const bool all_seen = F == kShared && q.group;
-        const int first = t, last = t + count - 1, pos = all_seen ? kNoPos - 256 : q.N - q.R + row0;
-        const int dest = F == kShared && q.pages > 0 ? (q.group ? 1 : 2) : 0;
+        const int first = t, last = t + count - 1, pos = F == kShared ? 0 : q.N - q.R + row0;
         auto marks = [&]() { return (t == first ? kFirst : 0) | (t == last ? kLast : 0); };
         const int slot = begin && end ? -1 : (begin ? 1 : 0);
         if (lane == 0) {
@@ -506,58 +497,134 @@ __global__ void __launch_bounds__(kThreads, 1)
           s.head = h;
           s.pos = pos;
           s.slot = slot;
-          if constexpr (F == kShared) s.dest = dest;
         }
         if (slot == 1) {
           hd.tail = 1;
           hd.row0 = q.r0 + row0;
           hd.rows = rows;
           hd.head = h;
-          if constexpr (F == kShared) hd.dest = dest;
         } else if (slot == 0) {
           hd.cont = 1;
           hd.cont_end = end;
         }
         __syncwarp();
-        const int gap = F == kWindow ? gap_of(p, q, ch) : F == kShared && !q.group ? q.pages : 0;
-        const int gap_at = F == kWindow ? p.sink_pages : 0;
-        for (int base = n_ids ? 0 : j0; base < (n_ids ? 1 : j1) && good; base += 32) {
-          int c = n_ids ? id : base + lane;
-          const bool on = n_ids ? (use >> lane) & 1u : c < j1;
-          if (F != kAll && c >= gap_at) c += gap;
-          int phys = -1;
-          float ks = 1.f, lv = 0.f, iv = 1.f;
-          bool vzero = false;
-          if (on) {
-            phys = table[c];
-            if (phys < 0 || phys >= p.num_pages) {
-              set_flag(p.flags, kFlagBadPage);
-              phys = -1;
-            } else {
-              const long long ph = static_cast<long long>(phys) * p.num_kv_heads + h;
-              ks = p.k_scale[ph];
-              const float vs = p.v_scale[ph];
-              vzero = vs == 0.f;
-              // a page of scale 0 has keys but no values: below every scale, so that its scores do not
-              // raise the reference and take the other pages' weights out of FP16's range
-              lv = vzero ? kZeroLog2 : log2f(vs);
-              iv = vzero ? exp2f(-kZeroLog2) : 1.f / vs;
-            }
+        // the page that a lane looks up, its scales
+        int phys = -1;
+        float ks = 1.f, lv = 0.f, iv = 1.f;
+        bool vzero = false;
+        auto look_up = [&](bool on, const int32_t* entry) {
+          phys = -1;
+          ks = iv = 1.f;
+          lv = 0.f;
+          vzero = false;
+          if (!on) return;
+          phys = *entry;
+          if (phys < 0 || phys >= p.num_pages) {
+            set_flag(p.flags, kFlagBadPage);
+            phys = -1;
+          } else {
+            const long long ph = static_cast<long long>(phys) * p.num_kv_heads + h;
+            ks = p.k_scale[ph];
+            const float vs = p.v_scale[ph];
+            vzero = vs == 0.f;
+            // a page of scale 0 has keys but no values: below every scale, so that its scores do not
+            // raise the reference and take the other pages' weights out of FP16's range
+            lv = vzero ? kZeroLog2 : log2f(vs);
+            iv = vzero ? exp2f(-kZeroLog2) : 1.f / vs;
           }
-          for (unsigned m = __ballot_sync(0xFFFFFFFFu, on); m != 0u && good; m &= m - 1u) {
-            const int src = __ffs(m) - 1;
-            const int cc = __shfl_sync(0xFFFFFFFFu, c, src), pp = __shfl_sync(0xFFFFFFFFu, phys, src);
-            const float kk = __shfl_sync(0xFFFFFFFFu, ks, src), ll = __shfl_sync(0xFFFFFFFFu, lv, src);
-            const float ii = __shfl_sync(0xFFFFFFFFu, iv, src);
-            const bool zz = __shfl_sync(0xFFFFFFFFu, static_cast<int>(vzero), src) != 0;
-            const int pos0 = all_seen ? 0 : cc * kBlock, nv = q.N - pos0 < kBlock ? q.N - pos0 : kBlock;
-            bool some = pos0 + nv - 1 > pos;  // some rows do not see some of its tokens
-            if constexpr (F == kWindow) {     // (tokens past the sinks that the last row's window has left)
-              const int t0 = pos0 > p.sinks ? pos0 : p.sinks, t1 = pos + rows - 1 - p.window;
-              some |= t0 <= t1 && t0 < pos0 + nv;
+        };
+        if constexpr (F == kShared) {
+          // 32 members at a time, one a lane: the rows of the chunk that are its own, the position of the first, its
+          // tiles behind the group's (all of a request that is in no group)
+          int m0 = q.pages > 0 ? q.chunks[ch].first : q.row, own0 = 0;  // the first lane's member; tiles of those before
+          int m_tiles, m_incl, m_span, m_pos, m_N;
+          auto members = [&]() {
+            m_tiles = m_span = m_pos = m_N = 0;
+            if (m0 + lane < q.end) {
+              const int s = p.q_indptr[m0 + lane] - q.r0, e = p.q_indptr[m0 + lane + 1] - q.r0;
+              const int a = s > row0 ? s : row0, z = e < row0 + rows ? e : row0 + rows;
+              if (a < z) {
+                m_N = p.context_lens[m0 + lane];
+                m_tiles = ((m_N - e + z - 1) >> 7) + 1 - q.pages;
+                m_span = (a - row0) | (z - row0) << 16;
+                m_pos = m_N - e + a;
+              }
             }
-            if (pp < 0) emit(kNoPos, 0, marks(), 0, 1.f, 0.f, 1.f, true);
-            else emit(pos0, nv, marks() | (some ? kPart : 0), pp * p.num_kv_heads + h, kk, ll, ii, zz);
+            m_incl = m_tiles;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+              const int o = __shfl_up_sync(0xFFFFFFFFu, m_incl, d);
+              if (lane >= d) m_incl += o;
+            }
+          };
+          bool have = false;
+          for (int base = j0; base < j1 && good;) {
+            int n, c, nv = kBlock, p0 = -(1 << 29), span = kSharedRows << 16;
+            const int32_t* entry = table;
+            if (base < q.pages) {
+              n = (j1 < q.pages ? j1 : q.pages) - base;
+              n = n < 32 ? n : 32;
+              c = base + lane;
+            } else {
+              if (!have) members();
+              have = true;
+              int own = base - q.pages, all = __shfl_sync(0xFFFFFFFFu, m_incl, 31);
+              while (own - own0 >= all && m0 + 32 < q.end) {
+                own0 += all;
+                m0 += 32;
+                members();
+                all = __shfl_sync(0xFFFFFFFFu, m_incl, 31);
+              }
+              own -= own0;
+              if (own >= all) break;  // never, unless the lengths changed meanwhile
+              n = j1 - base < all - own ? j1 - base : all - own;
+              n = n < 32 ? n : 32;
+              own += lane;
+              int m = 0;  // the member that the lane's tile is of
+              for (int k = 0; k < 31; ++k) m += own >= __shfl_sync(0xFFFFFFFFu, m_incl, k);
+              c = q.pages + own - __shfl_sync(0xFFFFFFFFu, m_incl - m_tiles, m);
+              span = __shfl_sync(0xFFFFFFFFu, m_span, m);
+              p0 = c * kBlock - __shfl_sync(0xFFFFFFFFu, m_pos, m) + (span & 0xFFFF);
+              const int left_over = __shfl_sync(0xFFFFFFFFu, m_N, m) - c * kBlock;
+              nv = left_over < kBlock ? left_over : kBlock;
+              entry = p.block_table + static_cast<long long>(m0 + m) * p.max_pages;
+            }
+            look_up(lane < n, entry + c);
+            for (int src = 0; src < n && good; ++src) {
+              const int pp = __shfl_sync(0xFFFFFFFFu, phys, src), at0 = __shfl_sync(0xFFFFFFFFu, p0, src);
+              const int sp = __shfl_sync(0xFFFFFFFFu, span, src), valid = __shfl_sync(0xFFFFFFFFu, nv, src);
+              const float kk = __shfl_sync(0xFFFFFFFFu, ks, src), ll = __shfl_sync(0xFFFFFFFFu, lv, src);
+              const float ii = __shfl_sync(0xFFFFFFFFu, iv, src);
+              const bool zz = __shfl_sync(0xFFFFFFFFu, static_cast<int>(vzero), src) != 0;
+              // its rows see all of its tokens; and they are all rows
+              const bool whole = at0 + valid - 1 <= (sp & 0xFFFF), full = whole && (sp & 0xFFFF) == 0 && (sp >> 16) >= rows;
+              if (pp < 0) emit(kNoPos, 0, marks(), 0, 1.f, 0.f, 1.f, true);
+              else emit(at0, valid, marks() | (full ? 0 : kPart) | (whole ? kOthers : 0), pp * p.num_kv_heads + h, kk, ll, ii, zz, sp);
+            }
+            base += n;
+          }
+        } else {
+          const int gap = F == kWindow ? gap_of(p, q, ch) : 0;
+          for (int base = n_ids ? 0 : j0; base < (n_ids ? 1 : j1) && good; base += 32) {
+            int c = n_ids ? id : base + lane;
+            const bool on = n_ids ? (use >> lane) & 1u : c < j1;
+            if (F == kWindow && c >= p.sink_pages) c += gap;
+            look_up(on, table + c);
+            for (unsigned m = __ballot_sync(0xFFFFFFFFu, on); m != 0u && good; m &= m - 1u) {
+              const int src = __ffs(m) - 1;
+              const int cc = __shfl_sync(0xFFFFFFFFu, c, src), pp = __shfl_sync(0xFFFFFFFFu, phys, src);
+              const float kk = __shfl_sync(0xFFFFFFFFu, ks, src), ll = __shfl_sync(0xFFFFFFFFu, lv, src);
+              const float ii = __shfl_sync(0xFFFFFFFFu, iv, src);
+              const bool zz = __shfl_sync(0xFFFFFFFFu, static_cast<int>(vzero), src) != 0;
+              const int pos0 = cc * kBlock, nv = q.N - pos0 < kBlock ? q.N - pos0 : kBlock;
+              bool some = pos0 + nv - 1 > pos;  // some rows do not see some of its tokens
+              if constexpr (F == kWindow) {     // (tokens past the sinks that the last row's window has left)
+                const int t0 = pos0 > p.sinks ? pos0 : p.sinks, t1 = pos + rows - 1 - p.window;
+                some |= t0 <= t1 && t0 < pos0 + nv;
+              }
+              if (pp < 0) emit(kNoPos, 0, marks(), 0, 1.f, 0.f, 1.f, true);
+              else emit(pos0, nv, marks() | (some ? kPart : 0), pp * p.num_kv_heads + h, kk, ll, ii, zz);
+            }
           }
         }
         if (n_ids && use == 0u && good) emit(kNoPos, 0, marks(), 0, 1.f, 0.f, 1.f, true);
@@ -707,18 +774,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pos = sm.seg[k % kRing].pos;
         // (a chunk has at most `window` rows, so a token is never before one row's window and after another row)
         const int left = F == kWindow ? pos + sm.seg[k % kRing].rows - 1 - p.window : 0;
+        const int span = F == kShared ? sm.tile[t % kRing].span : 0, seg_rows = F == kShared ? sm.seg[k % kRing].rows : 0;
+        int words = 16;
+        if constexpr (F != kAll) {
+          // Whether there is a NaN code at all: 0x7F + 1 reaches a byte's top bit. (Where a fifth of the tiles are seen
+          // in part, as with shared pages, the look at every word below took half of the time: four prompts of 16
+          // requests 224 us.)
+          uint32_t top = 0u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 w = lds_u4(raw + 2048u * i);
+            top |= ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) | ((w.z & 0x7F7F7F7Fu) + 0x01010101u) |
+                   ((w.w & 0x7F7F7F7Fu) + 0x01010101u);
+          }
+          words = top & 0x80808080u ? 16 : 0;
+        }
 #pragma unroll 1
-        for (int i = 0; i < 16; ++i) {  // word i % 4 of the piece of row 16 (i / 4) + vr
+        for (int i = 0; i < words; ++i) {  // word i % 4 of the piece of row 16 (i / 4) + vr
           const int token = 64 * h + 16 * (i >> 2) + vr;
           const uint32_t at = raw + 2048u * (i >> 2) + 4u * (i & 3);
           const uint32_t w = lds_u1(at), nan = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
           const int tpos = x.w + token;
           const bool low = F == kWindow && tpos <= pos && tpos <= left && tpos >= p.sinks;
-          if (nan == 0u || token >= x.y || (tpos <= pos && !low)) continue;
+          // kShared: the rows from `seen` on, before the tile's last, see the token
+          const int seen = max(span & 0xFFFF, tpos);
+          const bool everyone = F == kShared ? seen == 0 && (span >> 16) >= seg_rows : tpos <= pos && !low;
+          if (nan == 0u || token >= x.y || everyone) continue;
           for (int z = 0; z < 4; ++z)
             if ((nan >> (8 * z)) & 1u) {
               int* mark = &sm.nanpos[k % kRows][16 * vc + 4 * (i & 3) + z];
-              if constexpr (F == kWindow) mark_nan(mark, low ? 0xFFFF : tpos - pos, low ? tpos - pos + p.window : 0);
+              if constexpr (F == kShared) {
+                if (seen < (span >> 16))
+                  atomicOr(mark, static_cast<int>((0xFFFFFFFFu >> (kSharedRows - (span >> 16))) & (0xFFFFFFFFu << seen)));
+              } else if constexpr (F == kWindow) mark_nan(mark, low ? 0xFFFF : tpos - pos, low ? tpos - pos + p.window : 0);
               else atomicMin(mark, tpos);
             }
           sm.nanany[k % kRows] = 1;
@@ -891,15 +979,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           f[u] *= inv;
           if (nans) {
             const int mark = sm.nanpos[k % kRows][d + u], r = mm / G;
-            if (F == kWindow ? (mark & 0xFFFF) <= r || (mark >> 16) > r : mark <= sg.pos + r) f[u] = __int_as_float(0x7FFFFFFF);
+            if (F == kShared ? (mark >> r & 1) != 0 : F == kWindow ? (mark & 0xFFFF) <= r || (mark >> 16) > r : mark <= sg.pos + r) f[u] = __int_as_float(0x7FFFFFFF);
           }
         }
-        if (F == kShared && whole && sg.dest > 0) {
-          const long long orow = static_cast<long long>(sg.row0 + mm / G) * (p.num_kv_heads * G) + sg.head * G + mm % G;
-#pragma unroll
-          for (int u = 0; u < kF; u += 4)
-            *reinterpret_cast<float4*>(half_row(p, sg.dest, orow) + d + u) = make_float4(f[u], f[u + 1], f[u + 2], f[u + 3]);
-        } else if (whole) {
+        if (whole) {
           const long long orow = static_cast<long long>(sg.row0 + mm / G) * (p.num_kv_heads * G) + sg.head * G + mm % G;
           uint16_t* to = p.out + orow * kDim + d;
           if constexpr (kF % 8 == 0) {
@@ -917,11 +1000,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto put_lse = [&](float ref, float sum) {
-        if (F == kShared && sg.dest > 0) {
-          *half_lse(p, sg.dest, static_cast<long long>(sg.row0 + row) * (p.num_kv_heads * G) + sg.head * G + m % G) =
-              sum == 0.f ? -INFINITY : (ref == -INFINITY ? 0.f : ref) + log2f(sum);
-          return;
-        }
         if (p.lse != nullptr)
           p.lse[static_cast<long long>(sg.row0 + row) * (p.num_kv_heads * G) + sg.head * G + m % G] =
               sum == 0.f ? -INFINITY : ((ref == -INFINITY ? 0.f : ref) + log2f(sum)) * 0.69314718055994531f;
@@ -1041,7 +1119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       if (!meet(&sm.sets_met, met_all)) return false;
       if (nans) {
-        if (s == 0) sm.nanpos[k % kRows][l] = F == kWindow ? kNoNan : INT_MAX;
+        if (s == 0) sm.nanpos[k % kRows][l] = F == kWindow ? kNoNan : F == kShared ? 0 : INT_MAX;
         if (tid == 0) sm.nanany[k % kRows] = 0;
       }
       mref = -INFINITY;
@@ -1067,8 +1145,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const float lv = y.y, iv = y.z;
-      const bool full_vis = !(x.z & kPart) && x.y == kBlock;  // every token visible to every row
-      const int lim = pos_max - x.w - k0;                      // token k0 + n visible iff n <= lim
+      // every token visible to every row that sees any (the others' maxima and weights are dropped)
+      const bool full_vis = (!(x.z & kPart) || (F == kShared && kTurns && x.z & kOthers)) && x.y == kBlock;
+      int lim = pos_max - x.w - k0;                            // token k0 + n visible iff n <= lim
+      if constexpr (F == kShared) {  // rows of other members see nothing of a member's tile
+        const int span = __float_as_int(y.w);
+        if (row < (span & 0xFFFF) || row >= (span >> 16)) lim = -1;
+      }
       // the floor keeps a masked score at -inf when a scale is 0
       const float coef = fmaxf(coef_q * y.x, 1e-30f);
       const uint32_t s_cols = tbase + lane_base + kColS + kBlock * (rb.at < 3u ? rb.at : rb.at - 3u);
@@ -1082,7 +1165,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_wait_ld();
       };
       float mx = -INFINITY;
-      if (kCh > 1 && full_vis) {
+      // A warp none of whose rows sees any of its tokens (of a member's tile, most) only writes zeros.
+      const bool none = F == kShared && kTurns && !__any_sync(0xFFFFFFFFu, lim >= 0);
+      if (none) {
+      } else if (kCh > 1 && full_vis) {
 #pragma unroll 1
         for (int ch = 0; ch < kCh; ++ch) {  // the TMEM load reduces (two at a time spill: BF16 prompt 385 us, not 370)
           float m0 = tmem_ld32_max(s_cols + k0 + 32 * ch);
@@ -1109,6 +1195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (kCh > 1) tc_wait_st();
       }
+      if (F == kShared && kTurns && lim < 0) mx = -INFINITY;
       float* hm = &sm.half_max[t & 1][0][0];
       float r_old = mref;
       if constexpr (kTurns) {  // the reference goes from tile to tile and so from set to set
@@ -1157,6 +1244,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float off = !kTurns && faint ? -mxs : lv - ref;
       const float2 coef2 = make_float2(coef, coef), off2 = make_float2(off, off);
       float2 acc = make_float2(0.f, 0.f);
+      const bool dropped = F == kShared && kTurns && lim < 0;
+      if (F == kShared && none) {
+#pragma unroll
+        for (int ch = 0; ch < kCh; ++ch) tmem_zero16(s_cols + 64 * (ch >> 1) + 16 * (ch & 1));
+      } else
 #pragma unroll 1
       for (int ch = 0; ch < kCh; ++ch) {
         if (kCh > 1) load(ch);
@@ -1170,6 +1262,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!kTurns && some_faint)
 #pragma unroll
           for (int u = 0; u < kStep / 2; ++u) v[u] = faint ? 0u : v[u];
+        if constexpr (F == kShared && kTurns)
+#pragma unroll
+          for (int u = 0; u < kStep / 2; ++u) v[u] = dropped ? 0u : v[u];
         if constexpr (kTurns) tmem_st16(s_cols + 64 * (ch >> 1) + 16 * (ch & 1), v);
         else if constexpr (kStep == 32) tmem_st16(s_cols + p_off, v);
         else tmem_st8(s_cols + p_off, v);
@@ -1191,7 +1286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int d = kTurns ? 0 : 64 * s; d < (kTurns ? kDim : 64 * s + 64); d += 32)
           tmem_scale32(tbase + lane_base + kColO + d, a);
       }
-      const float sum = kTurns && faint ? own : acc.x + acc.y;
+      const float sum = dropped ? 0.f : kTurns && faint ? own : acc.x + acc.y;
       lrun = carry(lrun, mref, ref) + sum * (faint ? ex2(mxs - ref) : iv);  // mref -inf: nothing summed yet
       mref = m_new;
       tc_wait_st();
@@ -1222,16 +1317,33 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8At
   __shared__ float4 part_o[kPairs][64];
   __shared__ float part_l[kPairs][64], part_m[kPairs][64];
   pdl_wait_primary();
-  if constexpr (F == kShared) pdl_launch_dependents();
   const Header* hd = reinterpret_cast<const Header*>(p.parts);
-  const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Header me = hd[cta];
-  // partials: this CTA's, then those of the next ones up to the item's last
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int cta = blockIdx.x;  // where the item starts
+  Header me = hd[cta];
+  // partials: the starting CTA's, then those of the next ones up to the item's last
   auto middle = [&](int i) { return i < grid && hd[i].cont && !hd[i].cont_end; };
+  Header back;
+  if (F == kShared) back = hd[max(cta - 1 - lane, 0)];  // (on its way together with the next)
   unsigned ends = __ballot_sync(0xFFFFFFFFu, !middle(cta + 1 + lane));
+  if (F == kShared && !me.tail && me.cont && !me.cont_end) {  // inside an item: helps with it
+    unsigned tails = __ballot_sync(0xFFFFFFFFu, cta - 1 - lane >= 0 && back.tail);
+    for (; tails == 0u && cta > 32; cta -= 32) {
+      back = hd[max(cta - 33 - lane, 0)];
+      tails = __ballot_sync(0xFFFFFFFFu, cta - 33 - lane >= 0 && back.tail);
+    }
+    if (tails == 0u) return;
+    const int from = __ffs(tails) - 1;
+    cta -= 1 + from;
+    me.tail = 1;
+    me.row0 = __shfl_sync(0xFFFFFFFFu, back.row0, from);
+    me.rows = __shfl_sync(0xFFFFFFFFu, back.rows, from);
+    me.head = __shfl_sync(0xFFFFFFFFu, back.head, from);
+  }
   if (!me.tail) return;
-  int n = 1 + (ends ? __ffs(ends) : 32);
-  for (int base = cta + 33; ends == 0u && base < grid; base += 32) {
+  const int at = blockIdx.x;
+  int n = at - cta + 1 + (ends ? __ffs(ends) : 32);
+  for (int base = at + 33; ends == 0u && base < grid; base += 32) {
     ends = __ballot_sync(0xFFFFFFFFu, !middle(base + lane));
     n += ends ? __ffs(ends) : 32;
   }
@@ -1240,12 +1352,15 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8At
   auto part = [&](int i) { return parts + (i == 0 ? 2LL * cta + 1 : 2LL * (cta + i)) * kPartFloats; };
   const int rows = me.rows * p.q_per_kv;
   // (one token over 4,096 keys: 14.4 us shared, 18.5 not; 16 requests with 16 listed blocks: 32 and 25)
-  // With shared pages an item has many rows and many partials at once: 8 rows after the other would take longer than every
-  // pair's own rows over all partials (16 requests of one row on 8,192 shared keys 43.7 us, not 29.7).
-  const bool shared = n > kPairs && (F == kAll || (rows + 7) / 8 < (rows + 63) / 64 * ((n + 3) / 4));
+  // With shared pages an item has many rows and many partials at once. Its first CTA and those inside it share the rows then,
+  // 8 at a time, and each counts its turns: a run of partials, or of every eighth of them and the join. (16 requests of a row on
+  // 8,192 shared keys, 128 rows of 20 partials: 29.5 us, 42 by the first CTA alone.)
+  const int units = (rows + 7) / 8, ctas = F == kShared && n > 2 ? n - 1 : 1, mine = (units + ctas - 1) / ctas;
+  const bool shared = n > kPairs && (F != kShared || mine * ((n + 31) / 32 + 1) < (mine + 7) / 8 * ((n + 3) / 4));
   const int pair = warp >> 1, d = 32 * blockIdx.y + 16 * (warp & 1) + 4 * (lane >> 3);
   const int first = shared ? pair : 0, step = shared ? kPairs : 1;
-  for (int m0 = shared ? 0 : 8 * pair; m0 < rows; m0 += shared ? 8 : 8 * kPairs) {
+  const int by = 8 * ctas * (shared ? 1 : kPairs);
+  for (int m0 = 8 * (blockIdx.x - cta + (shared ? 0 : pair * ctas)); m0 < rows; m0 += by) {
     const int m = m0 + (lane & 7);
     const bool on = m < rows;
     constexpr int kRun = 4;  // partials whose loads are in flight at once
@@ -1313,14 +1428,9 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8At
       const float inv = lt == 0.f ? 0.f : 1.f / lt;
       const long long orow = static_cast<long long>(me.row0 + m / p.q_per_kv) * (p.num_kv_heads * p.q_per_kv) +
                              me.head * p.q_per_kv + m % p.q_per_kv;
-      if (F == kShared && me.dest > 0) {
-        *reinterpret_cast<float4*>(half_row(p, me.dest, orow) + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        if (d == 0) *half_lse(p, me.dest, orow) = lt == 0.f ? -INFINITY : ref + log2f(lt);
-      } else {
-        *reinterpret_cast<uint2*>(p.out + orow * kDim + d) =
-            make_uint2(bf16x2_bits(o.x * inv, o.y * inv), bf16x2_bits(o.z * inv, o.w * inv));
-        if (d == 0 && p.lse != nullptr) p.lse[orow] = lt == 0.f ? -INFINITY : (ref + log2f(lt)) * 0.69314718055994531f;
-      }
+      *reinterpret_cast<uint2*>(p.out + orow * kDim + d) =
+          make_uint2(bf16x2_bits(o.x * inv, o.y * inv), bf16x2_bits(o.z * inv, o.w * inv));
+      if (d == 0 && p.lse != nullptr) p.lse[orow] = lt == 0.f ? -INFINITY : (ref + log2f(lt)) * 0.69314718055994531f;
     }
     if (shared) __syncthreads();
   }

@@ -1,33 +1,38 @@
 // msa_kv8_attn_shared: attention over the 8-bit cache for requests whose block tables begin with the same pages, as
-// msa_pages_fork leaves them. Per group of requests
-//   * kv8_groups_kernel finds the leading pages that all members' rows list and that all their query rows see whole;
-//   * the attention kernel (msa_kv8_attn.cuh) has items of two kinds on its line of tiles: a group's shared pages for
-//     the rows of all members together, and each request's own pages. With O_i = sum_t 2^(x_t - y_i) v_t and
-//     y_i = log2 sum_t 2^(x_t) of half i, both in FP32,
-//   * kv8_join_kernel adds them up: out = sum_i 2^(y_i - y) O_i, y = log2(2^y_1 + 2^y_2).
-// Shared pages are read once for 128 / q_per_kv rows instead of once for each request, and a tile of the tensor cores
-// is full of rows instead of copies of a few.
+// msa_pages_fork leaves them. kv8_groups_kernel finds, per group of requests, the leading pages that all members' rows list
+// and that all their query rows see whole. The attention kernel (msa_kv8_attn.cuh) then takes chunks of all members' rows
+// together: an item's tiles are the group's pages, for all of its rows, and behind them each member's own, for that member's
+// rows alone (the others' weights are 0). So one softmax runs over a row's shared and own keys, shared pages are read once
+// for 128 / q_per_kv rows instead of once for each request, and a tile of the tensor cores is full of rows instead of copies
+// of a few. (Own pages as items of their own, whose FP32 results a further kernel joined with the shared pages', took 51 us
+// instead of 49 for 64 rows of one prompt and 122 instead of 116 for 4 prompts of 16 requests: hundreds of items of one or two
+// tiles, each of which starts and ends.)
+// Floor: the shared pages once a group and the own pages once, or the products: 9 us for 64 beams on 16,384 tokens, 49 for 4 x
+// 16 requests of 8 rows on 8,192 .. 32,768 tokens each. Measured 45 and 112 us (each page read for every request: 172 and 199).
+// Bound: of 64 beams, latency: the groups' kernel 7 us, 4 tiles a CTA, the partials 10; of 4 x 16 requests, own tiles, whose
+// steps cost as much with 8 rows as with 128.
 #include "msa_kv8_attn.cuh"
 
 namespace msa {
 namespace {
 
-constexpr int kGroupThreads = 512, kJoinThreads = 256;
-// Pages, over all KV heads and groups, that sharing has to save before it pays. The groups' kernel, the second kind of
-// items and the joining cost some 8 us against the plain call, which is taken where the sizes leave less than kMinSizes to
-// save. Behind the groups' kernel, with tiles laid out for a group's rows, it pays sooner: from kMinSaved on. Measured (4 KV
-// heads, BF16, one row a member; shared / behind the groups' kernel but alone / the plain call, us):
-//   768 saved, 4 members   28.7 / 24.6 / 20.5      1,536, 4 groups of 4   26.7 / 30.8 / 26.7
-//   896, 8 members         24.2 / 26.1 / 20.6      1,792, 8 members       26.4 / 30.7 / 26.7
-//   960, 16 members        24.9 / 26.7 / 22.5      3,840, 16 members      29.2 / 43.0 / 36.9
-constexpr int kMinSizes = 1536, kMinSaved = 768;
+constexpr int kGroupThreads = 1024;
+// Pages, over all KV heads and groups, that sharing has to save before it pays. The groups' kernel and more partials an item
+// cost some 8 us against the plain call, which is taken where the sizes leave less than kMinSizes to save. Behind the groups'
+// kernel, with tiles laid out for a group's rows, it pays sooner: from kMinSaved on. Measured (4 KV heads, BF16, one row a
+// member; shared / behind the groups' kernel but alone / the plain call, us):
+//     768 saved, 4 members   26.7 / 26.7 / 20.5      1,792, 8 members       25.4 / 32.1 / 26.7
+//     896, 8 members         25.5 / 26.7 / 20.9      1,920, 16 members      28.4 / 34.9 / 26.6
+//     960, 16 members        26.6 / 29.9 / 22.6      3,072, 4 groups of 4   32.1 / 41.0 / 36.9
+//   1,536, 4 groups of 4     28.8 / 32.8 / 26.7      3,840, 16 members      29.5 / 46.7 / 36.9
+constexpr int kMinSizes = 2048, kMinSaved = 768;
 
 // CTA g: group g; the last CTA: the requests outside every group. groups[g] = {shared pages (0: none), first row, rows,
 // first member}, skip[b] = shared pages of request b. Bound: latency, a chain of dependent reads (the bounds, the
 // lengths, the tables); the members' entries are compared kRun at a time, all on their way at once (one after the other
 // 64 members of 128 pages took 9.3 us).
 __global__ void __launch_bounds__(kGroupThreads) kv8_groups_kernel(const Kv8AttnParams p, const int32_t* indptr, int4* groups,
-                                                                   int32_t* skip, long long least) {
+                                                                   int32_t* skip, GroupChunk* chunks, long long least) {
   __shared__ int s_limit, s_members, s_pages;
   pdl_launch_dependents();
   const int tid = threadIdx.x, g = blockIdx.x, n = p.num_groups;
@@ -103,49 +108,56 @@ __global__ void __launch_bounds__(kGroupThreads) kv8_groups_kernel(const Kv8Attn
   int pages = min(most, s_pages);
   if (static_cast<long long>(members - 1) * pages * p.num_kv_heads < least) pages = 0;
   for (int b = b0 + tid; b < b1; b += kGroupThreads) skip[b] = pages;
-  if (tid == 0) groups[g] = make_int4(pages, b0 < b1 ? p.q_indptr[b0] : 0, b0 < b1 ? p.q_indptr[b1] - p.q_indptr[b0] : 0, b0);
-}
-
-// Joins the halves of the rows of the groups that share pages; CTA (x, g) takes heads of group g's rows, a warp a
-// head at a time. Bound: memory (1 KB read and 256 bytes written per head), latency for few rows.
-__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const Kv8AttnParams p) {
-  pdl_wait_primary();
-  const int4 g = p.groups[blockIdx.y];
-  if (g.x == 0) return;
-  const int lane = threadIdx.x & 31, heads = p.num_kv_heads * p.q_per_kv;
-  const long long n = static_cast<long long>(g.z) * heads, base = static_cast<long long>(g.y) * heads;
-  constexpr int kWarps = kJoinThreads / 32;
-  for (long long i = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < n; i += gridDim.x * kWarps) {
-    const long long orow = base + i;
-    const float4 a = *reinterpret_cast<const float4*>(half_row(p, 1, orow) + 4 * lane);
-    const float4 b = *reinterpret_cast<const float4*>(half_row(p, 2, orow) + 4 * lane);
-    const float ya = *half_lse(p, 1, orow), yb = *half_lse(p, 2, orow);
-    float wa = 0.f, wb = 0.f, y = -INFINITY;
-    const float top = fmaxf(ya, yb);
-    if (top != -INFINITY) {
-      const float ea = ex2(ya - top), eb = ex2(yb - top), inv = 1.f / (ea + eb);
-      wa = ea * inv;
-      wb = eb * inv;
-      y = top + log2f(ea + eb);
+  const int r0 = b0 < b1 ? p.q_indptr[b0] : 0, rows = b0 < b1 ? p.q_indptr[b1] - r0 : 0;
+  if (tid == 0) groups[g] = make_int4(pages, r0, rows, b0);
+  if (pages == 0) return;
+  // the row chunks: the members' own tiles in each, places on the line up to its end. (The groups before this one have at
+  // most r0 / chunk + g chunks.)
+  constexpr int kStep = 2 * kGroupThreads;
+  __shared__ int s_own[kStep], s_part[kGroupThreads / 32];
+  const int n_chunks = chunks_of(p, rows);
+  GroupChunk* mine = chunks + (r0 >> p.chunk_log2) + g;
+  long long before = 0;  // own tiles of the chunks before
+  for (int w0 = 0; w0 < n_chunks; w0 += kStep) {
+    for (int i = tid; i < kStep; i += kGroupThreads) s_own[i] = 0;
+    __syncthreads();
+    for (int b = b0 + tid; b < b1; b += kGroupThreads) {
+      const int s = p.q_indptr[b] - r0, e = p.q_indptr[b + 1] - r0, N = p.context_lens[b];
+      if (s == e) continue;
+      const int i1 = min((e - 1) >> p.chunk_log2, w0 + kStep - 1);
+      for (int i = max(s >> p.chunk_log2, w0); i <= i1; ++i) {
+        const int z = min(e, (i + 1) << p.chunk_log2);
+        atomicAdd(&s_own[i - w0], ((N - e + z - 1) >> 7) + 1 - pages);
+        if (s <= i << p.chunk_log2) mine[i].first = b;
+      }
     }
-    if (isnan(ya) || isnan(yb)) wa = wb = y = __int_as_float(0x7FFFFFFF);
-    // (a half of weight 0 counts for nothing, whatever it holds)
-    float o[4];
-    const float fa[4] = {a.x, a.y, a.z, a.w}, fb[4] = {b.x, b.y, b.z, b.w};
+    __syncthreads();
+    const int x = s_own[2 * tid], y = s_own[2 * tid + 1];
+    int incl = x + y;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) o[u] = (wa != 0.f ? wa * fa[u] : 0.f) + (wb != 0.f ? wb * fb[u] : 0.f);
-    *reinterpret_cast<uint2*>(p.out + orow * kDim + 4 * lane) = make_uint2(bf16x2_bits(o[0], o[1]), bf16x2_bits(o[2], o[3]));
-    if (lane == 0 && p.lse != nullptr) p.lse[orow] = y * 0.69314718055994531f;
+    for (int d = 1; d < 32; d *= 2) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if ((tid & 31) >= d) incl += o;
+    }
+    if ((tid & 31) == 31) s_part[tid >> 5] = incl;
+    __syncthreads();
+    const int lane = tid & 31, sum = lane < kGroupThreads / 32 ? s_part[lane] : 0;
+    const long long at = before + __reduce_add_sync(0xFFFFFFFFu, lane < tid >> 5 ? sum : 0) + incl - x - y;
+    const long long each = kItemCost<kShared> + pages;
+    const int i = w0 + 2 * tid;
+    if (i < n_chunks) mine[i].places = at + x + (i + 1) * each;
+    if (i + 1 < n_chunks) mine[i + 1].places = at + x + y + (i + 2) * each;
+    before += __reduce_add_sync(0xFFFFFFFFu, sum);
+    __syncthreads();
   }
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-// What the form adds to the workspace: the groups, the requests' shared pages, the rows' halves.
+// What the form adds to the workspace: the groups, the requests' shared pages, the groups' row chunks.
 size_t groups_bytes(int n) { return up256(static_cast<size_t>(n) * sizeof(int4)); }
 size_t skip_bytes(const msa_kv8_attn_args* a) { return up256(static_cast<size_t>(a->num_reqs) * sizeof(int32_t)); }
 size_t added_workspace(const msa_kv8_attn_args* a, int n) {
-  const size_t rows = static_cast<size_t>(a->total_rows) * a->num_kv_heads * a->q_per_kv;
-  return groups_bytes(n) + skip_bytes(a) + 2 * rows * (kDim + 1) * sizeof(float);
+  return groups_bytes(n) + skip_bytes(a) + (static_cast<size_t>(a->total_rows) + n + 1) * sizeof(GroupChunk);
 }
 
 msa_status check_groups(const msa_kv8_attn_args* a, int n) {
@@ -184,9 +196,9 @@ msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* a, int32_t num_groups, c
   Kv8AttnParams p;
   CUtensorMap kmap;
   int sms = 0, copies = 0;
-  // items of the shared pages have the rows of a group, on average
-  const int rows = (a->total_rows + num_groups - 1) / num_groups;
-  const int most = rows > a->max_rows_per_req ? rows : a->max_rows_per_req;
+  // items have the rows of a group, on average, and no more than kSharedRows
+  const int rows = (a->total_rows + num_groups - 1) / num_groups, some = rows > a->max_rows_per_req ? rows : a->max_rows_per_req;
+  const int most = some < kSharedRows ? some : kSharedRows;
   if ((s = set_params(a, ws, ws_bytes, added_workspace(a, num_groups), most, &p, &kmap, &sms, &copies)) != MSA_OK) return s;
   if (a->num_reqs == 0 || a->total_rows == 0) return MSA_OK;
   uint8_t* at = static_cast<uint8_t*>(ws) + up256(base_workspace(sms));
@@ -194,17 +206,17 @@ msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* a, int32_t num_groups, c
   int32_t* skip = reinterpret_cast<int32_t*>(at + groups_bytes(num_groups));
   p.num_groups = num_groups;
   p.groups = groups;
+  p.group_indptr = group_indptr;
   p.skip = skip;
-  p.halves = reinterpret_cast<float*>(at + groups_bytes(num_groups) + skip_bytes(a));
+  GroupChunk* chunks = reinterpret_cast<GroupChunk*>(at + groups_bytes(num_groups) + skip_bytes(a));
+  p.chunks = chunks;
+  while (p.chunk > kSharedRows) p.chunk /= 2, --p.chunk_log2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // (each group by itself: its part of what has to be saved)
-  kv8_groups_kernel<<<num_groups + 1, kGroupThreads, 0, st>>>(p, group_indptr, groups, skip, (saved + num_groups - 1) / num_groups);
+  kv8_groups_kernel<<<num_groups + 1, kGroupThreads, 0, st>>>(p, group_indptr, groups, skip, chunks,
+                                                          (saved + num_groups - 1) / num_groups);
   if (cudaGetLastError() != cudaSuccess) return MSA_ERR_CUDA;
-  if (launch_form<kShared>(kmap, p, copies, a->q_type == MSA_TYPE_BF16, sms, st) != cudaSuccess) return MSA_ERR_CUDA;
-  const long long heads = static_cast<long long>(a->total_rows) * a->num_kv_heads * a->q_per_kv;
-  const long long per = (heads / num_groups + kJoinThreads / 32 - 1) / (kJoinThreads / 32), cap = (4 * sms + num_groups - 1) / num_groups;
-  const int x = static_cast<int>(per < 1 ? 1 : per < cap ? per : cap);
-  return launch_after(kv8_join_kernel, dim3(x, num_groups), kJoinThreads, 0, st, p) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+  return launch_form<kShared>(kmap, p, copies, a->q_type == MSA_TYPE_BF16, sms, st) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -453,8 +453,8 @@ msa_status msa_kv8_attn_window(const msa_kv8_attn_args* args, int32_t window, in
  * min_saved: pages, over all KV heads and groups, that sharing has to save; a group that does not save its part
  * (min_saved / num_groups) is taken alone. Negative: the library's own choice, which is msa_kv8_attn itself, without a look
  * at group_indptr, when the sizes in args leave less to save ((num_reqs - num_groups) max_pages_per_req H).
- * block_ids NULL and n_block_ids 0. num_groups 0 .. 4096. The workspace holds both halves of every row in
- * FP32: msa_kv8_attn_shared_workspace_size (host-only), its first 256 bytes zero-filled once. */
+ * block_ids NULL and n_block_ids 0. num_groups 0 .. 4096. Workspace: msa_kv8_attn_shared_workspace_size (host-only),
+ * its first 256 bytes zero-filled once. */
 msa_status msa_kv8_attn_shared_workspace_size(const msa_kv8_attn_args* args, int32_t num_groups, size_t* bytes);
 msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* args, int32_t num_groups, const int32_t* group_indptr,
                                int32_t min_saved, void* ws, size_t ws_bytes, void* stream);
