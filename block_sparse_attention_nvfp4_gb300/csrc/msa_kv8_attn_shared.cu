@@ -121,14 +121,25 @@ __global__ void __launch_bounds__(kGroupThreads) kv8_groups_kernel(const Kv8Attn
   for (int w0 = 0; w0 < n_chunks; w0 += kStep) {
     for (int i = tid; i < kStep; i += kGroupThreads) s_own[i] = 0;
     __syncthreads();
-    for (int b = b0 + tid; b < b1; b += kGroupThreads) {
-      const int s = p.q_indptr[b] - r0, e = p.q_indptr[b + 1] - r0, N = p.context_lens[b];
-      if (s == e) continue;
-      const int i1 = min((e - 1) >> p.chunk_log2, w0 + kStep - 1);
-      for (int i = max(s >> p.chunk_log2, w0); i <= i1; ++i) {
-        const int z = min(e, (i + 1) << p.chunk_log2);
-        atomicAdd(&s_own[i - w0], ((N - e + z - 1) >> 7) + 1 - pages);
-        if (s <= i << p.chunk_log2) mine[i].first = b;
+    for (int base = b0; base < b1; base += kGroupThreads) {  // (whole warps: they exchange)
+      const int b = base + tid;
+      int s = 0, e = 0, N = 0;
+      if (b < b1) s = p.q_indptr[b] - r0, e = p.q_indptr[b + 1] - r0, N = p.context_lens[b];
+      // member b's own tiles in its chunks of the rows, every `by`-th from `from` on
+      auto add = [&](int b, int s, int e, int N, int from, int by) {
+        const int i1 = min((e - 1) >> p.chunk_log2, w0 + kStep - 1);
+        for (int i = max(s >> p.chunk_log2, w0) + from; i <= i1; i += by) {
+          const int z = min(e, (i + 1) << p.chunk_log2);
+          atomicAdd(&s_own[i - w0], ((N - e + z - 1) >> 7) + 1 - pages);
+          if (s <= i << p.chunk_log2) mine[i].first = b;
+        }
+      };
+      const bool many = e - s > 32 << p.chunk_log2;  // a prompt: its chunks for the whole warp
+      if (s < e && !many) add(b, s, e, N, 0, 1);
+      for (unsigned w = __ballot_sync(0xFFFFFFFFu, many); w != 0u; w &= w - 1u) {
+        const int k = __ffs(w) - 1;
+        add(__shfl_sync(0xFFFFFFFFu, b, k), __shfl_sync(0xFFFFFFFFu, s, k), __shfl_sync(0xFFFFFFFFu, e, k),
+            __shfl_sync(0xFFFFFFFFu, N, k), tid & 31, 32);
       }
     }
     __syncthreads();

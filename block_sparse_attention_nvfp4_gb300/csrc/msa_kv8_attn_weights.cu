@@ -16,7 +16,7 @@
 // up in order: no atomics, the same bits every time.
 //
 // Roles: a warp that finds the units and starts the copies (pages and query chunks by tensor copies, two stages
-// each), one that issues the products, and the four sets, which exponentiate and sum. A set has one score buffer: its
+// each), two that issue the products, and the four sets, which exponentiate and sum. A set has one score buffer: its
 // next scores are computed while the other sets are at work.
 //
 // Floors: few rows, memory (128 bytes of a key, 4 read and 4 written per token and head); prompts, exponentials and
@@ -689,8 +689,9 @@ Layout layout(const msa_kv8_attn_args* a, int sms) {
 msa_status check_weights(const msa_kv8_attn_args* a) {
   const msa_status s = check_args(a);
   if (s != MSA_OK) return s;
-  // rows of the query parts are counted in 32 bits
-  return 2LL * a->total_rows * a->num_kv_heads * a->q_per_kv + kBlock >= (1LL << 31) ? MSA_ERR_UNSUPPORTED : MSA_OK;
+  // rows of the query parts are counted in 32 bits, and so are the positions of a whole quad behind the last token
+  if (2LL * a->total_rows * a->num_kv_heads * a->q_per_kv + kBlock >= (1LL << 31)) return MSA_ERR_UNSUPPORTED;
+  return a->max_pages_per_req > (1 << 24) - 256 ? MSA_ERR_UNSUPPORTED : MSA_OK;
 }
 
 }  // namespace

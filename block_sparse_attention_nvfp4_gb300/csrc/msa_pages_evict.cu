@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kSelectThreads = 1024, kMoveThreads = 256;
 constexpr int kMaxCaches = MSA_MAX_PLANES / 4;
+constexpr int kMostPages = (1 << 24) - 256;     // of a sequence: positions past its end, of a whole round, are still ints
 
 struct EvictCache {
   uint8_t* k_data;
@@ -440,6 +441,7 @@ msa_status msa_pages_evict(const msa_page_pool* a, int32_t n, const int32_t* par
   Pool p;
   int sms = 0;
   if ((s = make_pool(a, true, ws, ws_bytes, &p)) != MSA_OK) return s;
+  if (a->max_pages_per_seq > kMostPages) return MSA_ERR_UNSUPPORTED;
   if (sinks < 0 || recent < 0 || static_cast<long long>(sinks) + recent > keep) return MSA_ERR_INVALID_ARG;
   if (n > 0 && (parents == nullptr || children == nullptr)) return MSA_ERR_INVALID_ARG;
   auto unaligned = [](const void* x, uintptr_t n) { return (reinterpret_cast<uintptr_t>(x) & (n - 1)) != 0; };

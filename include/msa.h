@@ -466,7 +466,8 @@ msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* args, int32_t num_groups
  * whose query holds an infinity or a NaN, are left out. The request's own tokens (t >= N - R) are new and start from
  * 0; old NULL or keep 0: so does every token. A request without rows gets keep old. Entries t >= N are left as they
  * are. old and new: FP32 [num_reqs][H][head_stride], head_stride >= 128 max_pages_per_req; new may be old, and
- * does not overlap it otherwise. keep: finite, >= 0 (below 1 for weights that fade).
+ * does not overlap it otherwise. keep: finite, >= 0 (below 1 for weights that fade). max_pages_per_req up to
+ * 2^24 - 256.
  * Scores are those of msa_kv8_attn, sums FP32 in an order that does not depend on timing. Tokens on pages
  * outside [0, num_pages) get nothing from the rows and set MSA_FLAG_BAD_PAGE; requests with inconsistent lengths
  * are left unwritten and set MSA_FLAG_BAD_LENGTH. Of args block_ids is NULL, n_block_ids 0, and v_data, v_scale,
@@ -576,8 +577,8 @@ msa_status msa_pages_compact(const msa_page_pool* pool, int32_t* new_block_table
  * MSA_FLAG_NO_PAGE (there have to be ceil(keep / 128) free pages for each, before any is given back) as
  * for msa_pages_fork: the entry does nothing.
  * The pool's planes are not looked at: `caches` (host array, 1 .. 4) are all the caches on its pages. keep >= 1,
- * sinks + recent <= keep, n <= num_seqs. scratch: device memory of msa_pages_evict_scratch_size bytes (host-only),
- * 16-byte aligned, whatever it holds; ws as for the other page operators. */
+ * sinks + recent <= keep, n <= num_seqs, max_pages_per_seq up to 2^24 - 256. scratch: device memory of
+ * msa_pages_evict_scratch_size bytes (host-only), 16-byte aligned, whatever it holds; ws as for the other page operators. */
 typedef struct {
   uint8_t* k_data;             /* planes of an 8-bit cache, as in msa_kv8_append_args */
   float* k_scale;

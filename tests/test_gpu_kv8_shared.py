@@ -73,6 +73,12 @@ def test_prompts_that_share_a_prefix():
     check(*setup([(12, [(200, 150), (333, 333), (140, 129)]), (6, [(90, 70), (300, 1)])], 2, 4, "bf16", 17))
 
 
+def test_prompts_of_many_chunks():
+    """64 queries a KV head: a chunk has two rows, and a prompt more chunks than a warp has lanes."""
+    check(*setup([(12, [(400, 300), (3, 1), (90, 70)]), (6, [(500, 480), (2, 2), (131, 129)])], 1, 64, "bf16", 19))
+    check(*setup([(5, [(4300, 4200), (1, 1), (4000, 1)])], 1, 64, "e4m3", 20))
+
+
 def test_more_members_than_a_plan_takes_at_once():
     check(*setup([(10, [(1 + i % 130, 1) for i in range(700)]), (12, [(3, 1)] * 40)], 1, 4, "e4m3", 27))
 

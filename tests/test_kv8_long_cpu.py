@@ -116,6 +116,13 @@ def test_evict_refusals(lib):
         assert _evict(lib, **kw) == -4, kw
 
 
+def test_positions_behind_the_longest_sequence_are_ints(lib):
+    for pages, code in (((1 << 24) - 255, -2), ((1 << 24) - 1, -2)):
+        tokens = pages * 128
+        assert _evict(lib, pool=_pool(max_pages_per_seq=pages), caches=_caches(head_stride=tokens)) == code
+        assert lib.msa_kv8_attn_weights(_attn(max_pages_per_req=pages), X, 1.0, X, X, tokens, WS, BIG, None) == code
+
+
 def test_evict_scratch_size(lib):
     n = ctypes.c_size_t(0)
     for count, keep, want in ((3, 100, 8 * 3 * 4 * 100), (0, 5, 0), (4, 10 ** 9, 8 * 4 * 4 * 512)):
