@@ -4,15 +4,20 @@
 //   * its others, one for each (sequence, cache, head): the weight of the last token kept is found by
 //     radix selection, three histograms over 11, 10 and 10 bits of the weights as numbers (non-negative FP32 numbers
 //     order like their bits), then the kept positions and weights are written in order; of equal weights the lowest
-//     positions stay. The weights are read once where they fit the registers (8,192 tokens), else four times.
-//     Bound: instructions and latency. (Clusters of two or four CTAs a head, whose histograms were added up through
-//     distributed shared memory, were no faster and slower: their reading took what the split saved.)
+//     positions stay. The weights are read once where they fit the registers (8,192 tokens), else four times, five
+//     when many are equal. A warp has a 32nd of the sequence. Bound: the integer units (65 % busy over 65,536 tokens,
+//     28 us). (Four counts of a digit, by lane, against conflicts: no faster. Warps that take their 128 tokens in turn and
+//     meet for their sums: as fast where tokens are counted once more instead. Clusters of two or four CTAs a head, whose
+//     histograms were added up through distributed shared memory: no faster and slower, the reading took what the split saved.)
 //   * kv8_evict_move_kernel: a CTA per (sequence, cache, head, new page) gathers the codes of 128 kept tokens. The new
 //     page's scale is the largest of its tokens' pages'; codes of pages with that scale move as they are, the
 //     others are multiplied by the scales' ratio and rounded once (exact between powers of two but for what falls
-//     among the subnormals). Bound: memory, 128 bytes read here and there for each K and V row. The last CTA of a
+//     among the subnormals). Bound: memory, 128 bytes read here and there for each K and V row (32 sequences of 4 heads
+//     cut to 8,192 tokens: 537 MB in 88 us). The last CTA of a
 //     sequence to have read its old row of the block table rewrites it, the length and the old pages' counts.
 // Ranks come from sums, so nothing depends on timing.
+#include <type_traits>
+
 #include "msa_kv8_pipe.cuh"
 #include "msa_pages.cuh"
 
@@ -39,8 +44,7 @@ struct EvictParams {
   int cap;                // kept tokens of any sequence: min(keep, the block table's)
   const int32_t* parents;
   const int32_t* children;
-  int32_t* pos;           // [n][heads][cap] kept positions of sequences longer than `keep`
-  float* weight;          // [n][heads][cap] their weights
+  int2* kept;             // [n][heads][cap] kept positions of sequences longer than `keep`, their weights' bits
   EvictCache caches[kMaxCaches];
 };
 
@@ -122,12 +126,15 @@ __device__ void plan(const Pool& p, const Lists& l, const EvictParams& e, int32_
 __global__ void __launch_bounds__(kSelectThreads) kv8_evict_select_kernel(const Pool p, const Lists l, const EvictParams e) {
   static_assert(kSelectThreads == kPlanThreads, "");
   constexpr int kWarps = kSelectThreads / 32;
-  // A round takes kRun x 4 tokens a thread: lanes have 4 in a row, warps 128, and the CTA's 4,096 follow each other.
-  constexpr int kRun = 2, kStep = 4 * kSelectThreads, kRound = kRun * kStep;
+  // A warp has a 32nd of the sequence, in whole 128s, and takes kRun of them at once: lanes have 4 tokens in a row.
+  constexpr int kRun = 2, kRound = kRun * 128;
   __shared__ int hist[kSmemSeqs];                    // by pass: 2,048, 1,024 and 1,024 digits; the plan's claims
-  static_assert(kSmemSeqs >= 4096, "");
-  __shared__ int w_part[kWarps], s_found[2];
-  __shared__ alignas(8) int2 w_kept[kRun * kWarps];  // by run and warp: tokens kept for sure, and ties
+  __shared__ int w_part[kWarps], s_found[3];
+  __shared__ int w_sure[kWarps], w_tie[kWarps];      // by warp: tokens kept for sure, and ties
+  // The tokens that the last pass counts, when they are few: digit and warp << 16.
+  constexpr int kFew = 1024;
+  __shared__ int few[kFew], s_few;
+  static_assert(kSmemSeqs >= 4096 && kFew <= kSelectThreads, "");
   pdl_launch_dependents();
   if (blockIdx.x == 0) {
     plan(p, l, e, hist);
@@ -142,15 +149,20 @@ __global__ void __launch_bounds__(kSelectThreads) kv8_evict_select_kernel(const 
   const EvictCache& c = e.caches[cache_of(e, x, &head)];
   const float* w = c.weights + (static_cast<long long>(par) * c.heads + head) * c.stride;
   const int lo = e.sinks, hi = N - e.recent;
-  auto key = [](float v) { return v > 0.f ? __float_as_uint(v) : 0u; };  // (negative and NaN: 0)
+  auto key = [](float v) { return __float_as_uint(fmaxf(v, 0.f)); };  // (negative and NaN: 0)
   const bool wide = (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
-  const int own = 128 * warp + 4 * lane;
+  const int seg = (N + 128 * kWarps - 1) / (128 * kWarps) * 128, begin = warp * seg, end = min(N, begin + seg);
   // the next round's tokens are on their way while these are looked at (7 us a pass of 65,536 tokens without)
   float4 v[kRun], next[kRun];
   auto load = [&](int base) {
+    if (wide && base + kRound <= N) {
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) next[k] = *reinterpret_cast<const float4*>(w + base + 128 * k + 4 * lane);
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < kRun; ++k) {
-      const int t = base + kStep * k + own;
+      const int t = base + 128 * k + 4 * lane;
       next[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (wide && t + 3 < N) {
         next[k] = *reinterpret_cast<const float4*>(w + t);
@@ -162,41 +174,63 @@ __global__ void __launch_bounds__(kSelectThreads) kv8_evict_select_kernel(const 
       }
     }
   };
-  const bool once = N <= kRound;
+  const bool once = seg <= kRound;
   auto step = [&](int base) {
 #pragma unroll
     for (int k = 0; k < kRun; ++k) v[k] = next[k];
-    if (!once) load(base + kRound < N ? base + kRound : 0);  // (the first again, for the pass that follows)
+    if (!once) load(base + kRound < end ? base + kRound : begin);  // (the first again, for the pass that follows)
   };
-  load(0);
+  load(begin);
   for (int k = tid; k < 4096; k += kSelectThreads) hist[k] = 0;
   __syncthreads();
 
   // the key of the last of the `m` heaviest in [lo, hi), and how many of the tokens that have it stay
   const int m = e.keep - e.sinks - e.recent;
-  uint32_t found = 0u;  // its bits so far
+  uint32_t found = m > 0 ? 0u : ~0u;  // its bits so far (no weight's, when there is none)
   int rest = m;         // tokens to find among those that share them
+  // Tokens of the warp that stay for sure: the first, the last, the lane's share of those above all that the last pass
+  // counts. Those are listed when they are few, so that no further pass has to look which of them stay (65,536 tokens 31.8 us
+  // with one, 28.3 without; of tokens that the registers hold it costs less than the list).
+  bool list = false;
+  int sure = lane == 0 ? max(min(end, lo) - begin, 0) + max(end - max(begin, hi), 0) : 0;
+  if (tid == 0) s_few = 0;
   if (m > 0) {
+    // Counts the digits of the tokens whose higher bits are those found so far: key - found is below 2^above then.
+    auto count = [&](auto which, int* h, int shift, uint32_t below) {
+      constexpr int pass = decltype(which)::value;
+      for (int base = begin; base < end; base += kRound) {
+        step(base);
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+          const int t0 = base + 128 * k, t = t0 + 4 * lane;
+          if (t0 >= end) break;
+          const float f[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+          auto add = [&](int c) {
+            const uint32_t d = key(f[c]) - found;
+            if (pass == 0 || d < below) {
+              atomicAdd(&h[d >> shift], 1);
+              if (pass == 2 && list) few[atomicAdd(&s_few, 1)] = static_cast<int>(d) | warp << 16;
+            }
+            if (pass == 2) sure += static_cast<int>(d) >= static_cast<int>(below);
+          };
+          if (t0 >= lo && t0 + 127 < hi) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) add(c);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (t + c >= lo && t + c < hi) add(c);
+          }
+        }
+      }
+    };
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int bits = pass == 0 ? 11 : 10, shift = 20 - 10 * pass, bins = 1 << bits, above = shift + bits;
       int* h = hist + (pass == 0 ? 0 : 1024 + 1024 * pass);
-      for (int base = 0; base < N; base += kRound) {
-        step(base);
-#pragma unroll
-        for (int k = 0; k < kRun; ++k) {
-          const int t0 = base + kStep * k + 128 * warp, t = t0 + 4 * lane;
-          if (t0 >= hi) break;
-          const float f[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-          const bool all = t0 >= lo && t0 + 127 < hi;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t u = key(f[c]);
-            if ((pass == 0 || u >> above == found >> above) && (all || (t + c >= lo && t + c < hi)))
-              atomicAdd(&h[u >> shift & (bins - 1)], 1);
-          }
-        }
-      }
+      if (pass == 0) count(std::integral_constant<int, 0>{}, h, shift, 0u);
+      else if (pass == 1) count(std::integral_constant<int, 1>{}, h, shift, 1u << above);
+      else count(std::integral_constant<int, 2>{}, h, shift, 1u << above);
       __syncthreads();
       // from the highest digit down: the one where the count reaches `rest`
       const int per = bins / kSelectThreads;  // 2 or 1
@@ -214,77 +248,104 @@ __global__ void __launch_bounds__(kSelectThreads) kv8_evict_select_kernel(const 
         const bool second = at + n0 < rest;
         s_found[0] = second ? d0 - 1 : d0;
         s_found[1] = second ? at + n0 : at;
+        s_found[2] = second ? n1 : n0;
       }
       __syncthreads();
       found |= static_cast<uint32_t>(s_found[0]) << shift;
       rest -= s_found[1];
+      if (pass == 1) list = !once && s_found[2] <= kFew;
     }
   }
   const int ties = rest;
-  // the kept tokens in order: sums over a lane's four, over lanes, over (run, warp); sure ones in the low half of a
-  // word, ties in the high one
-  int32_t* pos = e.pos + static_cast<long long>(item) * e.cap;
-  float* weight = e.weight + static_cast<long long>(item) * e.cap;
-  int sure_all = 0, tie_all = 0;
-  for (int base = 0; base < N; base += kRound) {
+  // The tokens of 4 in a row that stay for sure, as bits, and above them the ties.
+  auto kinds = [&](int k, int t0) {
+    const int t = t0 + 4 * lane;
+    const float f[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    uint32_t kind = 0u;
+    if (t0 >= end) return kind;
+    if (t0 >= lo && t0 + 127 < hi) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t u = key(f[c]);
+        kind |= u > found ? 1u << c : u == found ? 16u << c : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t u = key(f[c]);
+        if (t + c < N) kind |= t + c < lo || t + c >= hi || u > found ? 1u << c : u == found ? 16u << c : 0u;
+      }
+    }
+    return kind;
+  };
+  // how many each warp has, and so where its own begin
+  int tie = 0;
+  if (m > 0 && !list) {
+    sure = 0;
+    for (int base = begin; base < end; base += kRound) {
+      step(base);
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) {
+        const uint32_t kind = kinds(k, base + 128 * k);
+        sure += __popc(kind & 15u);
+        tie += __popc(kind >> 4);
+      }
+    }
+  }
+  sure = __reduce_add_sync(0xFFFFFFFFu, sure);
+  tie = __reduce_add_sync(0xFFFFFFFFu, tie);
+  if (lane == 0) {
+    w_sure[warp] = sure;
+    w_tie[warp] = tie;
+  }
+  __syncthreads();
+  if (list) {
+    if (tid < s_few) {
+      const int d = few[tid] & 1023, last = s_found[0], of = few[tid] >> 16;
+      if (d >= last) atomicAdd(d > last ? &w_sure[of] : &w_tie[of], 1);
+    }
+    __syncthreads();
+  }
+  int sure_at = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w_sure[lane] : 0);
+  int tie_at = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w_tie[lane] : 0);
+  int2* kept = e.kept + static_cast<long long>(item) * e.cap;
+  for (int base = begin; base < end; base += kRound) {
     step(base);
-    uint32_t kind[kRun], incl[kRun];  // kind: 4 bits of sure tokens, then 4 of ties
+    uint32_t kind[kRun], incl[kRun];  // sums over lanes: sure ones in the low half, ties in the high one
 #pragma unroll
     for (int k = 0; k < kRun; ++k) {
-      const int t0 = base + kStep * k + 128 * warp, t = t0 + 4 * lane;
-      const float f[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-      kind[k] = 0u;
-      if (t0 >= lo && t0 + 127 < hi) {
-        if (m > 0)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t u = key(f[c]);
-            kind[k] |= u > found ? 1u << c : u == found ? 16u << c : 0u;
-          }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t u = key(f[c]);
-          const bool fixed = t + c < lo || t + c >= hi;
-          if (t + c < N && (fixed || m > 0)) kind[k] |= fixed || u > found ? 1u << c : u == found ? 16u << c : 0u;
-        }
-      }
+      kind[k] = kinds(k, base + 128 * k);
       incl[k] = __popc(kind[k] & 15u) | __popc(kind[k] >> 4) << 16;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
         const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, incl[k], d);
         if (lane >= d) incl[k] += o;
       }
-      if (lane == 31) w_kept[k * kWarps + warp] = make_int2(incl[k] & 0xFFFFu, incl[k] >> 16);
     }
-    __syncthreads();
-    static_assert(kRun == 2 && kWarps == 32, "");  // a lane has the same warp of both runs
-    const int2 a = w_kept[lane], b = w_kept[kWarps + lane];
-    const int first_sure = __reduce_add_sync(0xFFFFFFFFu, a.x), first_tie = __reduce_add_sync(0xFFFFFFFFu, a.y);
 #pragma unroll
     for (int k = 0; k < kRun; ++k) {
-      const int2 n = k == 0 ? a : b;
-      int s_at = sure_all + (k == 0 ? 0 : first_sure) + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? n.x : 0);
-      int t_at = tie_all + (k == 0 ? 0 : first_tie) + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? n.y : 0);
-      s_at += (incl[k] & 0xFFFFu) - __popc(kind[k] & 15u);
-      t_at += (incl[k] >> 16) - __popc(kind[k] >> 4);
-      const int t = base + kStep * k + own;
+      const uint32_t all = __shfl_sync(0xFFFFFFFFu, incl[k], 31);
+      int s_at = sure_at + (incl[k] & 0xFFFFu) - __popc(kind[k] & 15u);
+      const int t = base + 128 * k + 4 * lane;
       const float f[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      if (all >> 16 == 0u) {  // no ties, as a rule
+        int2* at = kept + (s_at + min(tie_at, ties));
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const bool sure = kind[k] >> c & 1u, tie = kind[k] >> c & 16u;
-        if (sure || (tie && t_at < ties)) {
-          const int to = s_at + min(t_at, ties);
-          pos[to] = t + c;
-          weight[to] = f[c];
+        for (int c = 0; c < 4; ++c)
+          if (kind[k] >> c & 1u) *at++ = make_int2(t + c, __float_as_int(f[c]));
+      } else {
+        int t_at = tie_at + (incl[k] >> 16) - __popc(kind[k] >> 4);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const bool is_sure = kind[k] >> c & 1u, is_tie = kind[k] >> c & 16u;
+          if (is_sure || (is_tie && t_at < ties)) kept[s_at + min(t_at, ties)] = make_int2(t + c, __float_as_int(f[c]));
+          s_at += is_sure;
+          t_at += is_tie;
         }
-        s_at += sure;
-        t_at += tie;
       }
+      sure_at += all & 0xFFFFu;
+      tie_at += all >> 16;
     }
-    sure_all += first_sure + __reduce_add_sync(0xFFFFFFFFu, b.x);
-    tie_all += first_tie + __reduce_add_sync(0xFFFFFFFFu, b.y);
-    __syncthreads();  // the counts are free again
   }
 }
 
@@ -321,9 +382,10 @@ __global__ void __launch_bounds__(kMoveThreads) kv8_evict_move_kernel(const Pool
     if (tid < count) {
       const int k = j * kBlock + tid;
       const long long at = (static_cast<long long>(i) * e.heads + x) * e.cap + k;
-      const int t = len <= e.keep ? k : e.pos[at];
+      const int2 from_select = len <= e.keep ? make_int2(k, 0) : e.kept[at];
+      const int t = from_select.x;
       float* weights = c.weights + head * c.stride;
-      const float w = len <= e.keep ? weights[par * static_cast<long long>(c.heads) * c.stride + t] : e.weight[at];
+      const float w = len <= e.keep ? weights[par * static_cast<long long>(c.heads) * c.stride + t] : __int_as_float(from_select.y);
       weights[ch * static_cast<long long>(c.heads) * c.stride + k] = w;
       const int page = p.table[static_cast<long long>(par) * p.max_pages + t / kBlock];
       if (in(page, p.num_pages)) {
@@ -463,10 +525,9 @@ msa_status msa_pages_evict(const msa_page_pool* a, int32_t n, const int32_t* par
   e.cap = static_cast<int>(kept_cap(a, keep));
   e.parents = parents;
   e.children = children;
-  const size_t half = 4 * static_cast<size_t>(n) * e.heads * e.cap;
-  if (n > 0 && (scratch == nullptr || unaligned(scratch, 16) || scratch_bytes < 2 * half)) return MSA_ERR_WORKSPACE;
-  e.pos = static_cast<int32_t*>(scratch);
-  e.weight = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + half);
+  if (n > 0 && (scratch == nullptr || unaligned(scratch, 16) || scratch_bytes < sizeof(int2) * static_cast<size_t>(n) * e.heads * e.cap))
+    return MSA_ERR_WORKSPACE;
+  e.kept = static_cast<int2*>(scratch);
   const int pages = (e.cap + kBlock - 1) / kBlock;
   const long long items = static_cast<long long>(n) * e.heads, moves = items * pages;
   if (moves >= (1LL << 31) || items + 1 >= (1LL << 31)) return MSA_ERR_UNSUPPORTED;
