@@ -1307,7 +1307,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the partials of an item that starts in CTA blockIdx.x's range and ends in a later one's
 // (log-sum-exp), partials in tile order. CTA blockIdx.y has dims 32 y .. 32 y + 31; a warp 8 rows and
 // 16 dims, 4 dims of a row per lane. With at most 8 partials the 8 pairs of warps take 8 rows each; with
-// more they share 8 rows, every eighth partial each, and the first joins their sums.
+// more they share 8 rows, every eighth partial each, and the first joins their sums. With shared pages the item's other
+// CTAs help.
 // Bound: latency (headers, then all of a run's loads at once) and the time to start 4 CTAs per SM:
 // runs of 4 in 64 registers measured best (one token over 4,096 keys: 14.4 us, runs of 8 in 128
 // registers 16.5; 64 ragged requests 164 and 167).
