@@ -71,12 +71,13 @@ class PagePool:
         self._fns = {n: getattr(lib, n) for n in ("msa_pages_copy", "msa_pages_fork", "msa_pages_reserve",
                                                   "msa_pages_free", "msa_pages_compact", "msa_pages_evict")}
         self._scratch, self._scratches = None, []   # evict's; outgrown ones live on, as captured graphs may hold them
-        self._evict_caches, self._evict_heads = None, 0
+        self._evict_caches, self._evict_shapes, self._most = None, (), M * BLOCK   # and the heads of each one's weights
         if self.caches and all(isinstance(c, KV8Cache) for c in self.caches):
             self._evict_caches = (_lib.Kv8EvictCache * len(self.caches))()
             for x, c in zip(self._evict_caches, self.caches):
                 _, _, x.num_kv_heads, x.k_data, x.k_scale, x.v_data, x.v_scale = c._pointers()
-                self._evict_heads += x.num_kv_heads
+            self._evict_shapes = [(x, (S, x.num_kv_heads)) for x in self._evict_caches]
+            self._evict_bytes = 8 * sum(x.num_kv_heads for x in self._evict_caches)   # scratch of a kept token
         self._ref, self._ws, self._index = ctypes.byref(a), (self.ws.data_ptr(), self.ws.numel()), dev.index
 
     @staticmethod
@@ -149,7 +150,7 @@ class PagePool:
         block table's tokens, a row for each sequence as KV8Attention.add_weights fills them; the children's
         rows get the kept tokens' weights. A child is an empty sequence, or its own parent: the
         sequence is cut where it stands, and its old pages are given back. All caches have to be KV8Caches."""
-        a, caches = self.args, self._evict_caches
+        caches, most, index = self._evict_caches, self._most, self._index
         if caches is None:
             raise ValueError("evict: every cache of the pool has to be a KV8Cache, and at least one")
         weights = (weights,) if isinstance(weights, torch.Tensor) else tuple(weights)
@@ -157,23 +158,29 @@ class PagePool:
             raise ValueError(f"weights: expected {len(caches)} (one for each cache), got {len(weights)}")
         n = children.numel()
         at = self._list(parents, n, "parents"), self._list(children, n, "children")
-        for x, w in zip(caches, weights):
-            tokens = w.shape[-1] if w.dim() else 0
-            if tokens < a.max_pages_per_seq * BLOCK:
-                raise ValueError(f"weights: expected at least {a.max_pages_per_seq * BLOCK} tokens a head, got {tokens}")
-            x.weights, x.head_stride = _plain(w, torch.float32, (a.num_seqs, x.num_kv_heads, tokens), self.device, "weights"), tokens
+        for (x, heads), w in zip(self._evict_shapes, weights):
+            shape = w.shape
+            tokens = shape[-1] if shape else 0
+            if tokens < most:
+                raise ValueError(f"weights: expected at least {most} tokens a head, got {tokens}")
+            if w.dtype is torch.float32 and w.get_device() == index and shape == (*heads, tokens) and w.is_contiguous():
+                x.weights = w.data_ptr()
+            else:
+                x.weights = _plain(w, torch.float32, (*heads, tokens), self.device, "weights")   # (says what is wrong)
+            x.head_stride = tokens
         if not (0 < keep <= _INT_MAX and 0 <= sinks and 0 <= recent and sinks + recent <= keep):
             raise ValueError(f"evict: expected keep >= 1 and sinks + recent <= keep, got {keep}, {sinks}, {recent}")
         # (what msa_pages_evict_scratch_size says)
-        need = 8 * n * self._evict_heads * min(keep, a.max_pages_per_seq * BLOCK)
-        if self._scratch is None or self._scratch[1] < need:
-            if self._scratch is not None:
-                self._scratches.append(self._scratch)
-            size = max(need, 2 * (self._scratch[1] if self._scratch is not None else 0), 256)
+        need = n * self._evict_bytes * min(keep, most)
+        scratch = self._scratch
+        if scratch is None or scratch[1] < need:
+            if scratch is not None:
+                self._scratches.append(scratch)
+            size = max(need, 2 * (scratch[1] if scratch is not None else 0), 256)
             with torch.cuda.device(self.device), torch.cuda.stream(stream):
                 t = torch.empty(size, dtype=torch.uint8, device=self.device)
-            self._scratch = (t.data_ptr(), size, t)
-        self._run("msa_pages_evict", stream, n, *at, len(caches), caches, keep, sinks, recent, *self._scratch[:2])
+            scratch = self._scratch = (t.data_ptr(), size, t)
+        self._run("msa_pages_evict", stream, n, *at, len(caches), caches, keep, sinks, recent, scratch[0], scratch[1])
 
     def errors(self, stream=None) -> int:
         """Device error flags since the last read (synchronises the stream)."""
