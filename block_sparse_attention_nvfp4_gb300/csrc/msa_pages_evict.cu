@@ -5,7 +5,7 @@
 //     radix selection, three histograms over 11, 10 and 10 bits of the weights as numbers (non-negative FP32 numbers
 //     order like their bits), then the kept positions and weights are written in order; of equal weights the lowest
 //     positions stay. The weights are read once where they fit the registers (8,192 tokens), else four times, five
-//     when many are equal. A warp has a 32nd of the sequence. Bound: the integer units (65 % busy over 65,536 tokens,
+//     when many are equal. A warp has a 32nd of the sequence. Bound: instructions (issue slots 63 % busy over 65,536 tokens,
 //     28 us). (Four counts of a digit, by lane, against conflicts: no faster. Warps that take their 128 tokens in turn and
 //     meet for their sums: as fast where tokens are counted once more instead. Clusters of two or four CTAs a head, whose
 //     histograms were added up through distributed shared memory: no faster and slower, the reading took what the split saved.)

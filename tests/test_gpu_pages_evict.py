@@ -111,6 +111,28 @@ def test_weights_that_tie_or_are_none(kind):
     check(pool, [w], [0, 1, 2], [3, 4, 5], 1999, 3, 50)
 
 
+@pytest.mark.parametrize("count", [1, 1023, 1024, 1025, 3000])
+def test_tokens_that_share_all_but_the_last_digits(count):
+    """`count` weights between 1 and 1 + 1024 steps, equal ones among them, and the last token kept is one of them."""
+    N, heavy = 10_000, 500
+    pool, (w,) = setup([N], 1, [2], 12, spare=20)
+    rng = np.random.default_rng(count)
+    x = rng.random((2, N)).astype(np.float32) * 0.5
+    for h in range(2):
+        at = rng.permutation(np.arange(10, N - 100))
+        x[h, at[:heavy]] = 2 + rng.random(heavy)
+        x[h, at[heavy:heavy + count]] = (rng.integers(0, 1024, count) + 0x3F800000).astype(np.int32).view(np.float32)
+    w[0, :, :N] = torch.from_numpy(x).cuda()
+    check(pool, [w], [0], [1], heavy + (count + 1) // 2 + 7 + 90, 7, 90)
+
+
+@pytest.mark.parametrize("N", [4095, 4097, 8191, 8192, 8193, 8321, 12_289, 16_384, 20_481])
+def test_lengths_around_what_warps_take(N):
+    pool, weights = setup([N], 2, [1], 14, spare=60)
+    check(pool, weights, [0], [1], 1000, 5, 77)
+    check(pool, weights, [0], [2], 1000, 400, 600)   # none by its weight
+
+
 def test_scales_that_are_no_powers_of_two_and_none():
     pool, weights = setup([1200, 600], 2, [2], 13, spare=20, pow2=False)
     c = pool.caches[0]
