@@ -1181,12 +1181,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int ch = 0; ch < kCh; ++ch) {
           load(ch);
           if (!full_vis) {  // scores of tokens that the row does not see become -inf
-            // under a window tokens up to lo are no longer seen, but for the sinks before `sink`
-            const int lo = F == kWindow ? (lim > -1 ? lim : -1) - p.window - kStep * ch : 0;
-            const int sink = F == kWindow ? p.sinks - x.w - k0 - kStep * ch : 0;
+            if constexpr (F == kWindow) {
+              // tokens up to lim - window are no longer seen, but for the sinks: the tokens seen as bits (three comparisons a
+              // token are twice the code)
+              auto upto = [](int x) { return x < 0 ? 0u : 0xFFFFFFFFu >> (x < 31 ? 31 - x : 0); };
+              const uint32_t seen = upto(lim - kStep * ch) & (~upto((lim > -1 ? lim : -1) - p.window - kStep * ch) |
+                                                              upto(p.sinks - x.w - k0 - kStep * ch - 1));
 #pragma unroll
-            for (int u = 0; u < kStep; ++u) {
-              v[u] = kStep * ch + u <= lim && (F != kWindow || u > lo || u < sink) ? v[u] : __float_as_uint(-INFINITY);
+              for (int u = 0; u < kStep; ++u) v[u] = seen >> u & 1u ? v[u] : __float_as_uint(-INFINITY);
+            } else {
+#pragma unroll
+              for (int u = 0; u < kStep; ++u) v[u] = kStep * ch + u <= lim ? v[u] : __float_as_uint(-INFINITY);
             }
             if constexpr (kCh > 1) tmem_st32(s_cols + k0 + 32 * ch, v);  // in place: they are read again
           }

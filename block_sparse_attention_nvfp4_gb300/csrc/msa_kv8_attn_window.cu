@@ -5,9 +5,11 @@
 // that a token which its last row has left is never one that its first row does not see yet: what a NaN value
 // reaches is then a prefix or a suffix of the rows.
 // Floor: the codes of the tokens seen, or their products. Measured (4 KV heads of 8 queries; floor): one token at 32,768 with a
-// window of 4,096, 16.4 us (0.6); 64 ragged requests of up to 8 rows, 66 (33); 2,053 rows on 16,421 keys, 149 (72).
+// window of 4,096, 16.4 us (0.6); 64 ragged requests of up to 8 rows, 65 (33); 2,053 rows on 16,421 keys, 148 (72).
 // Bound: one token, latency, as over 4,096 keys without a window; 64 requests, the start and end of 2 or 3 parts a CTA (memory 49 %
-// busy); prompts, the roles' instruction streams (the tensor pipe 43 %), and two or three of an item's 34 tiles are masked.
+// busy); prompts, the roles' instruction streams (the tensor pipe 43 %): a set of warps takes 2,150 cycles for a tile, 3,500 for one of the two
+// or three of an item's 34 that are masked, and 6,800 at an item's end. (Masked tiles taken 32 tokens at a time, all, none or some
+// seen, have less to do but more code: 159 us.)
 #include "msa_kv8_attn.cuh"
 
 using namespace msa;
