@@ -1144,13 +1144,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       tc_fence_after();
-      const float lv = y.y, iv = y.z;
+      float lv = y.y, iv = y.z;
       // every token visible to every row that sees any (the others' maxima and weights are dropped)
       const bool full_vis = (!(x.z & kPart) || (F == kShared && kTurns && x.z & kOthers)) && x.y == kBlock;
       int lim = pos_max - x.w - k0;                            // token k0 + n visible iff n <= lim
       if constexpr (F == kShared) {  // rows of other members see nothing of a member's tile
         const int span = __float_as_int(y.w);
-        if (row < (span & 0xFFFF) || row >= (span >> 16)) lim = -1;
+        const bool apart = row < (span & 0xFFFF) || row >= (span >> 16);
+        if (apart) lim = -1;
+        // a value scale that is none (NaN, or one whose inverse is infinite) stays with the member that has the page: 0 times
+        // it would be NaN in the others' references and sums
+        if (apart) lv = 0.f, iv = 0.f;
       }
       // the floor keeps a masked score at -inf when a scale is 0
       const float coef = fmaxf(coef_q * y.x, 1e-30f);
