@@ -579,6 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long last = static_cast<long long>(x.y + kBlock * e + kBlock - 1 - x.z) * G - y.x;
         if (last <= 0) {  // (columns that are not there have factors that leave 0)
           const int n = (y.y + 31) / 32;
+          // (a sum for the unit first: one running sum of a prompt's thousands of exponentials loses the faint ones)
+          float2 unit = make_float2(0.f, 0.f);
 #pragma unroll 1
           for (int ch = 0; ch < n; ++ch) {
             uint32_t v[32];
@@ -590,14 +592,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 32; c += 4) {
               float2 a, b;
               args(v + c, 32 * ch + c, a, b);
-              acc = __fadd2_rn(acc, make_float2(ex2(a.x), ex2(a.y)));
+              unit = __fadd2_rn(unit, make_float2(ex2(a.x), ex2(a.y)));
               sum = __fadd2_rn(sum, make_float2(ex2(b.x), ex2(b.y)));
             }
-            acc = __fadd2_rn(acc, sum);
+            unit = __fadd2_rn(unit, sum);
           }
+          acc = __fadd2_rn(acc, unit);
         } else {
           const int ahead = t - x.z;  // of the first row
           const int lo = ahead > 0 ? ahead * G - y.x : 0, n = (y.y + 15) / 16;
+          float2 unit = make_float2(0.f, 0.f);
 #pragma unroll 1
           for (int ch = 0; ch < n; ++ch) {
             uint32_t v[16];
@@ -609,12 +613,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               float2 a, b;
               const int at = 16 * ch + c;
               args(v + c, at, a, b);
-              acc.x += at >= lo ? ex2(a.x) : 0.f;
-              acc.y += at + 1 >= lo ? ex2(a.y) : 0.f;
-              acc.x += at + 2 >= lo ? ex2(b.x) : 0.f;
-              acc.y += at + 3 >= lo ? ex2(b.y) : 0.f;
+              unit.x += at >= lo ? ex2(a.x) : 0.f;
+              unit.y += at + 1 >= lo ? ex2(a.y) : 0.f;
+              unit.x += at + 2 >= lo ? ex2(b.x) : 0.f;
+              unit.y += at + 3 >= lo ? ex2(b.y) : 0.f;
             }
           }
+          acc = __fadd2_rn(acc, unit);
         }
       } else {
         release();
