@@ -237,11 +237,12 @@ class KV8Attention:
         self._held = (batch.q, batch.context_lens, batch.q_indptr, batch.block_table,   # as long as they are bound
                       c.k_data, c.k_scale, c.v_data, c.v_scale)
         self.args, self._ref = args, ctypes.byref(args)
+        self._lse_of_all = False    # whether `lse` is that of the bound batch's rows over all keys they see
 
     def _batch_changed(self, batch) -> bool:
         """Whether a tensor or a size of the bound batch is another than the bound one."""
         a, held = self.args, self._held
-        if batch.q is not held[0] or batch.q.data_ptr() != a.q:
+        if batch.q is not held[0] or batch.q.data_ptr() != (a.q or 0):      # (no rows: the address is 0, which reads as None)
             return True
         if self._follows:
             return _geometry(batch, self.device) is not self._batch_at
@@ -253,8 +254,11 @@ class KV8Attention:
 
     def _current(self):
         """The arguments, marshalled again if a tensor was replaced."""
-        if self.cache._pointers() is not self._cache_at or self._batch_changed(self.batch):
+        moved = self._batch_changed(self.batch)
+        if moved or self.cache._pointers() is not self._cache_at:
+            of_all = self._lse_of_all and not moved     # (a cache that grew has the same keys)
             self.rebind(self.batch)
+            self._lse_of_all = of_all
         return self.args
 
     def attend(self, block_ids: Optional[torch.Tensor] = None, stream=None, *, window: Optional[int] = None,
@@ -270,6 +274,7 @@ class KV8Attention:
             a.block_ids, a.n_block_ids = None, 0
             _call(self.device, stream, _lib.load().msa_kv8_attn_window, "msa_kv8_attn_window", self._ref, window, sinks,
                   self._ws[0], self._ws[1])
+            self._lse_of_all = window >= a.max_pages_per_req * BLOCK
             return self.out
         _need(sinks == 0, "sinks: only with a window")
         if block_ids is None:
@@ -280,6 +285,7 @@ class KV8Attention:
             a.block_ids = _plain(block_ids, torch.int32, (a.num_reqs, a.num_kv_heads, n), self.device, "block_ids")
             a.n_block_ids = n
         _call(self.device, stream, _lib.load().msa_kv8_attn, "msa_kv8_attn", self._ref, self._ws[0], self._ws[1])
+        self._lse_of_all = block_ids is None
         return self.out
 
     def attend_shared(self, group_indptr: torch.Tensor, stream=None, *, min_saved: Optional[int] = None) -> torch.Tensor:
@@ -296,6 +302,7 @@ class KV8Attention:
         a.block_ids, a.n_block_ids = None, 0
         _call(self.device, stream, _lib.load().msa_kv8_attn_shared, "msa_kv8_attn_shared", self._ref, n, at,
               -1 if min_saved is None else min_saved, self._ws[0], self._ws[1])
+        self._lse_of_all = True
         return self.out
 
     def add_weights(self, old: Optional[torch.Tensor], new: torch.Tensor, keep: float = 1.0,
@@ -303,11 +310,15 @@ class KV8Attention:
         """new[b, h, t] = keep old[b, h, t] + the softmax weights that token t of request b got from this batch's rows, over the
         queries of KV head h; the batch's own tokens, whose slots are new, start from 0, and so does every token
         with old None. FP32 [B, H, L], L at least the block table's tokens; `new` may be `old`. lse (FP32
-        [rows, heads]) is what attend() to all keys left in `lse`, unless given. Needs with_weights."""
+        [rows, heads]) is what attend() to all keys left in `lse`, unless given: without it the last attention
+        call has to be one to all keys of this batch (attend() or attend_shared()). Needs with_weights."""
         _need(self.with_weights, "add_weights: make the object with with_weights=True")
         a = self._current()
-        lse = self.lse if lse is None else lse
-        _need(lse is not None, "lse: expected one, as the object keeps none")
+        if lse is None:
+            lse = self.lse
+            _need(lse is not None, "lse: expected one, as the object keeps none")
+            _need(self._lse_of_all, "lse: expected one, as the object's is not that of this batch over all keys "
+                                    "(attend() was not called, or last with a window or listed blocks)")
         shape = (a.num_reqs, a.num_kv_heads, int(new.shape[-1]) if new.dim() else 0)
         _need(shape[2] >= a.max_pages_per_req * BLOCK, f"new: expected at least {a.max_pages_per_req * BLOCK} tokens a head, got {shape[2]}")
         at = _plain(new, torch.float32, shape, self.device, "new")
