@@ -72,12 +72,6 @@ class PagePool:
                                                   "msa_pages_free", "msa_pages_compact", "msa_pages_evict")}
         self._scratch, self._scratches = None, []   # evict's; outgrown ones live on, as captured graphs may hold them
         self._evict_caches, self._evict_shapes, self._most = None, (), M * BLOCK   # and the heads of each one's weights
-        if self.caches and all(isinstance(c, KV8Cache) for c in self.caches):
-            self._evict_caches = (_lib.Kv8EvictCache * len(self.caches))()
-            for x, c in zip(self._evict_caches, self.caches):
-                _, _, x.num_kv_heads, x.k_data, x.k_scale, x.v_data, x.v_scale = c._pointers()
-            self._evict_shapes = [(x, (S, x.num_kv_heads)) for x in self._evict_caches]
-            self._evict_bytes = 8 * sum(x.num_kv_heads for x in self._evict_caches)   # scratch of a kept token
         self._ref, self._ws, self._index = ctypes.byref(a), (self.ws.data_ptr(), self.ws.numel()), dev.index
 
     @staticmethod
@@ -142,6 +136,18 @@ class PagePool:
             r = self._list(ref_counts, a.num_pages, "ref_counts")
         self._run("msa_pages_compact", stream, t, r, None if num_live is None else self._list(num_live, 1, "num_live"))
 
+    def _evictable(self):
+        """The caches as the eviction takes them: what it alone wants of their planes is checked at its first call."""
+        if not self.caches or not all(isinstance(c, KV8Cache) for c in self.caches):
+            raise ValueError("evict: every cache of the pool has to be a KV8Cache, and at least one")
+        caches = (_lib.Kv8EvictCache * len(self.caches))()
+        for x, c in zip(caches, self.caches):
+            _, _, x.num_kv_heads, x.k_data, x.k_scale, x.v_data, x.v_scale = c._pointers()
+        self._evict_shapes = [(x, (self.args.num_seqs, x.num_kv_heads)) for x in caches]
+        self._evict_bytes = 8 * sum(x.num_kv_heads for x in caches)   # scratch of a kept token
+        self._evict_caches = caches
+        return caches
+
     def evict(self, parents: torch.Tensor, children: torch.Tensor, weights: Union[torch.Tensor, Sequence[torch.Tensor]],
               keep: int, sinks: int = 0, recent: int = 0, stream=None):
         """Make children[i] the parents[i] cut to `keep` tokens, on pages of its own: of a longer sequence every KV head
@@ -152,7 +158,7 @@ class PagePool:
         sequence is cut where it stands, and its old pages are given back. All caches have to be KV8Caches."""
         caches, most, index = self._evict_caches, self._most, self._index
         if caches is None:
-            raise ValueError("evict: every cache of the pool has to be a KV8Cache, and at least one")
+            caches = self._evictable()
         weights = (weights,) if isinstance(weights, torch.Tensor) else tuple(weights)
         if len(weights) != len(caches):
             raise ValueError(f"weights: expected {len(caches)} (one for each cache), got {len(weights)}")
