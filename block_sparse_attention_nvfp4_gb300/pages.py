@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import ctypes
 import operator
+import threading
 from typing import Optional, Sequence, Union
 
 import torch
@@ -37,7 +38,8 @@ class PagePool:
     tensors (slices of them are the context_lens and block_table of a decode batch); the
     operators change them in place, in stream order. ref_counts[p] is the number of rows that
     hold page p, 0 = free. Sequence and page lists are int32 CUDA tensors. The tensors are bound when
-    the pool is made: after one is replaced, or its storage has moved, every operator raises."""
+    the pool is made: after one is replaced, or its storage has moved, every operator raises. Calls from several
+    threads are launched one after the other; on the device they have to be in stream order, as any two calls."""
 
     def __init__(self, caches: Sequence[Union[KVCache, KV8Cache]], seq_lens: torch.Tensor, block_table: torch.Tensor,
                  ref_counts: torch.Tensor):
@@ -71,7 +73,9 @@ class PagePool:
         self._fns = {n: getattr(lib, n) for n in ("msa_pages_copy", "msa_pages_fork", "msa_pages_reserve",
                                                   "msa_pages_free", "msa_pages_compact", "msa_pages_evict")}
         self._scratch, self._scratches = None, []   # evict's; outgrown ones live on, as captured graphs may hold them
-        self._evict_caches, self._evict_shapes, self._most = None, (), M * BLOCK   # and the heads of each one's weights
+        self._evict_caches, self._evict_shapes, self._most = None, (), M * BLOCK   # and the shapes of each one's weights
+        # An operator is several launches that share the workspace: no other thread's come between them.
+        self._lock = threading.RLock()
         self._ref, self._ws, self._index = ctypes.byref(a), (self.ws.data_ptr(), self.ws.numel()), dev.index
 
     @staticmethod
@@ -96,7 +100,8 @@ class PagePool:
             names = [n for x in self._bound for n in x[1]]
             changed = [n for n, t, a in zip(names, self._tensors, self._at) if _address(t) != a]
             raise ValueError(f"{', '.join(changed)}: moved after the pool was made")
-        _call(self.device, stream, self._fns[name], name, self._ref, *args, *self._ws)
+        with self._lock:
+            _call(self.device, stream, self._fns[name], name, self._ref, *args, *self._ws)
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor, tokens: Optional[torch.Tensor] = None, stream=None):
         """Copy page src[i] to dst[i] in every plane: the first tokens[i] slots, or all."""
@@ -143,7 +148,7 @@ class PagePool:
         caches = (_lib.Kv8EvictCache * len(self.caches))()
         for x, c in zip(caches, self.caches):
             _, _, x.num_kv_heads, x.k_data, x.k_scale, x.v_data, x.v_scale = c._pointers()
-        self._evict_shapes = [(x, (self.args.num_seqs, x.num_kv_heads)) for x in caches]
+        self._evict_shapes = [(self.args.num_seqs, x.num_kv_heads) for x in caches]
         self._evict_bytes = 8 * sum(x.num_kv_heads for x in caches)   # scratch of a kept token
         self._evict_caches = caches
         return caches
@@ -159,12 +164,13 @@ class PagePool:
         caches, most, index = self._evict_caches, self._most, self._index
         if caches is None:
             caches = self._evictable()
+        caches = type(caches).from_buffer_copy(caches)     # this call's: they get its weights
         weights = (weights,) if isinstance(weights, torch.Tensor) else tuple(weights)
         if len(weights) != len(caches):
             raise ValueError(f"weights: expected {len(caches)} (one for each cache), got {len(weights)}")
         n = children.numel()
         at = self._list(parents, n, "parents"), self._list(children, n, "children")
-        for (x, heads), w in zip(self._evict_shapes, weights):
+        for x, heads, w in zip(caches, self._evict_shapes, weights):
             shape = w.shape
             tokens = shape[-1] if shape else 0
             if tokens < most:
@@ -178,15 +184,16 @@ class PagePool:
             raise ValueError(f"evict: expected keep >= 1 and sinks + recent <= keep, got {keep}, {sinks}, {recent}")
         # (what msa_pages_evict_scratch_size says)
         need = n * self._evict_bytes * min(keep, most)
-        scratch = self._scratch
-        if scratch is None or scratch[1] < need:
-            if scratch is not None:
-                self._scratches.append(scratch)
-            size = max(need, 2 * (scratch[1] if scratch is not None else 0), 256)
-            with torch.cuda.device(self.device), torch.cuda.stream(stream):
-                t = torch.empty(size, dtype=torch.uint8, device=self.device)
-            scratch = self._scratch = (t.data_ptr(), size, t)
-        self._run("msa_pages_evict", stream, n, *at, len(caches), caches, keep, sinks, recent, scratch[0], scratch[1])
+        with self._lock:
+            scratch = self._scratch
+            if scratch is None or scratch[1] < need:
+                if scratch is not None:
+                    self._scratches.append(scratch)
+                size = max(need, 2 * (scratch[1] if scratch is not None else 0), 256)
+                with torch.cuda.device(self.device), torch.cuda.stream(stream):
+                    t = torch.empty(size, dtype=torch.uint8, device=self.device)
+                scratch = self._scratch = (t.data_ptr(), size, t)
+            self._run("msa_pages_evict", stream, n, *at, len(caches), caches, keep, sinks, recent, scratch[0], scratch[1])
 
     def errors(self, stream=None) -> int:
         """Device error flags since the last read (synchronises the stream)."""

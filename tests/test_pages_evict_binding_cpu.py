@@ -1,9 +1,13 @@
 """Host checks of what PagePool.evict binds: its demands on the caches' planes are its own, not the other operators'. The
 library is a stand-in that records what a launch would have got."""
+import contextlib
+import threading
+import time
+
 import pytest
 import torch
 
-from block_sparse_attention_nvfp4_gb300 import KV8Cache, PagePool, pages
+from block_sparse_attention_nvfp4_gb300 import KV8Cache, PagePool, _lib, pages
 from tests.test_kv8_binding_cpu import _i32, launches  # noqa: F401  (the fixture)
 
 
@@ -36,3 +40,66 @@ def test_planes_that_only_evict_refuses(host, kw):
         with pytest.raises(ValueError, match="data|scale"):
             pool.evict(seqs, seqs, torch.zeros((3, 2, 512)), 10)
     assert len(host) == 5
+
+
+def _in_threads(*calls):
+    """Runs the calls at once; raises what they raise."""
+    start, raised = threading.Barrier(len(calls)), []
+
+    def run(call):
+        start.wait()
+        try:
+            call()
+        except BaseException as e:      # noqa: BLE001  (told below)
+            raised.append(e)
+
+    threads = [threading.Thread(target=run, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    if raised:
+        raise raised[0]
+
+
+@pytest.fixture
+def slow(host, monkeypatch):
+    """Launches that take a while, with the interpreter free for other threads meanwhile, as a library call leaves it.
+    seen: (thread, operator, addresses of the weights at the launch's end, launches under way)."""
+    seen, inside = [], []
+
+    def call(dev, stream, fn, what, ref, *args):
+        inside.append(what)
+        together = len(inside)
+        time.sleep(0.05)
+        caches = next((a for a in args if isinstance(a, _lib.Kv8EvictCache * 1)), ())
+        seen.append((threading.get_ident(), what, [c.weights for c in caches], max(together, len(inside))))
+        inside.remove(what)
+
+    monkeypatch.setattr(pages, "_call", call)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    return seen
+
+
+def test_threads_evict_with_their_own_weights(slow):
+    pool = PagePool([_cache()], _i32(3), _i32(3, 4), _i32(6))
+    seqs, ws = _i32(2), [torch.zeros((3, 2, 512)) for _ in range(4)]
+    mine = {}
+
+    def evict(w):
+        mine[threading.get_ident()] = w.data_ptr()
+        pool.evict(seqs, seqs, w, 10)
+
+    _in_threads(*[lambda w=w: evict(w) for w in ws])
+    assert len(slow) == len(ws)
+    for thread, what, weights, together in slow:
+        assert what == "msa_pages_evict" and weights == [mine[thread]] and together == 1
+
+
+def test_operators_of_several_threads_are_launched_one_by_one(slow):
+    """Their launches share the workspace's lists."""
+    pool = PagePool([_cache()], _i32(3), _i32(3, 4), _i32(6))
+    seqs, w = _i32(2), torch.zeros((3, 2, 512))
+    _in_threads(lambda: pool.fork(seqs, seqs), lambda: pool.evict(seqs, seqs, w, 10), lambda: pool.free(seqs), pool.compact)
+    assert sorted(x[1] for x in slow) == ["msa_pages_compact", "msa_pages_evict", "msa_pages_fork", "msa_pages_free"]
+    assert [x[3] for x in slow] == [1] * 4
