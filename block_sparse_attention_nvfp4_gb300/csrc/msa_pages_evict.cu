@@ -525,7 +525,9 @@ msa_status msa_pages_evict(const msa_page_pool* a, int32_t n, const int32_t* par
   e.cap = static_cast<int>(kept_cap(a, keep));
   e.parents = parents;
   e.children = children;
-  if (n > 0 && (scratch == nullptr || unaligned(scratch, 16) || scratch_bytes < sizeof(int2) * static_cast<size_t>(n) * e.heads * e.cap))
+  // a `keep` as long as the block table: no sequence is longer, so none is selected from
+  const bool selects = n > 0 && keep < static_cast<long long>(a->max_pages_per_seq) * kBlock;
+  if (selects && (scratch == nullptr || unaligned(scratch, 16) || scratch_bytes < sizeof(int2) * static_cast<size_t>(n) * e.heads * e.cap))
     return MSA_ERR_WORKSPACE;
   e.kept = static_cast<int2*>(scratch);
   const int pages = (e.cap + kBlock - 1) / kBlock;

@@ -72,7 +72,9 @@ class PagePool:
         lib = _lib.load()
         self._fns = {n: getattr(lib, n) for n in ("msa_pages_copy", "msa_pages_fork", "msa_pages_reserve",
                                                   "msa_pages_free", "msa_pages_compact", "msa_pages_evict")}
-        self._scratch, self._scratches = None, []   # evict's; outgrown ones live on, as captured graphs may hold them
+        # evict's; outgrown ones live on, as captured graphs may hold them (together less than the one in use, each being at
+        # most half of the next)
+        self._scratch, self._scratches = None, []
         self._evict_caches, self._evict_shapes, self._most = None, (), M * BLOCK   # and the shapes of each one's weights
         # An operator is several launches that share the workspace: no other thread's come between them.
         self._lock = threading.RLock()
@@ -182,8 +184,8 @@ class PagePool:
             x.head_stride = tokens
         if not (0 < keep <= _INT_MAX and 0 <= sinks and 0 <= recent and sinks + recent <= keep):
             raise ValueError(f"evict: expected keep >= 1 and sinks + recent <= keep, got {keep}, {sinks}, {recent}")
-        # (what msa_pages_evict_scratch_size says)
-        need = n * self._evict_bytes * min(keep, most)
+        # (what msa_pages_evict_scratch_size says; none where no sequence can be longer than keep)
+        need = n * self._evict_bytes * keep if keep < most else 0
         with self._lock:
             scratch = self._scratch
             if scratch is None or scratch[1] < need:

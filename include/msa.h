@@ -578,7 +578,8 @@ msa_status msa_pages_compact(const msa_page_pool* pool, int32_t* new_block_table
  * for msa_pages_fork: the entry does nothing.
  * The pool's planes are not looked at: `caches` (host array, 1 .. 4) are all the caches on its pages. keep >= 1,
  * sinks + recent <= keep, n <= num_seqs, max_pages_per_seq up to 2^24 - 256. scratch: device memory of
- * msa_pages_evict_scratch_size bytes (host-only), 16-byte aligned, whatever it holds; ws as for the other page operators. */
+ * msa_pages_evict_scratch_size bytes (host-only), 16-byte aligned, whatever it holds; it is not used, and may be NULL, when
+ * keep is at least 128 max_pages_per_seq, as no sequence is longer. ws as for the other page operators. */
 typedef struct {
   uint8_t* k_data;             /* planes of an 8-bit cache, as in msa_kv8_append_args */
   float* k_scale;

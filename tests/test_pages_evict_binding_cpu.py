@@ -1,6 +1,7 @@
 """Host checks of what PagePool.evict binds: its demands on the caches' planes are its own, not the other operators'. The
 library is a stand-in that records what a launch would have got."""
 import contextlib
+import ctypes
 import threading
 import time
 
@@ -8,6 +9,7 @@ import pytest
 import torch
 
 from block_sparse_attention_nvfp4_gb300 import KV8Cache, PagePool, _lib, pages
+from block_sparse_attention_nvfp4_gb300 import build as msa_build
 from tests.test_kv8_binding_cpu import _i32, launches  # noqa: F401  (the fixture)
 
 
@@ -103,3 +105,24 @@ def test_operators_of_several_threads_are_launched_one_by_one(slow):
     _in_threads(lambda: pool.fork(seqs, seqs), lambda: pool.evict(seqs, seqs, w, 10), lambda: pool.free(seqs), pool.compact)
     assert sorted(x[1] for x in slow) == ["msa_pages_compact", "msa_pages_evict", "msa_pages_fork", "msa_pages_free"]
     assert [x[3] for x in slow] == [1] * 4
+
+
+def test_no_scratch_where_no_sequence_can_be_longer_than_keep(slow):
+    pool = PagePool([_cache()], _i32(3), _i32(3, 4), _i32(6))
+    seqs, w = _i32(2), torch.zeros((3, 2, 512))
+    for keep in (512, 10 ** 9):
+        pool.evict(seqs, seqs, w, keep)
+        assert pool._scratch[1] == 256
+    pool.evict(seqs, seqs, w, 511)
+    assert pool._scratch[1] == 8 * 2 * 2 * 511
+
+
+def test_the_library_wants_none_either():
+    """Seen by which refusal comes first: so many new pages that no grid holds them, or the scratch that is not there."""
+    msa_build.build()
+    lib, x = _lib.load(), 1 << 21       # (addresses that are never dereferenced)
+    pool = _lib.PagePoolArgs(num_seqs=1 << 20, num_pages=16, max_pages_per_seq=8, num_planes=0, seq_lens=x, block_table=x, ref_counts=x)
+    caches = (_lib.Kv8EvictCache * 4)(*[_lib.Kv8EvictCache(x, x, x, x, x, 1024, 64) for _ in range(4)])
+    for keep, code in ((1024, -2), (1 << 30, -2), (1023, -4)):
+        assert lib.msa_pages_evict(ctypes.byref(pool), 1 << 20, x, x, 4, caches, keep, 0, 0, None, 0, ctypes.c_void_p(1 << 20),
+                                   1 << 40, None) == code
