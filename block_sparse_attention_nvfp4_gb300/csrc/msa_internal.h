@@ -133,11 +133,15 @@ struct Kv8AttnParams {
   int window, sinks, sink_pages;
   // msa_kv8_attn_shared
   int num_groups;
+  int alone_log2;            // chunk_log2 of a request that shares nothing: the plain call's (a group's is chunk_log2)
   const int4* groups;        // [num_groups] {shared pages (0: none), first row, rows, first member}
   const int32_t* group_indptr;
   const int32_t* skip;       // [num_reqs] shared pages of a request's group
   const GroupChunk* chunks;  // group g's row chunks from (first row) / chunk + g on
 };
+
+cudaError_t launch_kv8_attn_shared_wide(const CUtensorMap& kmap, const Kv8AttnParams& prm, int copies, bool q_bf16, int grid,
+                                        cudaStream_t st);
 
 // Merge of the rank-local candidate lists of indexer decode context parallelism
 // (msa_dcp_merge_topk).

@@ -1,8 +1,10 @@
 // Attention over the 8-bit cache: E4M3 keys and values with one FP32 scale for each 128-token page and KV
-// head. One kernel in three forms, compiled one to a file:
+// head. One kernel in four forms, compiled one to a file:
 //   kAll     (msa_kv8_attn.cu)         every block, or listed ones
 //   kWindow  (msa_kv8_attn_window.cu)  the last tokens and the first ones
-//   kShared  (msa_kv8_attn_shared.cu)  requests whose block tables begin alike read those pages once
+//   kShared  (msa_kv8_attn_shared.cu)  requests whose block tables begin alike read those pages together
+//   kSharedWide  (msa_kv8_attn_shared_wide.cu)  the same, where requests that share nothing have chunks of more rows
+//                                      than a group's
 // What a form alone needs stands behind `if constexpr`, so that the others' code does not know of it.
 //
 // For a query row at position p, over the keys t <= p of the listed blocks (or of all), with
@@ -84,7 +86,9 @@
 namespace msa {
 namespace {
 
-enum Form : int { kAll, kWindow, kShared };
+enum Form : int { kAll, kWindow, kShared, kSharedWide };
+template <Form F>
+constexpr bool kIsShared = F == kShared || F == kSharedWide;
 
 constexpr int kSoftWarps = 8;                        // warps 0..7: two sets of 4, one per TMEM lane quadrant
 constexpr int kMmaWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11;
@@ -164,7 +168,8 @@ struct Smem {
   float red[2][kRedRows * kRedStride];               // by set: what the copies exchange
   float qscale[kRows][128];                          // 2^e of each tile row (BF16 queries)
   int nanpos[kRows][kDim];                           // first position with a NaN value in a dim, of partly seen tokens
-                                                     // (kWindow: see mark_nan; kShared: a bit for each row that sees one)
+                                                     // (kWindow: see mark_nan; kShared: a bit for each row that sees one, or
+                                                     // with more rows than bits 128 - the first of them)
   int nanany[kRows];
   float half_max[2][2][128];                         // by tile parity: each set's maxima, or the reference
   float xm[2][128], xl[2][128], xm2[2][128];
@@ -202,9 +207,9 @@ __host__ __device__ inline size_t headers_bytes(int grid) { return (grid * sizeo
 // Places of an item before its tiles. 64 ragged requests / 16 requests with 16 listed blocks each take
 // 168 / 24.7 us with 4 places, 164 / 25.0 with 5, 163 / 25.3 with 6.
 // (With shared pages 3, 6 and 10 places measure within 1 %.)
-constexpr int kSharedRows = 32;  // query rows of an item at most: a bit each
+constexpr int kSharedRows = 32;  // query rows of a group's item at most: a bit each
 template <Form F>
-constexpr int kItemCost = F == kShared ? 6 : 5;
+constexpr int kItemCost = kIsShared<F> ? 6 : 5;
 struct Req {
   int N, R, r0;
   int row;       // its row of the block table (a group: its first member)
@@ -217,12 +222,12 @@ struct Req {
 // rows: its tiles are the group's pages, which all rows see, and then each member's own, for the member's rows.
 template <Form F>
 __device__ __forceinline__ int units_of(const Kv8AttnParams& p) {
-  return F == kShared ? p.num_groups + p.num_reqs : p.num_reqs;
+  return kIsShared<F> ? p.num_groups + p.num_reqs : p.num_reqs;
 }
 template <Form F>
 __device__ __forceinline__ bool load_req(const Kv8AttnParams& p, int b, Req* q) {
   q->pages = 0;
-  if constexpr (F == kShared) {
+  if constexpr (kIsShared<F>) {
     if (b < p.num_groups) {
       const int4 g = p.groups[b];
       q->N = 0;
@@ -248,7 +253,15 @@ __device__ __forceinline__ bool load_req(const Kv8AttnParams& p, int b, Req* q) 
   return q->N >= 0 && q->N <= p.max_pages * static_cast<long long>(kBlock) && q->R >= 0 && q->R <= p.max_rows &&
          q->R <= q->N && q->r0 >= 0 && q->r0 <= p.total_rows - q->R;
 }
-__device__ __forceinline__ int chunks_of(const Kv8AttnParams& p, int R) { return (R + p.chunk - 1) >> p.chunk_log2; }
+// Rows of its items, log2.
+template <Form F>
+__device__ __forceinline__ int log2_of(const Kv8AttnParams& p, const Req& q) {
+  return F == kSharedWide && q.pages == 0 ? p.alone_log2 : p.chunk_log2;
+}
+template <Form F>
+__device__ __forceinline__ int chunks_of(const Kv8AttnParams& p, const Req& q) {
+  return (q.R + (1 << log2_of<F>(p, q)) - 1) >> log2_of<F>(p, q);
+}
 // Pages between the first tokens' and those of the window of row chunk i (its first row's), which no row sees.
 __device__ __forceinline__ int gap_of(const Kv8AttnParams& p, const Req& q, int i) {
   const int from = q.N - q.R + (i << p.chunk_log2) - p.window + 1;
@@ -259,9 +272,9 @@ __device__ __forceinline__ int gap_of(const Kv8AttnParams& p, const Req& q, int 
 template <Form F>
 __device__ __forceinline__ int tiles_of(const Kv8AttnParams& p, const Req& q, int i) {
   if (F == kAll && p.n_ids) return p.n_ids;
-  if (F == kShared && q.pages > 0)
+  if (kIsShared<F> && q.pages > 0)
     return static_cast<int>(q.chunks[i].places - (i > 0 ? q.chunks[i - 1].places : 0)) - kItemCost<F>;
-  const int end = (i + 1) << p.chunk_log2;
+  const int end = (i + 1) << log2_of<F>(p, q);
   const int last = q.N - q.R + (end < q.R ? end : q.R) - 1;
   const int n = (last >> 7) + 1;
   return F == kWindow ? n - gap_of(p, q, i) : n;
@@ -273,7 +286,8 @@ __device__ __forceinline__ int tiles_of(const Kv8AttnParams& p, const Req& q, in
 template <Form F>
 __device__ __forceinline__ long long tiles_before(const Kv8AttnParams& p, const Req& q, int i) {
   if (F == kAll && p.n_ids) return static_cast<long long>(i) * p.n_ids;
-  const int base = q.N - q.R - 1, a = base >> 7, c0 = (base & 127) >> p.chunk_log2, lu = 7 - p.chunk_log2;
+  const int log2 = log2_of<F>(p, q);
+  const int base = q.N - q.R - 1, a = base >> 7, c0 = (base & 127) >> log2, lu = 7 - log2;
   auto floors = [lu](long long m) {  // sum of j >> lu over j < m
     const long long w = m >> lu, rem = m & ((1LL << lu) - 1);
     return (w * (w - 1) / 2 << lu) + w * rem;
@@ -293,13 +307,13 @@ __device__ __forceinline__ long long tiles_before(const Kv8AttnParams& p, const 
 // Places on the line before row chunk i (at most the last one), and of one KV head of the request.
 template <Form F>
 __device__ __forceinline__ long long cost_before(const Kv8AttnParams& p, const Req& q, int i) {
-  if (F == kShared && q.pages > 0) return i > 0 ? q.chunks[i - 1].places : 0;
+  if (kIsShared<F> && q.pages > 0) return i > 0 ? q.chunks[i - 1].places : 0;
   return i > 0 ? tiles_before<F>(p, q, i) + static_cast<long long>(i) * kItemCost<F> : 0;
 }
 template <Form F>
 __device__ __forceinline__ long long head_cost(const Kv8AttnParams& p, const Req& q) {
   if (q.R == 0) return 0;
-  const int n = chunks_of(p, q.R);
+  const int n = chunks_of<F>(p, q);
   return cost_before<F>(p, q, n - 1) + kItemCost<F> + tiles_of<F>(p, q, n - 1);
 }
 // C copies of the query rows down the MMA tile (128 / C rows each); NP = E4M3 parts of a query.
@@ -337,14 +351,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     init(sm.row_told, 4, 74, kTurns ? 1 : 2);
     if (tid < 96) mbar_fence_init();
   }
-  for (int i = tid; i < kRows * kDim; i += kThreads) (&sm.nanpos[0][0])[i] = F == kWindow ? kNoNan : F == kShared ? 0 : INT_MAX;
+  for (int i = tid; i < kRows * kDim; i += kThreads) (&sm.nanpos[0][0])[i] = F == kWindow ? kNoNan : kIsShared<F> ? 0 : INT_MAX;
   if (tid < kRows) sm.nanany[tid] = 0;
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&sm.taddr), kTmemCols);
   if (warp == kKWarp && lane == 0)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
 
   // ---- the line: every thread sums a run of requests; the K warp finds the CTA's range in the sums
-  if constexpr (F == kShared) pdl_wait_primary();  // for the groups
+  if constexpr (kIsShared<F>) pdl_wait_primary();  // for the groups
   const int units = units_of<F>(p);
   const int per = (units + kThreads - 1) / kThreads;
   long long* sums = reinterpret_cast<long long*>(sm.red[0]);  // inclusive within a warp (red has no use yet)
@@ -447,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (left > 0) {
       Req q;
       load_req<F>(p, b, &q);
-      int h, ch, at, n_ch = chunks_of(p, q.R);  // at: the CTA's place in the item
+      int h, ch, at, n_ch = chunks_of<F>(p, q);  // at: the CTA's place in the item
       {
         const long long hc = head_cost<F>(p, q);
         h = start < (1LL << 31) && hc < (1LL << 31)
@@ -471,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j1 <= j0) break;  // the range ends before the item's first tile
         const int nb = (q.N + kBlock - 1) / kBlock;
         const bool begin = j0 == 0, end = j1 == nt;
-        const int row0 = ch << p.chunk_log2, rows = q.R - row0 < p.chunk ? q.R - row0 : p.chunk;
+        const int log2 = log2_of<F>(p, q), row0 = ch << log2, rows = q.R - row0 < 1 << log2 ? q.R - row0 : 1 << log2;
         const int32_t* table = p.block_table + static_cast<long long>(q.row) * p.max_pages;
         // listed blocks: lane j holds id j; the ones of this segment that count
         int id = -1;
@@ -486,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           use = __ballot_sync(0xFFFFFFFFu, in && !twice && lane >= j0 && lane < j1);
         }
         const int count = n_ids ? (use ? __popc(use) : 1) : j1 - j0;
-        const int first = t, last = t + count - 1, pos = F == kShared ? 0 : q.N - q.R + row0;
+        const int first = t, last = t + count - 1, pos = kIsShared<F> ? 0 : q.N - q.R + row0;
         auto marks = [&]() { return (t == first ? kFirst : 0) | (t == last ? kLast : 0); };
         const int slot = begin && end ? -1 : (begin ? 1 : 0);
         if (lane == 0) {
@@ -533,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             iv = vzero ? exp2f(-kZeroLog2) : 1.f / vs;
           }
         };
-        if constexpr (F == kShared) {
+        if constexpr (kIsShared<F>) {
           // 32 members at a time, one a lane: the rows of the chunk that are its own, the position of the first, its
           // tiles behind the group's (all of a request that is in no group)
           int m0 = q.pages > 0 ? q.chunks[ch].first : q.row, own0 = 0;  // the first lane's member; tiles of those before
@@ -638,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             h = 0;
             do ++b; while (b < units && (!load_req<F>(p, b, &q) || q.R == 0));
             if (b == units) break;  // never, unless the lengths changed meanwhile
-            n_ch = chunks_of(p, q.R);
+            n_ch = chunks_of<F>(p, q);
           }
         }
       }
@@ -774,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pos = sm.seg[k % kRing].pos;
         // (a chunk has at most `window` rows, so a token is never before one row's window and after another row)
         const int left = F == kWindow ? pos + sm.seg[k % kRing].rows - 1 - p.window : 0;
-        const int span = F == kShared ? sm.tile[t % kRing].span : 0, seg_rows = F == kShared ? sm.seg[k % kRing].rows : 0;
+        const int span = kIsShared<F> ? sm.tile[t % kRing].span : 0, seg_rows = kIsShared<F> ? sm.seg[k % kRing].rows : 0;
         int words = 16;
         if constexpr (F != kAll) {
           // Whether there is a NaN code at all: 0x7F + 1 reaches a byte's top bit. (Where a fifth of the tiles are seen
@@ -798,13 +812,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool low = F == kWindow && tpos <= pos && tpos <= left && tpos >= p.sinks;
           // kShared: the rows from `seen` on, before the tile's last, see the token
           const int seen = max(span & 0xFFFF, tpos);
-          const bool everyone = F == kShared ? seen == 0 && (span >> 16) >= seg_rows : tpos <= pos && !low;
+          const bool everyone = kIsShared<F> ? seen == 0 && (span >> 16) >= seg_rows : tpos <= pos && !low;
           if (nan == 0u || token >= x.y || everyone) continue;
           for (int z = 0; z < 4; ++z)
             if ((nan >> (8 * z)) & 1u) {
               int* mark = &sm.nanpos[k % kRows][16 * vc + 4 * (i & 3) + z];
-              if constexpr (F == kShared) {
-                if (seen < (span >> 16))
+              if constexpr (kIsShared<F>) {
+                // (more rows than bits: a request's own, which see a token from one row on)
+                if (F == kSharedWide && seen < (span >> 16) && seg_rows > kSharedRows) atomicMax(mark, 128 - seen);
+                else if (seen < (span >> 16))
                   atomicOr(mark, static_cast<int>((0xFFFFFFFFu >> (kSharedRows - (span >> 16))) & (0xFFFFFFFFu << seen)));
               } else if constexpr (F == kWindow) mark_nan(mark, low ? 0xFFFF : tpos - pos, low ? tpos - pos + p.window : 0);
               else atomicMin(mark, tpos);
@@ -979,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           f[u] *= inv;
           if (nans) {
             const int mark = sm.nanpos[k % kRows][d + u], r = mm / G;
-            if (F == kShared ? (mark >> r & 1) != 0 : F == kWindow ? (mark & 0xFFFF) <= r || (mark >> 16) > r : mark <= sg.pos + r) f[u] = __int_as_float(0x7FFFFFFF);
+            if (kIsShared<F> ? (F == kSharedWide && sg.rows > kSharedRows ? r + mark >= 128 : (mark >> r & 1) != 0) : F == kWindow ? (mark & 0xFFFF) <= r || (mark >> 16) > r : mark <= sg.pos + r) f[u] = __int_as_float(0x7FFFFFFF);
           }
         }
         if (whole) {
@@ -1119,7 +1135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       if (!meet(&sm.sets_met, met_all)) return false;
       if (nans) {
-        if (s == 0) sm.nanpos[k % kRows][l] = F == kWindow ? kNoNan : F == kShared ? 0 : INT_MAX;
+        if (s == 0) sm.nanpos[k % kRows][l] = F == kWindow ? kNoNan : kIsShared<F> ? 0 : INT_MAX;
         if (tid == 0) sm.nanany[k % kRows] = 0;
       }
       mref = -INFINITY;
@@ -1146,9 +1162,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       float lv = y.y, iv = y.z;
       // every token visible to every row that sees any (the others' maxima and weights are dropped)
-      const bool full_vis = (!(x.z & kPart) || (F == kShared && kTurns && x.z & kOthers)) && x.y == kBlock;
+      const bool full_vis = (!(x.z & kPart) || (kIsShared<F> && kTurns && x.z & kOthers)) && x.y == kBlock;
       int lim = pos_max - x.w - k0;                            // token k0 + n visible iff n <= lim
-      if constexpr (F == kShared) {  // rows of other members see nothing of a member's tile
+      if constexpr (kIsShared<F>) {  // rows of other members see nothing of a member's tile
         const int span = __float_as_int(y.w);
         const bool apart = row < (span & 0xFFFF) || row >= (span >> 16);
         if (apart) lim = -1;
@@ -1170,7 +1186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       float mx = -INFINITY;
       // A warp none of whose rows sees any of its tokens (of a member's tile, most) only writes zeros.
-      const bool none = F == kShared && kTurns && !__any_sync(0xFFFFFFFFu, lim >= 0);
+      const bool none = kIsShared<F> && kTurns && !__any_sync(0xFFFFFFFFu, lim >= 0);
       if (none) {
       } else if (kCh > 1 && full_vis) {
 #pragma unroll 1
@@ -1204,7 +1220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (kCh > 1) tc_wait_st();
       }
-      if (F == kShared && kTurns && lim < 0) mx = -INFINITY;
+      if (kIsShared<F> && kTurns && lim < 0) mx = -INFINITY;
       float* hm = &sm.half_max[t & 1][0][0];
       float r_old = mref;
       if constexpr (kTurns) {  // the reference goes from tile to tile and so from set to set
@@ -1253,8 +1269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float off = !kTurns && faint ? -mxs : lv - ref;
       const float2 coef2 = make_float2(coef, coef), off2 = make_float2(off, off);
       float2 acc = make_float2(0.f, 0.f);
-      const bool dropped = F == kShared && kTurns && lim < 0;
-      if (F == kShared && none) {
+      const bool dropped = kIsShared<F> && kTurns && lim < 0;
+      if (kIsShared<F> && none) {
 #pragma unroll
         for (int ch = 0; ch < kCh; ++ch) tmem_zero16(s_cols + 64 * (ch >> 1) + 16 * (ch & 1));
       } else
@@ -1271,7 +1287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!kTurns && some_faint)
 #pragma unroll
           for (int u = 0; u < kStep / 2; ++u) v[u] = faint ? 0u : v[u];
-        if constexpr (F == kShared && kTurns)
+        if constexpr (kIsShared<F> && kTurns)
 #pragma unroll
           for (int u = 0; u < kStep / 2; ++u) v[u] = dropped ? 0u : v[u];
         if constexpr (kTurns) tmem_st16(s_cols + 64 * (ch >> 1) + 16 * (ch & 1), v);
@@ -1334,9 +1350,9 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8At
   // partials: the starting CTA's, then those of the next ones up to the item's last
   auto middle = [&](int i) { return i < grid && hd[i].cont && !hd[i].cont_end; };
   Header back;
-  if (F == kShared) back = hd[max(cta - 1 - lane, 0)];  // (on its way together with the next)
+  if (kIsShared<F>) back = hd[max(cta - 1 - lane, 0)];  // (on its way together with the next)
   unsigned ends = __ballot_sync(0xFFFFFFFFu, !middle(cta + 1 + lane));
-  if (F == kShared && !me.tail && me.cont && !me.cont_end) {  // inside an item: helps with it
+  if (kIsShared<F> && !me.tail && me.cont && !me.cont_end) {  // inside an item: helps with it
     unsigned tails = __ballot_sync(0xFFFFFFFFu, cta - 1 - lane >= 0 && back.tail);
     for (; tails == 0u && cta > 32; cta -= 32) {
       back = hd[max(cta - 33 - lane, 0)];
@@ -1365,7 +1381,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv8_merge_kernel(const Kv8At
   // With shared pages an item has many rows and many partials at once. Its first CTA and those inside it share the rows then,
   // 8 at a time, and each counts its turns: a run of partials, or of every eighth of them and the join. (16 requests of a row on
   // 8,192 shared keys, 128 rows of 20 partials: 29.5 us, 42 by the first CTA alone.)
-  const int units = (rows + 7) / 8, ctas = F == kShared && n > 2 ? n - 1 : 1, mine = (units + ctas - 1) / ctas;
+  const int units = (rows + 7) / 8, ctas = kIsShared<F> && n > 2 ? n - 1 : 1, mine = (units + ctas - 1) / ctas;
   const bool shared = n > kPairs && (F != kShared || mine * ((n + 31) / 32 + 1) < (mine + 7) / 8 * ((n + 3) / 4));
   const int pair = warp >> 1, d = 32 * blockIdx.y + 16 * (warp & 1) + 4 * (lane >> 3);
   const int first = shared ? pair : 0, step = shared ? kPairs : 1;
@@ -1451,7 +1467,7 @@ cudaError_t launch(const CUtensorMap& kmap, const Kv8AttnParams& prm, int grid, 
   const int smem = static_cast<int>(sizeof(Smem<NP>)) + 1024;
   cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<C, NP, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  if constexpr (F == kShared) {
+  if constexpr (kIsShared<F>) {
     e = launch_after(kv8_attn_kernel<C, NP, F>, dim3(grid), kThreads, smem, st, kmap, prm);
   } else {
     kv8_attn_kernel<C, NP, F><<<grid, kThreads, smem, st>>>(kmap, prm);
@@ -1480,6 +1496,13 @@ inline int copies_for(int max_rows, int q_per_kv) {
   while (r < max_rows && r < 128) r *= 2;
   const long long m = r * q_per_kv;
   return m <= 32 ? 4 : m <= 64 ? 2 : 1;
+}
+// log2 of the rows of a chunk: a power of two.
+inline int chunk_log2_for(int max_rows, int q_per_kv) {
+  const int room = 128 / copies_for(max_rows, q_per_kv) / q_per_kv;
+  int n = 0;
+  while (2 << n <= room) ++n;
+  return n;
 }
 
 // Bytes of workspace before what a form adds: flags, the CTAs' headers, two partials for each CTA.
@@ -1533,9 +1556,8 @@ inline msa_status set_params(const msa_kv8_attn_args* a, void* ws, size_t ws_byt
   p.out = a->out;
   p.lse = a->lse;
   *copies = copies_for(rows, p.q_per_kv);
-  const int room = 128 / *copies / p.q_per_kv;
-  p.chunk = 1;
-  while (2 * p.chunk <= room) p.chunk *= 2, ++p.chunk_log2;
+  p.chunk_log2 = chunk_log2_for(rows, p.q_per_kv);
+  p.chunk = 1 << p.chunk_log2;
   *out = p;
   return encode_kv8_map(kmap, a->k_data, static_cast<long long>(a->num_pages) * a->num_kv_heads * kBlock);
 }

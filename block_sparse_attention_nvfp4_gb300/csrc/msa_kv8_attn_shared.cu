@@ -17,7 +17,14 @@ namespace msa {
 namespace {
 
 constexpr int kGroupThreads = 1024;
-// Pages, over all KV heads and groups, that sharing has to save before it pays. The groups' kernel and more partials an item
+// The sum over a warp's lanes of numbers from 0 to 2^50.
+__device__ __forceinline__ long long warp_sum(long long x) {
+  const unsigned low = __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(x & 0xFFFFFF));
+  return low + (static_cast<long long>(__reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(x >> 24))) << 24);
+}
+// Reads of a page by a row chunk, over all KV heads and groups, that sharing has to save before it pays. (A request's pages are
+// read once for each of its row chunks, a group's once for each of the group's: prompts, whose chunks are full
+// already, save next to nothing.) The groups' kernel and more partials an item
 // cost some 8 us against the plain call, which is taken where the sizes leave less than kMinSizes to save. Behind the groups'
 // kernel, with tiles laid out for a group's rows, it pays sooner: from kMinSaved on. Measured (4 KV heads, BF16, one row a
 // member; shared / behind the groups' kernel but alone / the plain call, us):
@@ -34,6 +41,8 @@ constexpr int kMinSizes = 2048, kMinSaved = 768;
 __global__ void __launch_bounds__(kGroupThreads) kv8_groups_kernel(const Kv8AttnParams p, const int32_t* indptr, int4* groups,
                                                                    int32_t* skip, GroupChunk* chunks, long long least) {
   __shared__ int s_limit, s_members, s_pages;
+  __shared__ long long s_apart[kGroupThreads / 32];
+  static_assert(kGroupThreads == 1024, "");
   pdl_launch_dependents();
   const int tid = threadIdx.x, g = blockIdx.x, n = p.num_groups;
   if (tid == 0) s_limit = s_pages = INT_MAX, s_members = 0;
@@ -56,6 +65,7 @@ __global__ void __launch_bounds__(kGroupThreads) kv8_groups_kernel(const Kv8Attn
     return;
   }
   int limit = INT_MAX, members = 0;
+  long long apart = 0;  // tiles of the members when they are alone
   bool wrong = false;
   for (int b = b0 + tid; b < b1; b += kGroupThreads) {
     Req q;
@@ -64,8 +74,14 @@ __global__ void __launch_bounds__(kGroupThreads) kv8_groups_kernel(const Kv8Attn
     } else if (q.R > 0) {
       limit = min(limit, (q.N - q.R) / kBlock);
       ++members;
+      q.pages = 0;
+      const int last = chunks_of<kSharedWide>(p, q) - 1;
+      apart += tiles_of<kSharedWide>(p, q, last);
+      if (last > 0) apart += tiles_before<kSharedWide>(p, q, last);
     }
   }
+  apart = warp_sum(apart);
+  if ((tid & 31) == 0) s_apart[tid >> 5] = apart;
   limit = __reduce_min_sync(0xFFFFFFFFu, limit);
   members = __reduce_add_sync(0xFFFFFFFFu, members);
   if ((tid & 31) == 0) {
@@ -105,62 +121,90 @@ __global__ void __launch_bounds__(kGroupThreads) kv8_groups_kernel(const Kv8Attn
   differs = __reduce_min_sync(0xFFFFFFFFu, differs);
   if (differs != INT_MAX && (tid & 31) == 0) atomicMin(&s_pages, differs);
   __syncthreads();
-  int pages = min(most, s_pages);
-  if (static_cast<long long>(members - 1) * pages * p.num_kv_heads < least) pages = 0;
-  for (int b = b0 + tid; b < b1; b += kGroupThreads) skip[b] = pages;
+  const int pages = min(most, s_pages);
   const int r0 = b0 < b1 ? p.q_indptr[b0] : 0, rows = b0 < b1 ? p.q_indptr[b1] - r0 : 0;
-  if (tid == 0) groups[g] = make_int4(pages, r0, rows, b0);
-  if (pages == 0) return;
-  // the row chunks: the members' own tiles in each, places on the line up to its end. (The groups before this one have at
-  // most r0 / chunk + g chunks.)
-  constexpr int kStep = 2 * kGroupThreads;
-  __shared__ int s_own[kStep], s_part[kGroupThreads / 32];
-  const int n_chunks = chunks_of(p, rows);
-  GroupChunk* mine = chunks + (r0 >> p.chunk_log2) + g;
-  long long before = 0;  // own tiles of the chunks before
-  for (int w0 = 0; w0 < n_chunks; w0 += kStep) {
-    for (int i = tid; i < kStep; i += kGroupThreads) s_own[i] = 0;
-    __syncthreads();
-    for (int base = b0; base < b1; base += kGroupThreads) {  // (whole warps: they exchange)
-      const int b = base + tid;
-      int s = 0, e = 0, N = 0;
-      if (b < b1) s = p.q_indptr[b] - r0, e = p.q_indptr[b + 1] - r0, N = p.context_lens[b];
-      // member b's own tiles in its chunks of the rows, every `by`-th from `from` on
-      auto add = [&](int b, int s, int e, int N, int from, int by) {
-        const int i1 = min((e - 1) >> p.chunk_log2, w0 + kStep - 1);
-        for (int i = max(s >> p.chunk_log2, w0) + from; i <= i1; i += by) {
-          const int z = min(e, (i + 1) << p.chunk_log2);
-          atomicAdd(&s_own[i - w0], ((N - e + z - 1) >> 7) + 1 - pages);
-          if (s <= i << p.chunk_log2) mine[i].first = b;
+  // What sharing saves: reads of a page by a row chunk. Of the shared pages at most those of all members but one, whose rows
+  // have a chunk at least each when they are alone and lie in as many when they are together.
+  const bool some = pages > 0 && static_cast<long long>(members - 1) * pages * p.num_kv_heads >= least;
+  auto decide = [&](int n) {
+    for (int b = b0 + tid; b < b1; b += kGroupThreads) skip[b] = n;
+    if (tid == 0) groups[g] = make_int4(n, r0, rows, b0);
+  };
+  decide(some ? pages : 0);
+  if (some) {
+    // the row chunks: the members' own tiles in each, places on the line up to its end. (The groups before this one have at
+    // most r0 / chunk + g chunks.)
+    constexpr int kStep = 2 * kGroupThreads;
+    __shared__ int s_own[kStep], s_part[kGroupThreads / 32];
+    const int n_chunks = (rows + p.chunk - 1) >> p.chunk_log2;
+    GroupChunk* mine = chunks + (r0 >> p.chunk_log2) + g;
+    long long before = 0;  // own tiles of the chunks before
+    for (int w0 = 0; w0 < n_chunks; w0 += kStep) {
+      for (int i = tid; i < kStep; i += kGroupThreads) s_own[i] = 0;
+      __syncthreads();
+      for (int base = b0; base < b1; base += kGroupThreads) {  // (whole warps: they exchange)
+        const int b = base + tid;
+        int s = 0, e = 0, N = 0;
+        if (b < b1) s = p.q_indptr[b] - r0, e = p.q_indptr[b + 1] - r0, N = p.context_lens[b];
+        // member b's own tiles in its chunks of the rows, every `by`-th from `from` on
+        auto add = [&](int b, int s, int e, int N, int from, int by) {
+          const int i1 = min((e - 1) >> p.chunk_log2, w0 + kStep - 1);
+          for (int i = max(s >> p.chunk_log2, w0) + from; i <= i1; i += by) {
+            const int z = min(e, (i + 1) << p.chunk_log2);
+            atomicAdd(&s_own[i - w0], ((N - e + z - 1) >> 7) + 1 - pages);
+            if (s <= i << p.chunk_log2) mine[i].first = b;
+          }
+        };
+        const bool many = e - s > 32 << p.chunk_log2;  // a prompt: its chunks for the whole warp
+        if (s < e && !many) add(b, s, e, N, 0, 1);
+        for (unsigned w = __ballot_sync(0xFFFFFFFFu, many); w != 0u; w &= w - 1u) {
+          const int k = __ffs(w) - 1;
+          add(__shfl_sync(0xFFFFFFFFu, b, k), __shfl_sync(0xFFFFFFFFu, s, k), __shfl_sync(0xFFFFFFFFu, e, k),
+              __shfl_sync(0xFFFFFFFFu, N, k), tid & 31, 32);
         }
-      };
-      const bool many = e - s > 32 << p.chunk_log2;  // a prompt: its chunks for the whole warp
-      if (s < e && !many) add(b, s, e, N, 0, 1);
-      for (unsigned w = __ballot_sync(0xFFFFFFFFu, many); w != 0u; w &= w - 1u) {
-        const int k = __ffs(w) - 1;
-        add(__shfl_sync(0xFFFFFFFFu, b, k), __shfl_sync(0xFFFFFFFFu, s, k), __shfl_sync(0xFFFFFFFFu, e, k),
-            __shfl_sync(0xFFFFFFFFu, N, k), tid & 31, 32);
       }
-    }
-    __syncthreads();
-    const int x = s_own[2 * tid], y = s_own[2 * tid + 1];
-    int incl = x + y;
+      __syncthreads();
+      const int x = s_own[2 * tid], y = s_own[2 * tid + 1];
+      int incl = x + y;
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-      if ((tid & 31) >= d) incl += o;
+      for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if ((tid & 31) >= d) incl += o;
+      }
+      if ((tid & 31) == 31) s_part[tid >> 5] = incl;
+      __syncthreads();
+      const int lane = tid & 31, sum = lane < kGroupThreads / 32 ? s_part[lane] : 0;
+      const long long at = before + __reduce_add_sync(0xFFFFFFFFu, lane < tid >> 5 ? sum : 0) + incl - x - y;
+      const long long each = kItemCost<kShared> + pages;
+      const int i = w0 + 2 * tid;
+      if (i < n_chunks) mine[i].places = at + x + (i + 1) * each;
+      if (i + 1 < n_chunks) mine[i + 1].places = at + x + y + (i + 2) * each;
+      before += __reduce_add_sync(0xFFFFFFFFu, sum);
+      __syncthreads();
     }
-    if ((tid & 31) == 31) s_part[tid >> 5] = incl;
-    __syncthreads();
-    const int lane = tid & 31, sum = lane < kGroupThreads / 32 ? s_part[lane] : 0;
-    const long long at = before + __reduce_add_sync(0xFFFFFFFFu, lane < tid >> 5 ? sum : 0) + incl - x - y;
-    const long long each = kItemCost<kShared> + pages;
-    const int i = w0 + 2 * tid;
-    if (i < n_chunks) mine[i].places = at + x + (i + 1) * each;
-    if (i + 1 < n_chunks) mine[i + 1].places = at + x + y + (i + 2) * each;
-    before += __reduce_add_sync(0xFFFFFFFFu, sum);
-    __syncthreads();
+    const long long together = before + static_cast<long long>(n_chunks) * pages;
+    // (each thread rewrites its own)
+    if ((warp_sum(s_apart[tid & 31]) - together) * p.num_kv_heads < least) decide(0);
   }
+}
+
+// Query rows of a request, or of a group, that the tile is laid out for: the rows of a group, on average and up to kSharedRows;
+// or of a request alone, whose items have as many rows as the plain call's.
+int layout_rows(const msa_kv8_attn_args* a, int num_groups) {
+  const int64_t rows = (static_cast<int64_t>(a->total_rows) + num_groups - 1) / num_groups;
+  const int some = rows < kSharedRows ? static_cast<int>(rows) : kSharedRows;
+  return some > a->max_rows_per_req ? some : a->max_rows_per_req;
+}
+// Whether sharing can pay, by the sizes. The row chunks that it saves at most: all members' but one in each group; where a
+// request has one chunk, no more than the chunks that its rows do not fill. Where that is less than a quarter of all row
+// chunks, as with prompts, what the form costs a tile (6 to 10 % more than the plain call's) takes the gain. (2 prompts of 512
+// rows behind 64 pages, 32 x 1 heads: 129 us, 141 with the groups looked at; 8 members of 33 rows, 159 and 166, pass.)
+bool may_pay(const msa_kv8_attn_args* a, int num_groups) {
+  const int alone = chunk_log2_for(layout_rows(a, num_groups), a->q_per_kv);
+  const long long chunks = (static_cast<long long>(a->total_rows) + (1 << alone) - 1) >> alone;
+  long long saved = a->num_reqs - num_groups;
+  if (a->max_rows_per_req <= 1 << alone && 1 << alone <= kSharedRows && a->num_reqs - chunks < saved) saved = a->num_reqs - chunks;
+  return saved * a->max_pages_per_req * a->num_kv_heads >= kMinSizes && 4 * saved >= chunks;
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
@@ -201,16 +245,11 @@ msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* a, int32_t num_groups, c
   if (s != MSA_OK) return s;
   if (a->n_block_ids != 0 || (num_groups > 0 && group_indptr == nullptr)) return MSA_ERR_INVALID_ARG;
   const long long saved = min_saved >= 0 ? min_saved : kMinSaved;
-  // what sharing could save at most, by the sizes
-  const long long most_saved = static_cast<long long>(a->num_reqs - num_groups) * a->max_pages_per_req * a->num_kv_heads;
-  if (num_groups == 0 || (min_saved < 0 && most_saved < kMinSizes)) return msa_kv8_attn(a, ws, ws_bytes, stream);
+  if (num_groups == 0 || (min_saved < 0 && !may_pay(a, num_groups))) return msa_kv8_attn(a, ws, ws_bytes, stream);
   Kv8AttnParams p;
   CUtensorMap kmap;
   int sms = 0, copies = 0;
-  // items have the rows of a group, on average, and no more than kSharedRows
-  const int rows = (a->total_rows + num_groups - 1) / num_groups, some = rows > a->max_rows_per_req ? rows : a->max_rows_per_req;
-  const int most = some < kSharedRows ? some : kSharedRows;
-  if ((s = set_params(a, ws, ws_bytes, added_workspace(a, num_groups), most, &p, &kmap, &sms, &copies)) != MSA_OK) return s;
+  if ((s = set_params(a, ws, ws_bytes, added_workspace(a, num_groups), layout_rows(a, num_groups), &p, &kmap, &sms, &copies)) != MSA_OK) return s;
   if (a->num_reqs == 0 || a->total_rows == 0) return MSA_OK;
   uint8_t* at = static_cast<uint8_t*>(ws) + up256(base_workspace(sms));
   int4* groups = reinterpret_cast<int4*>(at);
@@ -221,13 +260,17 @@ msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* a, int32_t num_groups, c
   p.skip = skip;
   GroupChunk* chunks = reinterpret_cast<GroupChunk*>(at + groups_bytes(num_groups) + skip_bytes(a));
   p.chunks = chunks;
+  p.alone_log2 = p.chunk_log2;
   while (p.chunk > kSharedRows) p.chunk /= 2, --p.chunk_log2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // (each group by itself: its part of what has to be saved)
   kv8_groups_kernel<<<num_groups + 1, kGroupThreads, 0, st>>>(p, group_indptr, groups, skip, chunks,
                                                           (saved + num_groups - 1) / num_groups);
   if (cudaGetLastError() != cudaSuccess) return MSA_ERR_CUDA;
-  return launch_form<kShared>(kmap, p, copies, a->q_type == MSA_TYPE_BF16, sms, st) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+  const bool q_bf16 = a->q_type == MSA_TYPE_BF16;
+  const cudaError_t e = p.alone_log2 > p.chunk_log2 ? launch_kv8_attn_shared_wide(kmap, p, copies, q_bf16, sms, st)
+                                                    : launch_form<kShared>(kmap, p, copies, q_bf16, sms, st);
+  return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
 
 }  // extern "C"

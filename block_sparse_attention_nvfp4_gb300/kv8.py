@@ -176,7 +176,7 @@ class KV8Attention:
     """Attention over a KV8Cache for a batch; owns its workspace and outputs (`out` BF16
     [rows, heads, 128], `lse` FP32 [rows, heads]). Single tokens, speculative rows and prompts
     (causal) take the same call, to all tokens, to listed blocks, to a window and sinks, or with the pages
-    that requests have in common read once (`attend_shared`, for up to `max_groups` groups);
+    that requests have in common read for their rows together (`attend_shared`, for up to `max_groups` groups);
     `add_weights` (with_weights) says how much attention each cached token got. The workspace is laid out
     for what is asked for here; a batch of the same sizes can be bound with `rebind`, and tensors
     that were replaced in the cache or in the batch (a KV8Batch or a DecodeBatch) are seen by the
@@ -291,9 +291,10 @@ class KV8Attention:
     def attend_shared(self, group_indptr: torch.Tensor, stream=None, *, min_saved: Optional[int] = None) -> torch.Tensor:
         """attend() to all keys, for requests whose block tables begin with the same pages: the leading pages
         that the requests group_indptr[g] .. group_indptr[g+1] - 1 (int32 on the GPU, at most
-        max_groups groups) have in common are found and read once for all of the group's rows. min_saved: pages,
-        over all KV heads and groups, that this has to save, else requests are taken alone (None: the
-        library's choice; where the sizes leave less to save, the call is attend() itself)."""
+        max_groups groups) have in common are found and read for the rows of the group together, once for each item
+        of them (128 / queries a KV head, 32 at most). min_saved: page reads, over all KV heads and groups, that this has to
+        save, else requests are taken alone, as prompts are (None: the library's choice; where the sizes, the block
+        table's width among them, leave little to save, the call is attend() itself)."""
         n = group_indptr.numel() - 1
         _need(min_saved is None or 0 <= min_saved <= _INT_MAX, f"min_saved: expected at least 0, got {min_saved}")
         _need(0 <= n <= self.max_groups, f"group_indptr: expected 1 to {self.max_groups + 1} entries (max_groups), got {n + 1}")

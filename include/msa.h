@@ -444,15 +444,20 @@ msa_status msa_kv8_attn_window(const msa_kv8_attn_args* args, int32_t window, in
                                void* stream);
 
 /* Attention for requests whose block tables begin with the same pages (as msa_pages_fork leaves them): what
- * msa_kv8_attn computes, within the same bounds, with each group's common pages read once for all of its rows.
+ * msa_kv8_attn computes, within the same bounds, with each group's common pages read for all of its rows together.
  * Group g is the requests group_indptr[g] .. group_indptr[g+1] - 1 (device int32 [num_groups + 1], not decreasing,
  * within 0 .. num_reqs); requests outside every group are taken alone. How many leading pages the rows of a
  * group's members list in common is found on the device, in each call; only pages that all query rows of
  * the group see whole are shared. A decreasing or out-of-range group_indptr sets MSA_FLAG_BAD_LENGTH and every
  * request is taken alone; so are the members of a group one of whose lengths is inconsistent.
- * min_saved: pages, over all KV heads and groups, that sharing has to save; a group that does not save its part
+ * A page is read once for an item of query rows: 128 / q_per_kv of them (rounded down to a power of two), of a group 32 at
+ * most. So single rows and short runs of rows save nearly all reads of their common pages but one an item, and prompts,
+ * whose items are full when they are taken alone, save next to nothing.
+ * min_saved: page reads, over all KV heads and groups, that sharing has to save; a group that does not save its part
  * (min_saved / num_groups) is taken alone. Negative: the library's own choice, which is msa_kv8_attn itself, without a look
- * at group_indptr, when the sizes in args leave less to save ((num_reqs - num_groups) max_pages_per_req H).
+ * at group_indptr, when the sizes in args leave little to save. Those are the numbers of requests, groups and rows and the
+ * width of the block table: the host does not know the contexts. Where they are far shorter than the table, so that
+ * nothing is saved after all, the look at the groups costs some 6 us; a caller who knows takes msa_kv8_attn.
  * block_ids NULL and n_block_ids 0. num_groups 0 .. 4096. Workspace: msa_kv8_attn_shared_workspace_size (host-only),
  * its first 256 bytes zero-filled once. */
 msa_status msa_kv8_attn_shared_workspace_size(const msa_kv8_attn_args* args, int32_t num_groups, size_t* bytes);
