@@ -34,6 +34,11 @@ __device__ __forceinline__ long long warp_sum(long long x) {
 //   1,536, 4 groups of 4     28.8 / 32.8 / 26.7      3,840, 16 members      29.5 / 46.7 / 36.9
 constexpr int kMinSizes = 2048, kMinSaved = 768;
 
+// Row chunks whose own tiles the groups' kernel adds up at once, in 32 bits. No more than kStep + kMaxReqs pieces of members'
+// rows lie in them, with a table's pages each: the plain call takes tables longer than kLongTable (44.7 million tokens).
+constexpr int kStep = 2 * kGroupThreads;
+constexpr int kLongTable = static_cast<int>((1LL << 31) / (kStep + kMaxReqs));
+
 // CTA g: group g; the last CTA: the requests outside every group. groups[g] = {shared pages (0: none), first row, rows,
 // first member}, skip[b] = shared pages of request b. Bound: latency, a chain of dependent reads (the bounds, the
 // lengths, the tables); the members' entries are compared kRun at a time, all on their way at once (one after the other
@@ -134,7 +139,6 @@ __global__ void __launch_bounds__(kGroupThreads) kv8_groups_kernel(const Kv8Attn
   if (some) {
     // the row chunks: the members' own tiles in each, places on the line up to its end. (The groups before this one have at
     // most r0 / chunk + g chunks.)
-    constexpr int kStep = 2 * kGroupThreads;
     __shared__ int s_own[kStep], s_part[kGroupThreads / 32];
     const int n_chunks = (rows + p.chunk - 1) >> p.chunk_log2;
     GroupChunk* mine = chunks + (r0 >> p.chunk_log2) + g;
@@ -245,7 +249,8 @@ msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* a, int32_t num_groups, c
   if (s != MSA_OK) return s;
   if (a->n_block_ids != 0 || (num_groups > 0 && group_indptr == nullptr)) return MSA_ERR_INVALID_ARG;
   const long long saved = min_saved >= 0 ? min_saved : kMinSaved;
-  if (num_groups == 0 || (min_saved < 0 && !may_pay(a, num_groups))) return msa_kv8_attn(a, ws, ws_bytes, stream);
+  if (num_groups == 0 || (min_saved < 0 && !may_pay(a, num_groups)) || a->max_pages_per_req > kLongTable)
+    return msa_kv8_attn(a, ws, ws_bytes, stream);
   Kv8AttnParams p;
   CUtensorMap kmap;
   int sms = 0, copies = 0;

@@ -172,3 +172,21 @@ def test_prompts_of_few_queries_a_head(groups, H, G, qtype, least):
     assert torch.isnan(want).any() and not torch.isnan(want).all()
     _kv8_long.close(out, want, tol, "out")
     _kv8_long.close(att.lse, lse, tol_lse, "lse")
+
+
+def test_tables_of_more_than_44_million_tokens_take_the_plain_call():
+    """The groups' kernel adds up the own tiles of 2,048 row chunks in 32 bits: as many as 2,048 + 4,096 pieces of members,
+    times the table's pages, have to fit."""
+    cache, batch, lens, indptr, table, g = setup([(16, [(100 + 7 * i, 1) for i in range(3)])], 2, 8, "bf16", 217)
+    for pages, shared in ((349_525, True), (349_526, False)):
+        assert ((2048 + 4096) * pages < 2 ** 31) == shared
+        wide = torch.full((3, pages), -1, dtype=torch.int32, device="cuda")
+        wide[:, :table.shape[1]] = torch.from_numpy(table).cuda()
+        batch.block_table = wide
+        att = KV8Attention(cache, batch, max_groups=1)
+        att.ws[256:].fill_(0x77)
+        plain = att.attend().clone(), att.lse.clone()
+        out = att.attend_shared(ints(g), min_saved=1)
+        assert att.errors() == 0
+        assert (decided(att, 3, 1)[0][0][0] == 16) == shared
+        assert shared or (torch.equal(out, plain[0]) and torch.equal(att.lse, plain[1]))
