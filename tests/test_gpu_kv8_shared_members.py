@@ -152,7 +152,8 @@ def test_the_common_pages_of_a_group():
 @pytest.mark.parametrize("groups", [
     [(12, [(500, 300), (333, 333), (140, 129)]), (6, [(90, 70), (300, 1)])],          # prompts, as a rule alone
     [(40, [(1 + 4 * i, 1) for i in range(50)] + [(700, 300), (40, 33)]), (3, [(260, 256)])],   # one among beams: shared
-], ids=["alone", "mixed"])
+    [(12, [(90, 50), (64, 64), (70, 33)]), (20, [(1 + i, 1) for i in range(10)] + [(60, 40)])],    # two copies of 64 rows
+], ids=["alone", "mixed", "short"])
 @pytest.mark.parametrize("least", [0, 1, 2 ** 31 - 1])
 def test_prompts_of_few_queries_a_head(groups, H, G, qtype, least):
     """1 to 3 queries a KV head: a chunk of a request alone has up to 128 rows, one of a group 32. NaN values that some rows
