@@ -3,13 +3,13 @@
 // and that all their query rows see whole. The attention kernel (msa_kv8_attn.cuh) then takes chunks of all members' rows
 // together: an item's tiles are the group's pages, for all of its rows, and behind them each member's own, for that member's
 // rows alone (the others' weights are 0). So one softmax runs over a row's shared and own keys, shared pages are read once
-// for 128 / q_per_kv rows instead of once for each request, and a tile of the tensor cores is full of rows instead of copies
-// of a few. (Own pages as items of their own, whose FP32 results a further kernel joined with the shared pages', took 51 us
-// instead of 49 for 64 rows of one prompt and 122 instead of 116 for 4 prompts of 16 requests: hundreds of items of one or two
-// tiles, each of which starts and ends.)
+// for a chunk of 128 / q_per_kv rows (kSharedRows at most) instead of once for each request, and a tile of the tensor cores is
+// full of rows instead of copies of a few. (Own pages as items of their own, whose FP32 results a further kernel joined with
+// the shared pages', took 5 % longer for 64 rows of one prompt and for 4 prompts of 16 requests: hundreds of items of one or
+// two tiles, each of which starts and ends.) Whether that pays is counted in reads of a page by a row chunk (below).
 // Floor: the shared pages once a group and the own pages once, or the products: 9 us for 64 beams on 16,384 tokens, 49 for 4 x
-// 16 requests of 8 rows on 8,192 .. 32,768 tokens each. Measured 45 and 112 us (each page read for every request: 172 and 199).
-// Bound: of 64 beams, latency: the groups' kernel 7 us, 4 tiles a CTA, the partials 10; of 4 x 16 requests, own tiles, whose
+// 16 requests of 8 rows on 8,192 .. 32,768 tokens each. Measured 49 and 115 us (msa_kv8_attn, each page read for every request: 173 and 198).
+// Bound: of 64 beams, latency: the groups' kernel 7 us, 17 tiles a CTA, the partials 9; of 4 x 16 requests, own tiles, whose
 // steps cost as much with 8 rows as with 128.
 #include "msa_kv8_attn.cuh"
 
@@ -24,14 +24,16 @@ __device__ __forceinline__ long long warp_sum(long long x) {
 }
 // Reads of a page by a row chunk, over all KV heads and groups, that sharing has to save before it pays. (A request's pages are
 // read once for each of its row chunks, a group's once for each of the group's: prompts, whose chunks are full
-// already, save next to nothing.) The groups' kernel and more partials an item
-// cost some 8 us against the plain call, which is taken where the sizes leave less than kMinSizes to save. Behind the groups'
-// kernel, with tiles laid out for a group's rows, it pays sooner: from kMinSaved on. Measured (4 KV heads, BF16, one row a
-// member; shared / behind the groups' kernel but alone / the plain call, us):
-//     768 saved, 4 members   26.7 / 26.7 / 20.5      1,792, 8 members       25.4 / 32.1 / 26.7
-//     896, 8 members         25.5 / 26.7 / 20.9      1,920, 16 members      28.4 / 34.9 / 26.6
-//     960, 16 members        26.6 / 29.9 / 22.6      3,072, 4 groups of 4   32.1 / 41.0 / 36.9
-//   1,536, 4 groups of 4     28.8 / 32.8 / 26.7      3,840, 16 members      29.5 / 46.7 / 36.9
+// already, save next to nothing.) The groups' kernel and more partials an item cost some 8 us against the plain call, which is
+// taken where the sizes leave less than kMinSizes to save. Behind the groups' kernel, with tiles laid out for a group's rows, it
+// pays sooner: from kMinSaved on. Measured (4 KV heads, BF16, one row a member; shared / behind the groups' kernel but
+// alone / the plain call, us):
+//     768 saved, 4 members   26.7 / 26.8 / 20.7      1,792, 8 members       26.7 / 32.9 / 26.8
+//     896, 8 members         26.4 / 26.8 / 22.6      1,920, 16 members      28.5 / 36.9 / 27.0
+//     960, 16 members        27.3 / 30.9 / 22.8      3,072, 4 groups of 4   32.9 / 42.8 / 37.0
+//   1,536, 4 groups of 4     28.9 / 32.9 / 26.9      3,840, 16 members      30.8 / 47.4 / 37.0
+// The sizes have the table's width, not the lengths, which are on the device: 4 samples on 31 shared pages take 16.6 us, the
+// plain call, with a table as wide as they are long, and 22.6 with one of 512 pages, behind the groups' kernel but alone.
 constexpr int kMinSizes = 2048, kMinSaved = 768;
 
 // Row chunks whose own tiles the groups' kernel adds up at once, in 32 bits. No more than kStep + kMaxReqs pieces of members'

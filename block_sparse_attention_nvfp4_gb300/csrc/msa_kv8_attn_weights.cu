@@ -22,10 +22,11 @@
 // Floors: few rows, memory (128 bytes of a key, 4 read and 4 written per token and head); prompts, exponentials and
 // products alike (two E4M3 products of 128 x 128 x 128 cost what 128 x 128 exponentials do).
 // Measured (4 KV heads of 8 queries; floor): one row over 4,096 keys 10.3 us (0.3), bound by latency; 64 ragged requests of up
-// to 8 rows 67.7 (46.8), memory and the start and end of a CTA; 2,053 rows on 16,421 keys 248 (135). There a unit costs 4,200
-// cycles against 2,048 of exponentials and 2,480 of products, and what bounds it is shared memory: the columns' factors
-// are read for every score (16 bytes at a time, the same for all lanes), 3,100 wavefronts a unit beside the products'
-// operands. (Warps with two pages each read them half as often, but tensor memory has one score buffer a page: half of the
+// to 8 rows 67.4 (46.8), memory and the start and end of a CTA; 2,053 rows on 16,421 keys 246 (135). There a unit costs 4,200
+// cycles against 2,048 of exponentials and 2,480 of products, with 3,150 wavefronts of shared memory beside the products'
+// operands: 1,024 reads of the columns' factors (16 warps, 16 bytes at a time, the same for all lanes), the rest polls of
+// barriers, descriptions and what the copies write. What a factor's read costs was not measured by itself; with E4M3
+// queries, which have half of them and half of the products, the same rows take 206 us (BF16 243 in that run). (Warps with two pages each read them half as often, but tensor memory has one score buffer a page: half of the
 // warps wait for the products then, 297 us in step and 305 with pairs of sets.)
 #include <climits>
 

@@ -1,19 +1,21 @@
 // Eviction (msa_pages_evict): a sequence cut to its first tokens, its last ones and, head by head, the heaviest
 // between, moved to pages of its own in the order of their positions. Two launches:
-//   * the first CTA of kv8_evict_select_kernel is the plan: checks, new pages (the lowest free ids in list order);
-//   * its others, one for each (sequence, cache, head): the weight of the last token kept is found by
+//   * kv8_evict_select_kernel. Its first CTA is the plan: checks, new pages (the lowest free ids in list order). Its
+//     others, one for each (sequence, cache, head), select: the weight of the last token kept is found by
 //     radix selection, three histograms over 11, 10 and 10 bits of the weights as numbers (non-negative FP32 numbers
 //     order like their bits), then the kept positions and weights are written in order; of equal weights the lowest
 //     positions stay. The weights are read once where they fit the registers (8,192 tokens), else four times, five
 //     when many are equal. A warp has a 32nd of the sequence. Bound: instructions (issue slots 63 % busy over 65,536 tokens,
-//     28 us). (Four counts of a digit, by lane, against conflicts: no faster. Warps that take their 128 tokens in turn and
-//     meet for their sums: as fast where tokens are counted once more instead. Clusters of two or four CTAs a head, whose
-//     histograms were added up through distributed shared memory: no faster and slower, the reading took what the split saved.)
+//     28 us); one CTA a head, whatever its length: a sequence of 524,288 tokens with 4 heads, cut to 65,536, takes 204 us on
+//     four SMs. (Over 32 sequences of up to 65,536 tokens: four counts of a digit, by lane, against conflicts: no faster. Warps
+//     that take their 128 tokens in turn and meet for their sums: as fast where tokens are counted once more instead. Clusters
+//     of two or four CTAs a head, whose histograms were added up through distributed shared memory: no faster and slower, the
+//     reading took what the split saved.)
 //   * kv8_evict_move_kernel: a CTA per (sequence, cache, head, new page) gathers the codes of 128 kept tokens. The new
 //     page's scale is the largest of its tokens' pages'; codes of pages with that scale move as they are, the
 //     others are multiplied by the scales' ratio and rounded once (exact between powers of two but for what falls
 //     among the subnormals). Bound: memory, 128 bytes read here and there for each K and V row (32 sequences of 4 heads
-//     cut to 8,192 tokens: 537 MB in 88 us). The last CTA of a
+//     cut to 8,192 tokens: 537 MB in 86 us). The last CTA of a
 //     sequence to have read its old row of the block table rewrites it, the length and the old pages' counts.
 // Ranks come from sums, so nothing depends on timing.
 #include <type_traits>

@@ -310,7 +310,8 @@ class KV8Attention:
                     lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """new[b, h, t] = keep old[b, h, t] + the softmax weights that token t of request b got from this batch's rows, over the
         queries of KV head h; the batch's own tokens, whose slots are new, start from 0, and so does every token
-        with old None. FP32 [B, H, L], L at least the block table's tokens; `new` may be `old`. lse (FP32
+        with old None. FP32 [B, H, L], L at least the block table's tokens; `new` may be `old`. Where PagePool.evict is to
+        go by them, they are rows of the pool's [S, H, L]: a slice, or rows gathered before and copied back after. lse (FP32
         [rows, heads]) is what attend() to all keys left in `lse`, unless given: without it the last attention
         call has to be one to all keys of this batch (attend() or attend_shared()). Needs with_weights."""
         _need(self.with_weights, "add_weights: make the object with with_weights=True")

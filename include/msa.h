@@ -473,7 +473,9 @@ msa_status msa_kv8_attn_shared(const msa_kv8_attn_args* args, int32_t num_groups
  * are. old and new: FP32 [num_reqs][H][head_stride], head_stride >= 128 max_pages_per_req; new may be old, and
  * does not overlap it otherwise. keep: finite, >= 0 (below 1 for weights that fade). max_pages_per_req up to
  * 2^24 - 256.
- * Scores are those of msa_kv8_attn, sums FP32 in an order that does not depend on timing. Tokens on pages
+ * Scores are those of msa_kv8_attn, a BF16 query taken as there. A weight is an FP32 exponential: off by 2^-21 of itself and, for
+ * the rounding of its argument, 2^-22 of it for each unit of the larger of |score| and |lse|. Sums are FP32 in an order that
+ * does not depend on timing. Tokens on pages
  * outside [0, num_pages) get nothing from the rows and set MSA_FLAG_BAD_PAGE; requests with inconsistent lengths
  * are left unwritten and set MSA_FLAG_BAD_LENGTH. Of args block_ids is NULL, n_block_ids 0, and v_data, v_scale,
  * out and lse are not used. Workspace: msa_kv8_attn_weights_workspace_size (host-only), its first 256 bytes
