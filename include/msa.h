@@ -449,7 +449,8 @@ msa_status msa_kv8_attn_window(const msa_kv8_attn_args* args, int32_t window, in
  * within 0 .. num_reqs); requests outside every group are taken alone. How many leading pages the rows of a
  * group's members list in common is found on the device, in each call; only pages that all query rows of
  * the group see whole are shared. A decreasing or out-of-range group_indptr sets MSA_FLAG_BAD_LENGTH and every
- * request is taken alone; so are the members of a group one of whose lengths is inconsistent.
+ * request is taken alone; so are the members of a group one of whose lengths is inconsistent. What is wrong with one member's
+ * own pages (a scale that is none, NaN codes, pages outside the pool) reaches that member's rows alone.
  * A page is read once for an item of query rows: 128 / q_per_kv of them (rounded down to a power of two), of a group 32 at
  * most. So single rows and short runs of rows save nearly all reads of their common pages but one an item, and prompts,
  * whose items are full when they are taken alone, save next to nothing.
