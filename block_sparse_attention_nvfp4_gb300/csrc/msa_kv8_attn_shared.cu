@@ -202,15 +202,18 @@ int layout_rows(const msa_kv8_attn_args* a, int num_groups) {
   return some > a->max_rows_per_req ? some : a->max_rows_per_req;
 }
 // Whether sharing can pay, by the sizes. The row chunks that it saves at most: all members' but one in each group; where a
-// request has one chunk, no more than the chunks that its rows do not fill. Where that is less than a quarter of all row
-// chunks, as with prompts, what the form costs a tile (6 to 10 % more than the plain call's) takes the gain. (2 prompts of 512
-// rows behind 64 pages, 32 x 1 heads: 129 us, 141 with the groups looked at; 8 members of 33 rows, 159 and 166, pass.)
+// request has one chunk, no more than the chunks that its rows do not fill. And where the rows show that all requests are
+// prompts (what they have less than max_rows together is less than one has), of four chunks at least, k members of a
+// group have more than (k - 1) max_rows rows, so 4 (k - 1) chunks, of which no more than k - 1 are saved, whatever the lengths: what
+// the form costs a tile, 6 to 10 % more than the plain call's, and the groups' kernel take that. (2 prompts of 512 rows
+// behind 64 pages, 32 x 1 heads: 129 us, 141 with the groups looked at.)
 bool may_pay(const msa_kv8_attn_args* a, int num_groups) {
   const int alone = chunk_log2_for(layout_rows(a, num_groups), a->q_per_kv);
-  const long long chunks = (static_cast<long long>(a->total_rows) + (1 << alone) - 1) >> alone;
+  const long long rows = a->total_rows, most = a->max_rows_per_req, chunks = (rows + (1 << alone) - 1) >> alone;
+  if (most >= 4LL << alone && rows > (a->num_reqs - 1) * most) return false;
   long long saved = a->num_reqs - num_groups;
-  if (a->max_rows_per_req <= 1 << alone && 1 << alone <= kSharedRows && a->num_reqs - chunks < saved) saved = a->num_reqs - chunks;
-  return saved * a->max_pages_per_req * a->num_kv_heads >= kMinSizes && 4 * saved >= chunks;
+  if (most <= 1 << alone && 1 << alone <= kSharedRows && a->num_reqs - chunks < saved) saved = a->num_reqs - chunks;
+  return saved * a->max_pages_per_req * a->num_kv_heads >= kMinSizes;
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }

@@ -191,3 +191,31 @@ def test_tables_of_more_than_44_million_tokens_take_the_plain_call():
         assert att.errors() == 0
         assert (decided(att, 3, 1)[0][0][0] == 16) == shared
         assert shared or (torch.equal(out, plain[0]) and torch.equal(att.lse, plain[1]))
+
+
+@pytest.mark.parametrize("H,G", [(32, 1), (16, 2), (4, 8)])
+@pytest.mark.parametrize("groups,at,looks", [
+    (BEAMS, [0, 64], True),
+    ([(256, [(1 + 4 * i, 1) for i in range(8)]), (0, [(2048, 2048)])], [0, 8], True),    # a long prompt beside them: 129 of its chunks
+    ([(256, [(1 + 4 * i, 1) for i in range(8)] + [(2100, 2048)])], [0, 9], True),        # or with them
+    ([(600, [(549, 512), (613, 512)])], [0, 2], False),                                   # nothing but prompts
+    ([(600, [(549, 512), (613, 300), (700, 250)])], [0, 3], False),
+    ([(600, [(549, 512), (613, 300), (700, 200)])], [0, 3], True),                        # 512 rows in all may be one request's
+    ([(600, [(549, 512), (613, 1)])], [0, 2], False),                                     # 1 of 5 chunks and more
+], ids=["beams", "beside", "among", "prompts", "uneven", "short", "one"])
+def test_the_librarys_own_choice(groups, at, looks, H, G):
+    """Whether the groups are looked at, by the sizes alone: where they are not, the call is attend() and their place in the
+    workspace stays as it was."""
+    cache, batch, lens, indptr, table, _ = setup(groups, H, G, "bf16", 227)
+    att = KV8Attention(cache, batch, max_groups=1)
+    att.ws[256:].fill_(0x77)
+    plain = att.attend().clone(), att.lse.clone()
+    out = att.attend_shared(ints(at))
+    assert att.errors() == 0
+    got, skip = decided(att, len(lens), 1)
+    assert (got[0][0] != 0x77777777) == looks
+    if looks:
+        want = expected(lens, indptr, table, at, H, G, 768)
+        assert got[0][0] == want[0][0][0] and skip[:at[1]] == want[1][:at[1]]
+    else:
+        assert torch.equal(out, plain[0]) and torch.equal(att.lse, plain[1])
