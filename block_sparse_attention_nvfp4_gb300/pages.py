@@ -93,7 +93,7 @@ class PagePool:
                              f"{tuple(t.shape)} on {t.device}")
         return t.data_ptr()
 
-    def _run(self, name: str, stream, *args):
+    def _unchanged(self):
         for owner, names, get, bound in self._bound:
             if not all(map(operator.is_, get(owner), bound)):
                 changed = [n for n, x, y in zip(names, get(owner), bound) if x is not y]
@@ -102,6 +102,9 @@ class PagePool:
             names = [n for x in self._bound for n in x[1]]
             changed = [n for n, t, a in zip(names, self._tensors, self._at) if _address(t) != a]
             raise ValueError(f"{', '.join(changed)}: moved after the pool was made")
+
+    def _run(self, name: str, stream, *args):
+        self._unchanged()
         with self._lock:
             _call(self.device, stream, self._fns[name], name, self._ref, *args, *self._ws)
 
@@ -166,27 +169,27 @@ class PagePool:
         caches, most, index = self._evict_caches, self._most, self._index
         if caches is None:
             caches = self._evictable()
-        caches = type(caches).from_buffer_copy(caches)     # this call's: they get its weights
         weights = (weights,) if isinstance(weights, torch.Tensor) else tuple(weights)
         if len(weights) != len(caches):
             raise ValueError(f"weights: expected {len(caches)} (one for each cache), got {len(weights)}")
         n = children.numel()
         at = self._list(parents, n, "parents"), self._list(children, n, "children")
-        for x, heads, w in zip(caches, self._evict_shapes, weights):
-            shape = w.shape
-            tokens = shape[-1] if shape else 0
-            if tokens < most:
-                raise ValueError(f"weights: expected at least {most} tokens a head, got {tokens}")
-            if w.dtype is torch.float32 and w.get_device() == index and shape == (*heads, tokens) and w.is_contiguous():
-                x.weights = w.data_ptr()
-            else:
-                x.weights = _plain(w, torch.float32, (*heads, tokens), self.device, "weights")   # (says what is wrong)
-            x.head_stride = tokens
         if not (0 < keep <= _INT_MAX and 0 <= sinks and 0 <= recent and sinks + recent <= keep):
             raise ValueError(f"evict: expected keep >= 1 and sinks + recent <= keep, got {keep}, {sinks}, {recent}")
         # (what msa_pages_evict_scratch_size says; none where no sequence can be longer than keep)
         need = n * self._evict_bytes * keep if keep < most else 0
-        with self._lock:
+        self._unchanged()
+        with self._lock:      # (the weights' addresses stand in `caches` until the launch)
+            for x, heads, w in zip(caches, self._evict_shapes, weights):
+                shape = w.shape
+                tokens = shape[-1] if shape else 0
+                if tokens < most:
+                    raise ValueError(f"weights: expected at least {most} tokens a head, got {tokens}")
+                if w.dtype is torch.float32 and w.get_device() == index and shape == (*heads, tokens) and w.is_contiguous():
+                    x.weights = w.data_ptr()
+                else:
+                    x.weights = _plain(w, torch.float32, (*heads, tokens), self.device, "weights")   # (says what is wrong)
+                x.head_stride = tokens
             scratch = self._scratch
             if scratch is None or scratch[1] < need:
                 if scratch is not None:
@@ -195,7 +198,8 @@ class PagePool:
                 with torch.cuda.device(self.device), torch.cuda.stream(stream):
                     t = torch.empty(size, dtype=torch.uint8, device=self.device)
                 scratch = self._scratch = (t.data_ptr(), size, t)
-            self._run("msa_pages_evict", stream, n, *at, len(caches), caches, keep, sinks, recent, scratch[0], scratch[1])
+            _call(self.device, stream, self._fns["msa_pages_evict"], "msa_pages_evict", self._ref, n, *at, len(caches), caches,
+                  keep, sinks, recent, scratch[0], scratch[1], *self._ws)
 
     def errors(self, stream=None) -> int:
         """Device error flags since the last read (synchronises the stream)."""
