@@ -30,7 +30,7 @@ __device__ __forceinline__ long long warp_sum(long long x) {
 // alone / the plain call, us):
 //     768 saved, 4 members   26.7 / 26.8 / 20.7      1,792, 8 members       26.7 / 32.9 / 26.8
 //     896, 8 members         26.4 / 26.8 / 22.6      1,920, 16 members      28.5 / 36.9 / 27.0
-//     960, 16 members        27.3 / 30.9 / 22.8      3,072, 4 groups of 4   32.9 / 42.8 / 37.0
+//     960, 16 members        27.3 / 30.9 / 22.8      3,360, 4 groups of 4   32.9 / 43.2 / 38.6
 //   1,536, 4 groups of 4     28.9 / 32.9 / 26.9      3,840, 16 members      30.8 / 47.4 / 37.0
 // The sizes have the table's width, not the lengths, which are on the device: 4 samples on 31 shared pages take 16.6 us, the
 // plain call, with a table as wide as they are long, and 22.6 with one of 512 pages, behind the groups' kernel but alone.
